@@ -5,12 +5,12 @@ batch built from its request lengths ("tables"), new keys and values quantised i
 slots ("append"), attention over the 4-bit cache ("attention"), and sampling of the next
 token from the logits ("sample").
 
-The cache is one uint8 tensor [pages][kv_heads][page_size * (head_dim + 6)]. A (page, head)
-block of P tokens and head dimension D holds, in this order:
-  K codes   [P][D/2]: byte j of a token holds d = 2j in bits 0..3 and d = 2j + 1 in bits 4..7;
-  V codes   [P/16][2][8][4][D/32][2] 16-bit words: word (tile, h, n, c, w, e) holds, in nibble
-            i (bits 4i..4i+3), d = n*D/8 + 4w + i of token 16*tile + 8h + 2c + e;
-  K scales  binary16 [P];  V scales  binary16 [P];  K zero-points  uint8 [P];  V zero-points.
+The cache is one uint8 tensor [pages][kv_heads][page_size / 16][16 * (head_dim + 6)]. A tile
+of 16 tokens and head dimension D holds, in this order:
+  K codes   [16][D/2]: byte j of a token holds d = 2j in bits 0..3 and d = 2j + 1 in bits 4..7;
+  V codes   [2][8][4][D/32][2] 16-bit words: word (h, n, c, w, e) holds, in nibble i (bits
+            4i..4i+3), d = n*D/8 + 4w + i of token 8h + 2c + e;
+  K scales  binary16 [16];  V scales  binary16 [16];  K zero-points  uint8 [16];  V zero-points.
 A stored value is (code - zero) * scale. A row x of D values is stored with
   lo = min(x, 0), hi = max(x, 0), s = fp16(min((hi - lo) / 15, 65504)), r = 1 / s,
   z = clamp(rint(-lo * r), 0, 15), code = clamp(rint(x * r) + z, 0, 15)   (s = 0: all zero),
@@ -215,7 +215,7 @@ def prepare(case, seed):
         s.update(logits=x.to(HALF[case["dtype"]]), temp=temp, top_k=top_k, top_p=top_p, min_p=min_p, u=u)
         return s
     h, kv, d, p = case["q_heads"], case["kv_heads"], case["dim"], case["page"]
-    block = p * (d + 6)
+    tile = 16 * (d + 6)
     dtype = HALF[case["dtype"]]
     width = (h + 2 * kv) * d
     if case["op"] == "append":
@@ -227,7 +227,7 @@ def prepare(case, seed):
         x = x.to(dtype).view(t, width)
         slots = torch.randperm(pages * p, generator=g, device=DEV)[:t].to(torch.int64)
         s.update(k=x[:, h * d:(h + kv) * d].view(t, kv, d), v=x[:, (h + kv) * d:].view(t, kv, d), slots=slots,
-                 cache=torch.zeros(pages, kv, block, dtype=torch.uint8, device=DEV))
+                 cache=torch.zeros(pages, kv, p // 16, tile, dtype=torch.uint8, device=DEV))
         return s
     new, seq = _lengths(case)
     cols = max(1, max(-(-b // p) for b in seq))
@@ -241,22 +241,23 @@ def prepare(case, seed):
     # codes bell-shaped about the zero-point, scales log-normal about 0.25
     normal = torch.erfinv((torch.arange(256, device=DEV) + 0.5) / 128 - 1) * math.sqrt(2)
     nib = (7.5 + 2.6 * normal).round().clamp(0, 15).to(torch.uint8)
-    cache = torch.empty(pages, kv, block, dtype=torch.uint8, device=DEV)
-    cache[:, :, :p * d] = nib[torch.randint(0, 256, (pages, kv, p * d), generator=g, device=DEV, dtype=torch.int32)]
-    cache[:, :, :p * d] |= nib[torch.randint(0, 256, (pages, kv, p * d), generator=g, device=DEV, dtype=torch.int32)] << 4
-    scale = torch.exp(0.3 * torch.randn(pages, kv, 2 * p, generator=g, device=DEV)) * 0.25
+    cache = torch.empty(pages, kv, p // 16, tile, dtype=torch.uint8, device=DEV)
+    shape = (pages, kv, p // 16, 16 * d)
+    cache[..., :16 * d] = nib[torch.randint(0, 256, shape, generator=g, device=DEV, dtype=torch.int32)]
+    cache[..., :16 * d] |= nib[torch.randint(0, 256, shape, generator=g, device=DEV, dtype=torch.int32)] << 4
+    scale = torch.exp(0.3 * torch.randn(pages, kv, p // 16, 2, 16, generator=g, device=DEV)) * 0.25
     # a page's tokens past its request's length, and pages that nobody holds, are memory as it was found: NaN
     end = torch.full((pages,), 0, dtype=torch.int64, device=DEV)
     left = (_ints(seq, torch.int64)[:, None] - col[None] * p).clamp(0, p)
     end[table[has].long()] = left[has]
-    stale = torch.arange(p, device=DEV)[None] >= end[:, None]
-    scale = torch.where(stale[:, None, None].expand(pages, kv, 2, p).reshape(pages, kv, 2 * p), math.nan, scale)
-    cache[:, :, p * d:p * d + 4 * p] = scale.to(torch.float16).view(torch.uint8)
-    cache[:, :, p * d + 4 * p:] = torch.randint(5, 11, (pages, kv, 2 * p), generator=g, device=DEV, dtype=torch.uint8)
+    stale = (torch.arange(p, device=DEV)[None] >= end[:, None]).view(pages, 1, p // 16, 1, 16)
+    scale = torch.where(stale, math.nan, scale).to(torch.float16)
+    cache[..., 16 * d:16 * d + 64] = scale.view(torch.uint8).view(pages, kv, p // 16, 64)
+    cache[..., 16 * d + 64:] = torch.randint(5, 11, (pages, kv, p // 16, 32), generator=g, device=DEV, dtype=torch.uint8)
     t = sum(new)
     x = (1.5 * torch.randn(t, width, generator=g, device=DEV)).to(dtype)
     s.update(q=x[:, :h * d].view(t, h, d), cache=cache, table=table, seq=_ints(seq), starts=_ints(_starts(new)),
-             max_q=max(new), max_seq=max(seq))
+             max_q=max(new))
     return s
 
 
@@ -271,10 +272,10 @@ def run(s):
             return [s["table"], slots, positions, starts, taken]
         if s["op"] == "append":
             w4a16.kv4_append(s["k"], s["v"], s["slots"], s["cache"], c["page"])
-            return w4a16.kv4_read(s["cache"], s["slots"], c["page"], c["dim"], dtype=s["k"].dtype)
+            return w4a16.kv4_read(s["cache"], s["slots"], c["page"], dtype=s["k"].dtype)
         if s["op"] == "attention":
             return w4a16.kv4_attention(s["q"], s["cache"], s["table"], s["seq"], s["starts"], c["page"], s["max_q"],
-                                       s["max_seq"], window=c["window"], return_lse=c["lse"])
+                                       window=c["window"], return_lse=c["lse"])
         return w4a16.sample(s["logits"], s["u"], s["temp"], s["top_k"], s["top_p"], s["min_p"])
     return {"tables": _tables, "append": _append, "attention": _attention, "sample": _sample}[s["op"]](s, c)
 
@@ -317,23 +318,23 @@ def _quantise(x):
     return code.to(torch.int32), scale, zero.to(torch.uint8)
 
 
-def _places(tok, d, p):
-    """Bytes of a block that hold a token's codes: K [..][d/2], V [..][d/2], and of its scales and zero-points."""
+def _places(tok, d):
+    """Bytes of a tile that hold a token's codes: K [..][d/2], V [..][d/2], and of its scales and zero-points."""
     j = torch.arange(d // 2, device=DEV)
     k = tok[:, None] * (d // 2) + j
     n, r = 2 * j // (d // 8), 2 * j % (d // 8)              # byte j of a V row: d = 2j and 2j + 1
-    tile, h, cc, e = tok // 16, tok % 16 // 8, tok % 8 // 2, tok % 2
-    word = (((tile * 2 + h)[:, None] * 8 + n) * 4 + cc[:, None]) * (d // 32) + r // 4
-    v = p * (d // 2) + (word * 2 + e[:, None]) * 2 + r % 4 // 2
-    return k, v, p * d + 2 * tok, p * d + 2 * p + 2 * tok, p * d + 4 * p + tok, p * d + 5 * p + tok
+    h, cc, e = tok // 8, tok % 8 // 2, tok % 2
+    word = ((h[:, None] * 8 + n) * 4 + cc[:, None]) * (d // 32) + r // 4
+    v = 8 * d + (word * 2 + e[:, None]) * 2 + r % 4 // 2
+    return k, v, 16 * d + 2 * tok, 16 * d + 32 + 2 * tok, 16 * d + 64 + tok, 16 * d + 80 + tok
 
 
 def _append(s, c):
     p, d, cache = c["page"], c["dim"], s["cache"]
-    kv, block = cache.shape[1], cache.shape[2]
+    kv, tile = cache.shape[1], cache.shape[3]
     page, tok = s["slots"] // p, s["slots"] % p
-    base = (page[:, None] * kv + torch.arange(kv, device=DEV)) * block       # [t][kv]
-    k_at, v_at, ks_at, vs_at, kz_at, vz_at = _places(tok, d, p)
+    base = ((page[:, None] * kv + torch.arange(kv, device=DEV)) * (p // 16) + tok[:, None] // 16) * tile   # [t][kv]
+    k_at, v_at, ks_at, vs_at, kz_at, vz_at = _places(tok % 16, d)
     flat = cache.view(-1)
     two = torch.arange(2, device=DEV)
     out = []
@@ -354,10 +355,10 @@ def _attention(s, c):
     table, seq, starts, q = s["table"].long(), s["seq"].long(), s["starts"].long(), s["q"]
     n, cols, t, m, group = table.shape[0], table.shape[1], q.shape[0], s["max_q"], h // kv
     length = cols * p
-    blocks = s["cache"][table.clamp(min=0)].transpose(1, 2)                     # [n][kv][cols][block]
-    par = blocks[..., p * d:].contiguous()
-    scale = par[..., :4 * p].contiguous().view(torch.float16).float().view(n, kv, cols, 2, p)
-    zero = par[..., 4 * p:].float().view(n, kv, cols, 2, p)
+    tiles = length // 16
+    raw = s["cache"][table.clamp(min=0)].transpose(1, 2).reshape(n, kv, tiles, 16 * (d + 6))
+    scale = raw[..., 16 * d:16 * d + 64].contiguous().view(torch.float16).float().view(n, kv, tiles, 2, 16)
+    zero = raw[..., 16 * d + 64:].float().view(n, kv, tiles, 2, 16)
     seen = torch.arange(length, device=DEV)[None] < seq[:, None]                # [n][length]
     ok = seen[:, None, :, None]
 
@@ -365,12 +366,12 @@ def _attention(s, c):
         x = (code.float() - zero[..., which, :, None]) * scale[..., which, :, None]
         return torch.where(ok, x.view(n, kv, length, d), 0.0)
 
-    byte = blocks[..., :p * d // 2]
-    k = value(torch.stack([byte & 15, byte >> 4], -1).view(n, kv, cols, p, d), 0)
-    byte = blocks[..., p * d // 2:p * d]
-    code = torch.stack([byte & 15, byte >> 4], -1).view(n, kv, cols, p // 16, 2, 8, 4, d // 32, 2, 4)
-    v = value(code.permute(0, 1, 2, 3, 4, 6, 8, 5, 7, 9).reshape(n, kv, cols, p, d), 1)
-    del blocks, byte, code
+    byte = raw[..., :8 * d]
+    k = value(torch.stack([byte & 15, byte >> 4], -1).view(n, kv, tiles, 16, d), 0)
+    byte = raw[..., 8 * d:16 * d]
+    code = torch.stack([byte & 15, byte >> 4], -1).view(n, kv, tiles, 2, 8, 4, d // 32, 2, 4)
+    v = value(code.permute(0, 1, 2, 3, 5, 7, 4, 6, 8).reshape(n, kv, tiles, 16, d), 1)
+    del raw, byte, code
     i = torch.arange(m, device=DEV)
     at = (starts[:-1, None] + i).clamp(max=max(t - 1, 0))                       # [n][m]
     qs = q[at].float().view(n, m, kv, group, d).permute(0, 2, 3, 1, 4).reshape(n, kv, group * m, d)
@@ -474,19 +475,18 @@ def exact(case, seed):
             continue
         pages = s["table"][b, :-(-n // p)].long()
         for g in range(kv):
-            raw = s["cache"][pages, g]                   # [pages][block]
-            kc, vc = raw[:, :p * d // 2].long(), raw[:, p * d // 2:p * d].reshape(-1, p // 16, 2, 8, 4, d // 32, 4).long()
-            sc = raw[:, p * d:p * d + 4 * p].contiguous().view(torch.float16).double()
-            zc = raw[:, p * d + 4 * p:].double()
-            key = torch.zeros(pages.numel(), p, d, dtype=torch.float64, device=DEV)
+            raw = s["cache"][pages, g].reshape(-1, 16 * (d + 6))                # [tiles][bytes]
+            kc, vc = raw[:, :8 * d].long().view(-1, 16, d // 2), raw[:, 8 * d:16 * d].long().view(-1, 2, 8, 4, d // 32, 4)
+            sc = raw[:, 16 * d:16 * d + 64].contiguous().view(torch.float16).double()
+            zc = raw[:, 16 * d + 64:].double()
+            key = torch.zeros(raw.shape[0], 16, d, dtype=torch.float64, device=DEV)
             val = torch.zeros_like(key)
-            kc = kc.view(-1, p, d // 2)
             key[..., 0::2], key[..., 1::2] = (kc % 16).double(), (kc // 16).double()
-            for tok in range(p):
-                two = vc[:, tok // 16, tok % 16 // 8, :, tok % 8 // 2, :, 2 * (tok % 2):2 * (tok % 2) + 2]  # [pages][8][d/32][2]
+            for tok in range(16):
+                two = vc[:, tok // 8, :, tok % 8 // 2, :, 2 * (tok % 2):2 * (tok % 2) + 2]        # [tiles][8][d/32][2]
                 val[:, tok] = torch.stack([two % 16, two // 16], -1).reshape(-1, d).double()
-            key = ((key - zc[:, :p, None]) * sc[:, :p, None]).view(-1, d)[:n]
-            val = ((val - zc[:, p:, None]) * sc[:, p:, None]).view(-1, d)[:n]
+            key = ((key - zc[:, :16, None]) * sc[:, :16, None]).view(-1, d)[:n]
+            val = ((val - zc[:, 16:, None]) * sc[:, 16:, None]).view(-1, d)[:n]
             pos = torch.arange(n - a, n, device=DEV)[:, None]
             col = torch.arange(n, device=DEV)[None]
             see = (col <= pos) if not case["window"] else (col <= pos) & (col > pos - case["window"])
