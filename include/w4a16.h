@@ -432,6 +432,140 @@ w4a16_status w4a16_gemm_noalloc(const uint16_t* x, const uint32_t* packed,
                                 const uint16_t* scales_packed, uint16_t* y,
                                 int M, int N, int K, int group_size, w4a16_stream_t stream);
 
+/* ---------------------------------------------------------------- the serving step
+ * What a decoder runs beside its 4-bit matmuls: a paged key-value cache held in 4
+ * bits (block tables, new keys and values, attention) and the sampling of the next
+ * token. The pages have no counterpart. All calls enqueue on `stream` without
+ * synchronising and can be captured into a CUDA Graph (the first call on a device
+ * outside capture); lengths, tables and settings are device arrays that are read
+ * when the kernels run. Results are the same on every call with equal inputs.
+ *
+ * The cache: uint8 [pages][kv_heads][page_size / 16][16 * (D + 6)], 16-byte aligned,
+ * w4a16_kv4_page_bytes() a page; D = head_dim is 64 or 128, page_size 16, 32, 64, 128
+ * or 256. Slot s is token s mod page_size of page s / page_size. A tile of 16 tokens:
+ *   K codes   [16][D/2]: byte j of a token holds d = 2j in bits 0..3, 2j + 1 in bits 4..7
+ *   V codes   [2][8][4][D/32][2] 16-bit words: word (h, n, c, w, e) holds, in bits
+ *             4i..4i+3, d = n*D/8 + 4w + i of token 8h + 2c + e
+ *   K scales  binary16 [16];  V scales  binary16 [16]
+ *   K zero-points  uint8 [16];  V zero-points  uint8 [16]
+ * A stored value is (code - zero) * scale, one scale and zero-point for a token's row
+ * of D values. A row x is stored, in FP32 with IEEE operations, as
+ *   lo = min(x, 0), hi = max(x, 0), s = binary16(min((hi - lo) / 15, 65504)), r = 1 / s,
+ *   zero = clamp(rint(-lo * r), 0, 15), code = clamp(rint(x * r) + zero, 0, 15)
+ * (s = 0: codes and zero-point 0). A row that holds an infinity or a NaN gets scale
+ * NaN, which shows in whatever reads it. Memory of the cache that no slot was written
+ * to may hold anything. */
+typedef enum { W4A16_FP16 = 0, W4A16_BF16 = 1, W4A16_FP32 = 2 } w4a16_dtype;
+
+/* Bytes of one page of the cache (0 for sizes it does not have). */
+size_t w4a16_kv4_page_bytes(int kv_heads, int head_dim, int page_size);
+
+/*
+ * Block tables and slot maps of a batch, from its lengths, in one launch.
+ *   seq_lens     device, int32 [batch]: tokens of each request with this step's new ones
+ *   new_lens     device, int32 [batch]: this step's new tokens (negative counts as 0)
+ *   free_pages   device, int32 [n_free]: pages nobody holds, taken in order
+ *   taken_in     device, int32 [1]: how many of them are taken already; NULL: none
+ *   taken_out    device out, int32 [1]: how many are taken after this call; more than
+ *                n_free means that pages were short. Must not be taken_in.
+ *   block_table  device in/out, int32 [batch][max_pages]: columns below
+ *                ceil((seq - new) / page_size) are kept; those below ceil(seq / page_size)
+ *                get pages from the free list, requests in order (-1 where it is short);
+ *                the others get -1
+ *   slots        device out, int64 [max_tokens]: the new tokens' slots, request by
+ *                request; -1 for a token without a page, at a negative position or
+ *                past max_pages, and for places past the batch's new tokens
+ *   positions    device out, int32 [max_tokens]: their positions, seq - new + i; -1 past them
+ *   starts       device out, int32 [batch + 1]: each request's first new token, and their
+ *                sum. Tokens past max_tokens are counted but get no slot.
+ */
+w4a16_status w4a16_kv4_tables(const int32_t* seq_lens, const int32_t* new_lens, int batch,
+                              const int32_t* free_pages, int n_free, const int32_t* taken_in,
+                              int32_t* taken_out, int32_t* block_table, int max_pages, int page_size,
+                              int64_t* slots, int32_t* positions, int max_tokens, int32_t* starts,
+                              w4a16_stream_t stream);
+
+/*
+ * Quantises new keys and values into their slots.
+ *   k, v     device, binary16 or bfloat16, token t's head h at t * token_stride +
+ *            h * head_stride elements (slices of a fused projection's output work);
+ *            16-byte aligned, strides multiples of 8 and at least head_dim
+ *   slots    device, int64 [tokens]; slots outside the cache (such as -1) are skipped.
+ *            A slot given twice ends with one of its rows, K and V each whole or mixed.
+ *   cache    device in/out, of `pages` pages
+ *   dtype    W4A16_FP16 or W4A16_BF16
+ */
+w4a16_status w4a16_kv4_append(const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                              const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                              const int64_t* slots, uint8_t* cache, int pages, int tokens,
+                              int kv_heads, int head_dim, int page_size, int dtype,
+                              w4a16_stream_t stream);
+
+/* The values that slots stand for, rounded once to dtype (any w4a16_dtype): k and v are
+ * device out, [tokens][kv_heads][head_dim], 16-byte aligned; slots outside the cache read 0. */
+w4a16_status w4a16_kv4_read(const uint8_t* cache, int pages, const int64_t* slots, void* k, void* v,
+                            int tokens, int kv_heads, int head_dim, int page_size, int dtype,
+                            w4a16_stream_t stream);
+
+/* Bytes of caller workspace w4a16_kv4_attention needs on the current device (0 if the
+ * device cannot be used). */
+size_t w4a16_kv4_workspace_bytes(void);
+
+/*
+ * Causal attention of new query tokens over the cache, which holds their own keys and
+ * values already: query i of a request with n queries and s cached tokens has position
+ * s - n + i and sees the cached tokens at positions up to its own and, if window > 0,
+ * above its own minus window. out = softmax(scale * q K^T) V; a query that sees nothing
+ * gets zeros (and lse -infinity). Query heads h * g .. h * g + g - 1 share KV head h
+ * (g = q_heads / kv_heads).
+ *   q, out       device, binary16 or bfloat16 [tokens][q_heads][head_dim] at token and
+ *                head strides in elements (multiples of 8, at least head_dim), 16-byte
+ *                aligned; out must not overlap an input
+ *   block_table  device, int32 rows of table_cols pages, table_stride apart; an entry
+ *                outside the cache hides its tokens
+ *   seq_lens     device, int32 [batch]; starts: device, int32 [batch + 1], request b's
+ *                queries are tokens starts[b] .. starts[b + 1] - 1 (as w4a16_kv4_tables
+ *                writes them). Tokens of no request are not written.
+ *   lse          device out, float [tokens][q_heads]: log of the softmax's sum, or NULL
+ *   max_q        the largest number of queries of a request, or more: it chooses the
+ *                kernel; results hold for any value
+ *   scale        the softmax scale, usually 1 / sqrt(head_dim)
+ *   workspace    w4a16_kv4_workspace_bytes() bytes, 256-byte aligned, zeroed once; or
+ *                NULL for the library's own (shared with the GEMMs: calls that use it
+ *                must not overlap in time on different streams)
+ */
+w4a16_status w4a16_kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                 const uint8_t* cache, int pages, const int32_t* block_table,
+                                 int64_t table_stride, int table_cols, const int32_t* seq_lens,
+                                 const int32_t* starts, void* out, int64_t out_token_stride,
+                                 int64_t out_head_stride, float* lse, int batch, int tokens,
+                                 int q_heads, int kv_heads, int head_dim, int page_size, int max_q,
+                                 float scale, int window, int dtype, void* workspace,
+                                 size_t ws_bytes, w4a16_stream_t stream);
+
+/*
+ * Samples one token per row. With m the row's maximum and e(x) = exp((x - m) / T) in
+ * FP32, a token weighs rint(2^31 e(x)), a whole number, so that sums are exact and do not
+ * depend on their order. Tokens are ranked by logit, equal ones by index. In turn, top-k
+ * keeps ranks below k; top-p keeps a token if the weight ranked before it is below p times
+ * the weight of what top-k kept; min-p keeps e(x) >= min_p; the first rank is always
+ * kept. The result is the first token, in index order, at which the running kept weight
+ * exceeds floor(u * kept weight). NaN logits count as -infinity; a row without a
+ * logit above -infinity gives token -1 and probability 0.
+ *   logits       device, [batch] rows row_stride elements apart, vocab (at most 262144)
+ *                valid; W4A16_FP16, W4A16_BF16 or W4A16_FP32, any element alignment
+ *   u            device, float [batch], uniform in [0, 1)
+ *   temperature  device, float [batch], or NULL for 1; not above 0: the largest logit
+ *   top_k        device, int32 [batch], or NULL; 0 or less: no limit
+ *   top_p, min_p device, float [batch], or NULL for 1 and 0
+ *   token        device out, int32 [batch];  prob: device out, float [batch], the token's
+ *                share of the kept weight, or NULL
+ */
+w4a16_status w4a16_sample(const void* logits, int64_t row_stride, const float* u,
+                          const float* temperature, const int32_t* top_k, const float* top_p,
+                          const float* min_p, int32_t* token, float* prob, int batch, int vocab,
+                          int dtype, w4a16_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,9 +8,12 @@
 #include <cstdlib>
 #include <mutex>
 
+#include "api_internal.cuh"
 #include "gemm_tc.cuh"
 #include "decode.cuh"
 #include "gemv.cuh"
+#include "kv4.cuh"
+#include "sample.cuh"
 #include "w4a16.h"
 
 namespace w4a16 {
@@ -63,9 +66,9 @@ w4a16_status from_cuda(cudaError_t e)
 
 // Workspace layout (fixed, whatever the shape): error word at 0, split-K
 // counters at 256 (one int per CTA, at most kMaxGrid), FP32 partials after.
-constexpr size_t kCountersOff = 256;
-constexpr int kMaxGrid = 1024;
-constexpr size_t kPartialsOff = kCountersOff + 4 * kMaxGrid;
+constexpr size_t kCountersOff = kWsCountersOff;
+constexpr int kMaxGrid = kWsMaxGrid;
+constexpr size_t kPartialsOff = kWsPartialsOff;
 constexpr int kMaxTileM = 256;
 constexpr int kMinItersPerCta = 4;
 // Split cost model for fewer tiles than work units (make_plan), fitted (least
@@ -397,7 +400,9 @@ w4a16_status device_state(DeviceState** out)
             (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
             return from_cuda(e);
         if (major != 10 || minor != 3) return W4A16_ERR_UNSUPPORTED;  // built for sm_103a only
-        if ((e = setup_gemv()) != cudaSuccess || (e = setup_decode()) != cudaSuccess) return from_cuda(e);
+        if ((e = setup_gemv()) != cudaSuccess || (e = setup_decode()) != cudaSuccess ||
+            (e = setup_kv4()) != cudaSuccess || (e = setup_sample()) != cudaSuccess)
+            return from_cuda(e);
         void* gs = nullptr;
         if ((e = cudaGetSymbolAddress(&gs, g_gemv_status)) != cudaSuccess) return from_cuda(e);
         st.gemv_status = static_cast<int*>(gs);
@@ -690,6 +695,30 @@ w4a16_status gemm_impl(const uint16_t* x, const uint32_t* packed, const uint16_t
 void* noalloc_scratch_if_set();
 
 }  // namespace
+
+namespace w4a16 {
+
+w4a16_status report_cuda(cudaError_t e) { return from_cuda(e); }
+
+w4a16_status device_info(DeviceInfo* info)
+{
+    DeviceState* st = nullptr;
+    const w4a16_status rc = device_state(&st);
+    if (rc != W4A16_OK) return rc;
+    info->sms = st->sms;
+    info->status = st->gemv_status;
+    info->wait_limit_ns = g_wait_limit_ns;
+    return W4A16_OK;
+}
+
+w4a16_status library_workspace(void** ws, size_t* bytes)
+{
+    DeviceState* st = nullptr;
+    const w4a16_status rc = device_state(&st);
+    return rc != W4A16_OK ? rc : own_workspace(st, ws, bytes);
+}
+
+}  // namespace w4a16
 
 extern "C" {
 

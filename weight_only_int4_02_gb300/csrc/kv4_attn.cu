@@ -1,0 +1,689 @@
+// Attention over the 4-bit paged cache for few query rows (a decode step, drafted
+// tokens): O = softmax(scale * Q K^T) V with K, V = (code - zero) * scale.
+//
+// A segment is one request's KV head and up to 8 NR rows (query token, query head of
+// the group); its cached tokens are cut into units of 32, and the units of all segments,
+// laid end to end, are dealt to the CTAs in equal runs (stream-K), so ragged lengths, one
+// long request and a thousand short ones fill the GPU alike. The lengths stay on the
+// device: every CTA sums them by itself. A segment cut by a run's end is joined through
+// the workspace by the last of its CTAs to arrive, in the CTAs' order.
+//
+// In a CTA, four warps take a run's units in turn, each with its own ring of bulk copies
+// and barriers (no CTA barrier in the loop), and keep their own running maximum, sum and
+// output. Mathematics, with c the code, z the zero-point, s the scale of a token:
+//   score = s_k (q . c_k - z_k sum(q)) * scale,   out = sum_t p_t s_v (c_v - z_v) / sum_t p_t
+// so the MMAs multiply by the bare codes: an unpacked register is one logic operation (two
+// codes as binary16 subnormals, exact), K's scale and zero-point act on scores and V's on
+// probabilities, once a (token, row). Tokens are the MMA's M for K (A = 16 tokens x
+// 16 d) and d is for V (A = 16 d x 16 tokens), so that eight rows are the MMA's N and cost
+// eight columns. Q is scaled per row by a power of two into binary16's range (exact
+// for binary16 and bfloat16 inputs). Probabilities times V's scale are fed as a high
+// and a low binary16 part, 22 bits: one part alone would add a rounding as large as that of
+// a binary16 output, and there is no time to gain (bound by bytes). Scores, sums, maxima
+// and outputs are FP32.
+#include "api_internal.cuh"
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+#include <float.h>
+#include <math_constants.h>
+
+namespace w4a16 {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnit = 32;      // tokens of a unit: two tiles
+constexpr int kStages = 4;     // units in flight per warp
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // e in -126 .. 127
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 bits_half2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+
+// One request as the kernel sees it: every length clamped to what the buffers hold.
+struct Request {
+    int seq, q0, nq, rows, tiles;   // cached tokens, first query token, query tokens, rows, row tiles
+    int base, units;                // first cached token looked at (a multiple of kUnit), units a segment
+    long long work;                 // units of all its segments
+};
+
+template <int ROWS>
+__device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b)
+{
+    Request r;
+    const long long held = (long long)p.table_cols * p.page_size;
+    int s = p.seq_lens[b];
+    s = s < 0 ? 0 : s;
+    r.seq = s < held ? s : (int)held;
+    int a = p.starts[b], e = p.starts[b + 1];
+    a = a < 0 ? 0 : a > p.tokens ? p.tokens : a;
+    e = e < a ? a : e > p.tokens ? p.tokens : e;
+    r.q0 = a;
+    r.nq = e - a;
+    r.rows = r.nq * p.group;
+    r.tiles = (r.rows + ROWS - 1) / ROWS;
+    const int first = r.seq - r.nq - p.window + 1;   // first token the first query's window holds
+    r.base = (p.window > 0 && first > 0) ? first / kUnit * kUnit : 0;
+    r.units = r.seq > r.base ? (r.seq - r.base + kUnit - 1) / kUnit : 1;   // an empty segment still writes its rows
+    r.work = (long long)r.tiles * p.kv_heads * r.units;
+    return r;
+}
+
+template <int D, int NR>
+struct Attn {
+    static constexpr int ROWS = 8 * NR;
+    static constexpr int TB = kv4_tile_bytes(D);
+    static constexpr int STAGE = 2 * TB;
+    static constexpr int RING = kStages * STAGE;
+    static constexpr int W = D / 32;            // words of a lane's share
+    static constexpr int PART = ROWS * (D + 2); // floats of one partial: O, then m and l
+    static_assert(RING >= ROWS * D * 4, "a warp's ring holds its output");
+    struct Shared {
+        uint64_t bar[kWarps][kStages];
+        float m[kWarps][ROWS], l[kWarps][ROWS];
+        float weight[kWarps][ROWS];
+        long long scan[kWarps];
+        long long start_off;
+        int start_b, abort_flag, last;
+    };
+    static constexpr int SMEM = kWarps * RING + sizeof(Shared);
+};
+
+template <int W>
+__device__ __forceinline__ void lds_share(const uint8_t* at, uint32_t (&w)[W])
+{
+    if constexpr (W == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(at);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
+        w[0] = v.x;
+        w[1] = v.y;
+    }
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams p)
+{
+    using A = Attn<D, NR>;
+    constexpr int W = A::W, ROWS = A::ROWS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    typename A::Shared& sh = *reinterpret_cast<typename A::Shared*>(smem + kWarps * A::RING);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = lane >> 2, c = lane & 3;
+    uint8_t* const ring = smem + warp * A::RING;
+
+    // ---- this CTA's run of units
+    long long sum = 0;
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int bl = tid * per, bh = bl + per < p.batch ? bl + per : p.batch;
+    for (int b = bl; b < bh; ++b) sum += request_of<ROWS>(p, b).work;
+    long long incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) sh.scan[warp] = incl;
+    if (tid == 0) {
+        sh.abort_flag = 0;
+        sh.start_b = p.batch;
+    }
+    if (lane < kStages) mbar_init(smem_addr(&sh.bar[warp][lane]), 1);
+    fence_mbar_init();
+    __syncthreads();
+    long long excl = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) excl += sh.scan[w];
+        total += sh.scan[w];
+    }
+    // as many CTAs as give each warp a unit
+    const long long want = (total + kWarps - 1) / kWarps;
+    const long long ctas = want < gridDim.x ? want : gridDim.x;
+    if (blockIdx.x >= ctas) return;
+    const long long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+    if (u0 >= excl && u0 < excl + sum) {
+        long long at = excl;
+        for (int b = bl; b < bh; ++b) {
+            const long long w = request_of<ROWS>(p, b).work;
+            if (u0 < at + w) {
+                sh.start_b = b;
+                sh.start_off = u0 - at;
+                break;
+            }
+            at += w;
+        }
+    }
+    __syncthreads();
+    int b = sh.start_b;
+    long long off = sh.start_off;
+    if (b >= p.batch) return;   // cannot happen: u0 < total
+
+    const WaitCtl ctl{&sh.abort_flag, p.status, p.wait_limit_ns};
+    uint32_t issued = 0, used = 0, ok_bits = 0;   // units issued and used by this warp; two bits a stage: tiles present
+    bool dead = false;
+    const int page_shift = __ffs(p.page_size) - 1;
+    const int tpp_shift = page_shift - 4;         // log2(tiles per page)
+
+    Request r = request_of<ROWS>(p, b);
+    for (long long u = u0; u < u1;) {
+        while (off >= r.work) {   // next request with work
+            off -= r.work;
+            r = request_of<ROWS>(p, ++b);
+        }
+        const long long seg = off / r.units;
+        const int pos = (int)(off - seg * r.units);
+        const int head = (int)(seg / r.tiles), rt = (int)(seg - (long long)head * r.tiles);
+        const int take = (int)(r.units - pos < u1 - u ? r.units - pos : u1 - u);
+        const int row0 = rt * ROWS;
+
+        // ---- issue: lanes 0 and 1 own a unit's tiles
+        const int32_t* const trow = p.table + (long long)b * p.table_stride;
+        auto page_of = [&](int t) {   // this lane's tile of unit t: its page, or -1
+            const int tile = ((r.base + t * kUnit) >> 4) + lane;
+            return (lane < 2 && t < pos + take && tile * kKv4Tile < r.seq) ? trow[tile >> tpp_shift] : -1;
+        };
+        auto issue = [&](int t, int page) {
+            const int s = issued % kStages;
+            const int tile = ((r.base + t * kUnit) >> 4) + lane;
+            const bool ok = page >= 0 && page < p.pages;   // false in lanes 2 and up
+            const uint32_t bits = __ballot_sync(0xffffffffu, ok) & 3u;
+            ok_bits = (ok_bits & ~(3u << (2 * s))) | bits << (2 * s);
+            const uint32_t bar = smem_addr(&sh.bar[warp][s]);
+            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(bits) * A::TB);
+            __syncwarp();
+            const int next = __shfl_down_sync(0xffffffffu, page, 1), prev = __shfl_up_sync(0xffffffffu, page, 1);
+            const int in_page = tile & ((1 << tpp_shift) - 1);
+            // two tiles of one page are one copy, lane 0's
+            const bool pair0 = bits == 3u && next == page && in_page + 1 < (1 << tpp_shift);
+            const bool pair1 = bits == 3u && prev == page && in_page > 0;
+            if (ok && !(lane == 1 && pair1)) {
+                const uint8_t* src = p.cache + ((((long long)page * p.kv_heads + head) << tpp_shift) + in_page) * A::TB;
+                bulk_load(smem_addr(ring + s * A::STAGE + lane * A::TB), src, (lane == 0 && pair0) ? A::STAGE : A::TB, bar);
+            }
+            ++issued;
+        };
+        int t_issue = pos + warp;
+        int page = page_of(t_issue);
+        auto issue_next = [&]() {
+            if (t_issue < pos + take && !dead) {
+                const int ahead = page_of(t_issue + kWarps);
+                issue(t_issue, page);
+                page = ahead;
+                t_issue += kWarps;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) issue_next();
+
+        // ---- Q fragments, scaled per row by a power of two; row constants of the columns 2c, 2c + 1
+        uint32_t ql[NR][W][2], qh[NR][W][2];
+        float row_a[NR][2], row_b[NR][2];
+        int row_pos[NR][2];
+#pragma unroll
+        for (int g = 0; g < NR; ++g) {
+            const int row = row0 + g * 8 + n;
+            uint32_t raw[4 * W];
+#pragma unroll
+            for (int i = 0; i < 4 * W; ++i) raw[i] = 0;
+            if (row < r.rows) {
+                const int qi = row / p.group, h = row - qi * p.group;
+                const uint16_t* src = (const uint16_t*)p.q + (long long)(r.q0 + qi) * p.q_token +
+                                      (long long)(head * p.group + h) * p.q_head + c * (D / 4);
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+                    raw[4 * i] = v.x;
+                    raw[4 * i + 1] = v.y;
+                    raw[4 * i + 2] = v.z;
+                    raw[4 * i + 3] = v.w;
+                }
+            }
+            auto lo_of = [&](uint32_t x) { return p.bf16 ? __uint_as_float(x << 16) : bits_half2(x).x; };
+            auto hi_of = [&](uint32_t x) { return p.bf16 ? __uint_as_float(x & 0xffff0000u) : bits_half2(x).y; };
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4 * W; ++i) top = fmaxf(top, fmaxf(fabsf(lo_of(raw[i])), fabsf(hi_of(raw[i]))));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // largest magnitude into [2^13, 2^14); an infinity or a NaN stays one
+            int e = ((__float_as_int(top) >> 23) & 255) - 127 - 13;
+            e = (top == 0.0f || !(top <= FLT_MAX)) ? 0 : e < -120 ? -120 : e;
+            const float f = pow2i(-e);
+            float qsum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[2 * i] = lo_of(raw[4 * w + i]) * f;
+                    x[2 * i + 1] = hi_of(raw[4 * w + i]) * f;
+                }
+                ql[g][w][0] = half2_bits(x[0], x[4]);
+                ql[g][w][1] = half2_bits(x[2], x[6]);
+                // codes in the high nibbles come times 16
+                qh[g][w][0] = half2_bits(x[1] * 0.0625f, x[5] * 0.0625f);
+                qh[g][w][1] = half2_bits(x[3] * 0.0625f, x[7] * 0.0625f);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 a = bits_half2(ql[g][w][i]), bb = bits_half2(qh[g][w][i]);
+                    qsum += (a.x + a.y) + 16.0f * (bb.x + bb.y);
+                }
+            }
+            qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
+            qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
+            const float unit = p.scale_log2 * pow2i(e > 127 ? 127 : e);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float un = __shfl_sync(0xffffffffu, unit, (2 * c + i) * 4);
+                row_a[g][i] = un * 16777216.0f;   // codes come as c * 2^-24
+                row_b[g][i] = un * __shfl_sync(0xffffffffu, qsum, (2 * c + i) * 4);
+                const int rr = row0 + g * 8 + 2 * c + i;
+                row_pos[g][i] = rr < r.rows ? r.seq - r.nq + rr / p.group : -1;
+            }
+        }
+        // a unit needs no mask if it lies below the first row's position and inside the last row's window
+        const int last_row = (row0 + ROWS < r.rows ? row0 + ROWS : r.rows) - 1;
+        const int pos_min = r.seq - r.nq + row0 / p.group, pos_max = r.seq - r.nq + last_row / p.group;
+
+        float m[NR][2], l[NR][2], zs[NR][2], o[NR][2 * W][4];
+        int ev = -126;   // V's scales seen so far are at most 2^ev
+#pragma unroll
+        for (int g = 0; g < NR; ++g) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[g][i] = -CUDART_INF_F;
+                l[g][i] = 0.0f;
+                zs[g][i] = 0.0f;
+            }
+#pragma unroll
+            for (int w = 0; w < 2 * W; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[g][w][i] = 0.0f;
+        }
+
+        for (int t = pos + warp; t < pos + take && !dead; t += kWarps) {
+            const int s = used % kStages;
+            if (!wait_warp(smem_addr(&sh.bar[warp][s]), (used / kStages) & 1, ctl)) {
+                dead = true;
+                break;
+            }
+            const uint8_t* const st = ring + s * A::STAGE;
+            const uint32_t have = (ok_bits >> (2 * s)) & 3u;
+            const int t0 = r.base + t * kUnit;
+            const bool full = have == 3u && t0 + kUnit - 1 <= pos_min && (p.window <= 0 || t0 > pos_max - p.window);
+
+            // scores of the unit's two tiles: tokens n and n + 8 of each, rows 2c and 2c + 1
+            float sc[2][NR][4];
+            float vs[2][2], vz[2][2];
+#pragma unroll
+            for (int tl = 0; tl < 2; ++tl) {
+                const uint8_t* const tile = st + tl * A::TB;
+                uint32_t ka[W], kb[W];
+                lds_share<W>(tile + lane * (4 * W), ka);
+                lds_share<W>(tile + 8 * (D / 2) + lane * (4 * W), kb);
+                float acc[NR][4];
+#pragma unroll
+                for (int g = 0; g < NR; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[g][i] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const uint32_t ka8 = ka[w] >> 8, kb8 = kb[w] >> 8;
+#pragma unroll
+                    for (int g = 0; g < NR; ++g)
+                        mma_16816(acc[g], ka[w] & kLow, kb[w] & kLow, ka8 & kLow, kb8 & kLow, ql[g][w][0], ql[g][w][1]);
+#pragma unroll
+                    for (int g = 0; g < NR; ++g)
+                        mma_16816(acc[g], ka[w] & kHigh, kb[w] & kHigh, ka8 & kHigh, kb8 & kHigh, qh[g][w][0], qh[g][w][1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int tok = n + 8 * j;
+                    const float ks = __half2float(*reinterpret_cast<const __half*>(tile + kv4_k_scale_off(D) + 2 * tok));
+                    const float kz = (float)tile[kv4_k_zero_off(D) + tok];
+                    vs[tl][j] = __half2float(*reinterpret_cast<const __half*>(tile + kv4_v_scale_off(D) + 2 * tok));
+                    vz[tl][j] = (float)tile[kv4_v_zero_off(D) + tok];
+#pragma unroll
+                    for (int g = 0; g < NR; ++g)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            sc[tl][g][2 * j + i] = ks * (acc[g][2 * j + i] * row_a[g][i] - kz * row_b[g][i]);
+                }
+            }
+            if (!full) {
+#pragma unroll
+                for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int key = t0 + tl * kKv4Tile + n + 8 * j;
+                        const bool there = (have >> tl & 1) && key < r.seq;
+                        bool any = false;
+#pragma unroll
+                        for (int g = 0; g < NR; ++g)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const bool see = there && key <= row_pos[g][i] &&
+                                                 (p.window <= 0 || key > row_pos[g][i] - p.window);
+                                if (!see) sc[tl][g][2 * j + i] = -CUDART_INF_F;
+                                any = any || see;
+                            }
+                        // what no row here sees may be any memory; what another row sees is a stored token
+                        if (!there) vs[tl][j] = vz[tl][j] = 0.0f;
+                    }
+            }
+            // running maximum, and the exponent that bounds V's scales
+            float top[NR][2];
+            bool grow = false;
+#pragma unroll
+            for (int g = 0; g < NR; ++g)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x = fmaxf(fmaxf(sc[0][g][i], sc[0][g][2 + i]), fmaxf(sc[1][g][i], sc[1][g][2 + i]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    top[g][i] = fmaxf(m[g][i], x);
+                    grow = grow || top[g][i] > m[g][i];
+                }
+            const float vmax = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));   // drops NaN
+            const uint32_t vbits = __reduce_max_sync(0xffffffffu, vmax > 0.0f && vmax <= 65504.0f ? __float_as_uint(vmax) : 0u);
+            const int ev_new = vbits == 0u ? -126 : (int)(vbits >> 23) - 126;   // scale < 2^ev_new
+            if (__any_sync(0xffffffffu, grow) || ev_new > ev) {
+                const int en = ev_new > ev ? ev_new : ev;
+                const float shift = ev <= -126 ? 0.0f : pow2i(ev - en);   // nothing yet: zero times anything is zero
+#pragma unroll
+                for (int g = 0; g < NR; ++g) {
+                    float f[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        f[i] = top[g][i] == m[g][i] ? 1.0f : ex2(m[g][i] - top[g][i]);
+                        l[g][i] *= f[i];
+                        f[i] *= shift;
+                        zs[g][i] *= f[i];
+                        m[g][i] = top[g][i];
+                    }
+#pragma unroll
+                    for (int w = 0; w < 2 * W; ++w)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[g][w][i] *= f[i & 1];
+                }
+                ev = en;
+            }
+            const float vf = ev <= -126 ? 0.0f : pow2i(15 - ev);   // probabilities are fed below 2^15, clear of subnormals
+            uint32_t ph[2][NR][2], pl[2][NR][2];
+#pragma unroll
+            for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float v = vs[tl][j] * vf;
+#pragma unroll
+                    for (int g = 0; g < NR; ++g) {
+                        float pv[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float x = sc[tl][g][2 * j + i];
+                            const float e = ex2(x - (m[g][i] == -CUDART_INF_F ? 0.0f : m[g][i]));
+                            l[g][i] += e;
+                            pv[i] = x == -CUDART_INF_F ? 0.0f : e * v;   // a masked token's scale may be NaN
+                            zs[g][i] += pv[i] * vz[tl][j];
+                        }
+                        const uint32_t h = half2_bits(pv[0], pv[1]);
+                        const float2 back = bits_half2(h);
+                        ph[tl][g][j] = transpose8(h);
+                        pl[tl][g][j] = transpose8(half2_bits(pv[0] - back.x, pv[1] - back.y));
+                    }
+                }
+#pragma unroll
+            for (int tl = 0; tl < 2; ++tl) {
+                const uint8_t* const tile = st + tl * A::TB + kv4_v_off(D);
+                uint32_t va[W], vb[W];
+                lds_share<W>(tile + lane * (4 * W), va);
+                lds_share<W>(tile + 4 * D + lane * (4 * W), vb);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const uint32_t va8 = va[w] >> 8, vb8 = vb[w] >> 8;
+#pragma unroll
+                    for (int g = 0; g < NR; ++g) {
+                        mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, ph[tl][g][0], ph[tl][g][1]);
+                        mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, pl[tl][g][0], pl[tl][g][1]);
+                        mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, ph[tl][g][0], ph[tl][g][1]);
+                        mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, pl[tl][g][0], pl[tl][g][1]);
+                    }
+                }
+            }
+            ++used;
+            fence_proxy_async_smem();
+            __syncwarp();
+            issue_next();
+        }
+        // copies in flight after a wait gave up
+        for (; used != issued; ++used)
+            wait_drain(smem_addr(&sh.bar[warp][used % kStages]), (used / kStages) & 1, p.wait_limit_ns);
+        __syncwarp();
+
+        // ---- the four warps' shares: into shared memory, each in its own ring
+        float* const mine = reinterpret_cast<float*>(ring);
+        const float o_unit = ev <= -126 ? 0.0f : pow2i(ev - 15);
+#pragma unroll
+        for (int g = 0; g < NR; ++g) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[g][i] += __shfl_xor_sync(0xffffffffu, l[g][i], d);
+                    zs[g][i] += __shfl_xor_sync(0xffffffffu, zs[g][i], d);
+                }
+                if (n == 0) {
+                    sh.m[warp][g * 8 + 2 * c + i] = m[g][i];
+                    sh.l[warp][g * 8 + 2 * c + i] = l[g][i];
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // codes in low nibbles come as c * 2^-24, in high ones as c * 2^-20
+                    float4 x;
+                    x.x = (o[g][2 * w][i] * 16777216.0f - zs[g][i]) * o_unit;
+                    x.y = (o[g][2 * w + 1][i] * 1048576.0f - zs[g][i]) * o_unit;
+                    x.z = (o[g][2 * w][2 + i] * 16777216.0f - zs[g][i]) * o_unit;
+                    x.w = (o[g][2 * w + 1][2 + i] * 1048576.0f - zs[g][i]) * o_unit;
+                    *reinterpret_cast<float4*>(mine + (g * 8 + 2 * c + i) * D + n * (D / 8) + 4 * w) = x;
+                }
+        }
+        __syncthreads();
+        const int live = r.rows - row0 < ROWS ? r.rows - row0 : ROWS;
+        const bool whole = pos == 0 && take == r.units;
+        // joined maximum, sum and the warps' weights of each row
+        float* const part = p.partials + (long long)(2 * blockIdx.x + (pos == 0 ? 1 : 0)) * A::PART;
+        if (tid < live) {
+            float mm = -CUDART_INF_F, ll = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][tid]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = sh.m[w][tid] == mm ? 1.0f : ex2(sh.m[w][tid] - mm);
+                ll += sh.l[w][tid] * f;
+                sh.weight[w][tid] = f;
+            }
+            if (whole) {
+                const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) sh.weight[w][tid] *= inv;
+                if (p.lse) {
+                    const int rr = row0 + tid, qi = rr / p.group;
+                    p.lse[(long long)(r.q0 + qi) * p.q_heads + head * p.group + rr - qi * p.group] =
+                        ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * CUDART_LN2_F;
+                }
+            } else {
+                __stcg(part + ROWS * D + tid, mm);
+                __stcg(part + ROWS * D + ROWS + tid, ll);
+            }
+        }
+        __syncthreads();
+        auto store_row = [&](int row, int d, const float4& x) {
+            const int rr = row0 + row, qi = rr / p.group;
+            uint16_t* dst = (uint16_t*)p.out + (long long)(r.q0 + qi) * p.o_token +
+                            (long long)(head * p.group + rr - qi * p.group) * p.o_head + d;
+            uint2 w;
+            if (p.bf16) {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), bb = __floats2bfloat162_rn(x.z, x.w);
+                w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&bb));
+            } else {
+                w = make_uint2(half2_bits(x.x, x.y), half2_bits(x.z, x.w));
+            }
+            *reinterpret_cast<uint2*>(dst) = w;
+        };
+        for (int i = tid; i < live * (D / 4); i += kThreads) {
+            const int row = i / (D / 4), d = i % (D / 4) * 4;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = sh.weight[w][row];
+                const float4 y = *reinterpret_cast<const float4*>(smem + w * A::RING + (row * D + d) * 4);
+                x.x += f * y.x;
+                x.y += f * y.y;
+                x.z += f * y.z;
+                x.w += f * y.w;
+            }
+            if (whole) store_row(row, d, x);
+            else __stcg(reinterpret_cast<float4*>(part + row * D + d), x);
+        }
+        if (!whole) {
+            // ---- the last CTA of the segment to arrive joins the partial results, in the CTAs' order
+            const long long g0 = u - pos;   // the segment's first unit
+            const int ca = (int)(((g0 + 1) * ctas - 1) / total), cb = (int)(((g0 + r.units) * ctas - 1) / total);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int before = atomicAdd(p.counters + ca, 1);
+                sh.last = before == cb - ca;
+                if (sh.last) p.counters[ca] = 0;   // ready for the next launch
+                __threadfence();
+            }
+            __syncthreads();
+            if (sh.last) {
+                for (int i = tid; i < live * (D / 4); i += kThreads) {
+                    const int row = i / (D / 4), d = i % (D / 4) * 4;
+                    float mm = -CUDART_INF_F, ll = 0.0f;
+                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int k = ca; k <= cb; ++k)
+                        mm = fmaxf(mm, __ldcg(p.partials + (long long)(2 * k + (k == ca)) * A::PART + ROWS * D + row));
+#pragma unroll 4
+                    for (int k = ca; k <= cb; ++k) {
+                        const float* q = p.partials + (long long)(2 * k + (k == ca)) * A::PART;
+                        const float mk = __ldcg(q + ROWS * D + row);
+                        const float f = mk == mm ? 1.0f : ex2(mk - mm);
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(q + row * D + d));
+                        ll += f * __ldcg(q + ROWS * D + ROWS + row);
+                        x.x += f * y.x;
+                        x.y += f * y.y;
+                        x.z += f * y.z;
+                        x.w += f * y.w;
+                    }
+                    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+                    store_row(row, d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+                    if (d == 0 && p.lse) {
+                        const int rr = row0 + row, qi = rr / p.group;
+                        p.lse[(long long)(r.q0 + qi) * p.q_heads + head * p.group + rr - qi * p.group] =
+                            ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * CUDART_LN2_F;
+                    }
+                }
+            }
+        }
+        // the rings are read: bulk copies may follow the plain accesses
+        fence_proxy_async_smem();
+        __syncthreads();
+        u += take;
+        off += take;
+    }
+}
+
+template <int D, int NR>
+struct Launch {
+    static inline int per_sm = 1;   // CTAs an SM holds
+
+    static cudaError_t setup()
+    {
+        cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Attn<D, NR>::SMEM);
+        if (e != cudaSuccess) return e;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kv4_attn_kernel<D, NR>, kThreads, Attn<D, NR>::SMEM);
+    }
+
+    static cudaError_t run(const Kv4AttnParams& p, int sms, cudaStream_t stream)
+    {
+        const int grid = sms * per_sm < kWsMaxGrid ? sms * per_sm : kWsMaxGrid;
+        kv4_attn_kernel<D, NR><<<grid, kThreads, Attn<D, NR>::SMEM, stream>>>(p);
+        return cudaGetLastError();
+    }
+};
+}  // namespace
+
+size_t kv4_partial_bytes(int sms)
+{
+    size_t need = 0;
+    auto most = [&](int per_sm, int part) {
+        const size_t grid = (size_t)(sms * per_sm < kWsMaxGrid ? sms * per_sm : kWsMaxGrid);
+        const size_t bytes = 2 * grid * part * sizeof(float);
+        need = bytes > need ? bytes : need;
+    };
+    most(Launch<64, 1>::per_sm, Attn<64, 1>::PART);
+    most(Launch<64, 2>::per_sm, Attn<64, 2>::PART);
+    most(Launch<128, 1>::per_sm, Attn<128, 1>::PART);
+    most(Launch<128, 2>::per_sm, Attn<128, 2>::PART);
+    return need;
+}
+
+cudaError_t setup_kv4()
+{
+    cudaError_t e;
+    if ((e = Launch<64, 1>::setup()) != cudaSuccess || (e = Launch<64, 2>::setup()) != cudaSuccess ||
+        (e = Launch<128, 1>::setup()) != cudaSuccess || (e = Launch<128, 2>::setup()) != cudaSuccess)
+        return e;
+    return cudaSuccess;
+}
+
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int head_dim, int max_q, int sms, cudaStream_t stream)
+{
+    const bool wide = (long long)max_q * p.group > 8;
+    if (head_dim == 128) return wide ? Launch<128, 2>::run(p, sms, stream) : Launch<128, 1>::run(p, sms, stream);
+    return wide ? Launch<64, 2>::run(p, sms, stream) : Launch<64, 1>::run(p, sms, stream);
+}
+
+}  // namespace w4a16

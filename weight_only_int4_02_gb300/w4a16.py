@@ -20,7 +20,9 @@ EXPORTS = ["w4a16_layout_version", "w4a16_status_string", "w4a16_last_cuda_error
            "w4a16_check_device_status", "w4a16_plan", "w4a16_gemm_noalloc", "w4a16_gemm_fused",
            "w4a16_zeros_bytes", "w4a16_pack_zeros", "w4a16_gemm_zp", "w4a16_w8_packed_bytes", "w4a16_w8_pack",
            "w4a16_w8_gemm", "w4a16_bf16_gemm", "w4a16_sp_packed_bytes", "w4a16_sp_pack", "w4a16_sp_gemm",
-           "w4a16_selftest_wait_timeout", "w4a16_force_path", "w4a16_set_wait_limit_ns", "w4a16_gemm_strided"]
+           "w4a16_selftest_wait_timeout", "w4a16_force_path", "w4a16_set_wait_limit_ns", "w4a16_gemm_strided",
+           "w4a16_kv4_page_bytes", "w4a16_kv4_tables", "w4a16_kv4_append", "w4a16_kv4_read",
+           "w4a16_kv4_workspace_bytes", "w4a16_kv4_attention", "w4a16_sample"]
 
 ACTIVATIONS = {"none": 0, "silu": 1, "relu": 2}
 
@@ -94,6 +96,22 @@ def lib():
         L.w4a16_w8_pack.restype = I
         L.w4a16_w8_gemm.argtypes = [P, P, P, P, I, I, I, I, P, P, I, P, Z, P]
         L.w4a16_w8_gemm.restype = I
+        L64, F = ctypes.c_int64, ctypes.c_float
+        L.w4a16_kv4_page_bytes.argtypes = [I, I, I]
+        L.w4a16_kv4_page_bytes.restype = Z
+        L.w4a16_kv4_tables.argtypes = [P, P, I, P, I, P, P, P, I, I, P, P, I, P, P]
+        L.w4a16_kv4_tables.restype = I
+        L.w4a16_kv4_append.argtypes = [P, L64, L64, P, L64, L64, P, P, I, I, I, I, I, I, P]
+        L.w4a16_kv4_append.restype = I
+        L.w4a16_kv4_read.argtypes = [P, I, P, P, P, I, I, I, I, I, P]
+        L.w4a16_kv4_read.restype = I
+        L.w4a16_kv4_workspace_bytes.argtypes = []
+        L.w4a16_kv4_workspace_bytes.restype = Z
+        L.w4a16_kv4_attention.argtypes = [P, L64, L64, P, I, P, L64, I, P, P, P, L64, L64, P, I, I, I, I, I, I, I, F, I,
+                                          I, P, Z, P]
+        L.w4a16_kv4_attention.restype = I
+        L.w4a16_sample.argtypes = [P, L64, P, P, P, P, P, P, P, I, I, I, P]
+        L.w4a16_sample.restype = I
         _lib = L
     return _lib
 
@@ -449,3 +467,149 @@ def sp_gemm(x, packed, scales_packed, N, group_size, bias=None, residual=None, a
                                _ptr(bias), _ptr(residual), ACTIVATIONS[activation], _ptr(workspace), ws_bytes,
                                _stream(stream)), "w4a16_sp_gemm")
     return y
+
+
+# ---------------------------------------------------------------- the serving step
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _need(ok, what):
+    if not ok:
+        raise W4A16Error(ERR_INVALID_ARG, what)
+
+
+def _addr(t, dtype, shape, what):
+    """Address of a contiguous CUDA tensor of this type and shape (None: any size there)."""
+    _need(t.dtype == dtype and t.is_cuda and t.is_contiguous() and t.dim() == len(shape) and
+          all(n is None or n == m for n, m in zip(shape, t.shape)),
+          "%s must be a contiguous %s CUDA tensor of shape %s" % (what, dtype, list(shape)))
+    return t.data_ptr()
+
+
+def kv4_page_bytes(kv_heads, head_dim, page_size):
+    return lib().w4a16_kv4_page_bytes(kv_heads, head_dim, page_size)
+
+
+def kv4_cache(pages, kv_heads, head_dim, page_size, device="cuda"):
+    """An empty 4-bit key-value cache: uint8 [pages][kv_heads][page_size / 16][16 * (head_dim + 6)]."""
+    _need(pages >= 0 and kv4_page_bytes(kv_heads, head_dim, page_size) > 0,
+          "no 4-bit cache of %d KV heads of %d in pages of %d" % (kv_heads, head_dim, page_size))
+    return torch.zeros((pages, kv_heads, page_size // 16, 16 * (head_dim + 6)), dtype=torch.uint8, device=device)
+
+
+def _kv4_sizes(cache, page_size):
+    """(pages, KV heads, head dimension) of a cache."""
+    _need(cache.dtype == torch.uint8 and cache.is_cuda and cache.is_contiguous() and cache.dim() == 4 and
+          cache.shape[2] * 16 == page_size and cache.shape[3] % 16 == 0,
+          "the cache must be a contiguous uint8 CUDA tensor [pages][kv_heads][page_size / 16][16 * (head_dim + 6)]")
+    return cache.shape[0], cache.shape[1], cache.shape[3] // 16 - 6
+
+
+def kv4_tables(seq_lens, new_lens, free_pages, block_table, page_size, max_tokens, taken=None, stream=None):
+    """Block tables and slot maps of a batch from its lengths (w4a16_kv4_tables).
+
+    seq_lens, new_lens: int32 [batch]; free_pages: int32 [n]; block_table: int32
+    [batch][max_pages], updated in place; taken: int32 [1], pages of the free list taken
+    before, or None. Returns (slots int64 [max_tokens], positions int32 [max_tokens],
+    starts int32 [batch + 1], taken int32 [1])."""
+    batch, dev = seq_lens.shape[0], seq_lens.device
+    slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+    out = torch.empty(max_tokens + batch + 2, dtype=torch.int32, device=dev)
+    positions, starts, after = out[:max_tokens], out[max_tokens:max_tokens + batch + 1], out[max_tokens + batch + 1:]
+    at = out.data_ptr()
+    _check(lib().w4a16_kv4_tables(
+        _addr(seq_lens, torch.int32, (batch,), "seq_lens"), _addr(new_lens, torch.int32, (batch,), "new_lens"), batch,
+        _addr(free_pages, torch.int32, (None,), "free_pages"), free_pages.shape[0],
+        None if taken is None else _addr(taken, torch.int32, (1,), "taken"), at + 4 * (max_tokens + batch + 1),
+        _addr(block_table, torch.int32, (batch, None), "block_table"), block_table.shape[1], page_size,
+        slots.data_ptr(), at, max_tokens, at + 4 * max_tokens, _stream(stream)), "w4a16_kv4_tables")
+    return slots, positions, starts, after
+
+
+def kv4_append(k, v, slots, cache, page_size, stream=None):
+    """Quantise k and v (float16 or bfloat16 [tokens][kv_heads][head_dim] views whose last
+    dimension is contiguous) into their slots (int64 [tokens]; -1 skips) of the cache."""
+    pages, heads, dim = _kv4_sizes(cache, page_size)
+    tokens = slots.shape[0]
+    for t, what in ((k, "k"), (v, "v")):
+        _need(t.dtype in (torch.float16, torch.bfloat16) and t.dtype == k.dtype and t.is_cuda and
+              tuple(t.shape) == (tokens, heads, dim) and t.stride(2) == 1,
+              "%s must be a float16 or bfloat16 CUDA tensor [%d][%d][%d]" % (what, tokens, heads, dim))
+    _check(lib().w4a16_kv4_append(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
+                                  _addr(slots, torch.int64, (tokens,), "slots"), cache.data_ptr(), pages, tokens, heads,
+                                  dim, page_size, _DTYPES[k.dtype], _stream(stream)), "w4a16_kv4_append")
+
+
+def kv4_read(cache, slots, page_size, dtype=torch.float16, stream=None):
+    """(k, v) [tokens][kv_heads][head_dim] that the slots stand for, in float16, bfloat16 or float32."""
+    pages, heads, dim = _kv4_sizes(cache, page_size)
+    tokens = slots.shape[0]
+    _need(dtype in _DTYPES, "kv4_read gives float16, bfloat16 or float32")
+    k = torch.empty((tokens, heads, dim), dtype=dtype, device=cache.device)
+    v = torch.empty_like(k)
+    _check(lib().w4a16_kv4_read(cache.data_ptr(), pages, _addr(slots, torch.int64, (tokens,), "slots"), k.data_ptr(),
+                                v.data_ptr(), tokens, heads, dim, page_size, _DTYPES[dtype], _stream(stream)),
+           "w4a16_kv4_read")
+    return k, v
+
+
+def kv4_workspace_bytes():
+    return lib().w4a16_kv4_workspace_bytes()
+
+
+def kv4_attention(q, cache, block_table, seq_lens, starts, page_size, max_q, scale=None, window=0, out=None,
+                  return_lse=False, workspace=None, stream=None):
+    """Causal attention of new query tokens over the 4-bit cache (w4a16_kv4_attention).
+
+    q: float16 or bfloat16 [tokens][q_heads][head_dim], last dimension contiguous; block_table:
+    int32 [batch][pages of a request]; seq_lens: int32 [batch], cached tokens with the new
+    ones; starts: int32 [batch + 1], each request's first query token; max_q: the most query
+    tokens of a request; scale: 1 / sqrt(head_dim) by default; window: keys a query sees at
+    most, 0 for all; workspace: uint8, kv4_workspace_bytes(), zeroed once, or None for the
+    library's own. Returns out, or (out, lse float32 [tokens][q_heads])."""
+    pages, heads, dim = _kv4_sizes(cache, page_size)
+    tokens, q_heads = q.shape[0], q.shape[1]
+    batch = seq_lens.shape[0]
+    _need(q.dtype in (torch.float16, torch.bfloat16) and q.is_cuda and q.dim() == 3 and q.shape[2] == dim and
+          q.stride(2) == 1, "q must be a float16 or bfloat16 CUDA tensor [tokens][q_heads][%d]" % dim)
+    if out is None:
+        out = torch.empty((tokens, q_heads, dim), dtype=q.dtype, device=q.device)
+    else:
+        _need(out.dtype == q.dtype and out.is_cuda and out.shape == q.shape and out.stride(2) == 1,
+              "out must be a CUDA tensor of q's type and shape")
+    _need(block_table.dtype == torch.int32 and block_table.is_cuda and block_table.dim() == 2 and
+          block_table.shape[0] == batch and (block_table.stride(1) == 1 or block_table.shape[1] <= 1),
+          "block_table must be an int32 CUDA tensor [%d][pages]" % batch)
+    lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=q.device) if return_lse else None
+    cols = block_table.shape[1]
+    _check(lib().w4a16_kv4_attention(
+        q.data_ptr(), q.stride(0), q.stride(1), cache.data_ptr(), pages, block_table.data_ptr(),
+        max(block_table.stride(0), cols), cols, _addr(seq_lens, torch.int32, (batch,), "seq_lens"),
+        _addr(starts, torch.int32, (batch + 1,), "starts"), out.data_ptr(), out.stride(0), out.stride(1),
+        None if lse is None else lse.data_ptr(), batch, tokens, q_heads, heads, dim, page_size, max_q,
+        dim ** -0.5 if scale is None else scale, window, _DTYPES[q.dtype],
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else _nbytes(workspace),
+        _stream(stream)), "w4a16_kv4_attention")
+    return (out, lse) if return_lse else out
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """One token per row of logits (float16, bfloat16 or float32 [batch][vocab], rows contiguous)
+    from uniform numbers u (float32 [batch]), after temperature, top-k, top-p and min-p
+    (float32, int32, float32, float32 [batch], each or None). Returns (token int32 [batch],
+    its probability among the kept tokens float32 [batch]); see w4a16_sample."""
+    _need(logits.dtype in _DTYPES and logits.is_cuda and logits.dim() == 2 and
+          (logits.stride(1) == 1 or logits.shape[1] == 1),
+          "logits must be a float16, bfloat16 or float32 CUDA tensor [batch][vocab]")
+    batch, vocab = logits.shape
+    f32 = torch.float32
+    token = torch.empty(batch, dtype=torch.int32, device=logits.device)
+    prob = torch.empty(batch, dtype=f32, device=logits.device)
+    _check(lib().w4a16_sample(
+        logits.data_ptr(), max(logits.stride(0), vocab), _addr(u, f32, (batch,), "u"),
+        None if temperature is None else _addr(temperature, f32, (batch,), "temperature"),
+        None if top_k is None else _addr(top_k, torch.int32, (batch,), "top_k"),
+        None if top_p is None else _addr(top_p, f32, (batch,), "top_p"),
+        None if min_p is None else _addr(min_p, f32, (batch,), "min_p"), token.data_ptr(), prob.data_ptr(), batch, vocab,
+        _DTYPES[logits.dtype], _stream(stream)), "w4a16_sample")
+    return token, prob
