@@ -19,7 +19,11 @@ bool valid_page(int page_size) { return page_size >= 16 && page_size <= 256 && (
 
 bool valid_dim(int head_dim) { return head_dim == 64 || head_dim == 128; }
 
-bool valid_stride(int64_t stride, int head_dim) { return stride >= head_dim && stride % 8 == 0; }
+// The stride of `count` items (that of one item is never used).
+bool valid_stride(int64_t stride, int head_dim, int count)
+{
+    return count <= 1 || (stride >= head_dim && stride % 8 == 0);
+}
 
 // The arguments that append and read share.
 bool valid_rows(const void* cache, int pages, const int64_t* slots, int tokens, int kv_heads, int head_dim,
@@ -72,8 +76,8 @@ w4a16_status w4a16_kv4_append(const void* k, int64_t k_token_stride, int64_t k_h
         return W4A16_ERR_INVALID_ARG;
     if (tokens == 0) return W4A16_OK;
     if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return W4A16_ERR_INVALID_ARG;
-    if (!valid_stride(k_token_stride, head_dim) || !valid_stride(k_head_stride, head_dim) ||
-        !valid_stride(v_token_stride, head_dim) || !valid_stride(v_head_stride, head_dim))
+    if (!valid_stride(k_token_stride, head_dim, tokens) || !valid_stride(k_head_stride, head_dim, kv_heads) ||
+        !valid_stride(v_token_stride, head_dim, tokens) || !valid_stride(v_head_stride, head_dim, kv_heads))
         return W4A16_ERR_INVALID_ARG;
     DeviceInfo dev;
     const w4a16_status rc = device_info(&dev);
@@ -138,16 +142,17 @@ w4a16_status w4a16_kv4_attention(const void* q, int64_t q_token_stride, int64_t 
         table_cols < 0 || window < 0 || !valid_dim(head_dim) || !valid_page(page_size))
         return W4A16_ERR_INVALID_ARG;
     if ((dtype != W4A16_FP16 && dtype != W4A16_BF16) || !(fabsf(scale) <= 3.0e38f)) return W4A16_ERR_INVALID_ARG;
-    // rows (query token, head of a group) are counted in 31 bits
-    if ((int64_t)tokens * (q_heads / kv_heads) >= ((int64_t)1 << 31)) return W4A16_ERR_INVALID_ARG;
+    // rows (query token, head) and tiles of them are counted in 31 bits
+    if ((int64_t)tokens * q_heads + (int64_t)batch * kv_heads >= ((int64_t)1 << 31)) return W4A16_ERR_INVALID_ARG;
     if (batch == 0 || tokens == 0) return W4A16_OK;
     if (!q || !out || !seq_lens || !starts || (pages > 0 && !cache) || (table_cols > 0 && !block_table))
         return W4A16_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(cache, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
         !aligned(starts, 4) || !aligned(lse, 4))
         return W4A16_ERR_INVALID_ARG;
-    if (!valid_stride(q_token_stride, head_dim) || !valid_stride(q_head_stride, head_dim) ||
-        !valid_stride(out_token_stride, head_dim) || !valid_stride(out_head_stride, head_dim) || table_stride < table_cols)
+    if (!valid_stride(q_token_stride, head_dim, tokens) || !valid_stride(q_head_stride, head_dim, q_heads) ||
+        !valid_stride(out_token_stride, head_dim, tokens) || !valid_stride(out_head_stride, head_dim, q_heads) ||
+        (batch > 1 && table_stride < table_cols))
         return W4A16_ERR_INVALID_ARG;
     if (workspace && !aligned(workspace, 256)) return W4A16_ERR_INVALID_ARG;
     DeviceInfo dev;

@@ -76,11 +76,15 @@ struct Kv4AttnParams {
     long long wait_limit_ns;
     float scale_log2;            // softmax scale * log2(e)
     int batch, tokens, q_heads, kv_heads, group, pages, page_size, table_cols, window;
+    int few_rows;                // requests of at most this many rows a KV head are the stream-K kernel's
     int bf16;
 };
 constexpr int kKv4MaxRows = 16;  // rows (query, head) of the widest row tile
 cudaError_t setup_kv4();
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int head_dim, int max_q, int sms, cudaStream_t stream);
+// The tcgen05 kernel, for requests of more than few_rows rows.
+cudaError_t setup_kv4_prompt();
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, int head_dim, cudaStream_t stream);
 // Bytes of partial sums that launch_kv4_attention may use.
 size_t kv4_partial_bytes(int sms);
 

@@ -26,6 +26,7 @@
 #include "ptx.cuh"
 
 #include <float.h>
+#include <limits.h>
 #include <math_constants.h>
 
 namespace w4a16 {
@@ -34,7 +35,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;      // tokens of a unit: two tiles
-constexpr int kStages = 4;     // units in flight per warp
+constexpr int kOverhead = 6;   // what starting and ending a segment costs, in units
+constexpr int kGrow = 8;       // log2 of how far probabilities may grow before their reference moves
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -74,7 +76,7 @@ __device__ __forceinline__ float2 bits_half2(uint32_t w) { return __half22float2
 struct Request {
     int seq, q0, nq, rows, tiles;   // cached tokens, first query token, query tokens, rows, row tiles
     int base, units;                // first cached token looked at (a multiple of kUnit), units a segment
-    long long work;                 // units of all its segments
+    long long work;                 // cost of all its segments: kOverhead, then the units, of each
 };
 
 template <int ROWS>
@@ -91,25 +93,27 @@ __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b)
     r.q0 = a;
     r.nq = e - a;
     r.rows = r.nq * p.group;
-    r.tiles = (r.rows + ROWS - 1) / ROWS;
+    r.tiles = r.rows > p.few_rows ? 0 : (r.rows + ROWS - 1) / ROWS;
     const int first = r.seq - r.nq - p.window + 1;   // first token the first query's window holds
     r.base = (p.window > 0 && first > 0) ? first / kUnit * kUnit : 0;
     r.units = r.seq > r.base ? (r.seq - r.base + kUnit - 1) / kUnit : 1;   // an empty segment still writes its rows
-    r.work = (long long)r.tiles * p.kv_heads * r.units;
+    r.work = (long long)r.tiles * p.kv_heads * (r.units + kOverhead);
     return r;
 }
 
 template <int D, int NR>
 struct Attn {
     static constexpr int ROWS = 8 * NR;
+    static constexpr int CTAS = NR == 1 ? 4 : D == 64 ? 3 : 2;   // on an SM, as registers and rings allow
+    static constexpr int STAGES = D == 128 ? 3 : 4;   // units in flight per warp
     static constexpr int TB = kv4_tile_bytes(D);
     static constexpr int STAGE = 2 * TB;
-    static constexpr int RING = kStages * STAGE;
+    static constexpr int RING = STAGES * STAGE;
     static constexpr int W = D / 32;            // words of a lane's share
     static constexpr int PART = ROWS * (D + 2); // floats of one partial: O, then m and l
     static_assert(RING >= ROWS * D * 4, "a warp's ring holds its output");
     struct Shared {
-        uint64_t bar[kWarps][kStages];
+        uint64_t bar[kWarps][STAGES];
         float m[kWarps][ROWS], l[kWarps][ROWS];
         float weight[kWarps][ROWS];
         long long scan[kWarps];
@@ -136,7 +140,7 @@ __device__ __forceinline__ void lds_share(const uint8_t* at, uint32_t (&w)[W])
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams p)
+__global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(const Kv4AttnParams p)
 {
     using A = Attn<D, NR>;
     constexpr int W = A::W, ROWS = A::ROWS;
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
         sh.abort_flag = 0;
         sh.start_b = p.batch;
     }
-    if (lane < kStages) mbar_init(smem_addr(&sh.bar[warp][lane]), 1);
+    if (lane < A::STAGES) mbar_init(smem_addr(&sh.bar[warp][lane]), 1);
     fence_mbar_init();
     __syncthreads();
     long long excl = incl - sum, total = 0;
@@ -194,10 +198,11 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
     if (b >= p.batch) return;   // cannot happen: u0 < total
 
     const WaitCtl ctl{&sh.abort_flag, p.status, p.wait_limit_ns};
-    uint32_t issued = 0, used = 0, ok_bits = 0;   // units issued and used by this warp; two bits a stage: tiles present
+    // the ring: stage and phase of the next unit to issue and to use; two bits a stage: tiles present
+    int s_issue = 0, s_use = 0;
+    uint32_t phase = 0, pending = 0, ok_bits = 0;
     bool dead = false;
-    const int page_shift = __ffs(p.page_size) - 1;
-    const int tpp_shift = page_shift - 4;         // log2(tiles per page)
+    const int tpp_shift = __ffs(p.page_size) - 5;   // log2(tiles per page)
 
     Request r = request_of<ROWS>(p, b);
     for (long long u = u0; u < u1;) {
@@ -205,54 +210,67 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
             off -= r.work;
             r = request_of<ROWS>(p, ++b);
         }
-        const long long seg = off / r.units;
-        const int pos = (int)(off - seg * r.units);
+        const int cost = r.units + kOverhead;
+        const long long seg = off / cost;
+        const int at = (int)(off - seg * cost);                                  // this run's first place in the segment
+        const int end = (int)(cost - at < u1 - u ? cost : at + (u1 - u));        // and its end
+        const long long seg_u = u - at;                                          // the segment's place among all
+        u += end - at;
+        off += end - at;
+        if (end <= kOverhead) continue;                                          // no unit of it is this run's
+        const int pos = at > kOverhead ? at - kOverhead : 0, take = end - kOverhead - pos;
         const int head = (int)(seg / r.tiles), rt = (int)(seg - (long long)head * r.tiles);
-        const int take = (int)(r.units - pos < u1 - u ? r.units - pos : u1 - u);
         const int row0 = rt * ROWS;
 
-        // ---- issue: lanes 0 and 1 own a unit's tiles
+        // ---- copies: a batch of 16 units at a time, lanes 2j and 2j + 1 own the tiles of its unit j
         const int32_t* const trow = p.table + (long long)b * p.table_stride;
-        auto page_of = [&](int t) {   // this lane's tile of unit t: its page, or -1
-            const int tile = ((r.base + t * kUnit) >> 4) + lane;
-            return (lane < 2 && t < pos + take && tile * kKv4Tile < r.seq) ? trow[tile >> tpp_shift] : -1;
+        const int mine_n = (take - warp + kWarps - 1) / kWarps;   // units of this warp: pos + warp, + kWarps, ...
+        auto page_of = [&](int k) {   // page of this lane's tile of the batch from unit k on, or -1
+            const int t = pos + warp + (k + (lane >> 1)) * kWarps;
+            const int tile = ((r.base + t * kUnit) >> 4) + (lane & 1);
+            return (k + (lane >> 1) < mine_n && tile * kKv4Tile < r.seq) ? trow[tile >> tpp_shift] : -1;
         };
-        auto issue = [&](int t, int page) {
-            const int s = issued % kStages;
-            const int tile = ((r.base + t * kUnit) >> 4) + lane;
-            const bool ok = page >= 0 && page < p.pages;   // false in lanes 2 and up
-            const uint32_t bits = __ballot_sync(0xffffffffu, ok) & 3u;
-            ok_bits = (ok_bits & ~(3u << (2 * s))) | bits << (2 * s);
-            const uint32_t bar = smem_addr(&sh.bar[warp][s]);
-            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(bits) * A::TB);
-            __syncwarp();
-            const int next = __shfl_down_sync(0xffffffffu, page, 1), prev = __shfl_up_sync(0xffffffffu, page, 1);
-            const int in_page = tile & ((1 << tpp_shift) - 1);
-            // two tiles of one page are one copy, lane 0's
-            const bool pair0 = bits == 3u && next == page && in_page + 1 < (1 << tpp_shift);
-            const bool pair1 = bits == 3u && prev == page && in_page > 0;
-            if (ok && !(lane == 1 && pair1)) {
-                const uint8_t* src = p.cache + ((((long long)page * p.kv_heads + head) << tpp_shift) + in_page) * A::TB;
-                bulk_load(smem_addr(ring + s * A::STAGE + lane * A::TB), src, (lane == 0 && pair0) ? A::STAGE : A::TB, bar);
-            }
-            ++issued;
-        };
-        int t_issue = pos + warp;
-        int page = page_of(t_issue);
+        int k_issue = 0, page = page_of(0);
+        uint32_t present = 0;
+        const uint8_t* src = nullptr;
+        uint32_t len = 0;
         auto issue_next = [&]() {
-            if (t_issue < pos + take && !dead) {
-                const int ahead = page_of(t_issue + kWarps);
-                issue(t_issue, page);
-                page = ahead;
-                t_issue += kWarps;
+            if (k_issue >= mine_n || dead) return;
+            const int j = k_issue & 15;
+            if (j == 0) {
+                const int t = pos + warp + (k_issue + (lane >> 1)) * kWarps;
+                const int in_page = (((r.base + t * kUnit) >> 4) + (lane & 1)) & ((1 << tpp_shift) - 1);
+                const bool ok = page >= 0 && page < p.pages;
+                present = __ballot_sync(0xffffffffu, ok);
+                const int other = __shfl_xor_sync(0xffffffffu, page, 1);
+                // a unit's two tiles in one page are one copy, the even lane's
+                const bool pair = (present >> (lane & 30) & 3u) == 3u && other == page && (in_page | 1) < (1 << tpp_shift);
+                len = !ok ? 0u : !pair ? (uint32_t)A::TB : (lane & 1) ? 0u : (uint32_t)A::STAGE;
+                src = p.cache + ((((long long)page * p.kv_heads + head) << tpp_shift) + in_page) * A::TB;
+                page = page_of(k_issue + 16);
+            }
+            const uint32_t bits = present >> (2 * j) & 3u;
+            ok_bits = (ok_bits & ~(3u << (2 * s_issue))) | bits << (2 * s_issue);
+            const uint32_t bar = smem_addr(&sh.bar[warp][s_issue]);
+            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(bits) * A::TB);
+            if ((lane >> 1) == j && len) bulk_load(smem_addr(ring + s_issue * A::STAGE + (lane & 1) * A::TB), src, len, bar);
+            ++k_issue;
+            ++pending;
+            s_issue = s_issue + 1 == A::STAGES ? 0 : s_issue + 1;
+        };
+        auto next_stage = [&]() {
+            --pending;
+            if (++s_use == A::STAGES) {
+                s_use = 0;
+                phase ^= 1;
             }
         };
-#pragma unroll
-        for (int i = 0; i < kStages; ++i) issue_next();
+#pragma unroll 1
+        for (int i = 0; i < A::STAGES; ++i) issue_next();
 
         // ---- Q fragments, scaled per row by a power of two; row constants of the columns 2c, 2c + 1
         uint32_t ql[NR][W][2], qh[NR][W][2];
-        float row_a[NR][2], row_b[NR][2];
+        float row_a[NR][2], row_z[NR][2];   // score = row_a * s_k * (MMA + z_k * row_z), in powers of two
         int row_pos[NR][2];
 #pragma unroll
         for (int g = 0; g < NR; ++g) {
@@ -262,11 +280,11 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
             for (int i = 0; i < 4 * W; ++i) raw[i] = 0;
             if (row < r.rows) {
                 const int qi = row / p.group, h = row - qi * p.group;
-                const uint16_t* src = (const uint16_t*)p.q + (long long)(r.q0 + qi) * p.q_token +
-                                      (long long)(head * p.group + h) * p.q_head + c * (D / 4);
+                const uint16_t* q = (const uint16_t*)p.q + (long long)(r.q0 + qi) * p.q_token +
+                                    (long long)(head * p.group + h) * p.q_head + c * (D / 4);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+                    const uint4 v = *reinterpret_cast<const uint4*>(q + 8 * i);
                     raw[4 * i] = v.x;
                     raw[4 * i + 1] = v.y;
                     raw[4 * i + 2] = v.z;
@@ -283,7 +301,8 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
             // largest magnitude into [2^13, 2^14); an infinity or a NaN stays one
             int e = ((__float_as_int(top) >> 23) & 255) - 127 - 13;
             e = (top == 0.0f || !(top <= FLT_MAX)) ? 0 : e < -120 ? -120 : e;
-            const float f = pow2i(-e);
+            // a negative softmax scale goes into Q, so that the largest score is that of the largest product
+            const float f = p.scale_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
             float qsum = 0.0f;
 #pragma unroll
             for (int w = 0; w < W; ++w) {
@@ -306,12 +325,13 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
             }
             qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
             qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
-            const float unit = p.scale_log2 * pow2i(e > 127 ? 127 : e);
+            // codes come as c * 2^-24
+            const float unit = fabsf(p.scale_log2) * pow2i(e > 103 ? 103 : e) * 16777216.0f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float un = __shfl_sync(0xffffffffu, unit, (2 * c + i) * 4);
-                row_a[g][i] = un * 16777216.0f;   // codes come as c * 2^-24
-                row_b[g][i] = un * __shfl_sync(0xffffffffu, qsum, (2 * c + i) * 4);
+                row_a[g][i] = un > 0.0f ? un : FLT_MIN;   // scale 0: all scores nearly equal, masked ones stay -infinity
+                row_z[g][i] = __shfl_sync(0xffffffffu, qsum, (2 * c + i) * 4) * -0x1p-24f;
                 const int rr = row0 + g * 8 + 2 * c + i;
                 row_pos[g][i] = rr < r.rows ? r.seq - r.nq + rr / p.group : -1;
             }
@@ -321,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
         const int pos_min = r.seq - r.nq + row0 / p.group, pos_max = r.seq - r.nq + last_row / p.group;
 
         float m[NR][2], l[NR][2], zs[NR][2], o[NR][2 * W][4];
-        int ev = -126;   // V's scales seen so far are at most 2^ev
+        int ev = -40;   // V's scales seen so far are at most 2^ev
 #pragma unroll
         for (int g = 0; g < NR; ++g) {
 #pragma unroll
@@ -336,18 +356,18 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
                 for (int i = 0; i < 4; ++i) o[g][w][i] = 0.0f;
         }
 
+#pragma unroll 1
         for (int t = pos + warp; t < pos + take && !dead; t += kWarps) {
-            const int s = used % kStages;
-            if (!wait_warp(smem_addr(&sh.bar[warp][s]), (used / kStages) & 1, ctl)) {
+            if (!wait_warp(smem_addr(&sh.bar[warp][s_use]), phase, ctl)) {
                 dead = true;
                 break;
             }
-            const uint8_t* const st = ring + s * A::STAGE;
-            const uint32_t have = (ok_bits >> (2 * s)) & 3u;
+            const uint8_t* const st = ring + s_use * A::STAGE;
+            const uint32_t have = (ok_bits >> (2 * s_use)) & 3u;
             const int t0 = r.base + t * kUnit;
             const bool full = have == 3u && t0 + kUnit - 1 <= pos_min && (p.window <= 0 || t0 > pos_max - p.window);
 
-            // scores of the unit's two tiles: tokens n and n + 8 of each, rows 2c and 2c + 1
+            // s_k times the products of the unit's two tiles: tokens n and n + 8 of each, rows 2c and 2c + 1
             float sc[2][NR][4];
             float vs[2][2], vz[2][2];
 #pragma unroll
@@ -356,34 +376,35 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
                 uint32_t ka[W], kb[W];
                 lds_share<W>(tile + lane * (4 * W), ka);
                 lds_share<W>(tile + 8 * (D / 2) + lane * (4 * W), kb);
-                float acc[NR][4];
+                float ks[2];
 #pragma unroll
-                for (int g = 0; g < NR; ++g)
+                for (int j = 0; j < 2; ++j) {
+                    const int tok = n + 8 * j;
+                    ks[j] = __half2float(*reinterpret_cast<const __half*>(tile + kv4_k_scale_off(D) + 2 * tok));
+                    const float kz = (float)tile[kv4_k_zero_off(D) + tok];
+                    vs[tl][j] = __half2float(*reinterpret_cast<const __half*>(tile + kv4_v_scale_off(D) + 2 * tok));
+                    vz[tl][j] = (float)tile[kv4_v_zero_off(D) + tok];
+                    // the sums start from the zero-points' share
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[g][i] = 0.0f;
+                    for (int g = 0; g < NR; ++g) {
+                        sc[tl][g][2 * j] = kz * row_z[g][0];
+                        sc[tl][g][2 * j + 1] = kz * row_z[g][1];
+                    }
+                }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     const uint32_t ka8 = ka[w] >> 8, kb8 = kb[w] >> 8;
 #pragma unroll
                     for (int g = 0; g < NR; ++g)
-                        mma_16816(acc[g], ka[w] & kLow, kb[w] & kLow, ka8 & kLow, kb8 & kLow, ql[g][w][0], ql[g][w][1]);
+                        mma_16816(sc[tl][g], ka[w] & kLow, kb[w] & kLow, ka8 & kLow, kb8 & kLow, ql[g][w][0], ql[g][w][1]);
 #pragma unroll
                     for (int g = 0; g < NR; ++g)
-                        mma_16816(acc[g], ka[w] & kHigh, kb[w] & kHigh, ka8 & kHigh, kb8 & kHigh, qh[g][w][0], qh[g][w][1]);
+                        mma_16816(sc[tl][g], ka[w] & kHigh, kb[w] & kHigh, ka8 & kHigh, kb8 & kHigh, qh[g][w][0], qh[g][w][1]);
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int tok = n + 8 * j;
-                    const float ks = __half2float(*reinterpret_cast<const __half*>(tile + kv4_k_scale_off(D) + 2 * tok));
-                    const float kz = (float)tile[kv4_k_zero_off(D) + tok];
-                    vs[tl][j] = __half2float(*reinterpret_cast<const __half*>(tile + kv4_v_scale_off(D) + 2 * tok));
-                    vz[tl][j] = (float)tile[kv4_v_zero_off(D) + tok];
+                for (int g = 0; g < NR; ++g)
 #pragma unroll
-                    for (int g = 0; g < NR; ++g)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            sc[tl][g][2 * j + i] = ks * (acc[g][2 * j + i] * row_a[g][i] - kz * row_b[g][i]);
-                }
+                    for (int i = 0; i < 4; ++i) sc[tl][g][i] *= ks[i >> 1];
             }
             if (!full) {
 #pragma unroll
@@ -392,7 +413,8 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
                     for (int j = 0; j < 2; ++j) {
                         const int key = t0 + tl * kKv4Tile + n + 8 * j;
                         const bool there = (have >> tl & 1) && key < r.seq;
-                        bool any = false;
+                        const bool odd = there && vs[tl][j] != vs[tl][j];   // a poisoned row of V
+                        if (!there || odd) vs[tl][j] = vz[tl][j] = 0.0f;
 #pragma unroll
                         for (int g = 0; g < NR; ++g)
 #pragma unroll
@@ -400,42 +422,42 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
                                 const bool see = there && key <= row_pos[g][i] &&
                                                  (p.window <= 0 || key > row_pos[g][i] - p.window);
                                 if (!see) sc[tl][g][2 * j + i] = -CUDART_INF_F;
-                                any = any || see;
+                                else if (odd) zs[g][i] = CUDART_NAN_F;      // shows in the rows that see it alone
                             }
-                        // what no row here sees may be any memory; what another row sees is a stored token
-                        if (!there) vs[tl][j] = vz[tl][j] = 0.0f;
                     }
             }
-            // running maximum, and the exponent that bounds V's scales
-            float top[NR][2];
+            // the references of the running sums move if a score passes its row's by 2^kGrow, or a scale 2^ev
+            float vf = pow2i(15 - kGrow - ev);
             bool grow = false;
 #pragma unroll
             for (int g = 0; g < NR; ++g)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float x = fmaxf(fmaxf(sc[0][g][i], sc[0][g][2 + i]), fmaxf(sc[1][g][i], sc[1][g][2 + i]));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    top[g][i] = fmaxf(m[g][i], x);
-                    grow = grow || top[g][i] > m[g][i];
+                    const float x = fmaxf(fmaxf(sc[0][g][i], sc[0][g][2 + i]), fmaxf(sc[1][g][i], sc[1][g][2 + i]));
+                    grow = grow || x * row_a[g][i] > m[g][i] + (float)kGrow;
                 }
             const float vmax = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));   // drops NaN
-            const uint32_t vbits = __reduce_max_sync(0xffffffffu, vmax > 0.0f && vmax <= 65504.0f ? __float_as_uint(vmax) : 0u);
-            const int ev_new = vbits == 0u ? -126 : (int)(vbits >> 23) - 126;   // scale < 2^ev_new
-            if (__any_sync(0xffffffffu, grow) || ev_new > ev) {
+            grow = grow || vmax * vf > (float)(1 << (15 - kGrow));
+            if (__any_sync(0xffffffffu, grow)) {
+                const uint32_t vbits = __reduce_max_sync(0xffffffffu, vmax > 0.0f && vmax <= 65504.0f ? __float_as_uint(vmax) : 0u);
+                const int ev_new = vbits == 0u ? ev : (int)(vbits >> 23) - 126;   // scale < 2^ev_new
                 const int en = ev_new > ev ? ev_new : ev;
-                const float shift = ev <= -126 ? 0.0f : pow2i(ev - en);   // nothing yet: zero times anything is zero
+                const float shift = pow2i(ev - en);
 #pragma unroll
                 for (int g = 0; g < NR; ++g) {
                     float f[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        f[i] = top[g][i] == m[g][i] ? 1.0f : ex2(m[g][i] - top[g][i]);
+                        float x = fmaxf(fmaxf(sc[0][g][i], sc[0][g][2 + i]), fmaxf(sc[1][g][i], sc[1][g][2 + i]));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * row_a[g][i];
+                        x = fmaxf(x, m[g][i]);
+                        f[i] = x == m[g][i] ? 1.0f : ex2(m[g][i] - x);
+                        m[g][i] = x;
                         l[g][i] *= f[i];
                         f[i] *= shift;
                         zs[g][i] *= f[i];
-                        m[g][i] = top[g][i];
                     }
 #pragma unroll
                     for (int w = 0; w < 2 * W; ++w)
@@ -443,11 +465,16 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
                         for (int i = 0; i < 4; ++i) o[g][w][i] *= f[i & 1];
                 }
                 ev = en;
+                vf = pow2i(15 - kGrow - ev);   // probabilities are fed below 2^15, clear of subnormals
             }
-            const float vf = ev <= -126 ? 0.0f : pow2i(15 - ev);   // probabilities are fed below 2^15, clear of subnormals
-            uint32_t ph[2][NR][2], pl[2][NR][2];
+            float ref[NR][2];
 #pragma unroll
-            for (int tl = 0; tl < 2; ++tl)
+            for (int g = 0; g < NR; ++g)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) ref[g][i] = m[g][i] == -CUDART_INF_F ? 0.0f : m[g][i];
+#pragma unroll
+            for (int tl = 0; tl < 2; ++tl) {
+                uint32_t ph[NR][2], pl[NR][2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float v = vs[tl][j] * vf;
@@ -456,20 +483,17 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
                         float pv[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float x = sc[tl][g][2 * j + i];
-                            const float e = ex2(x - (m[g][i] == -CUDART_INF_F ? 0.0f : m[g][i]));
+                            const float e = ex2(fmaf(sc[tl][g][2 * j + i], row_a[g][i], -ref[g][i]));
                             l[g][i] += e;
-                            pv[i] = x == -CUDART_INF_F ? 0.0f : e * v;   // a masked token's scale may be NaN
-                            zs[g][i] += pv[i] * vz[tl][j];
+                            pv[i] = e * v;
+                            zs[g][i] = fmaf(pv[i], vz[tl][j], zs[g][i]);
                         }
                         const uint32_t h = half2_bits(pv[0], pv[1]);
                         const float2 back = bits_half2(h);
-                        ph[tl][g][j] = transpose8(h);
-                        pl[tl][g][j] = transpose8(half2_bits(pv[0] - back.x, pv[1] - back.y));
+                        ph[g][j] = transpose8(h);
+                        pl[g][j] = transpose8(half2_bits(pv[0] - back.x, pv[1] - back.y));
                     }
                 }
-#pragma unroll
-            for (int tl = 0; tl < 2; ++tl) {
                 const uint8_t* const tile = st + tl * A::TB + kv4_v_off(D);
                 uint32_t va[W], vb[W];
                 lds_share<W>(tile + lane * (4 * W), va);
@@ -479,26 +503,28 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
                     const uint32_t va8 = va[w] >> 8, vb8 = vb[w] >> 8;
 #pragma unroll
                     for (int g = 0; g < NR; ++g) {
-                        mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, ph[tl][g][0], ph[tl][g][1]);
-                        mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, pl[tl][g][0], pl[tl][g][1]);
-                        mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, ph[tl][g][0], ph[tl][g][1]);
-                        mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, pl[tl][g][0], pl[tl][g][1]);
+                        mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, ph[g][0], ph[g][1]);
+                        mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, ph[g][0], ph[g][1]);
+                        mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, pl[g][0], pl[g][1]);
+                        mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, pl[g][0], pl[g][1]);
                     }
                 }
             }
-            ++used;
+            next_stage();
             fence_proxy_async_smem();
             __syncwarp();
             issue_next();
         }
         // copies in flight after a wait gave up
-        for (; used != issued; ++used)
-            wait_drain(smem_addr(&sh.bar[warp][used % kStages]), (used / kStages) & 1, p.wait_limit_ns);
+        while (pending != 0) {
+            wait_drain(smem_addr(&sh.bar[warp][s_use]), phase, p.wait_limit_ns);
+            next_stage();
+        }
         __syncwarp();
 
         // ---- the four warps' shares: into shared memory, each in its own ring
         float* const mine = reinterpret_cast<float*>(ring);
-        const float o_unit = ev <= -126 ? 0.0f : pow2i(ev - 15);
+        const float o_unit = pow2i(ev - (15 - kGrow));
 #pragma unroll
         for (int g = 0; g < NR; ++g) {
 #pragma unroll
@@ -586,7 +612,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
         }
         if (!whole) {
             // ---- the last CTA of the segment to arrive joins the partial results, in the CTAs' order
-            const long long g0 = u - pos;   // the segment's first unit
+            const long long g0 = seg_u + kOverhead;   // the place of the segment's first unit
             const int ca = (int)(((g0 + 1) * ctas - 1) / total), cb = (int)(((g0 + r.units) * ctas - 1) / total);
             __threadfence();
             __syncthreads();
@@ -598,45 +624,70 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const Kv4AttnParams 
             }
             __syncthreads();
             if (sh.last) {
+                // first every partial's weight (all rows and CTAs at once, kept where the rings were), then the sums
+                const int parts = cb - ca + 1;
+                float* const wt = reinterpret_cast<float*>(smem);
+                auto part_of = [&](int k) { return p.partials + (long long)(2 * (ca + k) + (k == 0)) * A::PART; };
+                for (int i = tid; i < parts * live; i += kThreads) wt[i] = __ldcg(part_of(i / live) + ROWS * D + i % live);
+                __syncthreads();
+                if (warp < live) {
+                    for (int row = warp; row < live; row += kWarps) {
+                        float mm = -CUDART_INF_F, ll = 0.0f;
+                        for (int k = lane; k < parts; k += 32) mm = fmaxf(mm, wt[k * live + row]);
+#pragma unroll
+                        for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+                        for (int k = lane; k < parts; k += 32) {
+                            const float mk = wt[k * live + row], f = mk == mm ? 1.0f : ex2(mk - mm);
+                            wt[k * live + row] = f;
+                            ll += f * __ldcg(part_of(k) + ROWS * D + ROWS + row);
+                        }
+#pragma unroll
+                        for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+                        if (lane == 0) {
+                            sh.l[0][row] = ll == 0.0f ? 0.0f : 1.0f / ll;
+                            if (p.lse) {
+                                const int rr = row0 + row, qi = rr / p.group;
+                                p.lse[(long long)(r.q0 + qi) * p.q_heads + head * p.group + rr - qi * p.group] =
+                                    ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * CUDART_LN2_F;
+                            }
+                        }
+                    }
+                }
+                __syncthreads();
                 for (int i = tid; i < live * (D / 4); i += kThreads) {
                     const int row = i / (D / 4), d = i % (D / 4) * 4;
-                    float mm = -CUDART_INF_F, ll = 0.0f;
                     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int k = ca; k <= cb; ++k)
-                        mm = fmaxf(mm, __ldcg(p.partials + (long long)(2 * k + (k == ca)) * A::PART + ROWS * D + row));
-#pragma unroll 4
-                    for (int k = ca; k <= cb; ++k) {
-                        const float* q = p.partials + (long long)(2 * k + (k == ca)) * A::PART;
-                        const float mk = __ldcg(q + ROWS * D + row);
-                        const float f = mk == mm ? 1.0f : ex2(mk - mm);
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(q + row * D + d));
-                        ll += f * __ldcg(q + ROWS * D + ROWS + row);
+#pragma unroll 8
+                    for (int k = 0; k < parts; ++k) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(part_of(k) + row * D + d));
+                        const float f = wt[k * live + row];
                         x.x += f * y.x;
                         x.y += f * y.y;
                         x.z += f * y.z;
                         x.w += f * y.w;
                     }
-                    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+                    const float inv = sh.l[0][row];
                     store_row(row, d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-                    if (d == 0 && p.lse) {
-                        const int rr = row0 + row, qi = rr / p.group;
-                        p.lse[(long long)(r.q0 + qi) * p.q_heads + head * p.group + rr - qi * p.group] =
-                            ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * CUDART_LN2_F;
-                    }
                 }
             }
         }
         // the rings are read: bulk copies may follow the plain accesses
         fence_proxy_async_smem();
         __syncthreads();
-        u += take;
-        off += take;
     }
 }
 
 template <int D, int NR>
 struct Launch {
     static inline int per_sm = 1;   // CTAs an SM holds
+
+    // CTAs of a launch: what the GPU holds, the workspace counts, and a join's weights in the rings leave room for
+    static int grid_of(int sms)
+    {
+        const int most = (int)(kWarps * Attn<D, NR>::RING / (Attn<D, NR>::ROWS * sizeof(float)));
+        const int fit = most < kWsMaxGrid ? most : kWsMaxGrid;
+        return sms * per_sm < fit ? sms * per_sm : fit;
+    }
 
     static cudaError_t setup()
     {
@@ -648,7 +699,7 @@ struct Launch {
 
     static cudaError_t run(const Kv4AttnParams& p, int sms, cudaStream_t stream)
     {
-        const int grid = sms * per_sm < kWsMaxGrid ? sms * per_sm : kWsMaxGrid;
+        const int grid = grid_of(sms);
         kv4_attn_kernel<D, NR><<<grid, kThreads, Attn<D, NR>::SMEM, stream>>>(p);
         return cudaGetLastError();
     }
@@ -658,15 +709,14 @@ struct Launch {
 size_t kv4_partial_bytes(int sms)
 {
     size_t need = 0;
-    auto most = [&](int per_sm, int part) {
-        const size_t grid = (size_t)(sms * per_sm < kWsMaxGrid ? sms * per_sm : kWsMaxGrid);
-        const size_t bytes = 2 * grid * part * sizeof(float);
+    auto most = [&](int grid, int part) {
+        const size_t bytes = (size_t)2 * grid * part * sizeof(float);
         need = bytes > need ? bytes : need;
     };
-    most(Launch<64, 1>::per_sm, Attn<64, 1>::PART);
-    most(Launch<64, 2>::per_sm, Attn<64, 2>::PART);
-    most(Launch<128, 1>::per_sm, Attn<128, 1>::PART);
-    most(Launch<128, 2>::per_sm, Attn<128, 2>::PART);
+    most(Launch<64, 1>::grid_of(sms), Attn<64, 1>::PART);
+    most(Launch<64, 2>::grid_of(sms), Attn<64, 2>::PART);
+    most(Launch<128, 1>::grid_of(sms), Attn<128, 1>::PART);
+    most(Launch<128, 2>::grid_of(sms), Attn<128, 2>::PART);
     return need;
 }
 
@@ -676,14 +726,24 @@ cudaError_t setup_kv4()
     if ((e = Launch<64, 1>::setup()) != cudaSuccess || (e = Launch<64, 2>::setup()) != cudaSuccess ||
         (e = Launch<128, 1>::setup()) != cudaSuccess || (e = Launch<128, 2>::setup()) != cudaSuccess)
         return e;
-    return cudaSuccess;
+    return setup_kv4_prompt();
 }
 
-cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int head_dim, int max_q, int sms, cudaStream_t stream)
+// Requests of up to kFewRows rows go to the stream-K kernel, longer ones to the tcgen05
+// kernel; which is which is known on the device, so a batch that may hold both gets both.
+constexpr int kFewRows = 32;
+
+cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_q, int sms, cudaStream_t stream)
 {
-    const bool wide = (long long)max_q * p.group > 8;
-    if (head_dim == 128) return wide ? Launch<128, 2>::run(p, sms, stream) : Launch<128, 1>::run(p, sms, stream);
-    return wide ? Launch<64, 2>::run(p, sms, stream) : Launch<64, 1>::run(p, sms, stream);
+    Kv4AttnParams p = in;
+    const long long rows = (long long)max_q * p.group;
+    p.few_rows = rows <= kFewRows ? INT_MAX : kFewRows;   // max_q may be too small: then this kernel serves all
+    const bool wide = rows > 8;
+    cudaError_t e;
+    if (head_dim == 128) e = wide ? Launch<128, 2>::run(p, sms, stream) : Launch<128, 1>::run(p, sms, stream);
+    else e = wide ? Launch<64, 2>::run(p, sms, stream) : Launch<64, 1>::run(p, sms, stream);
+    if (e != cudaSuccess || rows <= kFewRows) return e;
+    return launch_kv4_prompt(p, head_dim, stream);
 }
 
 }  // namespace w4a16

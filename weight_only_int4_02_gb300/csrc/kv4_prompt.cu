@@ -1,0 +1,708 @@
+// Attention over the 4-bit paged cache for many query rows (prompt chunks): the
+// mathematics of kv4_attn.cu on the tcgen05 tensor cores.
+//
+// A CTA owns 256 rows (query token, query head of the group) of one request's KV head, as
+// two tiles of 128, and walks the cached tokens in blocks of 128:
+//   S = Q (c_k - z_k)^T          both operands in shared memory, S in tensor memory
+//   P = 2^(a s_k S - m) s_v      by the rows' threads, written over S as binary16
+//   O += P (c_v - z_v)           P from tensor memory, V from shared memory
+// Codes less their zero-points are whole numbers of -15 .. 15, exact in binary16; the
+// scales act on scores and probabilities in FP32, so the one rounding of the chain is P's to
+// binary16. For bfloat16 outputs it is an eighth of theirs; for binary16 outputs it would be as
+// large as theirs, so there P is fed as a high and a low part (half as many products again).
+// V's scales are fed relative to the largest seen so far and P below 2^15, clear of
+// overflow and of subnormals.
+//
+// Warps: 0-3 and 4-7 the softmax of a tile each, one thread a row (no word between threads),
+// the row's 128 scores in registers; 8-11 unpack K (one thread a token) and V (one thread 8
+// tokens x D/8 values of d), reading codes straight from HBM or L2 into registers most of a
+// block ahead, so that there is no staging of packed data; 12 issues the MMAs. Two row tiles
+// share every unpacked block and keep the tensor pipe busy with one tile's products while
+// the other's softmax runs: O_A(i), S_A(i+1), O_B(i), S_B(i+1), ...
+// O is rescaled only when a row's maximum grew by more than 2^8 (its P stays below 2^15 until then).
+#include "api_internal.cuh"
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+#include <float.h>
+#include <math_constants.h>
+
+namespace w4a16 {
+namespace {
+
+constexpr int kRows = 128;            // rows of a tile
+constexpr int kBlock = 128;           // cached tokens of a block
+constexpr int kMmaWarp = 12;
+constexpr int kThreads = 512;         // four warpgroups, of the last the MMA warp alone at work
+// Registers a thread: 128 at launch, moved to the softmax from the warps that need fewer. Each
+// of the SM's four quarters holds one warp of every warpgroup and a quarter of the registers.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 184, kUnpackRegs = 88, kIssueRegs = 56;
+static_assert(2 * kSoftmaxRegs + kUnpackRegs + kIssueRegs <= 4 * kLaunchRegs, "registers of the block");
+constexpr int kScaleStages = 4;       // K's scales live until the softmax has read them: two blocks past K itself
+constexpr int kGrow = 8;              // log2 of how far P may grow before O is rescaled
+
+template <int D>
+struct Prompt {
+    static constexpr int TB = kv4_tile_bytes(D);
+    static constexpr int QT = kRows * D * 2;       // bytes of a Q tile, of a K block, of a V block
+    static constexpr int OFF_K = 2 * QT;
+    static constexpr int OFF_V = OFF_K + 2 * QT;
+    static constexpr int OFF_MISC = OFF_V + 2 * QT;
+    static constexpr int S_COL = 0, O_COL = 2 * kBlock;   // tensor memory columns: S of both tiles (P over it), O of both
+    struct Misc {
+        float sk[kScaleStages][kBlock];
+        float sv[2][kBlock];
+        uint32_t valid[kScaleStages][4];     // tokens that are stored and inside the request
+        uint32_t odd[2][4];                  // tokens whose V scale is NaN
+        uint32_t vred[2][4];
+        int ev[2];                           // V's scales so far are below 2^ev
+        uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], skfull[kScaleStages], sfull[2], pfull[2], odone[2], teardown;
+        uint32_t tmem;
+        int abort_flag, b, rt;
+    };
+    // one CTA an SM: it holds all of the SM's tensor memory
+    static constexpr int SMEM = (OFF_MISC + (int)sizeof(Misc) > 120 * 1024 ? OFF_MISC + (int)sizeof(Misc) : 120 * 1024) + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // e in -126 .. 127
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b)
+{
+    const __half2 h = __hsub2(as_half2(a), as_half2(b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c)
+{
+    const __half2 h = __hfma2(as_half2(a), as_half2(b), as_half2(c));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four registers of code - zero from a word: nibbles (0,4), (1,5), (2,6), (3,7). A nibble in the
+// mantissa of 1024.0 is 1024 + c, or 1024 + 16 c for the high one of a byte, exactly; lo = 1024 + z and
+// hi = -(64 + z), in the halves' order.
+__device__ __forceinline__ void unpack4(uint32_t w, uint32_t lo, uint32_t hi, uint32_t (&r)[4])
+{
+    constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kMagic = 0x64006400u, kSixteenth = 0x2c002c00u;
+    const uint32_t w8 = w >> 8;
+    r[0] = sub2(and_or(w, kLow, kMagic), lo);
+    r[1] = fma2(and_or(w, kHigh, kMagic), kSixteenth, hi);
+    r[2] = sub2(and_or(w8, kLow, kMagic), lo);
+    r[3] = fma2(and_or(w8, kHigh, kMagic), kSixteenth, hi);
+}
+
+// Byte offset of a 16-byte chunk of a K-major tile in 128-byte swizzle: blocks of 64 columns, rows of 128 bytes.
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk, int block_rows)
+{
+    return (uint32_t)((chunk >> 3) * block_rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <int D, bool BF>
+__global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnParams p)
+{
+    using C = Prompt<D>;
+    constexpr int W = D / 32;
+    extern __shared__ __align__(16) uint8_t raw_smem[];
+    uint8_t* const smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_addr(smem);
+    typename C::Misc& sh = *reinterpret_cast<typename C::Misc*>(smem + C::OFF_MISC);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // ---- this CTA's rows: CTAs count KV heads fastest, then row tiles, the last rows of a request
+    // (which see the most tokens) first
+    const int head = blockIdx.x % p.kv_heads;
+    if (warp == 0) {
+        const int want = blockIdx.x / p.kv_heads;
+        int at = 0;
+        if (lane == 0) sh.b = -1;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            int tiles = 0;
+            if (b0 + lane < p.batch) {
+                int a = p.starts[b0 + lane], e = p.starts[b0 + lane + 1];
+                a = a < 0 ? 0 : a > p.tokens ? p.tokens : a;
+                e = e < a ? a : e > p.tokens ? p.tokens : e;
+                const int rows = (e - a) * p.group;
+                tiles = rows > p.few_rows ? (rows + 2 * kRows - 1) / (2 * kRows) : 0;
+            }
+            int incl = tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += o;
+            }
+            if (want >= at + incl - tiles && want < at + incl) {
+                sh.b = b0 + lane;
+                sh.rt = at + incl - 1 - want;
+            }
+            at += __shfl_sync(0xffffffffu, incl, 31);
+            if (want < at) break;
+        }
+        __syncwarp();
+        if (lane == 0) {
+            sh.abort_flag = 0;
+            mbar_init(smem_addr(&sh.qfull), 2 * kRows);
+            mbar_init(smem_addr(&sh.teardown), 1);
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(smem_addr(&sh.kfull[s]), kBlock);
+                mbar_init(smem_addr(&sh.vfull[s]), kBlock);
+                mbar_init(smem_addr(&sh.kempty[s]), 1);
+                mbar_init(smem_addr(&sh.vempty[s]), 1);
+                mbar_init(smem_addr(&sh.sfull[s]), 1);
+                mbar_init(smem_addr(&sh.pfull[s]), kRows);
+                mbar_init(smem_addr(&sh.odone[s]), 1);
+            }
+            for (int s = 0; s < kScaleStages; ++s) mbar_init(smem_addr(&sh.skfull[s]), 4);
+            fence_mbar_init();
+        }
+    }
+    __syncthreads();
+    const int b = sh.b;
+    if (b < 0) return;   // more CTAs than row tiles
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(&sh.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const WaitCtl ctl{&sh.abort_flag, p.status, p.wait_limit_ns};
+
+    const long long held = (long long)p.table_cols * p.page_size;
+    int seq = p.seq_lens[b];
+    seq = seq < 0 ? 0 : seq < held ? seq : (int)held;
+    int q0 = p.starts[b], q1 = p.starts[b + 1];
+    q0 = q0 < 0 ? 0 : q0 > p.tokens ? p.tokens : q0;
+    q1 = q1 < q0 ? q0 : q1 > p.tokens ? p.tokens : q1;
+    const int nq = q1 - q0, rows = nq * p.group, row0 = sh.rt * 2 * kRows;
+    const int end_row = row0 + 2 * kRows < rows ? row0 + 2 * kRows : rows;
+    // cached tokens that some row here sees: from base to end
+    const int pos_first = seq - nq + row0 / p.group, pos_last = seq - nq + (end_row - 1) / p.group;
+    const int low = p.window > 0 ? pos_first - p.window + 1 : 0;
+    const int base = low > 0 ? low / kBlock * kBlock : 0;
+    const int blocks = pos_last >= base ? (pos_last - base) / kBlock + 1 : 0;
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax: one thread a row
+        setmaxnreg_inc<kSoftmaxRegs>();
+        const int tile = warp >> 2;
+        const int row = row0 + tile * kRows + (warp & 3) * 32 + lane;
+        const bool live = row < rows;
+        const int qi = row / p.group, hq = row - qi * p.group;
+        const int pos = live ? seq - nq + qi : -1;
+        float a;   // score = a * (s_k S) in powers of two
+        {
+            uint32_t raw[D / 2];
+#pragma unroll
+            for (int i = 0; i < D / 2; ++i) raw[i] = 0;
+            if (live) {
+                const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.q + (long long)(q0 + qi) * p.q_token +
+                                                                  (long long)(head * p.group + hq) * p.q_head);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = src[i];
+                    raw[4 * i] = v.x;
+                    raw[4 * i + 1] = v.y;
+                    raw[4 * i + 2] = v.z;
+                    raw[4 * i + 3] = v.w;
+                }
+            }
+            auto lo_of = [&](uint32_t x) { return BF ? __uint_as_float(x << 16) : __low2float(as_half2(x)); };
+            auto hi_of = [&](uint32_t x) { return BF ? __uint_as_float(x & 0xffff0000u) : __high2float(as_half2(x)); };
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 2; ++i) top = fmaxf(top, fmaxf(fabsf(lo_of(raw[i])), fabsf(hi_of(raw[i]))));
+            // largest magnitude into [2^9, 2^10), by a power of two; an infinity or a NaN stays one
+            int e = ((__float_as_int(top) >> 23) & 255) - 127 - 9;
+            e = (top == 0.0f || !(top <= FLT_MAX)) ? 0 : e < -120 ? -120 : e;
+            // a negative softmax scale goes into Q, so that the largest score is that of the largest product
+            const float f = p.scale_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
+            a = fabsf(p.scale_log2) * pow2i(e);
+            a = a > 0.0f ? a : FLT_MIN;   // scale 0: all scores nearly equal, and masked ones stay -infinity
+            const uint32_t qb = sbase + tile * C::QT;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[2 * i] = lo_of(raw[4 * j + i]) * f;
+                    x[2 * i + 1] = hi_of(raw[4 * j + i]) * f;
+                }
+                // the order in which a word of K's codes unpacks
+                sts128(qb + swizzled(row - row0 - tile * kRows, j, kRows), half2_bits(x[0], x[4]), half2_bits(x[1], x[5]),
+                       half2_bits(x[2], x[6]), half2_bits(x[3], x[7]));
+            }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(smem_addr(&sh.qfull));
+
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_at = lanes + C::S_COL + tile * kBlock, o_at = lanes + C::O_COL + tile * D;
+        const int t_row0 = row0 + tile * kRows;
+        const int t_last = t_row0 + kRows < rows ? t_row0 + kRows : rows;
+        const int pos_min = t_row0 < rows ? seq - nq + t_row0 / p.group : -1;
+        const int pos_max = t_row0 < rows ? seq - nq + (t_last - 1) / p.group : -1;
+        float m = -CUDART_INF_F;   // of s_k S
+        uint64_t l2 = 0;           // sums of even and odd columns
+        const uint64_t a2 = pack_f32x2(a, a);
+        int ev = -126;
+        bool ok = true, poisoned = false;
+#pragma unroll 1
+        for (int i = 0; i < blocks; ++i) {
+            const int s4 = i % kScaleStages, s2 = i & 1;
+            if (!wait_warp(smem_addr(&sh.skfull[s4]), (i / kScaleStages) & 1, ctl) ||
+                !wait_warp(smem_addr(&sh.sfull[tile]), i & 1, ctl)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // x: s_k times the products, then the exponent, pairs of columns
+            uint64_t x[kBlock / 2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t r[64];
+                tmem_ld64(s_at + 64 * c, r);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    x[32 * c + j] = pack_f32x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+            }
+#pragma unroll
+            for (int j = 0; j < kBlock / 2; j += 2) {
+                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sh.sk[s4][2 * j]);
+                x[j] = mul_f32x2(x[j], k.x);
+                x[j + 1] = mul_f32x2(x[j + 1], k.y);
+            }
+            const int t0 = base + i * kBlock;
+            const uint4 vw = *reinterpret_cast<const uint4*>(sh.valid[s4]);
+            const bool full = (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu && t0 + kBlock - 1 <= pos_min &&
+                              (p.window <= 0 || t0 > pos_max - p.window);
+            // this row's visible columns of the block, where stored: word w's bits
+            auto see = [&](int w) -> uint32_t {
+                const int hi = pos - t0 + 1 - 32 * w, lo = (p.window > 0 ? pos - p.window + 1 - t0 : 0) - 32 * w;
+                const uint32_t upto = hi <= 0 ? 0u : hi >= 32 ? 0xffffffffu : (1u << hi) - 1u;
+                const uint32_t below = lo <= 0 ? 0u : lo >= 32 ? 0xffffffffu : (1u << lo) - 1u;
+                return sh.valid[s4][w] & upto & ~below;
+            };
+            if (!full) {
+                // selected, not added: what a row does not see may be any memory
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t bits = see(w);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float u, v;
+                        unpack_f32x2(x[16 * w + j], u, v);
+                        u = bits >> (2 * j) & 1u ? u : -CUDART_INF_F;
+                        v = bits >> (2 * j + 1) & 1u ? v : -CUDART_INF_F;
+                        x[16 * w + j] = pack_f32x2(u, v);
+                    }
+                }
+            }
+            float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+            for (int j = 0; j < kBlock / 2; ++j) {
+                float u, v;
+                unpack_f32x2(x[j], u, v);
+                tops[j & 3] = fmaxf(tops[j & 3], fmaxf(u, v));
+            }
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            if (!wait_warp(smem_addr(&sh.vfull[s2]), (i >> 1) & 1, ctl)) {
+                ok = false;
+                break;
+            }
+            const int en = sh.ev[s2];
+            const uint4 ow = *reinterpret_cast<const uint4*>(sh.odd[s2]);
+            if (ow.x | ow.y | ow.z | ow.w)   // a NaN in V's scales shows in the rows that see it
+                poisoned = poisoned || ((ow.x & see(0)) | (ow.y & see(1)) | (ow.z & see(2)) | (ow.w & see(3))) != 0u;
+            float f = 1.0f;
+            if (top > m) {
+                if (m == -CUDART_INF_F) {
+                    m = top;       // nothing so far: l and O are zero
+                } else if ((top - m) * a > (float)kGrow) {
+                    f = ex2((m - top) * a);
+                    m = top;
+                    l2 = mul_f32x2(l2, pack_f32x2(f, f));
+                }
+            }
+            if (en != ev) {
+                if (ev > -126) f *= pow2i(ev - en > -126 ? ev - en : -126);
+                ev = en;
+            }
+            if (i > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                if (!wait_warp(smem_addr(&sh.odone[tile]), (i - 1) & 1, ctl)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    float y[16];
+                    uint32_t r[16];
+                    tmem_ld_f32<16>(o_at + c, y);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(y[j] * f);
+                    tmem_st16(o_at + c, r);
+                }
+            }
+            const float ma = m == -CUDART_INF_F ? 0.0f : m * a;
+            const uint64_t ma2 = pack_f32x2(-ma, -ma);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&sh.sv[s2][32 * c + 2 * j]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float u0, u1;
+                        unpack_f32x2(fma_f32x2(x[16 * c + j + q], a2, ma2), u0, u1);
+                        const uint64_t e = pack_f32x2(ex2(u0), ex2(u1));
+                        l2 = add_f32x2(l2, e);
+                        float p0, p1;
+                        unpack_f32x2(mul_f32x2(e, q ? v.y : v.x), p0, p1);
+                        hi[j + q] = half2_bits(p0, p1);
+                        if constexpr (!BF) {
+                            const float2 back = __half22float2(as_half2(hi[j + q]));
+                            lo[j + q] = half2_bits(p0 - back.x, p1 - back.y);
+                        }
+                    }
+                }
+                // the high parts of 32 columns over the first 16 of them, the low parts over the others
+                tmem_st16_async(s_at + 32 * c, hi);
+                if constexpr (!BF) tmem_st16_async(s_at + 32 * c + 16, lo);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_addr(&sh.pfull[tile]));
+        }
+        float l, l_odd;
+        unpack_f32x2(l2, l, l_odd);
+        l += l_odd;
+        if (ok && blocks > 0) {
+            ok = wait_warp(smem_addr(&sh.odone[tile]), (blocks - 1) & 1, ctl);
+            tc_fence_after();
+        }
+        if (ok) {
+            const float inv = l == 0.0f ? 0.0f : poisoned ? CUDART_NAN_F : pow2i(ev - 7 > -126 ? ev - 7 : -126) / l;
+            uint16_t* dst = (uint16_t*)p.out + (long long)(q0 + qi) * p.o_token + (long long)(head * p.group + hq) * p.o_head;
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+                float x[16];
+                if (blocks > 0) tmem_ld_f32<16>(o_at + c, x);
+                uint32_t r[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float u = l == 0.0f ? 0.0f : x[2 * j] * inv, v = l == 0.0f ? 0.0f : x[2 * j + 1] * inv;
+                    if constexpr (BF) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(u, v);
+                        r[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                        r[j] = half2_bits(u, v);
+                    }
+                }
+                if (live) {
+                    *reinterpret_cast<uint4*>(dst + c) = make_uint4(r[0], r[1], r[2], r[3]);
+                    *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+                }
+            }
+            if (live && p.lse)
+                p.lse[(long long)(q0 + qi) * p.q_heads + head * p.group + hq] =
+                    l == 0.0f ? -CUDART_INF_F : (m * a + log2f(l)) * CUDART_LN2_F;
+        }
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------------ unpack
+        setmaxnreg_dec<kUnpackRegs>();
+        const int t = tid - 8 * 32;   // 0 .. 127
+        const int32_t* const trow = p.table + (long long)b * p.table_stride;
+        const int tpp_shift = __ffs(p.page_size) - 1 - 4;
+        // K: token t, of tile t / 16. V: tokens 8 vh .. 8 vh + 7 of tile vt, values vn D/8 .. of d, so
+        // that the eight 16-byte chunks of a swizzled row are written by eight neighbouring lanes
+        const int vh = t & 1, vt = (t >> 6) * 4 + ((t >> 1) & 3), vn = (t >> 3) & 7;
+        auto page_of = [&](int i, int tile) {   // the page that holds a tile of block i, or -1
+            const int g = (base + i * kBlock) / kKv4Tile + tile;
+            if (i >= blocks || g * kKv4Tile >= seq) return -1;
+            const int page = trow[g >> tpp_shift];
+            return page >= 0 && page < p.pages ? page : -1;
+        };
+        auto tile_at = [&](int i, int tile, int page) {
+            const int g = (base + i * kBlock) / kKv4Tile + tile;
+            return p.cache + ((((long long)page * p.kv_heads + head) << tpp_shift) + (g & ((1 << tpp_shift) - 1))) * C::TB;
+        };
+        constexpr uint32_t kNotStored = 0x10000u;
+        uint4 kw[W], vw[W];
+        uint2 vz;
+        uint32_t kz, ks, vs;   // scales: binary16 bits of token t's, or kNotStored
+        auto load_k = [&](int i, int page) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) kw[j] = make_uint4(0, 0, 0, 0);
+            kz = 0;
+            ks = vs = kNotStored;
+            if (page >= 0) {
+                const uint8_t* const tile = tile_at(i, t >> 4, page);
+                const uint4* at = reinterpret_cast<const uint4*>(tile + (t & 15) * (D / 2));
+#pragma unroll
+                for (int j = 0; j < W; ++j) kw[j] = __ldg(at + j);
+                kz = __ldg(tile + kv4_k_zero_off(D) + (t & 15));
+                if (base + i * kBlock + t < seq) {
+                    ks = __ldg(reinterpret_cast<const uint16_t*>(tile + kv4_k_scale_off(D)) + (t & 15));
+                    vs = __ldg(reinterpret_cast<const uint16_t*>(tile + kv4_v_scale_off(D)) + (t & 15));
+                }
+            }
+        };
+        auto load_v = [&](int i, int page) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) vw[j] = make_uint4(0, 0, 0, 0);
+            vz = make_uint2(0, 0);
+            if (page >= 0) {
+                const uint8_t* const tile = tile_at(i, vt, page);
+                const uint4* at = reinterpret_cast<const uint4*>(tile + kv4_v_off(D) + (vh * 8 + vn) * (16 * W));
+#pragma unroll
+                for (int j = 0; j < W; ++j) vw[j] = __ldg(at + j);
+                vz = __ldg(reinterpret_cast<const uint2*>(tile + kv4_v_zero_off(D) + 8 * vh));
+            }
+        };
+        load_k(0, page_of(0, t >> 4));
+        load_v(0, page_of(0, vt));
+        int kpage = page_of(1, t >> 4), vpage = page_of(1, vt);
+        int ev = -126;
+#pragma unroll 1
+        for (int i = 0; i < blocks; ++i) {
+            const int s2 = i & 1, s4 = i % kScaleStages;
+            if (!wait_warp(smem_addr(&sh.kempty[s2]), ((i >> 1) & 1) ^ 1, ctl)) sh.abort_flag = 1;
+            {
+                const bool stored = ks != kNotStored;
+                sh.sk[s4][t] = stored ? __half2float(__ushort_as_half((uint16_t)ks)) : 0.0f;
+                const uint32_t bits = __ballot_sync(0xffffffffu, stored);
+                if (lane == 0) sh.valid[s4][warp & 3] = bits;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.skfull[s4]));
+                const uint32_t z = kz & 255u;
+                const uint32_t lo = (0x6400u + z) * 0x00010001u, hi = (0xd400u + (z << 4)) * 0x00010001u;
+                const uint32_t kb = sbase + C::OFF_K + s2 * C::QT;
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const uint32_t w[4] = {kw[j].x, kw[j].y, kw[j].z, kw[j].w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t r[4];
+                        unpack4(w[q], lo, hi, r);
+                        sts128(kb + swizzled(t, 4 * j + q, kBlock), r[0], r[1], r[2], r[3]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_addr(&sh.kfull[s2]));
+            const uint32_t my_vs = vs;
+            load_k(i + 1, kpage);
+            kpage = page_of(i + 2, t >> 4);
+
+            const bool ready = wait_warp(smem_addr(&sh.vempty[s2]), ((i >> 1) & 1) ^ 1, ctl);
+            {
+                // the exponent that bounds V's scales so far
+                const bool stored = my_vs != kNotStored;
+                float scale = stored ? __half2float(__ushort_as_half((uint16_t)my_vs)) : 0.0f;
+                const uint32_t odd = __ballot_sync(0xffffffffu, scale != scale);
+                if (scale != scale) scale = 0.0f;
+                const uint32_t wmax = __reduce_max_sync(0xffffffffu, scale <= 65504.0f ? __float_as_uint(scale) & 0x7fffffffu : 0u);
+                if (lane == 0) {
+                    sh.odd[s2][warp & 3] = odd;
+                    sh.vred[s2][warp & 3] = wmax;
+                }
+                if (named_bar_or(1, kBlock, !ready)) break;   // all of these warps or none
+                const uint4 red = *reinterpret_cast<const uint4*>(sh.vred[s2]);
+                uint32_t top = red.x > red.y ? red.x : red.y;
+                top = red.z > top ? red.z : top;
+                top = red.w > top ? red.w : top;
+                const int en = top == 0u ? -126 : (int)(top >> 23) - 126;
+                ev = en > ev ? en : ev;
+                sh.sv[s2][t] = scale * (ev <= -126 ? 0.0f : pow2i(15 - kGrow - ev));
+                if (t == 0) sh.ev[s2] = ev;
+                uint32_t lo[4], hi[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t zz = (c < 2 ? vz.x : vz.y) >> (16 * (c & 1));
+                    const uint32_t z2 = (zz & 255u) | (zz >> 8 & 255u) << 16;   // tokens 2c and 2c + 1
+                    lo[c] = 0x64006400u + z2;
+                    hi[c] = 0xd400d400u + (z2 << 4);
+                }
+                uint32_t w[4][W];   // [pair of tokens][word]
+                if constexpr (W == 4) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        w[c][0] = vw[c].x;
+                        w[c][1] = vw[c].y;
+                        w[c][2] = vw[c].z;
+                        w[c][3] = vw[c].w;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        w[2 * c][0] = vw[c].x;
+                        w[2 * c][1] = vw[c].y;
+                        w[2 * c + 1][0] = vw[c].z;
+                        w[2 * c + 1][1] = vw[c].w;
+                    }
+                }
+                const uint32_t vb = sbase + C::OFF_V + s2 * C::QT;
+                const int chunk = vt * 2 + vh;
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    uint32_t r[4][4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) unpack4(w[c][j], lo[c], hi[c], r[c]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        sts128(vb + swizzled(vn * (D / 8) + 4 * j + q, chunk, D), r[0][q], r[1][q], r[2][q], r[3][q]);
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_addr(&sh.vfull[s2]));
+            load_v(i + 1, vpage);
+            vpage = page_of(i + 2, vt);
+        }
+    } else {
+        // ------------------------------------------------------------ MMA issue
+        setmaxnreg_dec<kIssueRegs>();
+        if (warp == kMmaWarp) {
+        constexpr uint32_t idesc_s = idesc_f16_f32(128, kBlock), idesc_o = idesc_f16_f32(128, D);
+        auto scores = [&](int tile, int s2) {
+            const uint64_t qd = smem_desc_k_sw128(sbase + tile * C::QT), kd = smem_desc_k_sw128(sbase + C::OFF_K + s2 * C::QT);
+            const uint32_t d = tmem + C::S_COL + tile * kBlock;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint64_t off = (uint64_t)((k >> 2) * (kRows * 8) + (k & 3) * 2);
+                mma_f16_ss(d, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
+            }
+        };
+        auto outputs = [&](int tile, int s2, bool first) {
+            const uint64_t vd = smem_desc_k_sw128(sbase + C::OFF_V + s2 * C::QT);
+            const uint32_t d = tmem + C::O_COL + tile * D, a = tmem + C::S_COL + tile * kBlock;
+            // 32 columns of P lie in the first 16 of S's columns for them, their low parts in the others
+#pragma unroll
+            for (int k = 0; k < kBlock / 16; ++k)
+                mma_f16_ts(d, a + (k >> 1) * 32 + (k & 1) * 8, vd + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), idesc_o,
+                           (!first || k > 0) ? 1u : 0u);
+            if constexpr (!BF) {
+#pragma unroll
+                for (int k = 0; k < kBlock / 16; ++k)
+                    mma_f16_ts(d, a + (k >> 1) * 32 + 16 + (k & 1) * 8, vd + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2),
+                               idesc_o, 1u);
+            }
+        };
+        bool ok = blocks > 0 && wait_warp(smem_addr(&sh.qfull), 0, ctl) && wait_warp(smem_addr(&sh.kfull[0]), 0, ctl);
+        if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+                scores(0, 0);
+                mma_commit(smem_addr(&sh.sfull[0]));
+                scores(1, 0);
+                mma_commit(smem_addr(&sh.sfull[1]));
+                mma_commit(smem_addr(&sh.kempty[0]));
+            }
+            __syncwarp();
+        }
+        for (int i = 0; ok && i < blocks; ++i) {
+            const int s2 = i & 1, n2 = s2 ^ 1;
+            const bool more = i + 1 < blocks;
+            if (!wait_warp(smem_addr(&sh.vfull[s2]), (i >> 1) & 1, ctl)) break;
+            if (more && !wait_warp(smem_addr(&sh.kfull[n2]), ((i + 1) >> 1) & 1, ctl)) break;
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                if (ok && !wait_warp(smem_addr(&sh.pfull[tile]), i & 1, ctl)) ok = false;
+                if (!ok) continue;
+                tc_fence_after();
+                if (elect_one()) {
+                    outputs(tile, s2, i == 0);
+                    mma_commit(smem_addr(&sh.odone[tile]));
+                    if (tile == 1) mma_commit(smem_addr(&sh.vempty[s2]));
+                    if (more) {
+                        scores(tile, n2);
+                        mma_commit(smem_addr(&sh.sfull[tile]));
+                        if (tile == 1) mma_commit(smem_addr(&sh.kempty[n2]));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        // every MMA issued so far completes before the tensor memory is freed
+        if (elect_one()) {
+            mma_commit(smem_addr(&sh.teardown));
+            wait_drain(smem_addr(&sh.teardown), 0, 1000000000LL);
+        }
+        __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+namespace {
+
+template <int D, bool BF>
+cudaError_t setup_one()
+{
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, kv4_prompt_kernel<D, BF>);
+    if (e != cudaSuccess) return e;
+    // the warpgroups' shares have to fit the registers the block is launched with
+    if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(kv4_prompt_kernel<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Prompt<D>::SMEM);
+}
+
+template <int D, bool BF>
+cudaError_t launch_one(const Kv4AttnParams& p, unsigned grid, cudaStream_t stream)
+{
+    kv4_prompt_kernel<D, BF><<<grid, kThreads, Prompt<D>::SMEM, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t setup_kv4_prompt()
+{
+    cudaError_t e;
+    if ((e = setup_one<64, false>()) != cudaSuccess || (e = setup_one<64, true>()) != cudaSuccess ||
+        (e = setup_one<128, false>()) != cudaSuccess || (e = setup_one<128, true>()) != cudaSuccess)
+        return e;
+    return cudaSuccess;
+}
+
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, int head_dim, cudaStream_t stream)
+{
+    // the row tiles of any split of the tokens over the requests
+    const long long tiles = (long long)p.tokens * p.group / (2 * kRows) + p.batch;
+    const long long grid = tiles * p.kv_heads;
+    if (grid >= (1LL << 31)) return cudaErrorInvalidValue;
+    if (head_dim == 128) return p.bf16 ? launch_one<128, true>(p, (unsigned)grid, stream) : launch_one<128, false>(p, (unsigned)grid, stream);
+    return p.bf16 ? launch_one<64, true>(p, (unsigned)grid, stream) : launch_one<64, false>(p, (unsigned)grid, stream);
+}
+
+}  // namespace w4a16
