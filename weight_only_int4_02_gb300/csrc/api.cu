@@ -13,7 +13,6 @@
 #include "decode.cuh"
 #include "gemv.cuh"
 #include "kv4.cuh"
-#include "sample.cuh"
 #include "w4a16.h"
 
 namespace w4a16 {
@@ -401,7 +400,7 @@ w4a16_status device_state(DeviceState** out)
             return from_cuda(e);
         if (major != 10 || minor != 3) return W4A16_ERR_UNSUPPORTED;  // built for sm_103a only
         if ((e = setup_gemv()) != cudaSuccess || (e = setup_decode()) != cudaSuccess ||
-            (e = setup_kv4()) != cudaSuccess || (e = setup_sample()) != cudaSuccess)
+            (e = setup_kv4()) != cudaSuccess)
             return from_cuda(e);
         void* gs = nullptr;
         if ((e = cudaGetSymbolAddress(&gs, g_gemv_status)) != cudaSuccess) return from_cuda(e);

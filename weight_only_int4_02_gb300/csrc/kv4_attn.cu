@@ -35,7 +35,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;      // tokens of a unit: two tiles
-constexpr int kOverhead = 6;   // what starting and ending a segment costs, in units
+constexpr int kOverhead = 12;  // what starting and ending a segment costs, in units
 constexpr int kGrow = 8;       // log2 of how far probabilities may grow before their reference moves
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
@@ -391,6 +391,12 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                         sc[tl][g][2 * j + 1] = kz * row_z[g][1];
                     }
                 }
+                // low and high nibbles in sums of their own: two short chains of MMAs instead of a long one
+                float sh4[NR][4];
+#pragma unroll
+                for (int g = 0; g < NR; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sh4[g][i] = 0.0f;
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     const uint32_t ka8 = ka[w] >> 8, kb8 = kb[w] >> 8;
@@ -399,12 +405,12 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                         mma_16816(sc[tl][g], ka[w] & kLow, kb[w] & kLow, ka8 & kLow, kb8 & kLow, ql[g][w][0], ql[g][w][1]);
 #pragma unroll
                     for (int g = 0; g < NR; ++g)
-                        mma_16816(sc[tl][g], ka[w] & kHigh, kb[w] & kHigh, ka8 & kHigh, kb8 & kHigh, qh[g][w][0], qh[g][w][1]);
+                        mma_16816(sh4[g], ka[w] & kHigh, kb[w] & kHigh, ka8 & kHigh, kb8 & kHigh, qh[g][w][0], qh[g][w][1]);
                 }
 #pragma unroll
                 for (int g = 0; g < NR; ++g)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[tl][g][i] *= ks[i >> 1];
+                    for (int i = 0; i < 4; ++i) sc[tl][g][i] = (sc[tl][g][i] + sh4[g][i]) * ks[i >> 1];
             }
             if (!full) {
 #pragma unroll

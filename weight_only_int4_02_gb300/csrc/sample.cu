@@ -10,17 +10,31 @@
 // keeps exp((x - m) r) >= min_p; rank 0 is always kept. The token is the first, in index
 // order, whose running kept weight passes floor(u * total).
 //
-// A cluster of CTAs holds one row, each CTA a slice of it in shared memory (read from HBM
-// once). The kept set is a prefix of the ranking, so it is one cut: a key, and how many of
-// the tokens that tie with it (by index). The cut is found by histograms of counts and
-// weights: first over 1024 bins of (m - x) r, which spreads logits evenly where their bits
-// would not (fewer conflicts of shared atomics), then, inside the bin that holds the cut,
-// over the keys. Every CTA adds up the cluster's histograms for itself.
+// A cluster of CTAs shares one row, each CTA a slice, which it reads once from HBM and then
+// from L2: a slice kept in shared memory leaves room for too few CTAs on an SM to hide
+// the barriers between a row's steps (256 x 100003 FP32 with slices in shared memory: 193 us).
+// The kept set is a prefix of the ranking, so it is one cut: the last kept token's
+// logit and index. Ways to the cut, by what a row asks for:
+//  - top-k of up to kListMax / 2: the k-th largest of the maxima of groups of tokens (four a
+//    thread; found by a histogram of them) is below at least k tokens and, as a group has few
+//    tokens, not many more; those are listed, and one CTA does the rest on the list;
+//  - top-p alone: a histogram of the weights over 1024 bins of (m - x) r, which spreads logits
+//    evenly where their bits would not (fewer conflicts of shared atomics), finds the bin that
+//    holds the cut, and the tokens of that bin are listed and cut by one CTA;
+//  - a larger k, or a bin with more tokens than a list holds (many equal logits): histograms
+//    of counts and weights over the keys inside the bin, ten bits at a time.
+// A list is never sorted: the entry at which a running count or weight crosses a limit is
+// found by histograms over its keys, which are all different (logit, then index), and so is the
+// drawn token of a top-k row (keys: indices). Every other row sums the kept weights of each
+// warp's segment, in index order, and the segment that holds the drawn place looks it up.
+// Vectors whose largest logit is below what a pass looks for are skipped, at about one
+// instruction a token; a weight takes about 20.
 #include "ptx.cuh"
 #include "sample.cuh"
 #include "w4a16.h"
 
 #include <cooperative_groups.h>
+#include <float.h>
 #include <math_constants.h>
 
 namespace w4a16 {
@@ -35,26 +49,40 @@ constexpr int kPer = kBins / kThreads;   // bins a thread adds up
 constexpr int kMaxCluster = 8;
 constexpr float kSpan = 22.2f;           // exp(-22.2) * 2^31 rounds to 0
 
+constexpr int kListMax = 2048;           // tokens of a list
+constexpr int kListMine = kListMax / 2;  // of them, one CTA's share at most
+constexpr int kListPer = kListMax / kThreads;
+constexpr int kGroups = 4;               // groups of a thread's tokens, each with its maximum
+
+struct Histogram {
+    uint32_t cnt[kBins], part[3][kBins];   // a bin's count, and its weights' bits 0..10, 11..21 and 22..31 summed
+};
+
 struct Shared {
-    uint32_t cnt[3][kBins], lo[3][kBins], hi[3][kBins];   // a bin's count, and its weight's low and high 16 bits summed
+    Histogram bins;                      // over (m - x) r
+    Histogram keys;                      // over keys
+    unsigned long long list[kListMine];  // key, then ~index: greater is ranked before
     unsigned long long best[kWarps];
-    unsigned long long mine[4];          // what this CTA shows to the cluster: maximum; least and greatest key
+    unsigned long long range;            // what this CTA shows to the cluster: least and greatest key,
+    float top;                           // its maximum,
+    uint32_t listed;                     // the length of its list,
+    unsigned long long cut;              // and, of the first CTA, the cut
     unsigned long long scan_mass[kWarps];
     uint32_t scan_cnt[kWarps];
-    unsigned long long warp_mass[kWarps];   // kept weight above the cut's key, of each warp's segment
-    uint32_t warp_ties[kWarps];
+    unsigned long long warp_mass[kWarps];   // kept weight of each warp's segment
     unsigned long long all_mass[kMaxCluster * kWarps];
-    uint32_t all_ties[kMaxCluster * kWarps];
     // results of a search
     int bin;
     uint32_t base_cnt, bin_cnt;
-    unsigned long long base_mass, bin_mass;
+    unsigned long long base_mass, bin_mass, total;
+    unsigned long long picked, picked_before;
+    uint32_t picked_weight;
     // the chosen segment
     int seg;
-    uint32_t seg_ties;
-    unsigned long long seg_target, total;
+    unsigned long long seg_target;
 };
 
+// A 16-byte vector's elements: their type, bits as a float, and the largest of them (NaN aside).
 template <int DTYPE>
 struct Elem;
 template <>
@@ -62,18 +90,34 @@ struct Elem<W4A16_FP32> {
     using T = float;
     static constexpr int kShift = 0;
     static __device__ __forceinline__ float get(uint32_t bits) { return __uint_as_float(bits); }
+    static __device__ __forceinline__ float largest(const uint4& v)
+    {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
 };
 template <>
 struct Elem<W4A16_FP16> {
     using T = uint16_t;
     static constexpr int kShift = 13;
     static __device__ __forceinline__ float get(uint32_t bits) { return __half2float(__ushort_as_half((uint16_t)bits)); }
+    static __device__ __forceinline__ float largest(const uint4& v)
+    {
+        auto h = [](const uint32_t& w) { return *reinterpret_cast<const __half2*>(&w); };
+        const __half2 m = __hmax2(__hmax2(h(v.x), h(v.y)), __hmax2(h(v.z), h(v.w)));
+        return __half2float(__hmax(__low2half(m), __high2half(m)));
+    }
 };
 template <>
 struct Elem<W4A16_BF16> {
     using T = uint16_t;
     static constexpr int kShift = 16;
     static __device__ __forceinline__ float get(uint32_t bits) { return __uint_as_float(bits << 16); }
+    static __device__ __forceinline__ float largest(const uint4& v)
+    {
+        auto h = [](const uint32_t& w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(h(v.x), h(v.y)), __hmax2(h(v.z), h(v.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
 };
 
 // Whole numbers in the order of x (-inf lowest among numbers); equal exactly where x is equal.
@@ -90,14 +134,15 @@ struct Row {
 
 __device__ __forceinline__ float exp_of(float x, const Row& r)
 {
-    return x == r.top ? 1.0f : expf(__fmul_rn(__fsub_rn(x, r.top), r.inv));
+    const float e = expf(__fmul_rn(__fsub_rn(x, r.top), r.inv));
+    return x == r.top ? 1.0f : e;
 }
 
 __device__ __forceinline__ uint32_t weight_of(float e) { return __float2uint_rn(e * 2147483648.0f); }
 
 __device__ __forceinline__ int bin_of(float x, const Row& r)
 {
-    const int b = (int)(__fmul_rn(__fsub_rn(r.top, x), r.inv) * (kBins / kSpan));
+    const int b = x == r.top ? 0 : (int)(__fmul_rn(__fsub_rn(r.top, x), r.inv) * (kBins / kSpan));
     return b < kBins - 1 ? b : kBins - 1;
 }
 
@@ -120,73 +165,54 @@ __device__ __forceinline__ T warp_incl(T v, int lane)
     return v;
 }
 
-__device__ __forceinline__ void clear_bins(Shared& sh, int h)
+__device__ __forceinline__ void clear(Histogram& h)
 {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.cnt[h][i] = sh.lo[h][i] = sh.hi[h][i] = 0;
+    uint4* const at = reinterpret_cast<uint4*>(&h);
+    for (int i = threadIdx.x; i < (int)(sizeof(Histogram) / 16); i += kThreads) at[i] = make_uint4(0, 0, 0, 0);
 }
 
-__device__ __forceinline__ void count_in(Shared& sh, int h, int bin, uint32_t w)
+__device__ __forceinline__ void add_mass(Histogram& h, int bin, uint32_t w)
 {
-    atomicAdd(&sh.cnt[h][bin], 1u);
-    atomicAdd(&sh.lo[h][bin], w & 0xffffu);
-    if (w >> 16) atomicAdd(&sh.hi[h][bin], w >> 16);
+    if (w & 2047u) atomicAdd(&h.part[0][bin], w & 2047u);
+    if (w >> 11 & 2047u) atomicAdd(&h.part[1][bin], w >> 11 & 2047u);
+    if (w >> 22) atomicAdd(&h.part[2][bin], w >> 22);
 }
 
-// Adds up the cluster's histograms h and finds the first bin with done(count, mass of every bin up to
-// and with it); base counts come on top. Leaves bin = -1 if there is none. Every CTA finds the same.
-// A cluster barrier before (the histograms are complete) is in here; the caller keeps one between this
-// and the next use of the same histogram.
-template <typename F>
-__device__ __forceinline__ void search(cg::cluster_group& cl, Shared& sh, int h, uint32_t base_cnt,
-                                       unsigned long long base_mass, F done)
+__device__ __forceinline__ unsigned long long mass_of(uint32_t a, uint32_t b, uint32_t c)
+{
+    return a + ((unsigned long long)b << 11) + ((unsigned long long)c << 22);
+}
+
+// Finds the first bin with done(count, weight of every bin up to and with it, weight of all bins), from each
+// thread's two bins; base counts come on top. MASS: weights count, else only counts do. Leaves bin = -1 if there
+// is none; sh.bin is -1 on entry, and a barrier lies between that and here.
+template <bool MASS, typename F>
+__device__ __forceinline__ void scan_bins(Shared& sh, const uint32_t (&cnt)[kPer], const unsigned long long (&mass)[kPer],
+                                          uint32_t base_cnt, unsigned long long base_mass, F done)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) sh.bin = -1;
-    cl.sync();
-    uint32_t cnt[kPer];
-    unsigned long long mass[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        cnt[i] = 0;
-        mass[i] = 0;
-    }
-    const int ctas = (int)cl.num_blocks();
-    for (int k = 0; k < ctas; ++k) {
-        const Shared* o = cl.map_shared_rank(&sh, k);
-        const int at = threadIdx.x * kPer;
-        const uint2 a = *reinterpret_cast<const uint2*>(&o->cnt[h][at]);
-        const uint2 b = *reinterpret_cast<const uint2*>(&o->lo[h][at]);
-        const uint2 c = *reinterpret_cast<const uint2*>(&o->hi[h][at]);
-        cnt[0] += a.x;
-        cnt[1] += a.y;
-        mass[0] += b.x + ((unsigned long long)c.x << 16);
-        mass[1] += b.y + ((unsigned long long)c.y << 16);
-    }
-    static_assert(kPer == 2, "two bins a thread");
-    const uint32_t my_cnt = cnt[0] + cnt[1];
-    const unsigned long long my_mass = mass[0] + mass[1];
-    const uint32_t ic = warp_incl(my_cnt, lane);
-    const unsigned long long im = warp_incl(my_mass, lane);
+    const uint32_t ic = warp_incl(cnt[0] + cnt[1], lane);
+    const unsigned long long im = MASS ? warp_incl(mass[0] + mass[1], lane) : 0ull;
     if (lane == 31) {
         sh.scan_cnt[warp] = ic;
-        sh.scan_mass[warp] = im;
+        if (MASS) sh.scan_mass[warp] = im;
     }
     __syncthreads();
-    uint32_t c = base_cnt + ic - my_cnt;
-    unsigned long long m = base_mass + im - my_mass;
-    unsigned long long all = base_mass;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) {
-            c += sh.scan_cnt[w];
-            m += sh.scan_mass[w];
-        }
-        all += sh.scan_mass[w];
+    static_assert(kWarps <= 32, "a warp scans the warps' sums");
+    const uint32_t wc = warp_incl(lane < kWarps ? sh.scan_cnt[lane] : 0u, lane);
+    uint32_t c = base_cnt + __shfl_sync(0xffffffffu, wc, warp > 0 ? warp - 1 : 0) * (warp > 0) + ic - cnt[0] - cnt[1];
+    unsigned long long m = base_mass, all = base_mass;
+    if (MASS) {
+        const unsigned long long wm = warp_incl(lane < kWarps ? sh.scan_mass[lane] : 0ull, lane);
+        const unsigned long long upto = __shfl_sync(0xffffffffu, wm, warp > 0 ? warp - 1 : 0);
+        m += (warp > 0 ? upto : 0ull) + im - mass[0] - mass[1];
+        all += __shfl_sync(0xffffffffu, wm, 31);
+        if (threadIdx.x == 0) sh.total = all;
     }
-    if (threadIdx.x == 0) sh.total = all;
-    bool before = done(c, m);
+    bool before = done(c, m, all);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const bool now = done(c + cnt[i], m + mass[i]);
+        const bool now = done(c + cnt[i], m + mass[i], all);
         if (now && !before) {
             sh.bin = threadIdx.x * kPer + i;
             sh.base_cnt = c;
@@ -201,332 +227,671 @@ __device__ __forceinline__ void search(cg::cluster_group& cl, Shared& sh, int h,
     __syncthreads();
 }
 
-struct Cut {
-    uint32_t key, ties;           // kept: greater keys, and the first `ties` tokens with this key
-    unsigned long long mass;      // weight of what is greater
-    uint32_t weight;              // weight of a token with this key
-    uint32_t cnt;                 // tokens with greater keys
-};
+// scan_bins over the sum of the cluster's histograms; every CTA finds the same. A cluster barrier before
+// (the histograms are complete) is in here; the caller keeps one between this and the next use of the histogram.
+template <bool MASS, typename F>
+__device__ __forceinline__ void search(cg::cluster_group& cl, Shared& sh, Histogram& hist, uint32_t base_cnt,
+                                       unsigned long long base_mass, F done)
+{
+    if (threadIdx.x == 0) sh.bin = -1;
+    cl.sync();
+    static_assert(kPer == 2, "two bins a thread");
+    uint32_t cnt[kPer] = {0, 0};
+    unsigned long long mass[kPer] = {0, 0};
+    const int ctas = (int)cl.num_blocks();
+    const int at = threadIdx.x * kPer;
+#pragma unroll
+    for (int two = 0; two < kMaxCluster; two += 2) {   // two CTAs' loads in flight at a time
+        if (two >= ctas) break;
+        uint2 a[2], b[2][3];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            a[k] = b[k][0] = b[k][1] = b[k][2] = make_uint2(0, 0);
+            if (two + k < ctas) {
+                const Histogram* o = cl.map_shared_rank(&hist, two + k);
+                a[k] = *reinterpret_cast<const uint2*>(&o->cnt[at]);
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                    if (MASS) b[k][q] = *reinterpret_cast<const uint2*>(&o->part[q][at]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            cnt[0] += a[k].x;
+            cnt[1] += a[k].y;
+            if (MASS) {
+                mass[0] += mass_of(b[k][0].x, b[k][1].x, b[k][2].x);
+                mass[1] += mass_of(b[k][0].y, b[k][1].y, b[k][2].y);
+            }
+        }
+    }
+    scan_bins<MASS>(sh, cnt, mass, base_cnt, base_mass, done);
+}
+
+// In one CTA: of this thread's entries (0: none; all others different), the one at which done(count, weight of
+// every entry from the greatest key down to it) becomes true, in sh.picked (0 if there is none), with what is
+// before it and its weight. Ten bits of the keys' range at a time, until a bin has one entry.
+template <typename F>
+__device__ __forceinline__ void pick(Shared& sh, const unsigned long long (&key)[kListPer], const uint32_t (&w)[kListPer],
+                                     unsigned long long base_mass, F done)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned long long kmin = ~0ull, kmax = 0ull;
+#pragma unroll
+    for (int i = 0; i < kListPer; ++i) {
+        if (key[i] == 0) continue;
+        kmin = key[i] < kmin ? key[i] : kmin;
+        kmax = key[i] > kmax ? key[i] : kmax;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const unsigned long long a = __shfl_xor_sync(0xffffffffu, kmin, d), b = __shfl_xor_sync(0xffffffffu, kmax, d);
+        kmin = a < kmin ? a : kmin;
+        kmax = b > kmax ? b : kmax;
+    }
+    __syncthreads();
+    if (lane == 0) {
+        sh.best[warp] = kmax;
+        sh.scan_mass[warp] = kmin;
+    }
+    if (tid == 0) sh.picked = 0;
+    __syncthreads();
+    kmax = sh.best[lane % kWarps];
+    kmin = sh.scan_mass[lane % kWarps];
+#pragma unroll
+    for (int d = kWarps / 2; d > 0; d >>= 1) {
+        const unsigned long long a = __shfl_xor_sync(0xffffffffu, kmin, d), b = __shfl_xor_sync(0xffffffffu, kmax, d);
+        kmin = a < kmin ? a : kmin;
+        kmax = b > kmax ? b : kmax;
+    }
+    uint32_t base_cnt = 0;
+    for (int level = 0; level < 7; ++level) {
+        const unsigned long long range = kmax - kmin;
+        const int bits = 64 - __clzll((long long)range);
+        const int shift = bits > 10 ? bits - 10 : 0;
+#pragma unroll
+        for (int b = tid; b < kBins; b += kThreads)
+            sh.keys.cnt[b] = sh.keys.part[0][b] = sh.keys.part[1][b] = sh.keys.part[2][b] = 0;
+        if (tid == 0) sh.bin = -1;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kListPer; ++i)
+            if (key[i] != 0 && key[i] >= kmin && key[i] <= kmax) {
+                const int b = (int)((kmax - key[i]) >> shift);
+                atomicAdd(&sh.keys.cnt[b], 1u);
+                add_mass(sh.keys, b, w[i]);
+            }
+        __syncthreads();
+        uint32_t cnt[kPer];
+        unsigned long long mass[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int b = tid * kPer + i;
+            cnt[i] = sh.keys.cnt[b];
+            mass[i] = mass_of(sh.keys.part[0][b], sh.keys.part[1][b], sh.keys.part[2][b]);
+        }
+        scan_bins<true>(sh, cnt, mass, base_cnt, base_mass,
+                        [&](uint32_t c, unsigned long long m, unsigned long long) { return done(c, m); });
+        if (sh.bin < 0) break;
+        base_cnt = sh.base_cnt;
+        base_mass = sh.base_mass;
+        kmax -= (unsigned long long)sh.bin << shift;
+        const unsigned long long low = kmax - ((1ull << shift) - 1ull);
+        kmin = low > kmin && low <= kmax ? low : kmin;
+        const bool one = sh.bin_cnt == 1;
+        __syncthreads();
+        if (one) {
+#pragma unroll
+            for (int i = 0; i < kListPer; ++i)
+                if (key[i] != 0 && key[i] >= kmin && key[i] <= kmax) {
+                    sh.picked = key[i];
+                    sh.picked_before = base_mass;
+                    sh.picked_weight = w[i];
+                }
+            break;
+        }
+    }
+    __syncthreads();
+}
+
+template <int DTYPE>
+__device__ __forceinline__ float float_of(uint32_t key)
+{
+    const uint32_t k = key << Elem<DTYPE>::kShift;
+    // positive numbers had their top bit set, negative ones were complemented
+    return (k & 0x80000000u) ? __uint_as_float(k & 0x7fffffffu)
+                             : __uint_as_float(~(k | ((1u << Elem<DTYPE>::kShift) - 1u)));
+}
 
 template <int DTYPE>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p)
 {
     using T = typename Elem<DTYPE>::T;
     constexpr int VEC = 16 / sizeof(T);
-    extern __shared__ __align__(16) uint8_t dyn[];
-    Shared& sh = *reinterpret_cast<Shared*>(dyn);
-    T* const xs = reinterpret_cast<T*>(dyn + (sizeof(Shared) + 15) / 16 * 16);
+    __shared__ __align__(16) Shared sh;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), ctas = (int)cl.num_blocks();
     const int row = blockIdx.x / ctas;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    // ---- the slice: positions are counted from the 16-byte boundary at or before the row's first logit
+    // ---- the slice: places are counted from the 16-byte boundary at or before the row's first logit
     const T* const src = static_cast<const T*>(p.logits) + (long long)row * p.stride;
     const int mis = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
-    const int first = rank * p.slice;                 // this slice's first position; token = position - mis
+    const int first = rank * p.slice - mis;           // the token at this slice's first place (may be below 0)
     const int slice = p.slice;                        // a multiple of VEC * kThreads
-    unsigned long long best = 0;
-    for (int v = tid * VEC; v < slice; v += kThreads * VEC) {
-        uint4 raw;
-        const int at = first + v - mis;               // token of the first element
-        if (at >= 0 && at + VEC <= p.vocab) {
-            raw = __ldg(reinterpret_cast<const uint4*>(src + at));
-        } else {
-            uint32_t b[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const bool in = at + i >= 0 && at + i < p.vocab;
-                if constexpr (sizeof(T) == 4) b[i] = in ? __float_as_uint(src[at + i]) : 0xff800000u;
-                else b[i] = in ? src[at + i] : DTYPE == W4A16_FP16 ? 0xfc00u : 0xff80u;
-            }
-            if constexpr (sizeof(T) == 4) raw = make_uint4(b[0], b[1], b[2], b[3]);
-            else raw = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
-        }
-        uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    auto load = [&](int v) {                          // 16 bytes from place v on; -infinity outside the row
+        const int at = first + v;
+        if (at >= 0 && at + VEC <= p.vocab) return __ldg(reinterpret_cast<const uint4*>(src + at));
+        uint32_t b[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            uint32_t bits = sizeof(T) == 4 ? w[i] : (w[i / 2] >> (16 * (i & 1))) & 0xffffu;
-            float x = Elem<DTYPE>::get(bits);
-            if (x != x) {                              // NaN: never sampled
-                x = -CUDART_INF_F;
-                if constexpr (sizeof(T) == 4) w[i] = 0xff800000u;
-                else {
-                    const uint32_t inf = DTYPE == W4A16_FP16 ? 0xfc00u : 0xff80u;
-                    w[i / 2] = (w[i / 2] & (0xffff0000u >> (16 * (i & 1)))) | inf << (16 * (i & 1));
-                }
-            }
-            const unsigned long long k = (unsigned long long)key_of<DTYPE>(x) << 32 | (0xffffffffu - (uint32_t)(at + i));
-            if (at + i >= 0 && at + i < p.vocab) best = k > best ? k : best;
+            const bool in = at + i >= 0 && at + i < p.vocab;
+            if constexpr (sizeof(T) == 4) b[i] = in ? __float_as_uint(src[at + i]) : 0xff800000u;
+            else b[i] = in ? src[at + i] : DTYPE == W4A16_FP16 ? 0xfc00u : 0xff80u;
         }
-        *reinterpret_cast<uint4*>(xs + v) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    auto at = [&](int v) {
-        if constexpr (sizeof(T) == 4) return xs[v];
-        else return Elem<DTYPE>::get(xs[v]);
+        if constexpr (sizeof(T) == 4) return make_uint4(b[0], b[1], b[2], b[3]);
+        else return make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
     };
+    // a NaN never compares above anything and weighs nothing
+    auto expand = [](const uint4& raw, float (&x)[VEC]) {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const unsigned long long o = __shfl_xor_sync(0xffffffffu, best, d);
-        best = o > best ? o : best;
-    }
-    if (lane == 0) sh.best[warp] = best;
-    clear_bins(sh, 0);
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
-        sh.mine[0] = best;
-    }
-    cl.sync();
-    best = 0;
-    for (int k = 0; k < ctas; ++k) {
-        const unsigned long long o = cl.map_shared_rank(&sh, k)->mine[0];
-        best = o > best ? o : best;
-    }
-    const int top_token = (int)(0xffffffffu - (uint32_t)best);
+        for (int i = 0; i < VEC; ++i)
+            x[i] = Elem<DTYPE>::get(sizeof(T) == 4 ? w[i * 4 / VEC] : (w[i / 2] >> (16 * (i & 1))) & 0xffffu);
+    };
+    // runs f(place, x) over the vectors from place a on, `step` apart, below b, that hold an x >= low
+    auto sweep = [&](int a, int b, int step, float low, auto f) {
+        for (int v0 = a; v0 < b; v0 += 4 * step) {   // four loads in flight
+            uint4 raw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (v0 + i * step < b) raw[i] = load(v0 + i * step);
+#pragma unroll 1
+            for (int i = 0; i < 4 && v0 + i * step < b; ++i) {
+                const uint4 now = raw[0];
+                raw[0] = raw[1];
+                raw[1] = raw[2];
+                raw[2] = raw[3];
+                if (!(Elem<DTYPE>::largest(now) >= low)) continue;
+                float x[VEC];
+                expand(now, x);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) f(v0 + i * step + e, x[e]);
+            }
+        }
+    };
+    auto each = [&](float low, auto f) { sweep(tid * VEC, slice, kThreads * VEC, low, f); };
 
-    Row r;
-    {
-        const uint32_t k = (uint32_t)(best >> 32) << Elem<DTYPE>::kShift;
-        // back from the key: positive numbers had their top bit set, negative ones were complemented
-        r.top = (k & 0x80000000u) ? __uint_as_float(k & 0x7fffffffu)
-                                  : __uint_as_float(~(k | ((1u << Elem<DTYPE>::kShift) - 1u)));
+    float tops[kGroups], mine = -CUDART_INF_F;        // maxima of this thread's groups of tokens, and of all
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) tops[i] = -CUDART_INF_F;
+    for (int v0 = tid * VEC; v0 < slice; v0 += 2 * kGroups * kThreads * VEC) {   // eight loads in flight
+        uint4 raw[2 * kGroups];
+#pragma unroll
+        for (int i = 0; i < 2 * kGroups; ++i)
+            if (v0 + i * kThreads * VEC < slice) raw[i] = load(v0 + i * kThreads * VEC);
+#pragma unroll
+        for (int i = 0; i < 2 * kGroups; ++i)
+            if (v0 + i * kThreads * VEC < slice) tops[i % kGroups] = fmaxf(tops[i % kGroups], Elem<DTYPE>::largest(raw[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) mine = fmaxf(mine, tops[i]);
+    float wtop = mine;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xffffffffu, wtop, d));
+    float* const wtops = reinterpret_cast<float*>(sh.best);
+    if (lane == 0) wtops[warp] = wtop;
+    clear(sh.bins);
+    __syncthreads();
+    if (warp == 0) {
+        float t = lane < kWarps ? wtops[lane] : -CUDART_INF_F;
+#pragma unroll
+        for (int d = kWarps / 2; d > 0; d >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+        if (lane == 0) {
+            sh.top = t;
+            sh.listed = 0;
+        }
     }
     const float temp = p.temperature ? p.temperature[row] : 1.0f;
     const float top_p = p.top_p ? p.top_p[row] : 1.0f;
     const int k = p.top_k ? p.top_k[row] : 0;
+    const float u = p.u[row];
+    Row r;
     r.min_p = p.min_p ? p.min_p[row] : 0.0f;
+    r.inv = __frcp_rn(temp);
+    cl.sync();
+    r.top = cl.map_shared_rank(&sh, lane < ctas ? lane : 0)->top;
+#pragma unroll
+    for (int d = kMaxCluster / 2; d > 0; d >>= 1) r.top = fmaxf(r.top, __shfl_xor_sync(0xffffffffu, r.top, d));
+    r.top = __shfl_sync(0xffffffffu, r.top, 0);
+
+    auto result = [&](int token, double share) {
+        p.token[row] = token;
+        if (p.prob) p.prob[row] = (float)share;
+    };
+    // the place of the draw in a kept weight
+    auto target_of = [&](unsigned long long total) {
+        const unsigned long long t = (unsigned long long)((double)total * (double)u);
+        return t < total ? t : total - 1;
+    };
     const bool none = r.top == -CUDART_INF_F;
-    if (none || !(temp > 0.0f) || k == 1 || !(top_p > 0.0f) || !(r.min_p <= 1.0f)) {
-        if (rank == 0 && tid == 0) {
-            p.token[row] = none ? -1 : top_token;
-            if (p.prob) p.prob[row] = none ? 0.0f : 1.0f;
+    const bool greedy = !(temp > 0.0f) || k == 1 || !(top_p > 0.0f) || !(r.min_p <= 1.0f);
+    if (none || greedy) {
+        // the lowest index of the maximum
+        uint32_t at = 0xffffffffu;
+        if (!none && mine == r.top)
+            each(r.top, [&](int v, float x) {
+                if (x == r.top) at = min(at, (uint32_t)(first + v));
+            });
+        at = __reduce_min_sync(0xffffffffu, at);
+        if (lane == 0) sh.best[warp] = at;
+        __syncthreads();
+        if (warp == 0) {
+            at = __reduce_min_sync(0xffffffffu, lane < kWarps ? (uint32_t)sh.best[lane] : 0xffffffffu);
+            if (lane == 0) sh.range = at;
+        }
+        cl.sync();
+        if (rank == 0 && warp == 0) {
+            at = __reduce_min_sync(0xffffffffu, lane < ctas ? (uint32_t)cl.map_shared_rank(&sh, lane)->range : 0xffffffffu);
+            if (lane == 0) result(none ? -1 : (int)at, none ? 0.0 : 1.0);
         }
         cl.sync();   // no CTA leaves while another may read its shared memory
         return;
     }
-    r.inv = __frcp_rn(temp);
 
-    // ---- the cut
+    // ---- the cut: kept are logits above cut_x, and those equal to it up to index cut_at
+    float cut_x = -CUDART_INF_F;
+    int cut_at = -1;
     const bool need_k = k > 0 && k < p.vocab, need_p = top_p < 1.0f;
-    Cut cut = {0u, 0xffffffffu, 0ull, 0u, 0u};
-    int h = 1;   // histogram in turn: 1 and 2; 0 keeps the bins of (m - x) r
-    if (need_k || need_p) {
-        for (int v = tid; v < slice; v += kThreads) {
-            const float x = at(v);
-            const uint32_t w = weight_of(exp_of(x, r));
-            if (w) count_in(sh, 0, bin_of(x, r), w);
-        }
-        // the cut's key inside a bin: its range of keys, then histograms over the keys until one is left
-        auto refine = [&](auto done) {
-            const int bin = sh.bin;
-            uint32_t cnt0 = sh.base_cnt;
-            unsigned long long mass0 = sh.base_mass;
-            uint32_t kmin = 0xffffffffu, kmax = 0u;
-            for (int v = tid; v < slice; v += kThreads) {
-                const float x = at(v);
-                if (x == -CUDART_INF_F || bin_of(x, r) != bin || weight_of(exp_of(x, r)) == 0) continue;
-                const uint32_t key = key_of<DTYPE>(x);
-                kmin = key < kmin ? key : kmin;
-                kmax = key > kmax ? key : kmax;
-            }
-            kmin = __reduce_min_sync(0xffffffffu, kmin);
-            kmax = __reduce_max_sync(0xffffffffu, kmax);
-            if (lane == 0) sh.best[warp] = (unsigned long long)kmax << 32 | kmin;
-            __syncthreads();
-            if (tid == 0) {
-                for (int w = 0; w < kWarps; ++w) {
-                    const uint32_t a = (uint32_t)sh.best[w], b = (uint32_t)(sh.best[w] >> 32);
-                    kmin = a < kmin ? a : kmin;
-                    kmax = b > kmax ? b : kmax;
+    const float to_bin = kBins / kSpan;
+    // a logit below every one that is at most d below the maximum, whatever the roundings of either side
+    auto below = [&](float d) { return r.top <= FLT_MAX ? r.top - d * 1.00001f - 1e-6f * fabsf(r.top) : r.top; };
+    const float weightless = below(22.5f * temp);   // lower ones weigh nothing
+    auto place = [&](float x) { return x == r.top ? 0.0f : __fmul_rn(__fsub_rn(r.top, x), r.inv) * to_bin; };   // bin, before truncation
+    auto list_it = [&](int v, float x) {
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        if (at < kListMine)
+            sh.list[at] = (unsigned long long)key_of<DTYPE>(x) << 32 | (0xffffffffu - (uint32_t)(first + v));
+    };
+    auto logit_of = [](unsigned long long e) { return float_of<DTYPE>((uint32_t)(e >> 32)); };
+    auto token_of = [](unsigned long long e) { return (int)(0xffffffffu - (uint32_t)e); };
+    // The cluster's lists in the first CTA's registers, kListPer entries a thread (0: none), with their weights.
+    // Returns the number of entries, or -1 (everywhere) where they do not fit.
+    unsigned long long key[kListPer];
+    uint32_t w[kListPer];
+    auto gather = [&]() {
+        cl.sync();
+        const int len = lane < ctas ? (int)cl.map_shared_rank(&sh, lane)->listed : 0;
+        const int upto = warp_incl(len, lane), n = __shfl_sync(0xffffffffu, upto, 31);
+        if (__any_sync(0xffffffffu, len > kListMine) || n > kListMax) return -1;
+        if (rank == 0) {
+#pragma unroll
+            for (int i = 0; i < kListPer; ++i) {
+                const int at = i * kThreads + tid;
+                int c = 0, from = 0;   // the CTA that holds the entry
+                for (int o = 0; o < kMaxCluster; ++o) {
+                    const int e = __shfl_sync(0xffffffffu, upto, o);
+                    if (at >= e && o + 1 < ctas) {
+                        c = o + 1;
+                        from = e;
+                    }
                 }
-                sh.mine[1] = (unsigned long long)kmax << 32 | kmin;
+                key[i] = at < n ? cl.map_shared_rank(&sh, c)->list[at - from] : 0ull;
+                w[i] = at < n ? weight_of(exp_of(logit_of(key[i]), r)) : 0u;
             }
-            cl.sync();
-            for (int c = 0; c < ctas; ++c) {
-                const unsigned long long o = cl.map_shared_rank(&sh, c)->mine[1];
-                kmin = (uint32_t)o < kmin ? (uint32_t)o : kmin;
-                kmax = (uint32_t)(o >> 32) > kmax ? (uint32_t)(o >> 32) : kmax;
-            }
-            Cut res = {};
-            for (int level = 0; level < 4; ++level) {   // ten bits of the range a level
-                h ^= 3;
-                clear_bins(sh, h);
-                __syncthreads();
-                const uint32_t range = kmax - kmin;
-                const int bits = range ? 32 - __clz(range) : 0;
-                const int shift = bits > 10 ? bits - 10 : 0;
-                for (int v = tid; v < slice; v += kThreads) {
-                    const float x = at(v);
-                    const uint32_t key = key_of<DTYPE>(x);
-                    if (x != -CUDART_INF_F && key >= kmin && key <= kmax)
-                        count_in(sh, h, (int)((kmax - key) >> shift), weight_of(exp_of(x, r)));
-                }
-                search(cl, sh, h, cnt0, mass0, done);
-                cnt0 = sh.base_cnt;
-                mass0 = sh.base_mass;
-                if (shift == 0) {
-                    res.key = kmax - (uint32_t)sh.bin;
-                    res.cnt = cnt0;
-                    res.mass = mass0;
-                    res.ties = sh.bin_cnt;
-                    res.weight = (uint32_t)(sh.bin_mass / sh.bin_cnt);
-                    break;
-                }
-                kmax -= (uint32_t)sh.bin << shift;
-                const uint32_t low = kmax - ((1u << shift) - 1u);
-                kmin = low > kmin && low <= kmax ? low : kmin;
-                __syncthreads();   // sh.bin is read before the next search writes it
-            }
-            __syncthreads();
-            return res;
-        };
-        unsigned long long total = 0;
-        if (need_k) {
-            const uint32_t kk = (uint32_t)k;
-            auto done = [kk](uint32_t c, unsigned long long) { return c >= kk; };
-            search(cl, sh, 0, 0u, 0ull, done);
-            total = sh.total;
-            if (sh.bin >= 0) {
-                __syncthreads();
-                cut = refine(done);
-                cut.ties = kk - cut.cnt;
-                total = cut.mass + (unsigned long long)cut.ties * cut.weight;
-            }
-            __syncthreads();
         }
-        if (need_p) {
-            if (!need_k) {   // the whole weight
-                auto never = [](uint32_t, unsigned long long) { return false; };
-                search(cl, sh, 0, 0u, 0ull, never);
-                total = sh.total;
-                __syncthreads();
-            }
-            const double limit = (double)total * (double)top_p;
-            // the bin past which the weight before a token is no longer below the limit
-            auto done = [limit](uint32_t, unsigned long long m) { return !((double)m < limit); };
-            search(cl, sh, 0, 0u, 0ull, done);
-            if (sh.bin >= 0) {
-                __syncthreads();
-                Cut c = refine(done);
-                // ties kept: those with mass + j * weight below the limit
-                uint32_t n = (uint32_t)fmin((limit - (double)c.mass) / (double)c.weight, 4294967040.0);
-                n = n > c.ties ? c.ties : n;
-                while (n > 0 && !((double)(c.mass + (unsigned long long)(n - 1) * c.weight) < limit)) --n;
-                while (n < c.ties && (double)(c.mass + (unsigned long long)n * c.weight) < limit) ++n;
-                if (c.cnt == 0 && n == 0) n = 1;   // rank 0
-                c.ties = n;
-                if (c.key > cut.key || (c.key == cut.key && c.ties < cut.ties)) cut = c;
-            }
-            __syncthreads();
+        return n;
+    };
+    // this CTA's sum of 64-bit numbers
+    auto block_sum = [&](unsigned long long v) {
+        v = warp_sum(v);
+        __syncthreads();
+        if (lane == 0) sh.best[warp] = v;
+        __syncthreads();
+        v = lane < kWarps ? sh.best[lane] : 0ull;
+        return warp_sum(v);
+    };
+
+    if (need_k && k <= kListMax / 2) {
+        // a bound below at least k tokens: the bin of the k-th largest of the groups' maxima
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const float b = place(tops[i]);
+            if (tops[i] > -CUDART_INF_F && b < (float)kBins) atomicAdd(&sh.bins.cnt[(int)b], 1u);
         }
+        const uint32_t kk = (uint32_t)k;
+        search<false>(cl, sh, sh.bins, 0u, 0ull, [kk](uint32_t c, unsigned long long, unsigned long long) { return c >= kk; });
+        if (sh.bin >= 0) {
+            // down to the bin's lower end, and a few tokens more
+            const float low = below((float)(sh.bin + 1) / to_bin * temp);
+            if (mine >= low)   // else this thread has none
+                each(low, [&](int v, float x) {
+                    if (x >= low && x > -CUDART_INF_F) list_it(v, x);
+                });
+            const int n = gather();
+            if (n >= 0) {
+                if (rank == 0) {
+                    // the k-th entry, the entry at which top-p's limit is passed, and the drawn one among the kept
+                    if (n > k) {
+                        pick(sh, key, w, 0ull, [kk](uint32_t c, unsigned long long) { return c >= kk; });
+                        const unsigned long long last = sh.picked;
+#pragma unroll
+                        for (int i = 0; i < kListPer; ++i)
+                            if (key[i] < last) key[i] = 0, w[i] = 0;
+                    }
+                    unsigned long long sum = 0;
+#pragma unroll
+                    for (int i = 0; i < kListPer; ++i) sum += w[i];
+                    unsigned long long total = block_sum(sum);
+                    if (need_p) {
+                        const double limit = (double)total * (double)top_p;
+                        pick(sh, key, w, 0ull, [limit](uint32_t, unsigned long long m) { return !((double)m < limit); });
+                        const unsigned long long last = sh.picked;
+#pragma unroll
+                        for (int i = 0; i < kListPer; ++i)
+                            if (key[i] < last) key[i] = 0, w[i] = 0;
+                    }
+                    if (r.min_p > 0.0f) {
+#pragma unroll
+                        for (int i = 0; i < kListPer; ++i)
+                            if (key[i] && !(exp_of(logit_of(key[i]), r) >= r.min_p)) key[i] = 0, w[i] = 0;
+                    }
+                    if (need_p || r.min_p > 0.0f) {
+                        sum = 0;
+#pragma unroll
+                        for (int i = 0; i < kListPer; ++i) sum += w[i];
+                        total = block_sum(sum);
+                    }
+                    // by index now: the low halves, greatest first, are ascending indices
+#pragma unroll
+                    for (int i = 0; i < kListPer; ++i) key[i] &= 0xffffffffull;
+                    const unsigned long long target = target_of(total);
+                    pick(sh, key, w, 0ull, [target](uint32_t, unsigned long long m) { return m > target; });
+                    if (tid == 0) result(token_of(sh.picked), (double)sh.picked_weight / (double)total);
+                }
+                cl.sync();
+                return;
+            }
+        }
+        cl.sync();
+        clear(sh.bins);
+        __syncthreads();
     }
 
-    // ---- the kept weight of each warp's segment (in index order), ties counted apart
-    const int seg_len = slice / kWarps;
+    const int seg_len = slice / kWarps;               // a warp's segment: a multiple of 32 VEC
     const int s0 = warp * seg_len;
-    auto kept = [&](float x, uint32_t key) -> uint32_t {   // weight of a token at or above the cut's key
-        if (key < cut.key || x == -CUDART_INF_F) return 0u;
+    auto kept = [&](float x, int v) -> uint32_t {
+        // evaluated for every token of a vector: cheaper than a branch around it
         const float e = exp_of(x, r);
-        return e >= r.min_p || x == r.top ? weight_of(e) : 0u;
+        const bool in = (x > cut_x || (x == cut_x && first + v <= cut_at)) && (e >= r.min_p || x == r.top);
+        return in ? weight_of(e) : 0u;
     };
-    unsigned long long mass = 0;
-    uint32_t ties = 0;
-    for (int v = s0 + lane; v < s0 + seg_len; v += 32) {
-        const float x = at(v);
-        const uint32_t key = key_of<DTYPE>(x);
-        if (key > cut.key) mass += kept(x, key);
-        else if (key == cut.key && x != -CUDART_INF_F) ++ties;
-    }
-    mass = warp_sum(mass);
-    ties = __reduce_add_sync(0xffffffffu, ties);
-    if (lane == 0) {
-        sh.warp_mass[warp] = mass;
-        sh.warp_ties[warp] = ties;
-    }
-    cl.sync();
-    const int segs = ctas * kWarps;
-    if (tid < segs) {
-        const Shared* o = cl.map_shared_rank(&sh, tid / kWarps);
-        sh.all_mass[tid] = o->warp_mass[tid % kWarps];
-        sh.all_ties[tid] = o->warp_ties[tid % kWarps];
-    }
-    __syncthreads();
-    if (warp == 0) {
-        // weight of a tie: that of the cut's key, if min-p lets it
-        uint32_t tw = 0;
-        if (cut.weight) {
-            const uint32_t kb = cut.key << Elem<DTYPE>::kShift;
-            const float x = (kb & 0x80000000u) ? __uint_as_float(kb & 0x7fffffffu)
-                                               : __uint_as_float(~(kb | ((1u << Elem<DTYPE>::kShift) - 1u)));
-            tw = kept(x, cut.key);
-        }
+    // the segment that holds the draw, from sh.all_mass
+    auto choose = [&](int segs) {
+        if (warp != 0) return;
         constexpr int PER = kMaxCluster * kWarps / 32;
-        uint32_t t[PER], tsum = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int s = lane * PER + i;
-            t[i] = s < segs ? sh.all_ties[s] : 0u;
-            tsum += t[i];
-        }
-        uint32_t tb = warp_incl(tsum, lane) - tsum;
         unsigned long long ms[PER], msum = 0;
-        uint32_t left[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int s = lane * PER + i;
-            left[i] = tb < cut.ties ? cut.ties - tb : 0u;   // ties that may be kept from this segment on
-            const uint32_t n = t[i] < left[i] ? t[i] : left[i];
-            ms[i] = (s < segs ? sh.all_mass[s] : 0ull) + (unsigned long long)n * tw;
+            ms[i] = s < segs ? sh.all_mass[s] : 0ull;
             msum += ms[i];
-            tb += t[i];
         }
         const unsigned long long mi = warp_incl(msum, lane);
         const unsigned long long total = __shfl_sync(0xffffffffu, mi, 31);
-        const double want = (double)total * (double)p.u[row];
-        unsigned long long target = (unsigned long long)want;
-        target = target < total ? target : total - 1;
+        const unsigned long long target = target_of(total);
         unsigned long long b = mi - msum;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             if (target >= b && target < b + ms[i]) {
                 sh.seg = lane * PER + i;
                 sh.seg_target = target - b;
-                sh.seg_ties = left[i];
             }
             b += ms[i];
         }
         if (lane == 0) sh.total = total;
-    }
-    __syncthreads();
-    if (sh.seg == rank * kWarps + warp) {
-        unsigned long long run = 0;
-        uint32_t seen = 0;
-        for (int v = s0 + lane; v < s0 + seg_len; v += 32) {   // seg_len is a multiple of 32
-            const float x = at(v);
-            const uint32_t key = key_of<DTYPE>(x);
-            const bool tie = key == cut.key && x != -CUDART_INF_F && cut.weight != 0;
-            const uint32_t ties_here = __ballot_sync(0xffffffffu, tie);
-            const uint32_t before = seen + __popc(ties_here & ((1u << lane) - 1u));
-            const uint32_t w = key > cut.key || (tie && before < sh.seg_ties) ? kept(x, key) : 0u;
-            const unsigned long long incl = run + warp_incl((unsigned long long)w, lane);
-            const uint32_t hit = __ballot_sync(0xffffffffu, incl > sh.seg_target);
-            if (hit) {
-                if (lane == __ffs(hit) - 1) {
-                    p.token[row] = first + v - mis;
-                    if (p.prob) p.prob[row] = (float)((double)w / (double)sh.total);
-                }
-                break;
+    };
+    // the drawn token, by all threads of the CTA that holds its segment
+    auto locate = [&](int seg, unsigned long long target, unsigned long long total) {
+        if (seg / kWarps != rank) return;
+        const int from = seg % kWarps * seg_len;
+        unsigned long long before = 0;
+        for (int v0 = from; v0 < from + seg_len; v0 += kThreads * VEC) {
+            const int v = v0 + tid * VEC;
+            uint32_t weight[VEC];
+            unsigned long long sum = 0;
+            float x[VEC];
+            if (v < from + seg_len) expand(load(v), x);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                weight[i] = v < from + seg_len ? kept(x[i], v + i) : 0u;
+                sum += weight[i];
             }
-            run = __shfl_sync(0xffffffffu, incl, 31);
-            seen += __popc(ties_here);
+            const unsigned long long incl = warp_incl(sum, lane);
+            __syncthreads();
+            if (lane == 31) sh.best[warp] = incl;
+            __syncthreads();
+            const unsigned long long wm = warp_incl(lane < kWarps ? sh.best[lane] : 0ull, lane);
+            const unsigned long long upto = __shfl_sync(0xffffffffu, wm, warp > 0 ? warp - 1 : 0);
+            unsigned long long b = before + (warp > 0 ? upto : 0ull) + incl - sum;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                if (target >= b && target < b + weight[i]) result(first + v + i, (double)weight[i] / (double)total);
+                b += weight[i];
+            }
+            before += __shfl_sync(0xffffffffu, wm, 31);
+        }
+    };
+
+    // The cut inside a bin found by search(), where a list would not hold it: the bin's range of keys, then
+    // histograms over the keys until one is left; n(count before, weight before, ties, a tie's weight) of that
+    // key's tokens are kept, the first by index.
+    auto refine = [&](auto done, auto n) {
+        const int bin = sh.bin;
+        uint32_t cnt0 = sh.base_cnt;
+        unsigned long long mass0 = sh.base_mass;
+        uint32_t kmin = 0xffffffffu, kmax = 0u;
+        each(weightless, [&](int, float x) {
+            if (!(x > -CUDART_INF_F) || bin_of(x, r) != bin || weight_of(exp_of(x, r)) == 0) return;
+            const uint32_t key = key_of<DTYPE>(x);
+            kmin = key < kmin ? key : kmin;
+            kmax = key > kmax ? key : kmax;
+        });
+        kmin = __reduce_min_sync(0xffffffffu, kmin);
+        kmax = __reduce_max_sync(0xffffffffu, kmax);
+        if (lane == 0) sh.best[warp] = (unsigned long long)kmax << 32 | kmin;
+        __syncthreads();
+        if (tid == 0) {
+            for (int i = 0; i < kWarps; ++i) {
+                const uint32_t a = (uint32_t)sh.best[i], b = (uint32_t)(sh.best[i] >> 32);
+                kmin = a < kmin ? a : kmin;
+                kmax = b > kmax ? b : kmax;
+            }
+            sh.range = (unsigned long long)kmax << 32 | kmin;
+        }
+        cl.sync();
+        for (int c = 0; c < ctas; ++c) {
+            const unsigned long long o = cl.map_shared_rank(&sh, c)->range;
+            kmin = (uint32_t)o < kmin ? (uint32_t)o : kmin;
+            kmax = (uint32_t)(o >> 32) > kmax ? (uint32_t)(o >> 32) : kmax;
+        }
+        for (int level = 0; level < 4; ++level) {   // ten bits of the range a level
+            cl.sync();                              // the last level's counts are read
+            clear(sh.keys);
+            __syncthreads();
+            const uint32_t range = kmax - kmin;
+            const int bits = range ? 32 - __clz(range) : 0;
+            const int shift = bits > 10 ? bits - 10 : 0;
+            each(float_of<DTYPE>(kmin), [&](int, float x) {
+                const uint32_t key = key_of<DTYPE>(x);
+                if (x > -CUDART_INF_F && key >= kmin && key <= kmax) {
+                    const int at = (int)((kmax - key) >> shift);
+                    atomicAdd(&sh.keys.cnt[at], 1u);
+                    add_mass(sh.keys, at, weight_of(exp_of(x, r)));
+                }
+            });
+            search<true>(cl, sh, sh.keys, cnt0, mass0, done);
+            cnt0 = sh.base_cnt;
+            mass0 = sh.base_mass;
+            if (shift == 0) break;
+            kmax -= (uint32_t)sh.bin << shift;
+            const uint32_t low = kmax - ((1u << shift) - 1u);
+            kmin = low > kmin && low <= kmax ? low : kmin;
+        }
+        // the key's kept tokens end at an index: that of the last, by counts of the warps' segments
+        const uint32_t ties = sh.bin_cnt;
+        const uint32_t keep = n(cnt0, mass0, ties, (uint32_t)(sh.bin_mass / ties));
+        cut_x = float_of<DTYPE>(kmax - (uint32_t)sh.bin);
+        cut_at = 0x7fffffff;
+        if (keep < ties) {
+            auto tie_at = [&](int v) {
+                const int at = first + v;
+                if (at < 0 || at >= p.vocab) return false;
+                if constexpr (sizeof(T) == 4) return src[at] == cut_x;
+                else return Elem<DTYPE>::get(src[at]) == cut_x;
+            };
+            uint32_t here = 0;
+            for (int v = warp * seg_len + lane; v < (warp + 1) * seg_len; v += 32) here += tie_at(v);
+            here = __reduce_add_sync(0xffffffffu, here);
+            if (lane == 0) sh.scan_cnt[warp] = here;
+            __syncthreads();
+            if (tid == 0) {
+                uint32_t sum = 0;
+                for (int i = 0; i < kWarps; ++i) sum += sh.scan_cnt[i];
+                sh.listed = sum;
+            }
+            cl.sync();
+            uint32_t before = 0;
+            for (int c = 0; c < rank; ++c) before += cl.map_shared_rank(&sh, c)->listed;
+            for (int i = 0; i < warp; ++i) before += sh.scan_cnt[i];
+            if (before < keep && keep <= before + here) {   // one warp of the cluster
+                for (int v = warp * seg_len + lane; v < (warp + 1) * seg_len; v += 32) {
+                    const bool tie = tie_at(v);
+                    const uint32_t bits = __ballot_sync(0xffffffffu, tie);
+                    const uint32_t at = before + __popc(bits & ((2u << lane) - 1u));
+                    if (tie && at == keep) cl.map_shared_rank(&sh, 0)->cut = 0xffffffffu - (uint32_t)(first + v);
+                    before += __popc(bits);
+                }
+            }
+            cl.sync();
+            cut_at = (int)(0xffffffffu - (uint32_t)cl.map_shared_rank(&sh, 0)->cut);
+        }
+        __syncthreads();
+    };
+    // how many of a key's tokens top-p keeps
+    auto kept_ties = [](double limit, unsigned long long m, uint32_t ties, uint32_t weight) {
+        uint32_t n = (uint32_t)fmin((limit - (double)m) / (double)weight, 4294967040.0);
+        n = n > ties ? ties : n;
+        while (n > 0 && !((double)(m + (unsigned long long)(n - 1) * weight) < limit)) --n;
+        while (n < ties && (double)(m + (unsigned long long)n * weight) < limit) ++n;
+        return n > 0u ? n : 1u;
+    };
+
+    if (need_k) {
+        each(weightless, [&](int, float x) {
+            const uint32_t weight = weight_of(exp_of(x, r));
+            if (weight) {
+                const int b = bin_of(x, r);
+                atomicAdd(&sh.bins.cnt[b], 1u);
+                add_mass(sh.bins, b, weight);
+            }
+        });
+        const uint32_t kk = (uint32_t)k;
+        auto by_count = [kk](uint32_t c, unsigned long long, unsigned long long) { return c >= kk; };
+        search<true>(cl, sh, sh.bins, 0u, 0ull, by_count);
+        unsigned long long total = sh.total;
+        if (sh.bin >= 0)
+            refine(by_count, [&](uint32_t c, unsigned long long m, uint32_t, uint32_t weight) {
+                total = m + (unsigned long long)(kk - c) * weight;
+                return kk - c;
+            });
+        __syncthreads();
+        if (need_p) {
+            // both cuts are prefixes of one ranking: the shorter one holds
+            const float k_x = cut_x;
+            const int k_at = cut_at;
+            const double limit = (double)total * (double)top_p;
+            auto by_mass = [limit](uint32_t, unsigned long long m, unsigned long long) { return !((double)m < limit); };
+            search<true>(cl, sh, sh.bins, 0u, 0ull, by_mass);
+            if (sh.bin >= 0) {
+                refine(by_mass, [&](uint32_t, unsigned long long m, uint32_t ties, uint32_t weight) {
+                    return kept_ties(limit, m, ties, weight);
+                });
+                if (k_x > cut_x || (k_x == cut_x && k_at < cut_at)) {
+                    cut_x = k_x;
+                    cut_at = k_at;
+                }
+            }
+            __syncthreads();
+        }
+    } else if (need_p) {
+        each(weightless, [&](int, float x) {
+            const uint32_t weight = weight_of(exp_of(x, r));
+            if (weight) add_mass(sh.bins, bin_of(x, r), weight);
+        });
+        // the bin past which the weight before a token is no longer below top_p times the whole
+        search<true>(cl, sh, sh.bins, 0u, 0ull, [top_p](uint32_t, unsigned long long m, unsigned long long all) {
+            return !((double)m < (double)all * (double)top_p);
+        });
+        if (sh.bin >= 0) {
+            const double limit = (double)sh.total * (double)top_p;
+            const int bin = sh.bin;
+            const unsigned long long base = sh.base_mass;
+            // one pass sums what lies above the bin, by segments, and lists the bin's tokens
+            unsigned long long mass = 0;
+            sweep(s0 + lane * VEC, s0 + seg_len, 32 * VEC, below((float)(bin + 1) / to_bin * temp), [&](int v, float x) {
+                const float e = exp_of(x, r), at = place(x);
+                const int b = at < (float)kBins ? (int)at : kBins;   // NaN: no bin
+                mass += b < bin && (e >= r.min_p || x == r.top) ? weight_of(e) : 0u;
+                if (b == bin && x > -CUDART_INF_F) list_it(v, x);
+            });
+            mass = warp_sum(mass);
+            if (lane == 0) sh.warp_mass[warp] = mass;
+            const int n = gather();
+            if (n >= 0) {
+                if (rank == 0) {
+                    const int segs = ctas * kWarps;
+                    if (tid < segs) sh.all_mass[tid] = cl.map_shared_rank(&sh, tid / kWarps)->warp_mass[tid % kWarps];
+                    pick(sh, key, w, base, [limit](uint32_t, unsigned long long m) { return !((double)m < limit); });
+#pragma unroll
+                    for (int i = 0; i < kListPer; ++i)
+                        if (key[i] != 0 && key[i] >= sh.picked && (exp_of(logit_of(key[i]), r) >= r.min_p || logit_of(key[i]) == r.top)) {
+                            const int at = token_of(key[i]) + mis;   // place in the row
+                            atomicAdd(&sh.all_mass[at / p.slice * kWarps + at % p.slice / seg_len], (unsigned long long)w[i]);
+                        }
+                    if (tid == 0) sh.cut = sh.picked;
+                    __syncthreads();
+                    choose(segs);
+                }
+                cl.sync();
+                const Shared* o = cl.map_shared_rank(&sh, 0);
+                cut_x = logit_of(o->cut);
+                cut_at = token_of(o->cut);
+                locate(o->seg, o->seg_target, o->total);
+                cl.sync();
+                return;
+            }
+            refine([limit](uint32_t, unsigned long long m, unsigned long long) { return !((double)m < limit); },
+                   [&](uint32_t, unsigned long long m, uint32_t ties, uint32_t weight) {
+                       return kept_ties(limit, m, ties, weight);
+                   });
         }
     }
+
+    // ---- the kept weight of each warp's segment, in index order
+    unsigned long long mass = 0;
+    sweep(s0 + lane * VEC, s0 + seg_len, 32 * VEC, fmaxf(cut_x, weightless), [&](int v, float x) { mass += kept(x, v); });
+    mass = warp_sum(mass);
+    if (lane == 0) sh.warp_mass[warp] = mass;
+    cl.sync();
+    const int segs = ctas * kWarps;
+    if (tid < segs) sh.all_mass[tid] = cl.map_shared_rank(&sh, tid / kWarps)->warp_mass[tid % kWarps];
+    __syncthreads();
+    choose(segs);
+    __syncthreads();
+    locate(sh.seg, sh.seg_target, sh.total);
     cl.sync();   // no CTA leaves while another may read its shared memory
 }
-
-constexpr int kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
-constexpr int kMaxSmem = 227 * 1024;
 
 template <int DTYPE>
 cudaError_t launch_one(const SampleParams& p, int ctas, cudaStream_t stream)
@@ -534,7 +899,6 @@ cudaError_t launch_one(const SampleParams& p, int ctas, cudaStream_t stream)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.batch * ctas));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)kSharedBytes + (size_t)p.slice * sizeof(typename Elem<DTYPE>::T);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -547,31 +911,16 @@ cudaError_t launch_one(const SampleParams& p, int ctas, cudaStream_t stream)
 
 }  // namespace
 
-cudaError_t setup_sample()
-{
-    cudaError_t e;
-    if ((e = cudaFuncSetAttribute(sample_kernel<W4A16_FP32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem)) !=
-            cudaSuccess ||
-        (e = cudaFuncSetAttribute(sample_kernel<W4A16_FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem)) !=
-            cudaSuccess ||
-        (e = cudaFuncSetAttribute(sample_kernel<W4A16_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem)) !=
-            cudaSuccess)
-        return e;
-    return cudaSuccess;
-}
-
 cudaError_t launch_sample(const SampleParams& in, int sms, cudaStream_t stream)
 {
     SampleParams p = in;
     const int size = p.dtype == W4A16_FP32 ? 4 : 2;
     const int step = 16 / size * kThreads;   // a slice is whole rounds of 16-byte loads
-    // As many CTAs a row as give every SM one, and at least as many as hold the row
-    // with two CTAs on an SM; up to the portable cluster of eight.
+    // As many CTAs a row as give every SM the two it holds, while a slice is more than a round of loads; up
+    // to the portable cluster of eight. A row's steps are a chain, so that fewer, longer slices leave it waiting
+    // (256 x 100003 FP32: 239 us with one CTA a row, 93 with two, 100 with four).
     int ctas = 1;
-    const long long bytes = (long long)p.vocab * size;
-    while (ctas < kMaxCluster && ((long long)p.batch * ctas < sms || bytes / ctas > 80 * 1024) &&
-           p.vocab / ctas > step)
-        ctas *= 2;
+    while (ctas < kMaxCluster && (long long)p.batch * ctas < 2 * sms && p.vocab / ctas > step) ctas *= 2;
     p.slice = ((p.vocab + 16 / size + ctas - 1) / ctas + step - 1) / step * step;
     switch (p.dtype) {
         case W4A16_FP32: return launch_one<W4A16_FP32>(p, ctas, stream);

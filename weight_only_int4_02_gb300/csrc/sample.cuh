@@ -21,7 +21,6 @@ struct SampleParams {
     int dtype;                   // w4a16_dtype
     int slice;                   // elements of a CTA's slice (set by the launch)
 };
-cudaError_t setup_sample();
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t stream);
 
 }  // namespace w4a16
