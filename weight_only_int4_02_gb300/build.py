@@ -1,9 +1,11 @@
-"""Build libw4a16.so in-tree with nvcc for sm_103a (no GPU needed to compile)."""
+"""Build libw4a16.so in-tree with nvcc for sm_103a (no GPU needed to compile), and the
+Python module of the serving step's calls, which links it, with the host compiler."""
 import glob
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -11,6 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libw4a16.so")
+MODULE = os.path.join(OUT_DIR, "_w4a16_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
@@ -27,8 +30,23 @@ def _newest_header():
     return max(os.path.getmtime(h) for h in hdrs)
 
 
+def _module_commands(obj, out):
+    """To compile csrc/binding.cpp against the installed torch, and to link it with libw4a16.so."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    compile_cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] +
+                   ["-I" + i for i in inc] + ["-c", os.path.join(CSRC, "binding.cpp"), "-o", obj])
+    link_cmd = ["g++", "-shared", obj, "-o", out, "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+                "-L" + OUT_DIR, "-lw4a16", "-Wl,-rpath," + lib, "-Wl,-rpath,$ORIGIN"]
+    return compile_cmd, link_cmd
+
+
 def build(force=False, verbose=False, ptxas_verbose=False):
-    """Compile each csrc/*.cu in parallel, then link libw4a16.so. Returns the library path."""
+    """Compile each csrc/*.cu and the Python module in parallel, then link libw4a16.so. Returns the library path."""
     os.makedirs(os.path.join(OUT_DIR, "obj"), exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     hdr_time = _newest_header()
@@ -42,6 +60,14 @@ def build(force=False, verbose=False, ptxas_verbose=False):
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    binding, module_obj = os.path.join(CSRC, "binding.cpp"), os.path.join(OUT_DIR, "obj", "binding.o")
+    module_stale = (force or not os.path.exists(module_obj) or
+                    os.path.getmtime(module_obj) < max(os.path.getmtime(binding), hdr_time))
+    if module_stale:
+        cmd, _ = _module_commands(module_obj, None)
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        module = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     logs = []
     for src, pr in procs:
         out, _ = pr.communicate()
@@ -52,6 +78,15 @@ def build(force=False, verbose=False, ptxas_verbose=False):
         tmp = LIB + ".tmp%d" % os.getpid()
         subprocess.check_call([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, LIB)
+    if module_stale:
+        out, _ = module.communicate()
+        logs.append(out.decode(errors="replace"))
+        if module.returncode != 0:
+            raise RuntimeError("g++ failed on %s:\n%s" % (binding, logs[-1]))
+    if module_stale or not os.path.exists(MODULE):
+        tmp = MODULE + ".tmp%d" % os.getpid()
+        subprocess.check_call(_module_commands(module_obj, tmp)[1])
+        os.replace(tmp, MODULE)
     if verbose or ptxas_verbose:
         sys.stderr.write("".join(logs))
     return LIB

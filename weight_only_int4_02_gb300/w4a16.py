@@ -1,4 +1,5 @@
-"""Python binding of libw4a16.so (ctypes; argument marshalling only).
+"""Python binding of libw4a16.so (argument marshalling only: ctypes, and for the serving
+step's short calls the compiled module _w4a16_torch).
 
 Every step of the matmul runs in the library's CUDA kernels. Tensors are torch
 CUDA tensors used as plain device buffers; FP16 data crosses the ABI as binary16
@@ -6,6 +7,7 @@ bit patterns. There is no fallback: if the library is not built, or the device
 is not an sm_103 GPU, the calls raise.
 """
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -472,21 +474,26 @@ def sp_gemm(x, packed, scales_packed, N, group_size, bias=None, residual=None, a
 
 
 # ---------------------------------------------------------------- the serving step
-# These calls last a few microseconds on the GPU, so what they do on the host counts: messages are
-# built only for an error, and a tensor's attributes are read once.
-_F16, _BF16, _F32, _I32, _I64, _U8 = (torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8)
-_DTYPES = {_F16: 0, _BF16: 1, _F32: 2}
+# These calls last a few microseconds on the GPU, so their checks, their outputs and the
+# C call are in a compiled module (csrc/binding.cpp). Wrong tensors raise W4A16Error before any launch.
+_MODULE_PATH = os.path.join(os.path.dirname(_LIB_PATH), "_w4a16_torch.so")
+_module = None
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
-def _refuse(what):
-    raise W4A16Error(ERR_INVALID_ARG, what)
-
-
-def _vector(t, dtype, n, what):
-    """Address of a contiguous one-dimensional CUDA tensor of n elements."""
-    if not (t.dtype is dtype and t.is_cuda and t.dim() == 1 and t.shape[0] == n and t.is_contiguous()):
-        _refuse("%s must be a contiguous %s CUDA tensor of %d elements" % (what, dtype, n))
-    return t.data_ptr()
+def _torch_module():
+    """The compiled module; raises if it has not been built."""
+    global _module
+    if _module is None:
+        lib()
+        if not os.path.exists(_MODULE_PATH):
+            raise RuntimeError("_w4a16_torch.so is not built (%s); run __graft_entry__.build()" % _MODULE_PATH)
+        spec = importlib.util.spec_from_file_location("_w4a16_torch", _MODULE_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(W4A16Error)
+        _module = module
+    return _module
 
 
 def kv4_page_bytes(kv_heads, head_dim, page_size):
@@ -496,18 +503,8 @@ def kv4_page_bytes(kv_heads, head_dim, page_size):
 def kv4_cache(pages, kv_heads, head_dim, page_size, device="cuda"):
     """An empty 4-bit key-value cache: uint8 [pages][kv_heads][page_size / 16][16 * (head_dim + 6)]."""
     if pages < 0 or kv4_page_bytes(kv_heads, head_dim, page_size) == 0:
-        _refuse("no 4-bit cache of %d KV heads of %d in pages of %d" % (kv_heads, head_dim, page_size))
-    return torch.zeros((pages, kv_heads, page_size // 16, 16 * (head_dim + 6)), dtype=_U8, device=device)
-
-
-def _kv4_sizes(cache, page_size):
-    """(pages, KV heads, head dimension) of a cache."""
-    if cache.dtype is _U8 and cache.is_cuda and cache.dim() == 4 and cache.is_contiguous():
-        pages, heads, tiles, size = cache.shape
-        if tiles * 16 == page_size and size % 16 == 0:
-            return pages, heads, size // 16 - 6
-    return _refuse("the cache must be a contiguous uint8 CUDA tensor "
-                   "[pages][kv_heads][page_size / 16][16 * (head_dim + 6)]")
+        raise W4A16Error(ERR_INVALID_ARG, "no 4-bit cache of %d KV heads of %d in pages of %d" % (kv_heads, head_dim, page_size))
+    return torch.zeros((pages, kv_heads, page_size // 16, 16 * (head_dim + 6)), dtype=torch.uint8, device=device)
 
 
 def kv4_tables(seq_lens, new_lens, free_pages, block_table, page_size, max_tokens, taken=None, stream=None):
@@ -517,57 +514,22 @@ def kv4_tables(seq_lens, new_lens, free_pages, block_table, page_size, max_token
     [batch][max_pages], updated in place; taken: int32 [1], pages of the free list taken
     before, or None. Returns (slots int64 [max_tokens], positions int32 [max_tokens],
     starts int32 [batch + 1], taken int32 [1])."""
-    batch, device = seq_lens.shape[0], seq_lens.device
-    if not (block_table.dtype is _I32 and block_table.is_cuda and block_table.dim() == 2 and
-            block_table.shape[0] == batch and block_table.is_contiguous()):
-        _refuse("block_table must be a contiguous int32 CUDA tensor [%d][pages]" % batch)
-    if max_tokens < 0:
-        _refuse("max_tokens is negative")
-    n_free = free_pages.shape[0]
-    args = (_vector(seq_lens, _I32, batch, "seq_lens"), _vector(new_lens, _I32, batch, "new_lens"), batch,
-            _vector(free_pages, _I32, n_free, "free_pages"), n_free,
-            None if taken is None else _vector(taken, _I32, 1, "taken"))
-    slots = torch.empty(max_tokens, dtype=_I64, device=device)
-    positions, starts, after = torch.empty(max_tokens + batch + 2, dtype=_I32, device=device).split_with_sizes(
-        (max_tokens, batch + 1, 1))
-    rc = lib().w4a16_kv4_tables(*args, after.data_ptr(), block_table.data_ptr(), block_table.shape[1], page_size,
-                                slots.data_ptr(), positions.data_ptr(), max_tokens, starts.data_ptr(), _stream(stream))
-    if rc:
-        raise W4A16Error(rc, "w4a16_kv4_tables")
-    return slots, positions, starts, after
+    return (_module or _torch_module()).kv4_tables(seq_lens, new_lens, free_pages, block_table, page_size, max_tokens, taken,
+                                                   None if stream is None else stream.cuda_stream)
 
 
 def kv4_append(k, v, slots, cache, page_size, stream=None):
     """Quantise k and v (float16 or bfloat16 [tokens][kv_heads][head_dim] views whose last
     dimension is contiguous) into their slots (int64 [tokens]; -1 skips) of the cache."""
-    pages, heads, dim = _kv4_sizes(cache, page_size)
-    tokens = slots.shape[0]
-    dtype = k.dtype
-    shape = (tokens, heads, dim)
-    (kt, kh, kd), (vt, vh, vd) = k.stride() if k.dim() == 3 else (0, 0, 0), v.stride() if v.dim() == 3 else (0, 0, 0)
-    if not ((dtype is _F16 or dtype is _BF16) and v.dtype is dtype and k.is_cuda and v.is_cuda and k.shape == shape and
-            v.shape == shape and kd == 1 and vd == 1):
-        _refuse("k and v must be float16 or bfloat16 CUDA tensors [%d][%d][%d], the last dimension contiguous" % shape)
-    rc = lib().w4a16_kv4_append(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _vector(slots, _I64, tokens, "slots"),
-                                cache.data_ptr(), pages, tokens, heads, dim, page_size, _DTYPES[dtype], _stream(stream))
-    if rc:
-        raise W4A16Error(rc, "w4a16_kv4_append")
+    (_module or _torch_module()).kv4_append(k, v, slots, cache, page_size, None if stream is None else stream.cuda_stream)
 
 
 def kv4_read(cache, slots, page_size, dtype=torch.float16, stream=None):
     """(k, v) [tokens][kv_heads][head_dim] that the slots stand for, in float16, bfloat16 or float32."""
-    pages, heads, dim = _kv4_sizes(cache, page_size)
-    tokens = slots.shape[0]
     if dtype not in _DTYPES:
-        _refuse("kv4_read gives float16, bfloat16 or float32")
-    at = _vector(slots, _I64, tokens, "slots")
-    k = torch.empty((tokens, heads, dim), dtype=dtype, device=cache.device)
-    v = torch.empty_like(k)
-    rc = lib().w4a16_kv4_read(cache.data_ptr(), pages, at, k.data_ptr(), v.data_ptr(), tokens, heads, dim, page_size,
-                              _DTYPES[dtype], _stream(stream))
-    if rc:
-        raise W4A16Error(rc, "w4a16_kv4_read")
-    return k, v
+        raise W4A16Error(ERR_INVALID_ARG, "kv4_read gives float16, bfloat16 or float32")
+    return (_module or _torch_module()).kv4_read(cache, slots, page_size, _DTYPES[dtype],
+                                                 None if stream is None else stream.cuda_stream)
 
 
 def kv4_workspace_bytes():
@@ -584,35 +546,9 @@ def kv4_attention(q, cache, block_table, seq_lens, starts, page_size, max_q, sca
     tokens of a request; scale: 1 / sqrt(head_dim) by default; window: keys a query sees at
     most, 0 for all; workspace: uint8, kv4_workspace_bytes(), zeroed once, or None for the
     library's own. Returns out, or (out, lse float32 [tokens][q_heads])."""
-    pages, heads, dim = _kv4_sizes(cache, page_size)
-    dtype, batch = q.dtype, seq_lens.shape[0]
-    if not ((dtype is _F16 or dtype is _BF16) and q.is_cuda and q.dim() == 3 and q.shape[2] == dim and q.stride(2) == 1):
-        _refuse("q must be a float16 or bfloat16 CUDA tensor [tokens][q_heads][%d], the last dimension contiguous" % dim)
-    tokens, q_heads = q.shape[0], q.shape[1]
-    if block_table.dim() != 2 or block_table.dtype is not _I32 or not block_table.is_cuda or block_table.shape[0] != batch:
-        _refuse("block_table must be an int32 CUDA tensor [%d][pages]" % batch)
-    cols = block_table.shape[1]
-    row, col = block_table.stride()
-    if col != 1 and cols > 1:
-        _refuse("block_table's rows must be contiguous")
-    if out is None:
-        out = torch.empty((tokens, q_heads, dim), dtype=dtype, device=q.device)
-    elif not (out.dtype is dtype and out.is_cuda and out.shape == q.shape and out.stride(2) == 1):
-        _refuse("out must be a CUDA tensor of q's type and shape, the last dimension contiguous")
-    ws, ws_bytes = None, 0
-    if workspace is not None:
-        ws, ws_bytes = workspace.data_ptr(), _nbytes(workspace)
-    lse = torch.empty((tokens, q_heads), dtype=_F32, device=q.device) if return_lse else None
-    qt, qh, _ = q.stride()
-    ot, oh, _ = out.stride()
-    rc = lib().w4a16_kv4_attention(
-        q.data_ptr(), qt, qh, cache.data_ptr(), pages, block_table.data_ptr(), row if row > cols else cols, cols,
-        _vector(seq_lens, _I32, batch, "seq_lens"), _vector(starts, _I32, batch + 1, "starts"), out.data_ptr(), ot, oh,
-        lse.data_ptr() if return_lse else None, batch, tokens, q_heads, heads, dim, page_size, max_q,
-        dim ** -0.5 if scale is None else scale, window, _DTYPES[dtype], ws, ws_bytes, _stream(stream))
-    if rc:
-        raise W4A16Error(rc, "w4a16_kv4_attention")
-    return (out, lse) if return_lse else out
+    return (_module or _torch_module()).kv4_attention(q, cache, block_table, seq_lens, starts, page_size, max_q, scale, window,
+                                                      out, return_lse, workspace,
+                                                      None if stream is None else stream.cuda_stream)
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
@@ -620,21 +556,5 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stre
     from uniform numbers u (float32 [batch]), after temperature, top-k, top-p and min-p
     (float32, int32, float32, float32 [batch], each or None). Returns (token int32 [batch],
     its probability among the kept tokens float32 [batch]); see w4a16_sample."""
-    dtype = logits.dtype
-    if not (dtype in _DTYPES and logits.is_cuda and logits.dim() == 2):
-        _refuse("logits must be a float16, bfloat16 or float32 CUDA tensor [batch][vocab]")
-    batch, vocab = logits.shape
-    row, col = logits.stride()
-    if col != 1 and vocab > 1:
-        _refuse("the rows of logits must be contiguous")
-    args = (_vector(u, _F32, batch, "u"), None if temperature is None else _vector(temperature, _F32, batch, "temperature"),
-            None if top_k is None else _vector(top_k, _I32, batch, "top_k"),
-            None if top_p is None else _vector(top_p, _F32, batch, "top_p"),
-            None if min_p is None else _vector(min_p, _F32, batch, "min_p"))
-    token = torch.empty(batch, dtype=_I32, device=logits.device)
-    prob = torch.empty_like(token, dtype=_F32)
-    rc = lib().w4a16_sample(logits.data_ptr(), row if row > vocab else vocab, *args, token.data_ptr(), prob.data_ptr(),
-                            batch, vocab, _DTYPES[dtype], _stream(stream))
-    if rc:
-        raise W4A16Error(rc, "w4a16_sample")
-    return token, prob
+    return (_module or _torch_module()).sample(logits, u, temperature, top_k, top_p, min_p,
+                                               None if stream is None else stream.cuda_stream)
