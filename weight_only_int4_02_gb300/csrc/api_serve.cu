@@ -31,8 +31,8 @@ bool valid_rows(const void* cache, int pages, const int64_t* slots, int tokens, 
 {
     if (tokens < 0 || kv_heads <= 0 || pages < 0 || !valid_dim(head_dim) || !valid_page(page_size)) return false;
     if (dtype < 0 || dtype >= dtypes) return false;
-    // the kernels count blocks of rows in 31 bits
-    if ((int64_t)tokens * kv_heads >= ((int64_t)1 << 31)) return false;
+    // the kernels count rows (K and V of a token and head) in 32 bits, a last block past them too
+    if ((int64_t)tokens * kv_heads >= ((int64_t)1 << 31) - 256) return false;
     return tokens == 0 || (cache && slots && aligned(cache, 16) && aligned(slots, 8));
 }
 

@@ -1,6 +1,8 @@
 // The 4-bit cache's bookkeeping and rows: block tables and slot maps from request
 // lengths, quantisation of new keys and values into their slots, and the read back.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
 
 #include "kv4.cuh"
 #include "w4a16.h"
@@ -131,6 +133,21 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b)
     }
 }
 
+__device__ __forceinline__ uint32_t negate2(uint32_t w) { return w ^ 0x80008000u; }
+
+// The larger of each pair; a NaN on either side gives a NaN.
+template <int DTYPE>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+{
+    if constexpr (DTYPE == W4A16_BF16) {
+        const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    } else {
+        const __half2 m = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+}
+
 template <int DTYPE>
 __device__ __forceinline__ uint32_t pack2(float a, float b)
 {
@@ -148,92 +165,116 @@ __device__ __forceinline__ uint8_t* tile_of(const Kv4RowsParams& p, int token, i
 {
     const long long slot = p.slots[token];
     if (slot < 0 || slot >= p.n_slots) return nullptr;
-    const long long page = slot / p.page_size;
-    const int in_page = (int)(slot - page * p.page_size);
+    const int shift = __ffs(p.page_size) - 1;   // a power of two
+    const int in_page = (int)slot & (p.page_size - 1);
     *tok = in_page & 15;
-    return p.cache + ((page * p.kv_heads + head) * (p.page_size >> 4) + (in_page >> 4)) * (long long)kv4_tile_bytes(D);
+    return p.cache + ((((slot >> shift) * p.kv_heads + head) << (shift - 4)) + (in_page >> 4)) * (long long)kv4_tile_bytes(D);
 }
 
-// One row (token, KV head, K or V) per group of D/8 lanes, eight values a lane: the row's
-// extremes by shuffles, then
+// The rows of a group of D/8 lanes: K and V of a token and KV head.
+struct Rows {
+    int token, head;
+    bool live;
+};
+
+template <int D>
+__device__ __forceinline__ Rows rows_of(const Kv4RowsParams& p)
+{
+    const uint32_t i = blockIdx.x * (256u / (D / 8)) + threadIdx.x / (D / 8);   // below 2^32: checked on the host
+    Rows r;
+    r.token = (int)(i / (uint32_t)p.kv_heads);
+    r.head = (int)(i - (uint32_t)r.token * (uint32_t)p.kv_heads);
+    r.live = r.token < p.tokens;
+    return r;
+}
+
+// A row's codes, four to a 16-bit word, its scale's bits and its zero-point.
+struct Quantised {
+    uint32_t w0, w1, zero;
+    __half scale;
+};
+
+// One row per D/8 lanes, eight values a lane: the row's extremes by shuffles, then
 //   s = fp16(min((hi - lo) / 15, 65504)), z = clamp(rint(-lo / s), 0, 15),
 //   code = clamp(rint(x / s) + z, 0, 15)        (lo = min(x, 0), hi = max(x, 0))
-// with 1 / s rounded once to FP32; every operation is an IEEE one (no contraction, no
-// approximate division), so the codes are the same wherever the formula is evaluated. A row
-// that holds an infinity or a NaN gets scale NaN, so that it shows in whatever reads it.
-// Reads 4 D bytes a token and head and writes D + 6: bound by bandwidth for a prompt,
-// by latency for a decode step.
+// with hi - lo formed from max(x, 0) and max(-x, 0), and 1 / s rounded once to FP32; every
+// operation is an IEEE one (no contraction, no approximate division), so the codes are the same
+// wherever the formula is evaluated. A row that holds an infinity or a NaN gets scale NaN, so
+// that it shows in whatever reads it.
+template <int D, int DTYPE>
+__device__ __forceinline__ Quantised quantise(const uint4& raw)
+{
+    // the row's extremes as a pair (max x, max -x) of the inputs' own type, exact; a NaN stays one
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t up = w[0], dn = negate2(w[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        up = max2<DTYPE>(up, w[i]);
+        dn = max2<DTYPE>(dn, negate2(w[i]));
+    }
+    uint32_t ext = max2<DTYPE>(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632));
+    ext = max2<DTYPE>(ext, 0u);
+#pragma unroll
+    for (int d = D / 16; d > 0; d >>= 1) ext = max2<DTYPE>(ext, __shfl_xor_sync(0xffffffffu, ext, d));
+    float hi, neg;   // max(x, 0) and max(-x, 0)
+    unpack2<DTYPE>(ext, hi, neg);
+    const bool poisoned = !isfinite(hi) || !isfinite(neg);
+    Quantised q;
+    q.scale = poisoned ? __ushort_as_half(0x7fff) : __float2half_rn(fminf(__fdiv_rn(__fadd_rn(hi, neg), 15.0f), 65504.0f));
+    const float s = __half2float(q.scale);
+    const float inv = !poisoned && s > 0.0f ? __frcp_rn(s) : 0.0f;
+    // rint by adding 1.5 * 2^23, whose last bit is 1: the sum's low bits are the whole number
+    constexpr float kRound = 12582912.0f;
+    auto whole = [&](float v) { return __float_as_int(__fadd_rn(__fmul_rn(v, inv), kRound)) - __float_as_int(kRound); };
+    const int z = poisoned ? 0 : min(whole(neg), 15);
+    q.zero = (uint32_t)z;
+    uint32_t code[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        unpack2<DTYPE>(w[i], a, b);
+        code[2 * i] = (uint32_t)max(min(whole(a) + z, 15), 0);
+        code[2 * i + 1] = (uint32_t)max(min(whole(b) + z, 15), 0);
+    }
+    q.w0 = poisoned ? 0u : code[0] | code[1] << 4 | code[2] << 8 | code[3] << 12;
+    q.w1 = poisoned ? 0u : code[4] | code[5] << 4 | code[6] << 8 | code[7] << 12;
+    return q;
+}
+
+// Index of the 16-bit word of V's codes that holds d = 8j .. 8j + 3 of a token; the next four are two words on.
+template <int D>
+__device__ __forceinline__ int v_word(int tok, int j)
+{
+    const int n = 8 * j / (D / 8), w = (8 * j % (D / 8)) / 4;   // token 8h + 2c + e
+    return ((((tok >> 3) * 8 + n) * 4 + ((tok & 7) >> 1)) * (D / 32) + w) * 2 + (tok & 1);
+}
+
+// Quantises the new rows into their slots. Reads 4 D bytes a token and head and writes
+// 2 (D + 6): bound by bandwidth for a long prompt, by latency for a decode step. A thread has its K and
+// its V load in flight together (8191 tokens of eight heads of 128: 12.6 us against 16.2 with one
+// row a thread; half of that time is the bytes', the rest V's scattered 2-byte stores and the launch).
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowsParams p)
 {
-    constexpr int L = D / 8;   // lanes per row
-    const long long rows = (long long)p.tokens * p.kv_heads * 2;
-    const long long row = (long long)blockIdx.x * (256 / L) + threadIdx.x / L;
-    const int j = threadIdx.x % L;
-    const bool live = row < rows;
-    int token = 0, head = 0, tok = 0;
-    bool is_v = false;
+    const Rows r = rows_of<D>(p);
+    const int j = threadIdx.x % (D / 8);
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
     uint8_t* tile = nullptr;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) {
-        // K rows of a token, then its V rows
-        token = (int)(row / (2 * p.kv_heads));
-        const int r = (int)(row - (long long)token * 2 * p.kv_heads);
-        is_v = r >= p.kv_heads;
-        head = is_v ? r - p.kv_heads : r;
-        const uint16_t* src = is_v ? (const uint16_t*)p.v + token * p.v_token + head * p.v_head
-                                   : (const uint16_t*)p.k + token * p.k_token + head * p.k_head;
-        raw = *reinterpret_cast<const uint4*>(src + 8 * j);
-        tile = tile_of(p, token, head, D, &tok);
+    int tok = 0;
+    if (r.live) {
+        k = __ldg(reinterpret_cast<const uint4*>((const uint16_t*)p.k + r.token * p.k_token + r.head * p.k_head + 8 * j));
+        v = __ldg(reinterpret_cast<const uint4*>((const uint16_t*)p.v + r.token * p.v_token + r.head * p.v_head + 8 * j));
+        tile = tile_of(p, r.token, r.head, D, &tok);
     }
-    float x[8];
-    unpack2<DTYPE>(raw.x, x[0], x[1]);
-    unpack2<DTYPE>(raw.y, x[2], x[3]);
-    unpack2<DTYPE>(raw.z, x[4], x[5]);
-    unpack2<DTYPE>(raw.w, x[6], x[7]);
-    float lo = 0.0f, hi = 0.0f;
-    bool fine = true;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        fine = fine && isfinite(x[i]);
-    }
-    int odd = fine ? 0 : 1;
-#pragma unroll
-    for (int d = L / 2; d > 0; d >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-        odd |= __shfl_xor_sync(0xffffffffu, odd, d);
-    }
+    const Quantised a = quantise<D, DTYPE>(k), b = quantise<D, DTYPE>(v);
     if (tile == nullptr) return;
-    const __half s = odd ? __ushort_as_half(0x7fff)
-                         : __float2half_rn(fminf(__fdiv_rn(__fsub_rn(hi, lo), 15.0f), 65504.0f));
-    const float sf = __half2float(s);
-    const float inv = !odd && sf > 0.0f ? __frcp_rn(sf) : 0.0f;
-    const float z = odd ? 0.0f : fminf(rintf(__fmul_rn(-lo, inv)), 15.0f);
-    uint32_t code[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float c = odd ? 0.0f : fminf(fmaxf(rintf(__fmul_rn(x[i], inv)) + z, 0.0f), 15.0f);
-        code[i] = (uint32_t)c;
-    }
-    const uint32_t w0 = code[0] | code[1] << 4 | code[2] << 8 | code[3] << 12;
-    const uint32_t w1 = code[4] | code[5] << 4 | code[6] << 8 | code[7] << 12;
-    if (is_v) {
-        // d = 8j .. 8j+7 of token 8h + 2c + e: two 16-bit words
-        constexpr int PER = D / 8;   // d per n
-        const int n = 8 * j / PER, w = (8 * j % PER) / 4;
-        const int h = tok >> 3, c = (tok & 7) >> 1, e = tok & 1;
-        uint16_t* dst = reinterpret_cast<uint16_t*>(tile + kv4_v_off(D)) + ((((h * 8 + n) * 4 + c) * (D / 32) + w) * 2 + e);
-        dst[0] = (uint16_t)w0;
-        dst[2] = (uint16_t)w1;
-    } else {
-        *reinterpret_cast<uint32_t*>(tile + tok * (D / 2) + 4 * j) = w0 | w1 << 16;
-    }
-    if (j == 0) {
-        *reinterpret_cast<__half*>(tile + (is_v ? kv4_v_scale_off(D) : kv4_k_scale_off(D)) + 2 * tok) = s;
-        tile[(is_v ? kv4_v_zero_off(D) : kv4_k_zero_off(D)) + tok] = (uint8_t)z;
+    *reinterpret_cast<uint32_t*>(tile + tok * (D / 2) + 4 * j) = a.w0 | a.w1 << 16;
+    uint16_t* const dst = reinterpret_cast<uint16_t*>(tile + kv4_v_off(D)) + v_word<D>(tok, j);
+    dst[0] = (uint16_t)b.w0;
+    dst[2] = (uint16_t)b.w1;
+    if (j < 2) {   // lane 0 writes K's scale and zero-point, lane 1 V's
+        *reinterpret_cast<__half*>(tile + (j ? kv4_v_scale_off(D) : kv4_k_scale_off(D)) + 2 * tok) = j ? b.scale : a.scale;
+        tile[(j ? kv4_v_zero_off(D) : kv4_k_zero_off(D)) + tok] = (uint8_t)(j ? b.zero : a.zero);
     }
 }
 
@@ -241,52 +282,45 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowsParams p)
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4RowsParams p)
 {
-    constexpr int L = D / 8;
-    const long long rows = (long long)p.tokens * p.kv_heads * 2;
-    const long long row = (long long)blockIdx.x * (256 / L) + threadIdx.x / L;
-    const int j = threadIdx.x % L;
-    if (row >= rows) return;
-    const int token = (int)(row / (2 * p.kv_heads));
-    const int r = (int)(row - (long long)token * 2 * p.kv_heads);
-    const bool is_v = r >= p.kv_heads;
-    const int head = is_v ? r - p.kv_heads : r;
+    const Rows r = rows_of<D>(p);
+    const int j = threadIdx.x % (D / 8);
+    if (!r.live) return;
     int tok = 0;
-    const uint8_t* tile = tile_of(p, token, head, D, &tok);
-    uint32_t w = 0;
-    float s = 0.0f, z = 0.0f;
+    const uint8_t* tile = tile_of(p, r.token, r.head, D, &tok);
+    uint32_t w[2] = {0, 0};
+    float s[2] = {0.0f, 0.0f}, z[2] = {0.0f, 0.0f};
     if (tile) {
-        if (is_v) {
-            constexpr int PER = D / 8;
-            const int n = 8 * j / PER, wi = (8 * j % PER) / 4;
-            const int h = tok >> 3, c = (tok & 7) >> 1, e = tok & 1;
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(tile + kv4_v_off(D)) +
-                                  ((((h * 8 + n) * 4 + c) * (D / 32) + wi) * 2 + e);
-            w = src[0] | (uint32_t)src[2] << 16;
-        } else {
-            w = *reinterpret_cast<const uint32_t*>(tile + tok * (D / 2) + 4 * j);
-        }
-        s = __half2float(*reinterpret_cast<const __half*>(tile + (is_v ? kv4_v_scale_off(D) : kv4_k_scale_off(D)) + 2 * tok));
-        z = (float)tile[(is_v ? kv4_v_zero_off(D) : kv4_k_zero_off(D)) + tok];
+        w[0] = *reinterpret_cast<const uint32_t*>(tile + tok * (D / 2) + 4 * j);
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(tile + kv4_v_off(D)) + v_word<D>(tok, j);
+        w[1] = src[0] | (uint32_t)src[2] << 16;
+        s[0] = __half2float(*reinterpret_cast<const __half*>(tile + kv4_k_scale_off(D) + 2 * tok));
+        s[1] = __half2float(*reinterpret_cast<const __half*>(tile + kv4_v_scale_off(D) + 2 * tok));
+        z[0] = (float)tile[kv4_k_zero_off(D) + tok];
+        z[1] = (float)tile[kv4_v_zero_off(D) + tok];
     }
-    float x[8];
+    const long long at = ((long long)r.token * p.kv_heads + r.head) * D + 8 * j;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = ((float)((w >> (4 * i)) & 15u) - z) * s;
-    const long long at = ((long long)token * p.kv_heads + head) * D + 8 * j;
-    if constexpr (DTYPE == W4A16_FP32) {
-        float4* dst = reinterpret_cast<float4*>((float*)(is_v ? p.v_out : p.k_out) + at);
-        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-        *reinterpret_cast<uint4*>((uint16_t*)(is_v ? p.v_out : p.k_out) + at) =
-            make_uint4(pack2<DTYPE>(x[0], x[1]), pack2<DTYPE>(x[2], x[3]), pack2<DTYPE>(x[4], x[5]),
-                       pack2<DTYPE>(x[6], x[7]));
+    for (int o = 0; o < 2; ++o) {
+        void* const out = o ? p.v_out : p.k_out;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)   // 2^23 + code, exact, less 2^23 + zero
+            x[i] = __fmul_rn(__fsub_rn(__uint_as_float(0x4b000000u | (w[o] >> (4 * i) & 15u)), z[o] + 8388608.0f), s[o]);
+        if constexpr (DTYPE == W4A16_FP32) {
+            float4* dst = reinterpret_cast<float4*>((float*)out + at);
+            dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+            dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            *reinterpret_cast<uint4*>((uint16_t*)out + at) =
+                make_uint4(pack2<DTYPE>(x[0], x[1]), pack2<DTYPE>(x[2], x[3]), pack2<DTYPE>(x[4], x[5]), pack2<DTYPE>(x[6], x[7]));
+        }
     }
 }
 
 unsigned row_blocks(const Kv4RowsParams& p)
 {
     const long long per = 256 / (p.head_dim / 8);
-    return (unsigned)(((long long)p.tokens * p.kv_heads * 2 + per - 1) / per);
+    return (unsigned)(((long long)p.tokens * p.kv_heads + per - 1) / per);
 }
 
 }  // namespace
