@@ -101,6 +101,15 @@ at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Tensor& li
     return at::empty(size, at::TensorOptions().dtype(type).device(like.device()));
 }
 
+// A contiguous tensor over part of another's memory: outputs that come together share one
+// allocation (an allocation and its release take 1 us, as long as the kernels of a small call).
+at::Tensor part(const at::Tensor& base, int64_t byte, at::IntArrayRef size, at::ScalarType type) {
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(), c10::scalarTypeToTypeMeta(type));
+    impl->set_storage_offset(byte / (int64_t)c10::elementSize(type));
+    impl->set_sizes_contiguous(size);
+    return at::Tensor(std::move(impl));
+}
+
 PyObject* tuple(std::initializer_list<at::Tensor> list) {
     PyObject* r = PyTuple_New((Py_ssize_t)list.size());
     if (!r) return nullptr;
@@ -124,13 +133,17 @@ PyObject* tables(PyObject* const* a) {
     const int page_size = integer(a[4], "page_size"), max_tokens = integer(a[5], "max_tokens");
     if (max_tokens < 0) refuse("max_tokens is negative");
     const int32_t* taken = optional_vector<int32_t>(a[6], at::kInt, 1, "taken must be a contiguous int32 CUDA tensor of one element");
-    at::Tensor slots = empty({max_tokens}, at::kLong, seq), positions = empty({max_tokens}, at::kInt, seq);
-    at::Tensor starts = empty({batch + 1}, at::kInt, seq), after = empty({1}, at::kInt, seq);
-    check(w4a16_kv4_tables(seq_at, new_at, batch, free_at, n_free, taken, after.data_ptr<int32_t>(), table.data_ptr<int32_t>(),
-                           count(table.size(1), "too many pages"), page_size, slots.data_ptr<int64_t>(),
-                           positions.data_ptr<int32_t>(), max_tokens, starts.data_ptr<int32_t>(), stream_of(a[7], seq)),
+    const int64_t at_positions = 8 * (int64_t)max_tokens, at_starts = at_positions + 4 * (int64_t)max_tokens;
+    const int64_t at_after = at_starts + 4 * ((int64_t)batch + 1);
+    at::Tensor all = empty({at_after + 4}, at::kByte, seq);
+    char* const to = static_cast<char*>(all.data_ptr());
+    check(w4a16_kv4_tables(seq_at, new_at, batch, free_at, n_free, taken, reinterpret_cast<int32_t*>(to + at_after),
+                           table.data_ptr<int32_t>(), count(table.size(1), "too many pages"), page_size,
+                           reinterpret_cast<int64_t*>(to), reinterpret_cast<int32_t*>(to + at_positions), max_tokens,
+                           reinterpret_cast<int32_t*>(to + at_starts), stream_of(a[7], seq)),
           "w4a16_kv4_tables");
-    return tuple({slots, positions, starts, after});
+    return tuple({part(all, 0, {max_tokens}, at::kLong), part(all, at_positions, {max_tokens}, at::kInt),
+                  part(all, at_starts, {(int64_t)batch + 1}, at::kInt), part(all, at_after, {1}, at::kInt)});
 }
 
 // (k, v, slots, cache, page_size, stream)
@@ -159,11 +172,13 @@ PyObject* read(PyObject* const* a) {
     const int64_t* slots = vector<int64_t>(a[1], at::kLong, -1, "slots must be a contiguous int64 CUDA tensor");
     const int tokens = count(THPVariable_Unpack(a[1]).size(0), "too many slots");
     const at::ScalarType type = dtype == W4A16_FP16 ? at::kHalf : dtype == W4A16_BF16 ? at::kBFloat16 : at::kFloat;
-    at::Tensor k = empty({tokens, c.heads, c.dim}, type, c.t), v = empty({tokens, c.heads, c.dim}, type, c.t);
-    check(w4a16_kv4_read(c.t.data_ptr<uint8_t>(), c.pages, slots, k.data_ptr(), v.data_ptr(), tokens, c.heads, c.dim,
-                         page_size, dtype, stream_of(a[4], c.t)),
+    at::Tensor all = empty({2, tokens, c.heads, c.dim}, type, c.t);
+    const int64_t half = (int64_t)all.nbytes() / 2;
+    char* const to = static_cast<char*>(all.data_ptr());
+    check(w4a16_kv4_read(c.t.data_ptr<uint8_t>(), c.pages, slots, to, to + half, tokens, c.heads, c.dim, page_size, dtype,
+                         stream_of(a[4], c.t)),
           "w4a16_kv4_read");
-    return tuple({k, v});
+    return tuple({part(all, 0, {tokens, c.heads, c.dim}, type), part(all, half, {tokens, c.heads, c.dim}, type)});
 }
 
 // (q, cache, block_table, seq_lens, starts, page_size, max_q, scale, window, out, return_lse, workspace, stream)
@@ -224,11 +239,12 @@ PyObject* sample(PyObject* const* a) {
     const int32_t* top_k = optional_vector<int32_t>(a[3], at::kInt, batch, "top_k must be a contiguous int32 CUDA tensor [batch]");
     const float* top_p = optional_vector<float>(a[4], at::kFloat, batch, "top_p must be a contiguous float32 CUDA tensor [batch]");
     const float* min_p = optional_vector<float>(a[5], at::kFloat, batch, "min_p must be a contiguous float32 CUDA tensor [batch]");
-    at::Tensor token = empty({batch}, at::kInt, x), prob = empty({batch}, at::kFloat, x);
-    check(w4a16_sample(x.data_ptr(), x.stride(0) > vocab ? x.stride(0) : vocab, u, temperature, top_k, top_p, min_p,
-                       token.data_ptr<int32_t>(), prob.data_ptr<float>(), batch, vocab, dtype, stream_of(a[6], x)),
+    at::Tensor all = empty({2, batch}, at::kInt, x);
+    int32_t* const to = all.data_ptr<int32_t>();
+    check(w4a16_sample(x.data_ptr(), x.stride(0) > vocab ? x.stride(0) : vocab, u, temperature, top_k, top_p, min_p, to,
+                       reinterpret_cast<float*>(to + batch), batch, vocab, dtype, stream_of(a[6], x)),
           "w4a16_sample");
-    return tuple({token, prob});
+    return tuple({part(all, 0, {batch}, at::kInt), part(all, 4 * (int64_t)batch, {batch}, at::kFloat)});
 }
 
 template <PyObject* (*F)(PyObject* const*), int N>

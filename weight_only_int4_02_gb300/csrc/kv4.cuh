@@ -79,7 +79,6 @@ struct Kv4AttnParams {
     int few_rows;                // requests of at most this many rows a KV head are the stream-K kernel's
     int bf16;
 };
-constexpr int kKv4MaxRows = 16;  // rows (query, head) of the widest row tile
 cudaError_t setup_kv4();
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int head_dim, int max_q, int sms, cudaStream_t stream);
 // The tcgen05 kernel, for requests of more than few_rows rows.

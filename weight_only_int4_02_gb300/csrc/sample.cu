@@ -23,7 +23,7 @@
 //    holds the cut, and the tokens of that bin are listed and cut by one CTA;
 //  - a larger k, or a bin with more tokens than a list holds (many equal logits): histograms
 //    of counts and weights over the keys inside the bin, ten bits at a time.
-// A list is never sorted: the entry at which a running count or weight crosses a limit is
+// A list is never sorted: up to 128 entries are compared with each other; of more, the entry at which a running count or weight crosses a limit is
 // found by histograms over its keys, which are all different (logit, then index), and so is the
 // drawn token of a top-k row (keys: indices). Every other row sums the kept weights of each
 // warp's segment, in index order, and the segment that holds the drawn place looks it up.
@@ -52,6 +52,10 @@ constexpr float kSpan = 22.2f;           // exp(-22.2) * 2^31 rounds to 0
 constexpr int kListMax = 2048;           // tokens of a list
 constexpr int kListMine = kListMax / 2;  // of them, one CTA's share at most
 constexpr int kListPer = kListMax / kThreads;
+constexpr int kIndexBits = 18;
+constexpr uint32_t kIndexTop = (1u << kIndexBits) - 1u;
+static_assert(kSampleMaxVocab <= 1 << kIndexBits, "an entry holds a token's index");
+constexpr int kFew = kThreads / 4;       // entries that are compared with each other, four threads an entry
 constexpr int kGroups = 4;               // groups of a thread's tokens, each with its maximum
 
 struct Histogram {
@@ -61,7 +65,7 @@ struct Histogram {
 struct Shared {
     Histogram bins;                      // over (m - x) r
     Histogram keys;                      // over keys
-    unsigned long long list[kListMine];  // key, then ~index: greater is ranked before
+    unsigned long long list[kListMine];  // key, then the index from the top of kIndexBits down: greater is ranked before
     unsigned long long best[kWarps];
     unsigned long long range;            // what this CTA shows to the cluster: least and greatest key,
     float top;                           // its maximum,
@@ -173,9 +177,9 @@ __device__ __forceinline__ void clear(Histogram& h)
 
 __device__ __forceinline__ void add_mass(Histogram& h, int bin, uint32_t w)
 {
-    if (w & 2047u) atomicAdd(&h.part[0][bin], w & 2047u);
-    if (w >> 11 & 2047u) atomicAdd(&h.part[1][bin], w >> 11 & 2047u);
-    if (w >> 22) atomicAdd(&h.part[2][bin], w >> 22);
+    atomicAdd(&h.part[0][bin], w & 2047u);
+    if (w >= 1u << 11) atomicAdd(&h.part[1][bin], w >> 11 & 2047u);
+    if (w >= 1u << 22) atomicAdd(&h.part[2][bin], w >> 22);
 }
 
 __device__ __forceinline__ unsigned long long mass_of(uint32_t a, uint32_t b, uint32_t c)
@@ -511,10 +515,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     auto list_it = [&](int v, float x) {
         const uint32_t at = atomicAdd(&sh.listed, 1u);
         if (at < kListMine)
-            sh.list[at] = (unsigned long long)key_of<DTYPE>(x) << 32 | (0xffffffffu - (uint32_t)(first + v));
+            sh.list[at] = (unsigned long long)key_of<DTYPE>(x) << kIndexBits | (kIndexTop - (uint32_t)(first + v));
     };
-    auto logit_of = [](unsigned long long e) { return float_of<DTYPE>((uint32_t)(e >> 32)); };
-    auto token_of = [](unsigned long long e) { return (int)(0xffffffffu - (uint32_t)e); };
+    auto logit_of = [](unsigned long long e) { return float_of<DTYPE>((uint32_t)(e >> kIndexBits)); };
+    auto token_of = [](unsigned long long e) { return (int)(kIndexTop - ((uint32_t)e & kIndexTop)); };
     // The cluster's lists in the first CTA's registers, kListPer entries a thread (0: none), with their weights.
     // Returns the number of entries, or -1 (everywhere) where they do not fit.
     unsigned long long key[kListPer];
@@ -570,7 +574,48 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 });
             const int n = gather();
             if (n >= 0) {
-                if (rank == 0) {
+                if (rank == 0 && n <= kFew) {
+                    // few entries: each counts and weighs those ranked before it, then the kept ones of lower index
+                    unsigned long long* const keys = sh.list;   // the lists have been gathered
+                    uint32_t* const ws = sh.keys.cnt;
+                    __syncthreads();
+                    if (tid < n) {
+                        keys[tid] = key[0];
+                        ws[tid] = w[0];
+                    }
+                    __syncthreads();
+                    const int i = tid >> 2;
+                    const unsigned long long own = i < n ? keys[i] : 0ull;
+                    const uint32_t own_w = i < n ? ws[i] : 0u;
+                    int ahead = 0;
+                    unsigned long long before = 0;
+                    for (int j = tid & 3; j < n; j += 4)
+                        if (keys[j] > own) {
+                            ++ahead;
+                            before += ws[j];
+                        }
+#pragma unroll
+                    for (int d = 1; d < 4; d *= 2) {
+                        ahead += __shfl_xor_sync(0xffffffffu, ahead, d);
+                        before += __shfl_xor_sync(0xffffffffu, before, d);
+                    }
+                    bool keep = i < n && ahead < k;
+                    unsigned long long total = block_sum(keep && (tid & 3) == 0 ? own_w : 0u);
+                    const double limit = (double)total * (double)top_p;
+                    const float x = logit_of(own);
+                    keep = keep && (ahead == 0 || !need_p || (double)before < limit) && (ahead == 0 || exp_of(x, r) >= r.min_p || x == r.top);
+                    total = block_sum(keep && (tid & 3) == 0 ? own_w : 0u);
+                    if (!keep && i < n) ws[i] = 0u;
+                    __syncthreads();
+                    const unsigned long long target = target_of(total);
+                    before = 0;
+                    for (int j = tid & 3; j < n; j += 4)
+                        if (((uint32_t)keys[j] & kIndexTop) > ((uint32_t)own & kIndexTop)) before += ws[j];
+#pragma unroll
+                    for (int d = 1; d < 4; d *= 2) before += __shfl_xor_sync(0xffffffffu, before, d);
+                    if (keep && (tid & 3) == 0 && target >= before && target < before + own_w)
+                        result(token_of(own), (double)own_w / (double)total);
+                } else if (rank == 0) {
                     // the k-th entry, the entry at which top-p's limit is passed, and the drawn one among the kept
                     if (n > k) {
                         pick(sh, key, w, 0ull, [kk](uint32_t c, unsigned long long) { return c >= kk; });
@@ -602,9 +647,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                         for (int i = 0; i < kListPer; ++i) sum += w[i];
                         total = block_sum(sum);
                     }
-                    // by index now: the low halves, greatest first, are ascending indices
+                    // by index now: the low bits, greatest first, are ascending indices (one bit on top, as 0 is no entry)
 #pragma unroll
-                    for (int i = 0; i < kListPer; ++i) key[i] &= 0xffffffffull;
+                    for (int i = 0; i < kListPer; ++i) key[i] = key[i] ? 1ull << kIndexBits | (key[i] & kIndexTop) : 0ull;
                     const unsigned long long target = target_of(total);
                     pick(sh, key, w, 0ull, [target](uint32_t, unsigned long long m) { return m > target; });
                     if (tid == 0) result(token_of(sh.picked), (double)sh.picked_weight / (double)total);
@@ -827,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     } else if (need_p) {
         each(weightless, [&](int, float x) {
             const uint32_t weight = weight_of(exp_of(x, r));
-            if (weight) add_mass(sh.bins, bin_of(x, r), weight);
+            if (weight) add_mass(sh.bins, (int)place(x), weight);   // a token that weighs lies inside the bins
         });
         // the bin past which the weight before a token is no longer below top_p times the whole
         search<true>(cl, sh, sh.bins, 0u, 0ull, [top_p](uint32_t, unsigned long long m, unsigned long long all) {
