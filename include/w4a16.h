@@ -543,6 +543,13 @@ w4a16_status w4a16_kv4_attention(const void* q, int64_t q_token_stride, int64_t 
                                  float scale, int window, int dtype, void* workspace,
                                  size_t ws_bytes, w4a16_stream_t stream);
 
+/* Forces the kernel of w4a16_kv4_attention, for tests and ablations: 0 = automatic (the
+ * default), 1 = the stream-K kernel for every request, 2 = the tcgen05 kernel for every
+ * request of more than 32 rows (query token, head of a group) of a call whose max_q says
+ * that there may be one. Applies to every later call in the process. Returns the previous
+ * setting, or -1 (nothing changed) for another value. */
+int w4a16_kv4_force_path(int path);
+
 /*
  * Samples one token per row. With m the row's maximum and e(x) = exp((x - m) / T) in
  * FP32, a token weighs rint(2^31 e(x)), a whole number, so that sums are exact and do not

@@ -1,5 +1,6 @@
-"""Attention of prompt chunks over the 4-bit cache (the tcgen05 kernel: more than 32 rows a KV head)
-against its definition in 64 bits, over several row tiles and blocks of cached tokens.
+"""Attention of prompt chunks over the 4-bit cache by the tcgen05 kernel (forced where the
+dispatcher would leave so few rows to the stream-K kernel) against its definition in 64 bits, over
+several row tiles and blocks of cached tokens.
 
 Tolerance, beside what test_kv4_gpu.py derives for scores and sums: probabilities times V's scale are
 rounded to binary16 once (2^-12 each side of a half step: a relative 2^-11 of sum p |v| bounds it) when
@@ -18,6 +19,10 @@ pytestmark = pytest.mark.gpu
 def _gpu():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
+    from weight_only_int4_02_gb300 import w4a16
+    before = w4a16.kv4_force_path(2)
+    yield
+    w4a16.kv4_force_path(before)
 
 
 def value_mass(q, cache, table, seq, starts, page, scale, window):
@@ -124,6 +129,14 @@ def test_missing_pages_and_poisoned_tokens():
         cache = good
         assert torch.isnan(got[70:]).all() and torch.equal(got[:70], out[:70])
         assert torch.isnan(got_lse[70:]).all() if which == 0 else torch.equal(got_lse, lse)
+
+
+@pytest.mark.parametrize("path", [0, 1, 2])
+def test_every_path_serves_a_batch_of_prompts_and_decodes(path):
+    from weight_only_int4_02_gb300 import w4a16
+    w4a16.kv4_force_path(path)
+    # 7500 rows over eight query heads: the dispatcher's own choice is the tcgen05 kernel with the stream-K one
+    run_and_check(batch_of([940, 300, 65, 0], [900, 1, 38, 1], 2, 4, 128, 64, "bfloat16", 3), 64)
 
 
 def test_repeats_are_the_same_and_strided_views_too():

@@ -80,6 +80,10 @@ def test_attention_refusals(lib, ptr):
         assert lib.w4a16_kv4_attention(*args) == w.OK
 
 
+def test_force_path_takes_its_values(lib):
+    assert lib.w4a16_kv4_force_path(2) == 0 and lib.w4a16_kv4_force_path(3) == -1 and lib.w4a16_kv4_force_path(0) == 2
+
+
 def test_sample_refusals(lib, ptr):
     from weight_only_int4_02_gb300 import w4a16 as w
     p = ptr[1]

@@ -7,9 +7,13 @@
 
 #include <math.h>
 
+#include <atomic>
+
 namespace {
 
 using namespace w4a16;
+
+std::atomic<int> g_kv4_path{0};   // forced attention kernel, for tests and ablations
 
 constexpr float kLog2E = 1.44269504088896340736f;
 
@@ -192,7 +196,13 @@ w4a16_status w4a16_kv4_attention(const void* q, int64_t q_token_stride, int64_t 
     p.table_cols = table_cols;
     p.window = window;
     p.bf16 = dtype == W4A16_BF16;
-    return report_cuda(launch_kv4_attention(p, head_dim, max_q, dev.sms, stream));
+    return report_cuda(launch_kv4_attention(p, head_dim, max_q, g_kv4_path.load(), dev.sms, stream));
+}
+
+int w4a16_kv4_force_path(int path)
+{
+    if (path < 0 || path > 2) return -1;
+    return g_kv4_path.exchange(path);
 }
 
 w4a16_status w4a16_sample(const void* logits, int64_t row_stride, const float* u, const float* temperature,

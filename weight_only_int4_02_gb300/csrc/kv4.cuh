@@ -80,7 +80,8 @@ struct Kv4AttnParams {
     int bf16;
 };
 cudaError_t setup_kv4();
-cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int head_dim, int max_q, int sms, cudaStream_t stream);
+// path: 0 as measured, 1 the stream-K kernel, 2 the tcgen05 kernel for every request of more than 32 rows.
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int head_dim, int max_q, int path, int sms, cudaStream_t stream);
 // The tcgen05 kernel, for requests of more than few_rows rows.
 cudaError_t setup_kv4_prompt();
 cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, int head_dim, cudaStream_t stream);

@@ -221,12 +221,19 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
         const int pos = at > kOverhead ? at - kOverhead : 0, take = end - kOverhead - pos;
         const int head = (int)(seg / r.tiles), rt = (int)(seg - (long long)head * r.tiles);
         const int row0 = rt * ROWS;
+        // a unit needs no mask if it lies below the first row's position and inside the last row's window;
+        // units that no row of the tile sees are left out: [first, last) of the run are looked at
+        const int last_row = (row0 + ROWS < r.rows ? row0 + ROWS : r.rows) - 1;
+        const int pos_min = r.seq - r.nq + row0 / p.group, pos_max = r.seq - r.nq + last_row / p.group;
+        const int seen = pos_max >= r.base ? (pos_max - r.base) / kUnit + 1 : 0;
+        const int low = p.window > 0 && pos_min - p.window + 1 > r.base ? (pos_min - p.window + 1 - r.base) / kUnit : 0;
+        const int first = low > pos ? low : pos, last = seen < pos + take ? seen : pos + take;
 
         // ---- copies: a batch of 16 units at a time, lanes 2j and 2j + 1 own the tiles of its unit j
         const int32_t* const trow = p.table + (long long)b * p.table_stride;
-        const int mine_n = (take - warp + kWarps - 1) / kWarps;   // units of this warp: pos + warp, + kWarps, ...
+        const int mine_n = last > first + warp ? (last - first - warp + kWarps - 1) / kWarps : 0;   // units of this warp: first + warp, + kWarps, ...
         auto page_of = [&](int k) {   // page of this lane's tile of the batch from unit k on, or -1
-            const int t = pos + warp + (k + (lane >> 1)) * kWarps;
+            const int t = first + warp + (k + (lane >> 1)) * kWarps;
             const int tile = ((r.base + t * kUnit) >> 4) + (lane & 1);
             return (k + (lane >> 1) < mine_n && tile * kKv4Tile < r.seq) ? trow[tile >> tpp_shift] : -1;
         };
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
             if (k_issue >= mine_n || dead) return;
             const int j = k_issue & 15;
             if (j == 0) {
-                const int t = pos + warp + (k_issue + (lane >> 1)) * kWarps;
+                const int t = first + warp + (k_issue + (lane >> 1)) * kWarps;
                 const int in_page = (((r.base + t * kUnit) >> 4) + (lane & 1)) & ((1 << tpp_shift) - 1);
                 const bool ok = page >= 0 && page < p.pages;
                 present = __ballot_sync(0xffffffffu, ok);
@@ -336,10 +343,6 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                 row_pos[g][i] = rr < r.rows ? r.seq - r.nq + rr / p.group : -1;
             }
         }
-        // a unit needs no mask if it lies below the first row's position and inside the last row's window
-        const int last_row = (row0 + ROWS < r.rows ? row0 + ROWS : r.rows) - 1;
-        const int pos_min = r.seq - r.nq + row0 / p.group, pos_max = r.seq - r.nq + last_row / p.group;
-
         float m[NR][2], l[NR][2], zs[NR][2], o[NR][2 * W][4];
         int ev = -40;   // V's scales seen so far are at most 2^ev
 #pragma unroll
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
         }
 
 #pragma unroll 1
-        for (int t = pos + warp; t < pos + take && !dead; t += kWarps) {
+        for (int t = first + warp; t < last && !dead; t += kWarps) {
             if (!wait_warp(smem_addr(&sh.bar[warp][s_use]), phase, ctl)) {
                 dead = true;
                 break;
@@ -735,20 +738,27 @@ cudaError_t setup_kv4()
     return setup_kv4_prompt();
 }
 
-// Requests of up to kFewRows rows go to the stream-K kernel, longer ones to the tcgen05
-// kernel; which is which is known on the device, so a batch that may hold both gets both.
+// The tcgen05 kernel takes requests of more than kFewRows rows a KV head where the batch's rows (query
+// tokens times query heads) fill the GPU with its tiles of 256; which request is which is known on
+// the device, so such a batch gets both kernels. With fewer rows the stream-K kernel takes everything:
+// it cuts the cached tokens too. Measured for one request, D = 128, tcgen05 and stream-K in us:
+// 2000 rows over 8000 tokens 170 / 55; 8192 over 4000 96 / 98; 16384 over 4000 97 / 178; 8400
+// over 300 21 / 31; 800 over 1000 32 / 20. D = 64: 8192 over 4000 89 / 67.
 constexpr int kFewRows = 32;
+constexpr long long prompt_rows(int head_dim) { return head_dim == 128 ? 7168 : 10752; }
 
-cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_q, int sms, cudaStream_t stream)
+cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_q, int path, int sms, cudaStream_t stream)
 {
     Kv4AttnParams p = in;
     const long long rows = (long long)max_q * p.group;
-    p.few_rows = rows <= kFewRows ? INT_MAX : kFewRows;   // max_q may be too small: then this kernel serves all
+    const bool prompt = rows > kFewRows && path != 1 &&
+                        (path == 2 || (long long)p.tokens * p.q_heads >= prompt_rows(head_dim));
+    p.few_rows = prompt ? kFewRows : INT_MAX;
     const bool wide = rows > 8;
     cudaError_t e;
     if (head_dim == 128) e = wide ? Launch<128, 2>::run(p, sms, stream) : Launch<128, 1>::run(p, sms, stream);
     else e = wide ? Launch<64, 2>::run(p, sms, stream) : Launch<64, 1>::run(p, sms, stream);
-    if (e != cudaSuccess || rows <= kFewRows) return e;
+    if (e != cudaSuccess || !prompt) return e;
     return launch_kv4_prompt(p, head_dim, stream);
 }
 

@@ -24,7 +24,7 @@ EXPORTS = ["w4a16_layout_version", "w4a16_status_string", "w4a16_last_cuda_error
            "w4a16_w8_gemm", "w4a16_bf16_gemm", "w4a16_sp_packed_bytes", "w4a16_sp_pack", "w4a16_sp_gemm",
            "w4a16_selftest_wait_timeout", "w4a16_force_path", "w4a16_set_wait_limit_ns", "w4a16_gemm_strided",
            "w4a16_kv4_page_bytes", "w4a16_kv4_tables", "w4a16_kv4_append", "w4a16_kv4_read",
-           "w4a16_kv4_workspace_bytes", "w4a16_kv4_attention", "w4a16_sample"]
+           "w4a16_kv4_workspace_bytes", "w4a16_kv4_attention", "w4a16_kv4_force_path", "w4a16_sample"]
 
 ACTIVATIONS = {"none": 0, "silu": 1, "relu": 2}
 
@@ -112,6 +112,8 @@ def lib():
         L.w4a16_kv4_attention.argtypes = [P, L64, L64, P, I, P, L64, I, P, P, P, L64, L64, P, I, I, I, I, I, I, I, F, I,
                                           I, P, Z, P]
         L.w4a16_kv4_attention.restype = I
+        L.w4a16_kv4_force_path.argtypes = [I]
+        L.w4a16_kv4_force_path.restype = I
         L.w4a16_sample.argtypes = [P, L64, P, P, P, P, P, P, P, I, I, I, P]
         L.w4a16_sample.restype = I
         _lib = L
@@ -549,6 +551,15 @@ def kv4_attention(q, cache, block_table, seq_lens, starts, page_size, max_q, sca
     return (_module or _torch_module()).kv4_attention(q, cache, block_table, seq_lens, starts, page_size, max_q, scale, window,
                                                       out, return_lse, workspace,
                                                       None if stream is None else stream.cuda_stream)
+
+
+def kv4_force_path(path):
+    """Force kv4_attention's kernel: 0 automatic, 1 stream-K for every request, 2 tcgen05 for
+    every request of more than 32 rows a KV head. Returns the previous setting."""
+    prev = lib().w4a16_kv4_force_path(int(path))
+    if prev < 0:
+        raise W4A16Error(ERR_INVALID_ARG, "w4a16_kv4_force_path(%r)" % (path,))
+    return prev
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
