@@ -367,6 +367,58 @@ __device__ __forceinline__ float float_of(uint32_t key)
                              : __uint_as_float(~(k | ((1u << Elem<DTYPE>::kShift) - 1u)));
 }
 
+// What a row asks for.
+struct Settings {
+    float temp, top_p, min_p;
+    int k;
+    __device__ __forceinline__ bool greedy() const { return !(temp > 0.0f) || k == 1 || !(top_p > 0.0f) || !(min_p <= 1.0f); }
+    __device__ __forceinline__ bool need_k(int vocab) const { return k > 0 && k < vocab; }
+    __device__ __forceinline__ bool need_p() const { return top_p < 1.0f; }
+    // The longest first: a cut without a list of top-k's, the sum of all weights, a list, the maximum.
+    __device__ __forceinline__ int turn(int vocab) const
+    {
+        return greedy() ? 3 : need_k(vocab) ? (k > kListMax / 2 ? 0 : 2) : need_p() ? 0 : 1;
+    }
+};
+
+__device__ __forceinline__ Settings settings_of(const SampleParams& p, int row)
+{
+    return {p.temperature ? p.temperature[row] : 1.0f, p.top_p ? p.top_p[row] : 1.0f, p.min_p ? p.min_p[row] : 0.0f,
+            p.top_k ? p.top_k[row] : 0};
+}
+
+// The row that is number `at` when rows are taken in order of their turns (batches of more than a wave:
+// a long row begun last would leave the GPU waiting for it).
+__device__ __forceinline__ int row_in_turn(const SampleParams& p, Shared& sh, int at)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned long long counts = 0;   // of each turn, sixteen bits
+    for (int i = tid; i < p.batch; i += kThreads) counts += 1ull << (16 * settings_of(p, i).turn(p.vocab));
+    counts = warp_sum(counts);
+    if (lane == 0) sh.best[warp] = counts;
+    __syncthreads();
+    counts = warp_sum(lane < kWarps ? sh.best[lane] : 0ull);
+    int turn = 0;
+    for (; turn < 3 && at >= (int)(counts >> (16 * turn) & 0xffffu); ++turn) at -= (int)(counts >> (16 * turn) & 0xffffu);
+    for (int base = 0; base < p.batch; base += kThreads) {
+        const int i = base + tid;
+        const bool mine = i < p.batch && settings_of(p, i).turn(p.vocab) == turn;
+        const uint32_t bits = __ballot_sync(0xffffffffu, mine);
+        __syncthreads();
+        if (lane == 0) sh.scan_cnt[warp] = __popc(bits);
+        __syncthreads();
+        const uint32_t upto = warp_incl(lane < kWarps ? sh.scan_cnt[lane] : 0u, lane);
+        const int before = (int)__shfl_sync(0xffffffffu, upto, warp > 0 ? warp - 1 : 0) * (warp > 0) + __popc(bits & ((1u << lane) - 1u));
+        if (mine && before == at) sh.bin = i;
+        at -= (int)__shfl_sync(0xffffffffu, upto, kWarps - 1);
+        if (at < 0) break;
+    }
+    __syncthreads();
+    const int row = sh.bin;
+    __syncthreads();
+    return row;
+}
+
 template <int DTYPE>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p)
 {
@@ -375,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     __shared__ __align__(16) Shared sh;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), ctas = (int)cl.num_blocks();
-    const int row = blockIdx.x / ctas;
+    const int row = p.in_turn ? row_in_turn(p, sh, blockIdx.x / ctas) : blockIdx.x / ctas;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     // ---- the slice: places are counted from the 16-byte boundary at or before the row's first logit
@@ -456,12 +508,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             sh.listed = 0;
         }
     }
-    const float temp = p.temperature ? p.temperature[row] : 1.0f;
-    const float top_p = p.top_p ? p.top_p[row] : 1.0f;
-    const int k = p.top_k ? p.top_k[row] : 0;
-    const float u = p.u[row];
+    const Settings s = settings_of(p, row);
+    const float temp = s.temp, top_p = s.top_p, u = p.u[row];
+    const int k = s.k;
     Row r;
-    r.min_p = p.min_p ? p.min_p[row] : 0.0f;
+    r.min_p = s.min_p;
     r.inv = __frcp_rn(temp);
     cl.sync();
     r.top = cl.map_shared_rank(&sh, lane < ctas ? lane : 0)->top;
@@ -479,8 +530,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         return t < total ? t : total - 1;
     };
     const bool none = r.top == -CUDART_INF_F;
-    const bool greedy = !(temp > 0.0f) || k == 1 || !(top_p > 0.0f) || !(r.min_p <= 1.0f);
-    if (none || greedy) {
+    if (none || s.greedy()) {
         // the lowest index of the maximum
         uint32_t at = 0xffffffffu;
         if (!none && mine == r.top)
@@ -506,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     // ---- the cut: kept are logits above cut_x, and those equal to it up to index cut_at
     float cut_x = -CUDART_INF_F;
     int cut_at = -1;
-    const bool need_k = k > 0 && k < p.vocab, need_p = top_p < 1.0f;
+    const bool need_k = s.need_k(p.vocab), need_p = s.need_p();
     const float to_bin = kBins / kSpan;
     // a logit below every one that is at most d below the maximum, whatever the roundings of either side
     auto below = [&](float d) { return r.top <= FLT_MAX ? r.top - d * 1.00001f - 1e-6f * fabsf(r.top) : r.top; };
@@ -966,6 +1016,7 @@ cudaError_t launch_sample(const SampleParams& in, int sms, cudaStream_t stream)
     // (256 x 100003 FP32: 239 us with one CTA a row, 93 with two, 100 with four).
     int ctas = 1;
     while (ctas < kMaxCluster && (long long)p.batch * ctas < 2 * sms && p.vocab / ctas > step) ctas *= 2;
+    p.in_turn = (long long)p.batch * ctas > 2 * sms && p.batch <= 16384;
     p.slice = ((p.vocab + 16 / size + ctas - 1) / ctas + step - 1) / step * step;
     switch (p.dtype) {
         case W4A16_FP32: return launch_one<W4A16_FP32>(p, ctas, stream);

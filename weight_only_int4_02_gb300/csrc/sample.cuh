@@ -20,6 +20,7 @@ struct SampleParams {
     int batch, vocab;
     int dtype;                   // w4a16_dtype
     int slice;                   // elements of a CTA's slice (set by the launch)
+    int in_turn;                 // rows are taken in order of their work, not of their index (set by the launch)
 };
 cudaError_t launch_sample(const SampleParams& p, int sms, cudaStream_t stream);
 
