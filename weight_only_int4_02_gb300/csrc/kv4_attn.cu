@@ -23,6 +23,7 @@
 // and outputs are FP32.
 #include "api_internal.cuh"
 #include "kv4.cuh"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 #include <float.h>
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = lane >> 2, c = lane & 3;
     uint8_t* const ring = smem + warp * A::RING;
+    chained_kernel();
 
     // ---- this CTA's run of units
     long long sum = 0;
@@ -709,8 +711,7 @@ struct Launch {
     static cudaError_t run(const Kv4AttnParams& p, int sms, cudaStream_t stream)
     {
         const int grid = grid_of(sms);
-        kv4_attn_kernel<D, NR><<<grid, kThreads, Attn<D, NR>::SMEM, stream>>>(p);
-        return cudaGetLastError();
+        return launch_chained(kv4_attn_kernel<D, NR>, grid, kThreads, Attn<D, NR>::SMEM, 1, stream, p);
     }
 };
 }  // namespace

@@ -5,6 +5,7 @@
 
 
 #include "kv4.cuh"
+#include "launch.cuh"
 #include "w4a16.h"
 
 namespace w4a16 {
@@ -41,6 +42,7 @@ __device__ __forceinline__ Need need_of(int seq, int fresh_tokens, const Kv4Tabl
 __global__ void __launch_bounds__(kTabWarps * 32) kv4_tables_kernel(const Kv4TablesParams p)
 {
     __shared__ int part[2][kTabWarps], own[2][kTabWarps];
+    chained_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b0 = blockIdx.x * kTabWarps, b = b0 + warp;
     int seq = 0, fresh_tokens = 0;
@@ -256,6 +258,7 @@ __device__ __forceinline__ int v_word(int tok, int j)
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowsParams p)
 {
+    chained_kernel();
     const Rows r = rows_of<D>(p);
     const int j = threadIdx.x % (D / 8);
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
@@ -282,6 +285,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowsParams p)
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4RowsParams p)
 {
+    chained_kernel();
     const Rows r = rows_of<D>(p);
     const int j = threadIdx.x % (D / 8);
     if (!r.live) return;
@@ -328,36 +332,23 @@ unsigned row_blocks(const Kv4RowsParams& p)
 cudaError_t launch_kv4_tables(const Kv4TablesParams& p, cudaStream_t stream)
 {
     const unsigned blocks = p.batch > 0 ? (unsigned)((p.batch - 1) / kTabWarps + 1) : 1u;   // an empty batch still has ends to write
-    kv4_tables_kernel<<<blocks, kTabWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kv4_tables_kernel, blocks, kTabWarps * 32, 0, 1, stream, p);
 }
 
 cudaError_t launch_kv4_append(const Kv4RowsParams& p, cudaStream_t stream)
 {
-    const unsigned g = row_blocks(p);
-    if (p.head_dim == 128) {
-        if (p.dtype == W4A16_BF16) kv4_append_kernel<128, W4A16_BF16><<<g, 256, 0, stream>>>(p);
-        else kv4_append_kernel<128, W4A16_FP16><<<g, 256, 0, stream>>>(p);
-    } else {
-        if (p.dtype == W4A16_BF16) kv4_append_kernel<64, W4A16_BF16><<<g, 256, 0, stream>>>(p);
-        else kv4_append_kernel<64, W4A16_FP16><<<g, 256, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
+    const bool bf = p.dtype == W4A16_BF16;
+    auto* const kernel = p.head_dim == 128 ? (bf ? kv4_append_kernel<128, W4A16_BF16> : kv4_append_kernel<128, W4A16_FP16>)
+                                           : (bf ? kv4_append_kernel<64, W4A16_BF16> : kv4_append_kernel<64, W4A16_FP16>);
+    return launch_chained(kernel, row_blocks(p), 256, 0, 1, stream, p);
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsParams& p, cudaStream_t stream)
 {
-    const unsigned g = row_blocks(p);
-    if (p.head_dim == 128) {
-        if (p.dtype == W4A16_BF16) kv4_read_kernel<128, W4A16_BF16><<<g, 256, 0, stream>>>(p);
-        else if (p.dtype == W4A16_FP16) kv4_read_kernel<128, W4A16_FP16><<<g, 256, 0, stream>>>(p);
-        else kv4_read_kernel<128, W4A16_FP32><<<g, 256, 0, stream>>>(p);
-    } else {
-        if (p.dtype == W4A16_BF16) kv4_read_kernel<64, W4A16_BF16><<<g, 256, 0, stream>>>(p);
-        else if (p.dtype == W4A16_FP16) kv4_read_kernel<64, W4A16_FP16><<<g, 256, 0, stream>>>(p);
-        else kv4_read_kernel<64, W4A16_FP32><<<g, 256, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
+    auto* kernel = p.head_dim == 128 ? kv4_read_kernel<128, W4A16_FP32> : kv4_read_kernel<64, W4A16_FP32>;
+    if (p.dtype == W4A16_BF16) kernel = p.head_dim == 128 ? kv4_read_kernel<128, W4A16_BF16> : kv4_read_kernel<64, W4A16_BF16>;
+    if (p.dtype == W4A16_FP16) kernel = p.head_dim == 128 ? kv4_read_kernel<128, W4A16_FP16> : kv4_read_kernel<64, W4A16_FP16>;
+    return launch_chained(kernel, row_blocks(p), 256, 0, 1, stream, p);
 }
 
 }  // namespace w4a16

@@ -22,6 +22,7 @@
 // O is rescaled only when a row's maximum grew by more than 2^8 (its P stays below 2^15 until then).
 #include "api_internal.cuh"
 #include "kv4.cuh"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 #include <float.h>
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     typename C::Misc& sh = *reinterpret_cast<typename C::Misc*>(smem + C::OFF_MISC);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+    chained_kernel();
     // ---- this CTA's rows: CTAs count KV heads fastest, then row tiles, the last rows of a request
     // (which see the most tokens) first
     const int head = blockIdx.x % p.kv_heads;
@@ -680,8 +682,7 @@ cudaError_t setup_one()
 template <int D, bool BF>
 cudaError_t launch_one(const Kv4AttnParams& p, unsigned grid, cudaStream_t stream)
 {
-    kv4_prompt_kernel<D, BF><<<grid, kThreads, Prompt<D>::SMEM, stream>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kv4_prompt_kernel<D, BF>, grid, kThreads, Prompt<D>::SMEM, 1, stream, p);
 }
 
 }  // namespace

@@ -29,6 +29,7 @@
 // warp's segment, in index order, and the segment that holds the drawn place looks it up.
 // Vectors whose largest logit is below what a pass looks for are skipped, at about one
 // instruction a token; a weight takes about 20.
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "sample.cuh"
 #include "w4a16.h"
@@ -425,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     using T = typename Elem<DTYPE>::T;
     constexpr int VEC = 16 / sizeof(T);
     __shared__ __align__(16) Shared sh;
+    chained_kernel();
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), ctas = (int)cl.num_blocks();
     const int row = p.in_turn ? row_in_turn(p, sh, blockIdx.x / ctas) : blockIdx.x / ctas;
@@ -988,22 +990,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     cl.sync();   // no CTA leaves while another may read its shared memory
 }
 
-template <int DTYPE>
-cudaError_t launch_one(const SampleParams& p, int ctas, cudaStream_t stream)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.batch * ctas));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<DTYPE>, p);
-}
-
 }  // namespace
 
 cudaError_t launch_sample(const SampleParams& in, int sms, cudaStream_t stream)
@@ -1018,10 +1004,11 @@ cudaError_t launch_sample(const SampleParams& in, int sms, cudaStream_t stream)
     while (ctas < kMaxCluster && (long long)p.batch * ctas < 2 * sms && p.vocab / ctas > step) ctas *= 2;
     p.in_turn = (long long)p.batch * ctas > 2 * sms && p.batch <= 16384;
     p.slice = ((p.vocab + 16 / size + ctas - 1) / ctas + step - 1) / step * step;
+    const unsigned grid = (unsigned)(p.batch * ctas);
     switch (p.dtype) {
-        case W4A16_FP32: return launch_one<W4A16_FP32>(p, ctas, stream);
-        case W4A16_FP16: return launch_one<W4A16_FP16>(p, ctas, stream);
-        default: return launch_one<W4A16_BF16>(p, ctas, stream);
+        case W4A16_FP32: return launch_chained(sample_kernel<W4A16_FP32>, grid, kThreads, 0, (unsigned)ctas, stream, p);
+        case W4A16_FP16: return launch_chained(sample_kernel<W4A16_FP16>, grid, kThreads, 0, (unsigned)ctas, stream, p);
+        default: return launch_chained(sample_kernel<W4A16_BF16>, grid, kThreads, 0, (unsigned)ctas, stream, p);
     }
 }
 
