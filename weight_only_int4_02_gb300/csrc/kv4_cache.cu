@@ -28,7 +28,7 @@ struct Need {
 
 __device__ __forceinline__ int pages_of(int tokens, const Kv4TablesParams& p)
 {
-    const int n = tokens <= 0 ? 0 : (tokens - 1) / p.page_size + 1;
+    const int n = tokens <= 0 ? 0 : ((tokens - 1) >> (__ffs(p.page_size) - 1)) + 1;   // a power of two
     return n < p.max_pages ? n : p.max_pages;
 }
 
@@ -105,19 +105,24 @@ __global__ void __launch_bounds__(kTabWarps * 32) kv4_tables_kernel(const Kv4Tab
     int c4 = head + 4 * lane;
     for (; c4 + 3 < p.max_pages; c4 += 128) *reinterpret_cast<int4*>(row + c4) = make_int4(-1, -1, -1, -1);
     for (; c4 < p.max_pages; ++c4) row[c4] = -1;
-    for (int i = lane; i < mine.tokens; i += 32) {
-        const long long at = (long long)start + i;
-        if (at >= p.max_tokens) break;
-        const int pos = seq - mine.tokens + i;
-        long long slot = -1;
-        if (pos >= 0) {
-            const int c = pos / p.page_size;
-            int page = -1;
-            if (c < p.max_pages) page = c >= old ? fresh_page(c) : row[c];
-            if (page >= 0) slot = (long long)page * p.page_size + (pos - c * p.page_size);
+    const int shift = __ffs(p.page_size) - 1;   // a power of two
+    const int count = (long long)p.max_tokens - start < mine.tokens ? p.max_tokens - start : mine.tokens;
+    for (int i0 = lane; i0 < count; i0 += 128) {   // four tokens' pages are looked up together
+        int page[4], pos[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            pos[q] = seq - mine.tokens + i0 + 32 * q;
+            const int c = pos[q] >> shift;
+            page[q] = -1;
+            if (i0 + 32 * q < count && pos[q] >= 0 && c < p.max_pages) page[q] = c >= old ? fresh_page(c) : row[c];
         }
-        p.slots[at] = slot;
-        p.positions[at] = pos;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (i0 + 32 * q >= count) break;
+            const long long at = (long long)start + i0 + 32 * q;
+            p.slots[at] = page[q] >= 0 ? (long long)page[q] << shift | (pos[q] & (p.page_size - 1)) : -1;
+            p.positions[at] = pos[q];
+        }
     }
 }
 
