@@ -2,7 +2,7 @@
 // mathematics of kv4_attn.cu on the tcgen05 tensor cores.
 //
 // A CTA owns 256 rows (query token, query head of the group) of one request's KV head, as
-// two tiles of 128, and walks the cached tokens in blocks of 128:
+// two tiles of 128, and walks the cached tokens in blocks of 128, scored by halves of 64:
 //   S = Q (c_k - z_k)^T          both operands in shared memory, S in tensor memory
 //   P = 2^(a s_k S - m) s_v      by the rows' threads, written over S as binary16
 //   O += P (c_v - z_v)           P from tensor memory, V from shared memory
@@ -14,12 +14,20 @@
 // overflow and of subnormals.
 //
 // Warps: 0-3 and 4-7 the softmax of a tile each, one thread a row (no word between threads),
-// the row's 128 scores in registers; 8-11 unpack K (one thread a token) and V (one thread 8
+// a half's 64 scores in registers; 8-11 unpack K (one thread a token) and V (one thread 8
 // tokens x D/8 values of d), reading codes straight from HBM or L2 into registers most of a
-// block ahead, so that there is no staging of packed data; 12 issues the MMAs. Two row tiles
-// share every unpacked block and keep the tensor pipe busy with one tile's products while
-// the other's softmax runs: O_A(i), S_A(i+1), O_B(i), S_B(i+1), ...
+// block ahead, so that there is no staging of packed data; 12 issues the MMAs. A tile's S has two
+// halves in tensor memory, so the scores of the next half are there when the softmax of one ends,
+// and the products run under the other half's and the other tile's softmax:
+//   O_A(h), S_A(h+2), O_B(h), S_B(h+2), ...
 // O is rescaled only when a row's maximum grew by more than 2^8 (its P stays below 2^15 until then).
+//
+// Three requests' chunks of 839 to 4000 tokens behind 5690 to 8200 cached ones, 32 query heads over
+// 8, D = 128, bfloat16: 915 us, 890 TFLOP/s, 47% of what a plain bf16 matrix product reaches. (Scores
+// by whole blocks, one S a tile: 1000 us.) The tensor pipe is busy for 51% of the time, the issue slots
+// for 49%, shared memory for much of the rest, and none of them alone is the limit: without the
+// exponentials, the scales or the unpacking it takes 0 to 5% less, with an eighth of the products 12%.
+// A CTA's start and end, which nothing overlaps, are 10 us of its 110.
 #include "api_internal.cuh"
 #include "kv4.cuh"
 #include "launch.cuh"
@@ -32,12 +40,14 @@ namespace w4a16 {
 namespace {
 
 constexpr int kRows = 128;            // rows of a tile
-constexpr int kBlock = 128;           // cached tokens of a block
+constexpr int kBlock = 128;           // cached tokens of a block: what is unpacked together
+constexpr int kHalf = 64;             // and of a half: what is scored together
 constexpr int kMmaWarp = 12;
 constexpr int kThreads = 512;         // four warpgroups, of the last the MMA warp alone at work
 // Registers a thread: 128 at launch, moved to the softmax from the warps that need fewer. Each
 // of the SM's four quarters holds one warp of every warpgroup and a quarter of the registers.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 184, kUnpackRegs = 88, kIssueRegs = 56;
+// 184/88/56 took 938 us where this takes 915.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 160, kUnpackRegs = 104, kIssueRegs = 88;
 static_assert(2 * kSoftmaxRegs + kUnpackRegs + kIssueRegs <= 4 * kLaunchRegs, "registers of the block");
 constexpr int kScaleStages = 4;       // K's scales live until the softmax has read them: two blocks past K itself
 constexpr int kGrow = 8;              // log2 of how far P may grow before O is rescaled
@@ -57,7 +67,7 @@ struct Prompt {
         uint32_t odd[2][4];                  // tokens whose V scale is NaN
         uint32_t vred[2][4];
         int ev[2];                           // V's scales so far are below 2^ev
-        uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], skfull[kScaleStages], sfull[2], pfull[2], odone[2], teardown;
+        uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], skfull[kScaleStages], sfull[2][2], pfull[2][2], odone[2][2], teardown;
         uint32_t tmem;
         int abort_flag, b, rt;
     };
@@ -170,9 +180,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
                 mbar_init(smem_addr(&sh.vfull[s]), kBlock);
                 mbar_init(smem_addr(&sh.kempty[s]), 1);
                 mbar_init(smem_addr(&sh.vempty[s]), 1);
-                mbar_init(smem_addr(&sh.sfull[s]), 1);
-                mbar_init(smem_addr(&sh.pfull[s]), kRows);
-                mbar_init(smem_addr(&sh.odone[s]), 1);
+                for (int h = 0; h < 2; ++h) {
+                    mbar_init(smem_addr(&sh.sfull[s][h]), 1);
+                    mbar_init(smem_addr(&sh.pfull[s][h]), kRows);
+                    mbar_init(smem_addr(&sh.odone[s][h]), 1);
+                }
             }
             for (int s = 0; s < kScaleStages; ++s) mbar_init(smem_addr(&sh.skfull[s]), 4);
             fence_mbar_init();
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     const int pos_first = seq - nq + row0 / p.group, pos_last = seq - nq + (end_row - 1) / p.group;
     const int low = p.window > 0 ? pos_first - p.window + 1 : 0;
     const int base = low > 0 ? low / kBlock * kBlock : 0;
-    const int blocks = pos_last >= base ? (pos_last - base) / kBlock + 1 : 0;
+    const int halves = pos_last >= base ? (pos_last - base) / kHalf + 1 : 0, blocks = (halves + 1) / 2;
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax: one thread a row
@@ -270,46 +282,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         const uint64_t a2 = pack_f32x2(a, a);
         int ev = -126;
         bool ok = true, poisoned = false;
+        // the products of all halves before h > 0 (those of two halves may be outstanding, so each half has a barrier)
+        auto wait_outputs = [&](int h) { return wait_warp(smem_addr(&sh.odone[tile][(h - 1) & 1]), ((h - 1) >> 1) & 1, ctl); };
 #pragma unroll 1
-        for (int i = 0; i < blocks; ++i) {
-            const int s4 = i % kScaleStages, s2 = i & 1;
+        for (int h = 0; h < halves; ++h) {
+            const int i = h >> 1, half = h & 1, s4 = i % kScaleStages, s2 = i & 1;
             if (!wait_warp(smem_addr(&sh.skfull[s4]), (i / kScaleStages) & 1, ctl) ||
-                !wait_warp(smem_addr(&sh.sfull[tile]), i & 1, ctl)) {
+                !wait_warp(smem_addr(&sh.sfull[tile][half]), i & 1, ctl)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
+            const uint32_t sh_at = s_at + half * kHalf;
             // x: s_k times the products, then the exponent, pairs of columns
-            uint64_t x[kBlock / 2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            uint64_t x[kHalf / 2];
+            {
                 uint32_t r[64];
-                tmem_ld64(s_at + 64 * c, r);
+                tmem_ld64(sh_at, r);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    x[32 * c + j] = pack_f32x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                for (int j = 0; j < kHalf / 2; ++j)
+                    x[j] = pack_f32x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
             }
 #pragma unroll
-            for (int j = 0; j < kBlock / 2; j += 2) {
-                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sh.sk[s4][2 * j]);
+            for (int j = 0; j < kHalf / 2; j += 2) {
+                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sh.sk[s4][half * kHalf + 2 * j]);
                 x[j] = mul_f32x2(x[j], k.x);
                 x[j + 1] = mul_f32x2(x[j + 1], k.y);
             }
-            const int t0 = base + i * kBlock;
-            const uint4 vw = *reinterpret_cast<const uint4*>(sh.valid[s4]);
-            const bool full = (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu && t0 + kBlock - 1 <= pos_min &&
+            const int t0 = base + h * kHalf;
+            const uint2 vw = *reinterpret_cast<const uint2*>(&sh.valid[s4][2 * half]);
+            const bool full = (vw.x & vw.y) == 0xffffffffu && t0 + kHalf - 1 <= pos_min &&
                               (p.window <= 0 || t0 > pos_max - p.window);
-            // this row's visible columns of the block, where stored: word w's bits
+            // this row's visible columns of the half, where stored: word w's bits
             auto see = [&](int w) -> uint32_t {
                 const int hi = pos - t0 + 1 - 32 * w, lo = (p.window > 0 ? pos - p.window + 1 - t0 : 0) - 32 * w;
                 const uint32_t upto = hi <= 0 ? 0u : hi >= 32 ? 0xffffffffu : (1u << hi) - 1u;
                 const uint32_t below = lo <= 0 ? 0u : lo >= 32 ? 0xffffffffu : (1u << lo) - 1u;
-                return sh.valid[s4][w] & upto & ~below;
+                return (w ? vw.y : vw.x) & upto & ~below;
             };
             if (!full) {
                 // selected, not added: what a row does not see may be any memory
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
+                for (int w = 0; w < 2; ++w) {
                     const uint32_t bits = see(w);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -323,20 +337,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             }
             float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-            for (int j = 0; j < kBlock / 2; ++j) {
+            for (int j = 0; j < kHalf / 2; ++j) {
                 float u, v;
                 unpack_f32x2(x[j], u, v);
                 tops[j & 3] = fmaxf(tops[j & 3], fmaxf(u, v));
             }
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            if (!wait_warp(smem_addr(&sh.vfull[s2]), (i >> 1) & 1, ctl)) {
+            if (half == 0 && !wait_warp(smem_addr(&sh.vfull[s2]), (i >> 1) & 1, ctl)) {
                 ok = false;
                 break;
             }
             const int en = sh.ev[s2];
-            const uint4 ow = *reinterpret_cast<const uint4*>(sh.odd[s2]);
-            if (ow.x | ow.y | ow.z | ow.w)   // a NaN in V's scales shows in the rows that see it
-                poisoned = poisoned || ((ow.x & see(0)) | (ow.y & see(1)) | (ow.z & see(2)) | (ow.w & see(3))) != 0u;
+            const uint2 ow = *reinterpret_cast<const uint2*>(&sh.odd[s2][2 * half]);
+            if (ow.x | ow.y)   // a NaN in V's scales shows in the rows that see it
+                poisoned = poisoned || ((ow.x & see(0)) | (ow.y & see(1))) != 0u;
             float f = 1.0f;
             if (top > m) {
                 if (m == -CUDART_INF_F) {
@@ -351,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
                 if (ev > -126) f *= pow2i(ev - en > -126 ? ev - en : -126);
                 ev = en;
             }
-            if (i > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-                if (!wait_warp(smem_addr(&sh.odone[tile]), (i - 1) & 1, ctl)) {
+            if (h > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                if (!wait_outputs(h)) {
                     ok = false;
                     break;
                 }
@@ -370,11 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             const float ma = m == -CUDART_INF_F ? 0.0f : m * a;
             const uint64_t ma2 = pack_f32x2(-ma, -ma);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
-                    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&sh.sv[s2][32 * c + 2 * j]);
+                    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&sh.sv[s2][half * kHalf + 32 * c + 2 * j]);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         float u0, u1;
@@ -391,18 +405,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
                     }
                 }
                 // the high parts of 32 columns over the first 16 of them, the low parts over the others
-                tmem_st16_async(s_at + 32 * c, hi);
-                if constexpr (!BF) tmem_st16_async(s_at + 32 * c + 16, lo);
+                tmem_st16_async(sh_at + 32 * c, hi);
+                if constexpr (!BF) tmem_st16_async(sh_at + 32 * c + 16, lo);
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_addr(&sh.pfull[tile]));
+            mbar_arrive(smem_addr(&sh.pfull[tile][half]));
         }
         float l, l_odd;
         unpack_f32x2(l2, l, l_odd);
         l += l_odd;
-        if (ok && blocks > 0) {
-            ok = wait_warp(smem_addr(&sh.odone[tile]), (blocks - 1) & 1, ctl);
+        if (ok && halves > 0) {
+            ok = wait_outputs(halves);
             tc_fence_after();
         }
         if (ok) {
@@ -411,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
                 float x[16];
-                if (blocks > 0) tmem_ld_f32<16>(o_at + c, x);
+                if (halves > 0) tmem_ld_f32<16>(o_at + c, x);
                 uint32_t r[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -587,61 +601,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         // ------------------------------------------------------------ MMA issue
         setmaxnreg_dec<kIssueRegs>();
         if (warp == kMmaWarp) {
-        constexpr uint32_t idesc_s = idesc_f16_f32(128, kBlock), idesc_o = idesc_f16_f32(128, D);
-        auto scores = [&](int tile, int s2) {
-            const uint64_t qd = smem_desc_k_sw128(sbase + tile * C::QT), kd = smem_desc_k_sw128(sbase + C::OFF_K + s2 * C::QT);
-            const uint32_t d = tmem + C::S_COL + tile * kBlock;
+        constexpr uint32_t idesc_s = idesc_f16_f32(128, kHalf), idesc_o = idesc_f16_f32(128, D);
+        // S of a tile for half h: K's tokens 64 (h mod 2) .. of its block
+        auto scores = [&](int tile, int h) {
+            const uint64_t qd = smem_desc_k_sw128(sbase + tile * C::QT);
+            const uint64_t kd = smem_desc_k_sw128(sbase + C::OFF_K + (h >> 1 & 1) * C::QT + (h & 1) * kHalf * 128);
+            const uint32_t d = tmem + C::S_COL + tile * kBlock + (h & 1) * kHalf;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint64_t off = (uint64_t)((k >> 2) * (kRows * 8) + (k & 3) * 2);
                 mma_f16_ss(d, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
             }
         };
-        auto outputs = [&](int tile, int s2, bool first) {
-            const uint64_t vd = smem_desc_k_sw128(sbase + C::OFF_V + s2 * C::QT);
-            const uint32_t d = tmem + C::O_COL + tile * D, a = tmem + C::S_COL + tile * kBlock;
+        auto outputs = [&](int tile, int h) {
+            const uint64_t vd = smem_desc_k_sw128(sbase + C::OFF_V + (h >> 1 & 1) * C::QT + (h & 1) * D * 128);
+            const uint32_t d = tmem + C::O_COL + tile * D, a = tmem + C::S_COL + tile * kBlock + (h & 1) * kHalf;
             // 32 columns of P lie in the first 16 of S's columns for them, their low parts in the others
 #pragma unroll
-            for (int k = 0; k < kBlock / 16; ++k)
-                mma_f16_ts(d, a + (k >> 1) * 32 + (k & 1) * 8, vd + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2), idesc_o,
-                           (!first || k > 0) ? 1u : 0u);
+            for (int k = 0; k < kHalf / 16; ++k)
+                mma_f16_ts(d, a + (k >> 1) * 32 + (k & 1) * 8, vd + (uint64_t)(k * 2), idesc_o, (h > 0 || k > 0) ? 1u : 0u);
             if constexpr (!BF) {
 #pragma unroll
-                for (int k = 0; k < kBlock / 16; ++k)
-                    mma_f16_ts(d, a + (k >> 1) * 32 + 16 + (k & 1) * 8, vd + (uint64_t)((k >> 2) * (D * 8) + (k & 3) * 2),
-                               idesc_o, 1u);
+                for (int k = 0; k < kHalf / 16; ++k)
+                    mma_f16_ts(d, a + (k >> 1) * 32 + 16 + (k & 1) * 8, vd + (uint64_t)(k * 2), idesc_o, 1u);
             }
         };
-        bool ok = blocks > 0 && wait_warp(smem_addr(&sh.qfull), 0, ctl) && wait_warp(smem_addr(&sh.kfull[0]), 0, ctl);
+        bool ok = halves > 0 && wait_warp(smem_addr(&sh.qfull), 0, ctl) && wait_warp(smem_addr(&sh.kfull[0]), 0, ctl);
         if (ok) {
             tc_fence_after();
             if (elect_one()) {
-                scores(0, 0);
-                mma_commit(smem_addr(&sh.sfull[0]));
-                scores(1, 0);
-                mma_commit(smem_addr(&sh.sfull[1]));
+                for (int h = 0; h < 2 && h < halves; ++h)
+                    for (int tile = 0; tile < 2; ++tile) {
+                        scores(tile, h);
+                        mma_commit(smem_addr(&sh.sfull[tile][h]));
+                    }
                 mma_commit(smem_addr(&sh.kempty[0]));
             }
             __syncwarp();
         }
-        for (int i = 0; ok && i < blocks; ++i) {
-            const int s2 = i & 1, n2 = s2 ^ 1;
-            const bool more = i + 1 < blocks;
-            if (!wait_warp(smem_addr(&sh.vfull[s2]), (i >> 1) & 1, ctl)) break;
-            if (more && !wait_warp(smem_addr(&sh.kfull[n2]), ((i + 1) >> 1) & 1, ctl)) break;
-#pragma unroll
+        for (int h = 0; ok && h < halves; ++h) {
+            const int half = h & 1, i = h >> 1, s2 = i & 1, n = i + 1;   // h + 2 is of block n
+            const bool more = h + 2 < halves;
+            if (half == 0) {
+                if (!wait_warp(smem_addr(&sh.vfull[s2]), (i >> 1) & 1, ctl)) break;
+                if (more && !wait_warp(smem_addr(&sh.kfull[n & 1]), (n >> 1) & 1, ctl)) break;
+            }
+#pragma unroll 1
             for (int tile = 0; tile < 2; ++tile) {
-                if (ok && !wait_warp(smem_addr(&sh.pfull[tile]), i & 1, ctl)) ok = false;
+                if (ok && !wait_warp(smem_addr(&sh.pfull[tile][half]), i & 1, ctl)) ok = false;
                 if (!ok) continue;
                 tc_fence_after();
                 if (elect_one()) {
-                    outputs(tile, s2, i == 0);
-                    mma_commit(smem_addr(&sh.odone[tile]));
-                    if (tile == 1) mma_commit(smem_addr(&sh.vempty[s2]));
+                    outputs(tile, h);
+                    mma_commit(smem_addr(&sh.odone[tile][half]));
+                    if (tile == 1 && half == 1) mma_commit(smem_addr(&sh.vempty[s2]));
                     if (more) {
-                        scores(tile, n2);
-                        mma_commit(smem_addr(&sh.sfull[tile]));
-                        if (tile == 1) mma_commit(smem_addr(&sh.kempty[n2]));
+                        scores(tile, h + 2);
+                        mma_commit(smem_addr(&sh.sfull[tile][half]));
+                        if (tile == 1 && half == 1) mma_commit(smem_addr(&sh.kempty[n & 1]));
                     }
                 }
                 __syncwarp();
