@@ -626,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 });
             const int n = gather();
             if (n >= 0) {
+                cl.sync();   // the first CTA has read the lists: the others leave their place to another row
                 if (rank == 0 && n <= kFew) {
                     // few entries: each counts and weighs those ranked before it, then the kept ones of lower index
                     unsigned long long* const keys = sh.list;   // the lists have been gathered
@@ -706,7 +707,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     pick(sh, key, w, 0ull, [target](uint32_t, unsigned long long m) { return m > target; });
                     if (tid == 0) result(token_of(sh.picked), (double)sh.picked_weight / (double)total);
                 }
-                cl.sync();
                 return;
             }
         }
@@ -748,10 +748,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         if (lane == 0) sh.total = total;
     };
-    // the drawn token, by all threads of the CTA that holds its segment
+    // the drawn token, by all threads of a CTA
     auto locate = [&](int seg, unsigned long long target, unsigned long long total) {
-        if (seg / kWarps != rank) return;
-        const int from = seg % kWarps * seg_len;
+        const int from = seg % kWarps * seg_len + (seg / kWarps - rank) * slice;   // counted in this CTA's places
         unsigned long long before = 0;
         for (int v0 = from; v0 < from + seg_len; v0 += kThreads * VEC) {
             const int v = v0 + tid * VEC;
@@ -946,9 +945,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             if (lane == 0) sh.warp_mass[warp] = mass;
             const int n = gather();
             if (n >= 0) {
+                const int segs = ctas * kWarps;
+                if (rank == 0 && tid < segs) sh.all_mass[tid] = cl.map_shared_rank(&sh, tid / kWarps)->warp_mass[tid % kWarps];
+                cl.sync();   // the others leave, as above
                 if (rank == 0) {
-                    const int segs = ctas * kWarps;
-                    if (tid < segs) sh.all_mass[tid] = cl.map_shared_rank(&sh, tid / kWarps)->warp_mass[tid % kWarps];
                     pick(sh, key, w, base, [limit](uint32_t, unsigned long long m) { return !((double)m < limit); });
 #pragma unroll
                     for (int i = 0; i < kListPer; ++i)
@@ -956,16 +956,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                             const int at = token_of(key[i]) + mis;   // place in the row
                             atomicAdd(&sh.all_mass[at / p.slice * kWarps + at % p.slice / seg_len], (unsigned long long)w[i]);
                         }
-                    if (tid == 0) sh.cut = sh.picked;
+                    cut_x = logit_of(sh.picked);
+                    cut_at = token_of(sh.picked);
                     __syncthreads();
                     choose(segs);
+                    __syncthreads();
+                    locate(sh.seg, sh.seg_target, sh.total);
                 }
-                cl.sync();
-                const Shared* o = cl.map_shared_rank(&sh, 0);
-                cut_x = logit_of(o->cut);
-                cut_at = token_of(o->cut);
-                locate(o->seg, o->seg_target, o->total);
-                cl.sync();
                 return;
             }
             refine([limit](uint32_t, unsigned long long m, unsigned long long) { return !((double)m < limit); },
@@ -983,11 +980,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     cl.sync();
     const int segs = ctas * kWarps;
     if (tid < segs) sh.all_mass[tid] = cl.map_shared_rank(&sh, tid / kWarps)->warp_mass[tid % kWarps];
-    __syncthreads();
+    cl.sync();   // no CTA leaves while another may read its shared memory
     choose(segs);
     __syncthreads();
-    locate(sh.seg, sh.seg_target, sh.total);
-    cl.sync();   // no CTA leaves while another may read its shared memory
+    if (sh.seg / kWarps == rank) locate(sh.seg, sh.seg_target, sh.total);
 }
 
 }  // namespace
