@@ -48,6 +48,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kPer = kBins / kThreads;   // bins a thread adds up
 constexpr int kMaxCluster = 8;
+constexpr int kMaxSlice = 65536;         // tokens of a CTA's slice
 constexpr float kSpan = 22.2f;           // exp(-22.2) * 2^31 rounds to 0
 
 constexpr int kListMax = 2048;           // tokens of a list
@@ -60,7 +61,7 @@ constexpr int kFew = kThreads / 4;       // entries that are compared with each 
 constexpr int kGroups = 4;               // groups of a thread's tokens, each with its maximum
 
 struct Histogram {
-    uint32_t cnt[kBins], part[3][kBins];   // a bin's count, and its weights' bits 0..10, 11..21 and 22..31 summed
+    uint32_t cnt[kBins], part[2][kBins];   // a bin's count, and its weights' bits 0..15 and 16..31 summed
 };
 
 struct Shared {
@@ -137,19 +138,23 @@ struct Row {
     float top, inv, min_p;
 };
 
+__device__ __forceinline__ float scaled(float x, const Row& r) { return __fmul_rn(__fsub_rn(x, r.top), r.inv); }
+
 __device__ __forceinline__ float exp_of(float x, const Row& r)
 {
-    const float e = expf(__fmul_rn(__fsub_rn(x, r.top), r.inv));
+    const float e = expf(scaled(x, r));
     return x == r.top ? 1.0f : e;
 }
 
 __device__ __forceinline__ uint32_t weight_of(float e) { return __float2uint_rn(e * 2147483648.0f); }
 
-__device__ __forceinline__ int bin_of(float x, const Row& r)
-{
-    const int b = x == r.top ? 0 : (int)(__fmul_rn(__fsub_rn(r.top, x), r.inv) * (kBins / kSpan));
-    return b < kBins - 1 ? b : kBins - 1;
-}
+// A logit's bin, before truncation: kBins or more past kSpan.
+__device__ __forceinline__ float place(float x, const Row& r) { return x == r.top ? 0.0f : scaled(x, r) * (-kBins / kSpan); }
+
+// The whole part of a number in 0 .. kBins, without the conversion unit that the weights keep busy.
+__device__ __forceinline__ int whole(float at) { return (int)(__float_as_uint(__fadd_rz(at, 8388608.0f)) & (2u * kBins - 1u)); }
+
+__device__ __forceinline__ int bin_of(float x, const Row& r) { return whole(fminf(place(x, r), (float)(kBins - 1))); }
 
 // Sums of 64-bit numbers over a warp.
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v)
@@ -176,17 +181,14 @@ __device__ __forceinline__ void clear(Histogram& h)
     for (int i = threadIdx.x; i < (int)(sizeof(Histogram) / 16); i += kThreads) at[i] = make_uint4(0, 0, 0, 0);
 }
 
+// 32 bits hold the low parts of kMaxSlice weights, and as many high parts: a weight is at most 2^31.
 __device__ __forceinline__ void add_mass(Histogram& h, int bin, uint32_t w)
 {
-    atomicAdd(&h.part[0][bin], w & 2047u);
-    if (w >= 1u << 11) atomicAdd(&h.part[1][bin], w >> 11 & 2047u);
-    if (w >= 1u << 22) atomicAdd(&h.part[2][bin], w >> 22);
+    atomicAdd(&h.part[0][bin], w & 0xffffu);
+    if (w >= 1u << 16) atomicAdd(&h.part[1][bin], w >> 16);
 }
 
-__device__ __forceinline__ unsigned long long mass_of(uint32_t a, uint32_t b, uint32_t c)
-{
-    return a + ((unsigned long long)b << 11) + ((unsigned long long)c << 22);
-}
+__device__ __forceinline__ unsigned long long mass_of(uint32_t a, uint32_t b) { return a + ((unsigned long long)b << 16); }
 
 // Finds the first bin with done(count, weight of every bin up to and with it, weight of all bins), from each
 // thread's two bins; base counts come on top. MASS: weights count, else only counts do. Leaves bin = -1 if there
@@ -248,15 +250,15 @@ __device__ __forceinline__ void search(cg::cluster_group& cl, Shared& sh, Histog
 #pragma unroll
     for (int two = 0; two < kMaxCluster; two += 2) {   // two CTAs' loads in flight at a time
         if (two >= ctas) break;
-        uint2 a[2], b[2][3];
+        uint2 a[2], b[2][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            a[k] = b[k][0] = b[k][1] = b[k][2] = make_uint2(0, 0);
+            a[k] = b[k][0] = b[k][1] = make_uint2(0, 0);
             if (two + k < ctas) {
                 const Histogram* o = cl.map_shared_rank(&hist, two + k);
                 a[k] = *reinterpret_cast<const uint2*>(&o->cnt[at]);
 #pragma unroll
-                for (int q = 0; q < 3; ++q)
+                for (int q = 0; q < 2; ++q)
                     if (MASS) b[k][q] = *reinterpret_cast<const uint2*>(&o->part[q][at]);
             }
         }
@@ -265,8 +267,8 @@ __device__ __forceinline__ void search(cg::cluster_group& cl, Shared& sh, Histog
             cnt[0] += a[k].x;
             cnt[1] += a[k].y;
             if (MASS) {
-                mass[0] += mass_of(b[k][0].x, b[k][1].x, b[k][2].x);
-                mass[1] += mass_of(b[k][0].y, b[k][1].y, b[k][2].y);
+                mass[0] += mass_of(b[k][0].x, b[k][1].x);
+                mass[1] += mass_of(b[k][0].y, b[k][1].y);
             }
         }
     }
@@ -316,7 +318,7 @@ __device__ __forceinline__ void pick(Shared& sh, const unsigned long long (&key)
         const int shift = bits > 10 ? bits - 10 : 0;
 #pragma unroll
         for (int b = tid; b < kBins; b += kThreads)
-            sh.keys.cnt[b] = sh.keys.part[0][b] = sh.keys.part[1][b] = sh.keys.part[2][b] = 0;
+            sh.keys.cnt[b] = sh.keys.part[0][b] = sh.keys.part[1][b] = 0;
         if (tid == 0) sh.bin = -1;
         __syncthreads();
 #pragma unroll
@@ -333,7 +335,7 @@ __device__ __forceinline__ void pick(Shared& sh, const unsigned long long (&key)
         for (int i = 0; i < kPer; ++i) {
             const int b = tid * kPer + i;
             cnt[i] = sh.keys.cnt[b];
-            mass[i] = mass_of(sh.keys.part[0][b], sh.keys.part[1][b], sh.keys.part[2][b]);
+            mass[i] = mass_of(sh.keys.part[0][b], sh.keys.part[1][b]);
         }
         scan_bins<true>(sh, cnt, mass, base_cnt, base_mass,
                         [&](uint32_t c, unsigned long long m, unsigned long long) { return done(c, m); });
@@ -563,7 +565,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     // a logit below every one that is at most d below the maximum, whatever the roundings of either side
     auto below = [&](float d) { return r.top <= FLT_MAX ? r.top - d * 1.00001f - 1e-6f * fabsf(r.top) : r.top; };
     const float weightless = below(22.5f * temp);   // lower ones weigh nothing
-    auto place = [&](float x) { return x == r.top ? 0.0f : __fmul_rn(__fsub_rn(r.top, x), r.inv) * to_bin; };   // bin, before truncation
     auto list_it = [&](int v, float x) {
         const uint32_t at = atomicAdd(&sh.listed, 1u);
         if (at < kListMine)
@@ -612,8 +613,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         // a bound below at least k tokens: the bin of the k-th largest of the groups' maxima
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            const float b = place(tops[i]);
-            if (tops[i] > -CUDART_INF_F && b < (float)kBins) atomicAdd(&sh.bins.cnt[(int)b], 1u);
+            const float b = place(tops[i], r);
+            if (tops[i] > -CUDART_INF_F && b < (float)kBins) atomicAdd(&sh.bins.cnt[whole(b)], 1u);
         }
         const uint32_t kk = (uint32_t)k;
         search<false>(cl, sh, sh.bins, 0u, 0ull, [kk](uint32_t c, unsigned long long, unsigned long long) { return c >= kk; });
@@ -923,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     } else if (need_p) {
         each(weightless, [&](int, float x) {
             const uint32_t weight = weight_of(exp_of(x, r));
-            if (weight) add_mass(sh.bins, (int)place(x), weight);   // a token that weighs lies inside the bins
+            if (weight) add_mass(sh.bins, whole(place(x, r)), weight);   // a token that weighs lies inside the bins
         });
         // the bin past which the weight before a token is no longer below top_p times the whole
         search<true>(cl, sh, sh.bins, 0u, 0ull, [top_p](uint32_t, unsigned long long m, unsigned long long all) {
@@ -936,10 +937,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             // one pass sums what lies above the bin, by segments, and lists the bin's tokens
             unsigned long long mass = 0;
             sweep(s0 + lane * VEC, s0 + seg_len, 32 * VEC, below((float)(bin + 1) / to_bin * temp), [&](int v, float x) {
-                const float e = exp_of(x, r), at = place(x);
-                const int b = at < (float)kBins ? (int)at : kBins;   // NaN: no bin
-                mass += b < bin && (e >= r.min_p || x == r.top) ? weight_of(e) : 0u;
-                if (b == bin && x > -CUDART_INF_F) list_it(v, x);
+                const float e = exp_of(x, r), at = place(x, r);   // NaN: no bin
+                mass += at < (float)bin && (e >= r.min_p || x == r.top) ? weight_of(e) : 0u;
+                if (at >= (float)bin && at < (float)(bin + 1) && x > -CUDART_INF_F) list_it(v, x);
             });
             mass = warp_sum(mass);
             if (lane == 0) sh.warp_mass[warp] = mass;
@@ -974,7 +974,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
     // ---- the kept weight of each warp's segment, in index order
     unsigned long long mass = 0;
-    sweep(s0 + lane * VEC, s0 + seg_len, 32 * VEC, fmaxf(cut_x, weightless), [&](int v, float x) { mass += kept(x, v); });
+    if (cut_x == -CUDART_INF_F && !(r.min_p > 0.0f))   // nothing is cut
+        sweep(s0 + lane * VEC, s0 + seg_len, 32 * VEC, weightless, [&](int, float x) { mass += weight_of(exp_of(x, r)); });
+    else
+        sweep(s0 + lane * VEC, s0 + seg_len, 32 * VEC, fmaxf(cut_x, weightless), [&](int v, float x) { mass += kept(x, v); });
     mass = warp_sum(mass);
     if (lane == 0) sh.warp_mass[warp] = mass;
     cl.sync();
@@ -996,10 +999,11 @@ cudaError_t launch_sample(const SampleParams& in, int sms, cudaStream_t stream)
     // As many CTAs a row as give every SM the two it holds, while a slice is more than a round of loads; up
     // to the portable cluster of eight. A row's steps are a chain, so that fewer, longer slices leave it waiting
     // (256 x 100003 FP32: 239 us with one CTA a row, 93 with two, 100 with four).
+    auto slice_of = [&](int n) { return ((p.vocab + 16 / size + n - 1) / n + step - 1) / step * step; };
     int ctas = 1;
-    while (ctas < kMaxCluster && (long long)p.batch * ctas < 2 * sms && p.vocab / ctas > step) ctas *= 2;
+    while (ctas < kMaxCluster && (((long long)p.batch * ctas < 2 * sms && p.vocab / ctas > step) || slice_of(ctas) > kMaxSlice)) ctas *= 2;
     p.in_turn = (long long)p.batch * ctas > 2 * sms && p.batch <= 16384;
-    p.slice = ((p.vocab + 16 / size + ctas - 1) / ctas + step - 1) / step * step;
+    p.slice = slice_of(ctas);
     const unsigned grid = (unsigned)(p.batch * ctas);
     switch (p.dtype) {
         case W4A16_FP32: return launch_chained(sample_kernel<W4A16_FP32>, grid, kThreads, 0, (unsigned)ctas, stream, p);
