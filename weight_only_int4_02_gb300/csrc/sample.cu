@@ -275,42 +275,16 @@ __device__ __forceinline__ void search(cg::cluster_group& cl, Shared& sh, Histog
     scan_bins<MASS>(sh, cnt, mass, base_cnt, base_mass, done);
 }
 
-// In one CTA: of this thread's entries (0: none; all others different), the one at which done(count, weight of
-// every entry from the greatest key down to it) becomes true, in sh.picked (0 if there is none), with what is
-// before it and its weight. Ten bits of the keys' range at a time, until a bin has one entry.
+// In one CTA: of this thread's entries (0: none; all others different and in kmin .. kmax), the one at which
+// done(count, weight of every entry from the greatest key down to it) becomes true, in sh.picked (0 if there is
+// none), with what is before it and its weight. Ten bits of the keys' range at a time, until a bin has one entry.
 template <typename F>
 __device__ __forceinline__ void pick(Shared& sh, const unsigned long long (&key)[kListPer], const uint32_t (&w)[kListPer],
-                                     unsigned long long base_mass, F done)
+                                     unsigned long long kmin, unsigned long long kmax, unsigned long long base_mass, F done)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned long long kmin = ~0ull, kmax = 0ull;
-#pragma unroll
-    for (int i = 0; i < kListPer; ++i) {
-        if (key[i] == 0) continue;
-        kmin = key[i] < kmin ? key[i] : kmin;
-        kmax = key[i] > kmax ? key[i] : kmax;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const unsigned long long a = __shfl_xor_sync(0xffffffffu, kmin, d), b = __shfl_xor_sync(0xffffffffu, kmax, d);
-        kmin = a < kmin ? a : kmin;
-        kmax = b > kmax ? b : kmax;
-    }
-    __syncthreads();
-    if (lane == 0) {
-        sh.best[warp] = kmax;
-        sh.scan_mass[warp] = kmin;
-    }
+    const int tid = threadIdx.x;
+    __syncthreads();   // what was picked before has been read
     if (tid == 0) sh.picked = 0;
-    __syncthreads();
-    kmax = sh.best[lane % kWarps];
-    kmin = sh.scan_mass[lane % kWarps];
-#pragma unroll
-    for (int d = kWarps / 2; d > 0; d >>= 1) {
-        const unsigned long long a = __shfl_xor_sync(0xffffffffu, kmin, d), b = __shfl_xor_sync(0xffffffffu, kmax, d);
-        kmin = a < kmin ? a : kmin;
-        kmax = b > kmax ? b : kmax;
-    }
     uint32_t base_cnt = 0;
     for (int level = 0; level < 7; ++level) {
         const unsigned long long range = kmax - kmin;
@@ -564,11 +538,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     const float to_bin = kBins / kSpan;
     // a logit below every one that is at most d below the maximum, whatever the roundings of either side
     auto below = [&](float d) { return r.top <= FLT_MAX ? r.top - d * 1.00001f - 1e-6f * fabsf(r.top) : r.top; };
+    // and one at or above every one that is at least d below it
+    auto above = [&](float d) { return r.top <= FLT_MAX ? fminf(r.top - fminf(d, FLT_MAX) * 0.99999f + 1e-6f * fabsf(r.top), r.top) : r.top; };
     const float weightless = below(22.5f * temp);   // lower ones weigh nothing
+    auto entry_of = [](float x, uint32_t low) { return (unsigned long long)key_of<DTYPE>(x) << kIndexBits | low; };
     auto list_it = [&](int v, float x) {
         const uint32_t at = atomicAdd(&sh.listed, 1u);
         if (at < kListMine)
-            sh.list[at] = (unsigned long long)key_of<DTYPE>(x) << kIndexBits | (kIndexTop - (uint32_t)(first + v));
+            sh.list[at] = entry_of(x, kIndexTop - (uint32_t)(first + v));
     };
     auto logit_of = [](unsigned long long e) { return float_of<DTYPE>((uint32_t)(e >> kIndexBits)); };
     auto token_of = [](unsigned long long e) { return (int)(kIndexTop - ((uint32_t)e & kIndexTop)); };
@@ -670,13 +647,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     if (keep && (tid & 3) == 0 && target >= before && target < before + own_w)
                         result(token_of(own), (double)own_w / (double)total);
                 } else if (rank == 0) {
+                    unsigned long long least = entry_of(low, 0), greatest = entry_of(r.top, kIndexTop);
                     // the k-th entry, the entry at which top-p's limit is passed, and the drawn one among the kept
                     if (n > k) {
-                        pick(sh, key, w, 0ull, [kk](uint32_t c, unsigned long long) { return c >= kk; });
-                        const unsigned long long last = sh.picked;
+                        pick(sh, key, w, least, greatest, 0ull, [kk](uint32_t c, unsigned long long) { return c >= kk; });
+                        least = sh.picked;
 #pragma unroll
                         for (int i = 0; i < kListPer; ++i)
-                            if (key[i] < last) key[i] = 0, w[i] = 0;
+                            if (key[i] < least) key[i] = 0, w[i] = 0;
                     }
                     unsigned long long sum = 0;
 #pragma unroll
@@ -684,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     unsigned long long total = block_sum(sum);
                     if (need_p) {
                         const double limit = (double)total * (double)top_p;
-                        pick(sh, key, w, 0ull, [limit](uint32_t, unsigned long long m) { return !((double)m < limit); });
+                        pick(sh, key, w, least, greatest, 0ull, [limit](uint32_t, unsigned long long m) { return !((double)m < limit); });
                         const unsigned long long last = sh.picked;
 #pragma unroll
                         for (int i = 0; i < kListPer; ++i)
@@ -705,7 +683,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
                     for (int i = 0; i < kListPer; ++i) key[i] = key[i] ? 1ull << kIndexBits | (key[i] & kIndexTop) : 0ull;
                     const unsigned long long target = target_of(total);
-                    pick(sh, key, w, 0ull, [target](uint32_t, unsigned long long m) { return m > target; });
+                    pick(sh, key, w, 1ull << kIndexBits, (2ull << kIndexBits) - 1ull, 0ull,
+                         [target](uint32_t, unsigned long long m) { return m > target; });
                     if (tid == 0) result(token_of(sh.picked), (double)sh.picked_weight / (double)total);
                 }
                 return;
@@ -936,7 +915,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const unsigned long long base = sh.base_mass;
             // one pass sums what lies above the bin, by segments, and lists the bin's tokens
             unsigned long long mass = 0;
-            sweep(s0 + lane * VEC, s0 + seg_len, 32 * VEC, below((float)(bin + 1) / to_bin * temp), [&](int v, float x) {
+            const float low = below((float)(bin + 1) / to_bin * temp);
+            sweep(s0 + lane * VEC, s0 + seg_len, 32 * VEC, low, [&](int v, float x) {
                 const float e = exp_of(x, r), at = place(x, r);   // NaN: no bin
                 mass += at < (float)bin && (e >= r.min_p || x == r.top) ? weight_of(e) : 0u;
                 if (at >= (float)bin && at < (float)(bin + 1) && x > -CUDART_INF_F) list_it(v, x);
@@ -949,7 +929,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 if (rank == 0 && tid < segs) sh.all_mass[tid] = cl.map_shared_rank(&sh, tid / kWarps)->warp_mass[tid % kWarps];
                 cl.sync();   // the others leave, as above
                 if (rank == 0) {
-                    pick(sh, key, w, base, [limit](uint32_t, unsigned long long m) { return !((double)m < limit); });
+                    pick(sh, key, w, entry_of(low, 0), entry_of(above((float)bin / to_bin * temp), kIndexTop), base,
+                         [limit](uint32_t, unsigned long long m) { return !((double)m < limit); });
 #pragma unroll
                     for (int i = 0; i < kListPer; ++i)
                         if (key[i] != 0 && key[i] >= sh.picked && (exp_of(logit_of(key[i]), r) >= r.min_p || logit_of(key[i]) == r.top)) {
