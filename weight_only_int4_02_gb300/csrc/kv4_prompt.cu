@@ -22,12 +22,16 @@
 //   O_A(h), S_A(h+2), O_B(h), S_B(h+2), ...
 // O is rescaled only when a row's maximum grew by more than 2^8 (its P stays below 2^15 until then).
 //
+// Queries and outputs go between registers and memory by way of shared memory, so that 16 (D = 64: 8) lanes
+// read or write a row together; a row a lane cost a CTA 4 us more.
+//
 // Three requests' chunks of 839 to 4000 tokens behind 5690 to 8200 cached ones, 32 query heads over
-// 8, D = 128, bfloat16: 915 us, 890 TFLOP/s, 47% of what a plain bf16 matrix product reaches. (Scores
-// by whole blocks, one S a tile: 1000 us.) The tensor pipe is busy for 51% of the time, the issue slots
-// for 49%, shared memory for much of the rest, and none of them alone is the limit: without the
+// 8, D = 128, bfloat16: 897 us, 910 TFLOP/s, 48% of what a plain bf16 matrix product reaches. (Scores
+// by whole blocks, one S a tile: 1000 us.) The tensor pipe is busy for half of the time, the issue slots
+// too, shared memory for much of the rest, and none of them alone is the limit: without the
 // exponentials, the scales or the unpacking it takes 0 to 5% less, with an eighth of the products 12%.
-// A CTA's start and end, which nothing overlaps, are 10 us of its 110.
+// Of a CTA's 110 us its start and end, which nothing overlaps, are about 9; CTAs that stay and
+// take the next rows themselves gained nothing there (929 us).
 #include "api_internal.cuh"
 #include "kv4.cuh"
 #include "launch.cuh"
@@ -46,8 +50,8 @@ constexpr int kMmaWarp = 12;
 constexpr int kThreads = 512;         // four warpgroups, of the last the MMA warp alone at work
 // Registers a thread: 128 at launch, moved to the softmax from the warps that need fewer. Each
 // of the SM's four quarters holds one warp of every warpgroup and a quarter of the registers.
-// 184/88/56 took 938 us where this takes 915.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 160, kUnpackRegs = 104, kIssueRegs = 88;
+// 160/104/88 take 904 us where this takes 897.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kUnpackRegs = 112, kIssueRegs = 96;
 static_assert(2 * kSoftmaxRegs + kUnpackRegs + kIssueRegs <= 4 * kLaunchRegs, "registers of the block");
 constexpr int kScaleStages = 4;       // K's scales live until the softmax has read them: two blocks past K itself
 constexpr int kGrow = 8;              // log2 of how far P may grow before O is rescaled
@@ -66,6 +70,7 @@ struct Prompt {
         uint32_t valid[kScaleStages][4];     // tokens that are stored and inside the request
         uint32_t odd[2][4];                  // tokens whose V scale is NaN
         uint32_t vred[2][4];
+        int exponent[2][kRows];              // of the queries' rows
         int ev[2];                           // V's scales so far are below 2^ev
         uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], skfull[kScaleStages], sfull[2][2], pfull[2][2], odone[2][2], teardown;
         uint32_t tmem;
@@ -225,48 +230,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         const bool live = row < rows;
         const int qi = row / p.group, hq = row - qi * p.group;
         const int pos = live ? seq - nq + qi : -1;
+        // lanes that move a row between memory and shared memory together, and rows of a warp's access
+        constexpr int kLanes = D / 8, kTogether = 32 / kLanes;
+        const int warp_row = (warp & 3) * 32;   // of the tile's rows
+        const long long q_off = live ? (long long)(q0 + qi) * p.q_token + (long long)(head * p.group + hq) * p.q_head : -1;
+        const long long o_off = live ? (long long)(q0 + qi) * p.o_token + (long long)(head * p.group + hq) * p.o_head : -1;
         float a;   // score = a * (s_k S) in powers of two
         {
-            uint32_t raw[D / 2];
-#pragma unroll
-            for (int i = 0; i < D / 2; ++i) raw[i] = 0;
-            if (live) {
-                const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.q + (long long)(q0 + qi) * p.q_token +
-                                                                  (long long)(head * p.group + hq) * p.q_head);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = src[i];
-                    raw[4 * i] = v.x;
-                    raw[4 * i + 1] = v.y;
-                    raw[4 * i + 2] = v.z;
-                    raw[4 * i + 3] = v.w;
-                }
-            }
             auto lo_of = [&](uint32_t x) { return BF ? __uint_as_float(x << 16) : __low2float(as_half2(x)); };
             auto hi_of = [&](uint32_t x) { return BF ? __uint_as_float(x & 0xffff0000u) : __high2float(as_half2(x)); };
-            float top = 0.0f;
+            // kLanes lanes read a row together, so that a warp's load is of few lines
+            uint4 raw[kLanes];
 #pragma unroll
-            for (int i = 0; i < D / 2; ++i) top = fmaxf(top, fmaxf(fabsf(lo_of(raw[i])), fabsf(hi_of(raw[i]))));
-            // largest magnitude into [2^9, 2^10), by a power of two; an infinity or a NaN stays one
-            int e = ((__float_as_int(top) >> 23) & 255) - 127 - 9;
-            e = (top == 0.0f || !(top <= FLT_MAX)) ? 0 : e < -120 ? -120 : e;
-            // a negative softmax scale goes into Q, so that the largest score is that of the largest product
-            const float f = p.scale_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
-            a = fabsf(p.scale_log2) * pow2i(e);
-            a = a > 0.0f ? a : FLT_MIN;   // scale 0: all scores nearly equal, and masked ones stay -infinity
+            for (int i = 0; i < kLanes; ++i) {
+                const long long off = __shfl_sync(0xffffffffu, q_off, i * kTogether + lane / kLanes);
+                raw[i] = off < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>((const uint16_t*)p.q + off) + lane % kLanes);
+            }
             const uint32_t qb = sbase + tile * C::QT;
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
+            for (int i = 0; i < kLanes; ++i) {
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                float top = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) top = fmaxf(top, fmaxf(fabsf(lo_of(w[c])), fabsf(hi_of(w[c]))));
+#pragma unroll
+                for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                // largest magnitude into [2^9, 2^10), by a power of two; an infinity or a NaN stays one
+                int e = ((__float_as_int(top) >> 23) & 255) - 127 - 9;
+                e = (top == 0.0f || !(top <= FLT_MAX)) ? 0 : e < -120 ? -120 : e;
+                // a negative softmax scale goes into Q, so that the largest score is that of the largest product
+                const float f = p.scale_log2 < 0.0f ? -pow2i(-e) : pow2i(-e);
                 float x[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = lo_of(raw[4 * j + i]) * f;
-                    x[2 * i + 1] = hi_of(raw[4 * j + i]) * f;
+                for (int c = 0; c < 4; ++c) {
+                    x[2 * c] = lo_of(w[c]) * f;
+                    x[2 * c + 1] = hi_of(w[c]) * f;
                 }
+                const int r = warp_row + i * kTogether + lane / kLanes;
+                if (lane % kLanes == 0) sh.exponent[tile][r] = e;
                 // the order in which a word of K's codes unpacks
-                sts128(qb + swizzled(row - row0 - tile * kRows, j, kRows), half2_bits(x[0], x[4]), half2_bits(x[1], x[5]),
+                sts128(qb + swizzled(r, lane % kLanes, kRows), half2_bits(x[0], x[4]), half2_bits(x[1], x[5]),
                        half2_bits(x[2], x[6]), half2_bits(x[3], x[7]));
             }
+            __syncwarp();
+            a = fabsf(p.scale_log2) * pow2i(sh.exponent[tile][warp_row + lane]);
+            a = a > 0.0f ? a : FLT_MIN;   // scale 0: all scores nearly equal, and masked ones stay -infinity
         }
         fence_proxy_async_smem();
         mbar_arrive(smem_addr(&sh.qfull));
@@ -421,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         }
         if (ok) {
             const float inv = l == 0.0f ? 0.0f : poisoned ? CUDART_NAN_F : pow2i(ev - 7 > -126 ? ev - 7 : -126) / l;
-            uint16_t* dst = (uint16_t*)p.out + (long long)(q0 + qi) * p.o_token + (long long)(head * p.group + hq) * p.o_head;
+            // through the tile's queries, which have been read, so that kLanes lanes write a row together
+            const uint32_t qb = sbase + tile * C::QT;
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
                 float x[16];
@@ -437,11 +446,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
                         r[j] = half2_bits(u, v);
                     }
                 }
-                if (live) {
-                    *reinterpret_cast<uint4*>(dst + c) = make_uint4(r[0], r[1], r[2], r[3]);
-                    *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(r[4], r[5], r[6], r[7]);
-                }
+                sts128(qb + swizzled(warp_row + lane, c / 8, kRows), r[0], r[1], r[2], r[3]);
+                sts128(qb + swizzled(warp_row + lane, c / 8 + 1, kRows), r[4], r[5], r[6], r[7]);
             }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i) {
+                const int r = i * kTogether + lane / kLanes;
+                const long long off = __shfl_sync(0xffffffffu, o_off, r);
+                const uint4 v = *reinterpret_cast<const uint4*>(smem + tile * C::QT + swizzled(warp_row + r, lane % kLanes, kRows));
+                if (off >= 0) *(reinterpret_cast<uint4*>((uint16_t*)p.out + off) + lane % kLanes) = v;
+            }
+            __syncwarp();
             if (live && p.lse)
                 p.lse[(long long)(q0 + qi) * p.q_heads + head * p.group + hq] =
                     l == 0.0f ? -CUDART_INF_F : (m * a + log2f(l)) * CUDART_LN2_F;
