@@ -439,6 +439,11 @@ w4a16_status w4a16_gemm_noalloc(const uint16_t* x, const uint32_t* packed,
  * synchronising and can be captured into a CUDA Graph (the first call on a device
  * outside capture); lengths, tables and settings are device arrays that are read
  * when the kernels run. Results are the same on every call with equal inputs.
+ * The kernels are launched with programmatic dependent launch too: one may take its
+ * place on the GPU early, but reads and writes nothing in memory before the kernel
+ * enqueued ahead of it has finished, and lets the next one start only after that.
+ * So any kernel may precede them, and a GEMM that follows one of them directly
+ * reads its weights early only from what was complete before that call's kernel.
  *
  * The cache: uint8 [pages][kv_heads][page_size / 16][16 * (D + 6)], 16-byte aligned,
  * w4a16_kv4_page_bytes() a page; D = head_dim is 64 or 128, page_size 16, 32, 64, 128

@@ -19,8 +19,15 @@
 // eight columns. Q is scaled per row by a power of two into binary16's range (exact
 // for binary16 and bfloat16 inputs). Probabilities times V's scale are fed as a high
 // and a low binary16 part, 22 bits: one part alone would add a rounding as large as that of
-// a binary16 output, and there is no time to gain (bound by bytes). Scores, sums, maxima
+// a binary16 output, for 5% of the time (62.8 us against 66.3 below). Scores, sums, maxima
 // and outputs are FP32.
+//
+// Measured, D = 128: 64 requests of 17 to 9000 cached tokens 67 us, 3.8 TB/s, 56% of a copy's rate; one of
+// 131072 tokens 43 us; D = 64, 48 requests of 1 to 5 drafted tokens and a window of 4096 21 us; one of 1000
+// tokens 11 us, most of it latency. Four CTAs an SM (128 registers a thread) keep the issue slots busy for 51% of the
+// time and the tensor pipe for 32%: a unit is about 610 warp instructions (241 of them integer, 117 FP32, 71 binary16
+// and MMAs), which wait for one another more than for memory. Eight or two warps a CTA, five CTAs an SM
+// (fewer registers) and tokens' scales through shared memory were slower.
 #include "api_internal.cuh"
 #include "kv4.cuh"
 #include "launch.cuh"
@@ -743,10 +750,12 @@ cudaError_t setup_kv4()
 // tokens times query heads) fill the GPU with its tiles of 256; which request is which is known on
 // the device, so such a batch gets both kernels. With fewer rows the stream-K kernel takes everything:
 // it cuts the cached tokens too. Measured for one request, D = 128, tcgen05 and stream-K in us:
-// 2000 rows over 8000 tokens 170 / 55; 8192 over 4000 96 / 98; 16384 over 4000 97 / 178; 8400
-// over 300 21 / 31; 800 over 1000 32 / 20. D = 64: 8192 over 4000 89 / 67.
+// 4096 rows over 4000 tokens 82 / 58; 6144 82 / 78; 8192 83 / 98; 16384 84 / 177; 8400 over 300
+// 14 / 30; 800 over 1000 26 / 20. D = 64: 8192 over 4000 80 / 67; 10752 84 / 84; 16384 81 / 119.
+// (Of few tokens the tcgen05 kernel takes fewer rows as well: 3200 over 300 14 / 21. How many tokens
+// are cached is not known on the host.)
 constexpr int kFewRows = 32;
-constexpr long long prompt_rows(int head_dim) { return head_dim == 128 ? 7168 : 10752; }
+constexpr long long prompt_rows(int head_dim) { return head_dim == 128 ? 6400 : 10752; }
 
 cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_q, int path, int sms, cudaStream_t stream)
 {
