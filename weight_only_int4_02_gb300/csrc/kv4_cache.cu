@@ -197,23 +197,18 @@ __device__ __forceinline__ Rows rows_of(const Kv4RowsParams& p)
     return r;
 }
 
-// A row's codes, four to a 16-bit word, its scale's bits and its zero-point.
-struct Quantised {
-    uint32_t w0, w1, zero;
-    __half scale;
+// What a row is stored with: 1 / s as a number, and s as binary16 bits below the zero-point and a poisoned row's flag.
+struct Stored {
+    float inv;
+    uint32_t word;
+    __device__ __forceinline__ uint32_t zero() const { return word >> 16 & 15u; }
+    __device__ __forceinline__ bool poisoned() const { return word >> 31; }
 };
 
-// One row per D/8 lanes, eight values a lane: the row's extremes by shuffles, then
-//   s = fp16(min((hi - lo) / 15, 65504)), z = clamp(rint(-lo / s), 0, 15),
-//   code = clamp(rint(x / s) + z, 0, 15)        (lo = min(x, 0), hi = max(x, 0))
-// with hi - lo formed from max(x, 0) and max(-x, 0), and 1 / s rounded once to FP32; every
-// operation is an IEEE one (no contraction, no approximate division), so the codes are the same
-// wherever the formula is evaluated. A row that holds an infinity or a NaN gets scale NaN, so
-// that it shows in whatever reads it.
-template <int D, int DTYPE>
-__device__ __forceinline__ Quantised quantise(const uint4& raw)
+// The extremes of eight values as a pair (max x, max -x) of the inputs' own type, exact; a NaN stays one.
+template <int DTYPE>
+__device__ __forceinline__ uint32_t extremes(const uint4& raw)
 {
-    // the row's extremes as a pair (max x, max -x) of the inputs' own type, exact; a NaN stays one
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t up = w[0], dn = negate2(w[0]);
 #pragma unroll
@@ -221,33 +216,54 @@ __device__ __forceinline__ Quantised quantise(const uint4& raw)
         up = max2<DTYPE>(up, w[i]);
         dn = max2<DTYPE>(dn, negate2(w[i]));
     }
-    uint32_t ext = max2<DTYPE>(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632));
-    ext = max2<DTYPE>(ext, 0u);
-#pragma unroll
-    for (int d = D / 16; d > 0; d >>= 1) ext = max2<DTYPE>(ext, __shfl_xor_sync(0xffffffffu, ext, d));
-    float hi, neg;   // max(x, 0) and max(-x, 0)
-    unpack2<DTYPE>(ext, hi, neg);
-    const bool poisoned = !isfinite(hi) || !isfinite(neg);
-    Quantised q;
-    q.scale = poisoned ? __ushort_as_half(0x7fff) : __float2half_rn(fminf(__fdiv_rn(__fadd_rn(hi, neg), 15.0f), 65504.0f));
-    const float s = __half2float(q.scale);
-    const float inv = !poisoned && s > 0.0f ? __frcp_rn(s) : 0.0f;
-    // rint by adding 1.5 * 2^23, whose last bit is 1: the sum's low bits are the whole number
+    return max2<DTYPE>(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632));
+}
+
+// rint by adding 1.5 * 2^23, whose last bit is 1: the sum's low bits are the whole number
+__device__ __forceinline__ int whole(float v, float inv)
+{
     constexpr float kRound = 12582912.0f;
-    auto whole = [&](float v) { return __float_as_int(__fadd_rn(__fmul_rn(v, inv), kRound)) - __float_as_int(kRound); };
-    const int z = poisoned ? 0 : min(whole(neg), 15);
-    q.zero = (uint32_t)z;
+    return __float_as_int(__fadd_rn(__fmul_rn(v, inv), kRound)) - __float_as_int(kRound);
+}
+
+// From a row's extremes
+//   s = fp16(min((hi - lo) / 15, 65504)), z = clamp(rint(-lo / s), 0, 15),
+// with hi - lo formed from max(x, 0) and max(-x, 0), and 1 / s rounded once to FP32; every
+// operation is an IEEE one (no contraction, no approximate division), so the codes are the same
+// wherever the formula is evaluated. A row that holds an infinity or a NaN gets scale NaN, so
+// that it shows in whatever reads it.
+template <int DTYPE>
+__device__ __forceinline__ Stored stored_of(uint32_t ext)
+{
+    float hi, neg;   // max(x, 0) and max(-x, 0)
+    unpack2<DTYPE>(max2<DTYPE>(ext, 0u), hi, neg);
+    if (!isfinite(hi) || !isfinite(neg)) return {0.0f, 0x80007fffu};
+    const __half scale = __float2half_rn(fminf(__fdiv_rn(__fadd_rn(hi, neg), 15.0f), 65504.0f));
+    const float s = __half2float(scale);
+    Stored r;
+    r.inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+    r.word = (uint32_t)__half_as_ushort(scale) | (uint32_t)min(whole(neg, r.inv), 15) << 16;
+    return r;
+}
+
+// Eight codes, four to a 16-bit word: clamp(rint(x / s) + z, 0, 15).
+template <int DTYPE>
+__device__ __forceinline__ uint32_t codes_of(const uint4& raw, const Stored& r)
+{
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    const int z = (int)r.zero();
     uint32_t code[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float a, b;
         unpack2<DTYPE>(w[i], a, b);
-        code[2 * i] = (uint32_t)max(min(whole(a) + z, 15), 0);
-        code[2 * i + 1] = (uint32_t)max(min(whole(b) + z, 15), 0);
+        code[2 * i] = (uint32_t)__vimin_s32_relu(whole(a, r.inv) + z, 15);
+        code[2 * i + 1] = (uint32_t)__vimin_s32_relu(whole(b, r.inv) + z, 15);
     }
-    q.w0 = poisoned ? 0u : code[0] | code[1] << 4 | code[2] << 8 | code[3] << 12;
-    q.w1 = poisoned ? 0u : code[4] | code[5] << 4 | code[6] << 8 | code[7] << 12;
-    return q;
+    uint32_t out = code[7];
+#pragma unroll
+    for (int i = 6; i >= 0; --i) out = out << 4 | code[i];
+    return r.poisoned() ? 0u : out;
 }
 
 // Index of the 16-bit word of V's codes that holds d = 8j .. 8j + 3 of a token; the next four are two words on.
@@ -276,15 +292,23 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowsParams p)
         v = __ldg(reinterpret_cast<const uint4*>((const uint16_t*)p.v + r.token * p.v_token + r.head * p.v_head + 8 * j));
         tile = tile_of(p, r.token, r.head, D, &tok);
     }
-    const Quantised a = quantise<D, DTYPE>(k), b = quantise<D, DTYPE>(v);
+    // Even lanes go on with K's row and odd ones with V's: extremes, scale and zero-point once a lane, not twice.
+    const uint32_t ek = extremes<DTYPE>(k), ev = extremes<DTYPE>(v);
+    const bool odd = j & 1;
+    uint32_t ext = max2<DTYPE>(odd ? ev : ek, __shfl_xor_sync(0xffffffffu, odd ? ek : ev, 1));
+#pragma unroll
+    for (int d = 2; d < D / 8; d <<= 1) ext = max2<DTYPE>(ext, __shfl_xor_sync(0xffffffffu, ext, d));
+    const Stored mine = stored_of<DTYPE>(ext);
+    const Stored other = {__shfl_xor_sync(0xffffffffu, mine.inv, 1), __shfl_xor_sync(0xffffffffu, mine.word, 1)};
+    const uint32_t a = codes_of<DTYPE>(k, odd ? other : mine), b = codes_of<DTYPE>(v, odd ? mine : other);
     if (tile == nullptr) return;
-    *reinterpret_cast<uint32_t*>(tile + tok * (D / 2) + 4 * j) = a.w0 | a.w1 << 16;
+    *reinterpret_cast<uint32_t*>(tile + tok * (D / 2) + 4 * j) = a;
     uint16_t* const dst = reinterpret_cast<uint16_t*>(tile + kv4_v_off(D)) + v_word<D>(tok, j);
-    dst[0] = (uint16_t)b.w0;
-    dst[2] = (uint16_t)b.w1;
+    dst[0] = (uint16_t)b;
+    dst[2] = (uint16_t)(b >> 16);
     if (j < 2) {   // lane 0 writes K's scale and zero-point, lane 1 V's
-        *reinterpret_cast<__half*>(tile + (j ? kv4_v_scale_off(D) : kv4_k_scale_off(D)) + 2 * tok) = j ? b.scale : a.scale;
-        tile[(j ? kv4_v_zero_off(D) : kv4_k_zero_off(D)) + tok] = (uint8_t)(j ? b.zero : a.zero);
+        *reinterpret_cast<uint16_t*>(tile + (j ? kv4_v_scale_off(D) : kv4_k_scale_off(D)) + 2 * tok) = (uint16_t)mine.word;
+        tile[(j ? kv4_v_zero_off(D) : kv4_k_zero_off(D)) + tok] = (uint8_t)mine.zero();
     }
 }
 
