@@ -33,8 +33,8 @@
 //
 // Bound by the chain of a row's steps (barriers of the CTA and the cluster, about 1 us each under load), a
 // weight's instructions where weights are summed, and shared atomics where they are binned: 128 rows of 131072
-// bfloat16 logits take 17 us greedy, 33 with no filter or top-k 50, 46 with top-k 500, 88 with top-p 0.95 alone,
-// and 49 mixed; one row of 32000 10 us.
+// bfloat16 logits take 17 us greedy, 33 with no filter or top-k 50, 45 with top-k 500, 86 with top-p 0.95 alone,
+// and 48 mixed; one row of 32000 9.6 us.
 #include "launch.cuh"
 #include "ptx.cuh"
 #include "sample.cuh"
@@ -87,6 +87,7 @@ struct Shared {
     int bin;
     uint32_t base_cnt, bin_cnt;
     unsigned long long base_mass, bin_mass, total;
+    unsigned long long limit;            // what a search compares with
     unsigned long long picked, picked_before;
     uint32_t picked_weight;
     // the chosen segment
@@ -196,12 +197,19 @@ __device__ __forceinline__ void add_mass(Histogram& h, int bin, uint32_t w)
 
 __device__ __forceinline__ unsigned long long mass_of(uint32_t a, uint32_t b) { return a + ((unsigned long long)b << 16); }
 
-// Finds the first bin with done(count, weight of every bin up to and with it, weight of all bins), from each
-// thread's two bins; base counts come on top. MASS: weights count, else only counts do. Leaves bin = -1 if there
-// is none; sh.bin is -1 on entry, and a barrier lies between that and here.
-template <bool MASS, typename F>
+// The least whole number that is not below a share of a weight: m < limit_of(...) is (double)m < (double)total * share.
+// 64-bit floating point is slow here, so one thread does it for a search, and the search compares whole numbers.
+__device__ __forceinline__ unsigned long long limit_of(unsigned long long total, float share)
+{
+    return __double2ull_ru((double)total * (double)share);
+}
+
+// Finds the first bin with done(count, weight of every bin up to and with it, limit), from each thread's two bins;
+// base counts come on top. MASS: weights count, else only counts do. The limit is bound(weight of all bins). Leaves
+// bin = -1 if there is none; sh.bin is -1 on entry, and a barrier lies between that and here.
+template <bool MASS, typename F, typename B>
 __device__ __forceinline__ void scan_bins(Shared& sh, const uint32_t (&cnt)[kPer], const unsigned long long (&mass)[kPer],
-                                          uint32_t base_cnt, unsigned long long base_mass, F done)
+                                          uint32_t base_cnt, unsigned long long base_mass, F done, B bound)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t ic = warp_incl(cnt[0] + cnt[1], lane);
@@ -222,10 +230,11 @@ __device__ __forceinline__ void scan_bins(Shared& sh, const uint32_t (&cnt)[kPer
         all += __shfl_sync(0xffffffffu, wm, 31);
         if (threadIdx.x == 0) sh.total = all;
     }
-    bool before = done(c, m, all);
+    const unsigned long long limit = bound(all);
+    bool before = done(c, m, limit);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const bool now = done(c + cnt[i], m + mass[i], all);
+        const bool now = done(c + cnt[i], m + mass[i], limit);
         if (now && !before) {
             sh.bin = threadIdx.x * kPer + i;
             sh.base_cnt = c;
@@ -242,9 +251,9 @@ __device__ __forceinline__ void scan_bins(Shared& sh, const uint32_t (&cnt)[kPer
 
 // scan_bins over the sum of the cluster's histograms; every CTA finds the same. A cluster barrier before
 // (the histograms are complete) is in here; the caller keeps one between this and the next use of the histogram.
-template <bool MASS, typename F>
+template <bool MASS, typename F, typename B>
 __device__ __forceinline__ void search(cg::cluster_group& cl, Shared& sh, Histogram& hist, uint32_t base_cnt,
-                                       unsigned long long base_mass, F done)
+                                       unsigned long long base_mass, F done, B bound)
 {
     if (threadIdx.x == 0) sh.bin = -1;
     cl.sync();
@@ -278,19 +287,22 @@ __device__ __forceinline__ void search(cg::cluster_group& cl, Shared& sh, Histog
             }
         }
     }
-    scan_bins<MASS>(sh, cnt, mass, base_cnt, base_mass, done);
+    scan_bins<MASS>(sh, cnt, mass, base_cnt, base_mass, done, bound);
 }
 
 // In one CTA: of this thread's entries (0: none; all others different and in kmin .. kmax), the one at which
-// done(count, weight of every entry from the greatest key down to it) becomes true, in sh.picked (0 if there is
-// none), with what is before it and its weight. Ten bits of the keys' range at a time, until a bin has one entry.
-template <typename F>
+// done(count, weight of every entry from the greatest key down to it, limit) becomes true, in sh.picked (0 if there is
+// none), with what is before it and its weight; the limit is bound(), by one thread. Ten bits of the keys' range at a time, until a bin has one entry.
+template <typename F, typename B>
 __device__ __forceinline__ void pick(Shared& sh, const unsigned long long (&key)[kListPer], const uint32_t (&w)[kListPer],
-                                     unsigned long long kmin, unsigned long long kmax, unsigned long long base_mass, F done)
+                                     unsigned long long kmin, unsigned long long kmax, unsigned long long base_mass, F done, B bound)
 {
     const int tid = threadIdx.x;
     __syncthreads();   // what was picked before has been read
-    if (tid == 0) sh.picked = 0;
+    if (tid == 0) {
+        sh.picked = 0;
+        sh.limit = bound();
+    }
     uint32_t base_cnt = 0;
     for (int level = 0; level < 7; ++level) {
         const unsigned long long range = kmax - kmin;
@@ -317,8 +329,7 @@ __device__ __forceinline__ void pick(Shared& sh, const unsigned long long (&key)
             cnt[i] = sh.keys.cnt[b];
             mass[i] = mass_of(sh.keys.part[0][b], sh.keys.part[1][b]);
         }
-        scan_bins<true>(sh, cnt, mass, base_cnt, base_mass,
-                        [&](uint32_t c, unsigned long long m, unsigned long long) { return done(c, m); });
+        scan_bins<true>(sh, cnt, mass, base_cnt, base_mass, done, [&](unsigned long long) { return sh.limit; });
         if (sh.bin < 0) break;
         base_cnt = sh.base_cnt;
         base_mass = sh.base_mass;
@@ -592,6 +603,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         return warp_sum(v);
     };
 
+    const uint32_t kk = (uint32_t)k;
+    auto by_count = [kk](uint32_t c, unsigned long long, unsigned long long) { return c >= kk; };
+    auto by_mass = [](uint32_t, unsigned long long m, unsigned long long limit) { return m >= limit; };
+    auto no_bound = [](unsigned long long) { return 0ull; };
     if (need_k && k <= kListMax / 2) {
         // a bound below at least k tokens: the bin of the k-th largest of the groups' maxima
 #pragma unroll
@@ -599,8 +614,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const float b = place(tops[i], r);
             if (tops[i] > -CUDART_INF_F && b < (float)kBins) atomicAdd(&sh.bins.cnt[whole(b)], 1u);
         }
-        const uint32_t kk = (uint32_t)k;
-        search<false>(cl, sh, sh.bins, 0u, 0ull, [kk](uint32_t c, unsigned long long, unsigned long long) { return c >= kk; });
+        search<false>(cl, sh, sh.bins, 0u, 0ull, by_count, no_bound);
         if (sh.bin >= 0) {
             // down to the bin's lower end, and a few tokens more
             const float low = below((float)(sh.bin + 1) / to_bin * temp);
@@ -638,13 +652,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     }
                     bool keep = i < n && ahead < k;
                     unsigned long long total = block_sum(keep && (tid & 3) == 0 ? own_w : 0u);
-                    const double limit = (double)total * (double)top_p;
+                    if (tid == 0) sh.limit = need_p ? limit_of(total, top_p) : ~0ull;
+                    __syncthreads();
                     const float x = logit_of(own);
-                    keep = keep && (ahead == 0 || !need_p || (double)before < limit) && (ahead == 0 || exp_of(x, r) >= r.min_p || x == r.top);
+                    keep = keep && (ahead == 0 || before < sh.limit) && (ahead == 0 || exp_of(x, r) >= r.min_p || x == r.top);
                     total = block_sum(keep && (tid & 3) == 0 ? own_w : 0u);
                     if (!keep && i < n) ws[i] = 0u;
+                    if (tid == 0) sh.limit = target_of(total);
                     __syncthreads();
-                    const unsigned long long target = target_of(total);
+                    const unsigned long long target = sh.limit;
                     before = 0;
                     for (int j = tid & 3; j < n; j += 4)
                         if (((uint32_t)keys[j] & kIndexTop) > ((uint32_t)own & kIndexTop)) before += ws[j];
@@ -656,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     unsigned long long least = entry_of(low, 0), greatest = entry_of(r.top, kIndexTop);
                     // the k-th entry, the entry at which top-p's limit is passed, and the drawn one among the kept
                     if (n > k) {
-                        pick(sh, key, w, least, greatest, 0ull, [kk](uint32_t c, unsigned long long) { return c >= kk; });
+                        pick(sh, key, w, least, greatest, 0ull, by_count, [] { return 0ull; });
                         least = sh.picked;
 #pragma unroll
                         for (int i = 0; i < kListPer; ++i)
@@ -667,8 +683,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     for (int i = 0; i < kListPer; ++i) sum += w[i];
                     unsigned long long total = block_sum(sum);
                     if (need_p) {
-                        const double limit = (double)total * (double)top_p;
-                        pick(sh, key, w, least, greatest, 0ull, [limit](uint32_t, unsigned long long m) { return !((double)m < limit); });
+                        pick(sh, key, w, least, greatest, 0ull, by_mass, [&] { return limit_of(total, top_p); });
                         const unsigned long long last = sh.picked;
 #pragma unroll
                         for (int i = 0; i < kListPer; ++i)
@@ -688,9 +703,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     // by index now: the low bits, greatest first, are ascending indices (one bit on top, as 0 is no entry)
 #pragma unroll
                     for (int i = 0; i < kListPer; ++i) key[i] = key[i] ? 1ull << kIndexBits | (key[i] & kIndexTop) : 0ull;
-                    const unsigned long long target = target_of(total);
                     pick(sh, key, w, 1ull << kIndexBits, (2ull << kIndexBits) - 1ull, 0ull,
-                         [target](uint32_t, unsigned long long m) { return m > target; });
+                         [](uint32_t, unsigned long long m, unsigned long long target) { return m > target; },
+                         [&] { return target_of(total); });
                     if (tid == 0) result(token_of(sh.picked), (double)sh.picked_weight / (double)total);
                 }
                 return;
@@ -768,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     // The cut inside a bin found by search(), where a list would not hold it: the bin's range of keys, then
     // histograms over the keys until one is left; n(count before, weight before, ties, a tie's weight) of that
     // key's tokens are kept, the first by index.
-    auto refine = [&](auto done, auto n) {
+    auto refine = [&](auto done, unsigned long long limit, auto n) {
         const int bin = sh.bin;
         uint32_t cnt0 = sh.base_cnt;
         unsigned long long mass0 = sh.base_mass;
@@ -812,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     add_mass(sh.keys, at, weight_of(exp_of(x, r)));
                 }
             });
-            search<true>(cl, sh, sh.keys, cnt0, mass0, done);
+            search<true>(cl, sh, sh.keys, cnt0, mass0, done, [limit](unsigned long long) { return limit; });
             cnt0 = sh.base_cnt;
             mass0 = sh.base_mass;
             if (shift == 0) break;
@@ -878,12 +893,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 add_mass(sh.bins, b, weight);
             }
         });
-        const uint32_t kk = (uint32_t)k;
-        auto by_count = [kk](uint32_t c, unsigned long long, unsigned long long) { return c >= kk; };
-        search<true>(cl, sh, sh.bins, 0u, 0ull, by_count);
+        search<true>(cl, sh, sh.bins, 0u, 0ull, by_count, no_bound);
         unsigned long long total = sh.total;
         if (sh.bin >= 0)
-            refine(by_count, [&](uint32_t c, unsigned long long m, uint32_t, uint32_t weight) {
+            refine(by_count, 0ull, [&](uint32_t c, unsigned long long m, uint32_t, uint32_t weight) {
                 total = m + (unsigned long long)(kk - c) * weight;
                 return kk - c;
             });
@@ -893,10 +906,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const float k_x = cut_x;
             const int k_at = cut_at;
             const double limit = (double)total * (double)top_p;
-            auto by_mass = [limit](uint32_t, unsigned long long m, unsigned long long) { return !((double)m < limit); };
-            search<true>(cl, sh, sh.bins, 0u, 0ull, by_mass);
+            const unsigned long long least = limit_of(total, top_p);
+            search<true>(cl, sh, sh.bins, 0u, 0ull, by_mass, [least](unsigned long long) { return least; });
             if (sh.bin >= 0) {
-                refine(by_mass, [&](uint32_t, unsigned long long m, uint32_t ties, uint32_t weight) {
+                refine(by_mass, least, [&](uint32_t, unsigned long long m, uint32_t ties, uint32_t weight) {
                     return kept_ties(limit, m, ties, weight);
                 });
                 if (k_x > cut_x || (k_x == cut_x && k_at < cut_at)) {
@@ -912,13 +925,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             if (weight) add_mass(sh.bins, whole(place(x, r)), weight);   // a token that weighs lies inside the bins
         });
         // the bin past which the weight before a token is no longer below top_p times the whole
-        search<true>(cl, sh, sh.bins, 0u, 0ull, [top_p](uint32_t, unsigned long long m, unsigned long long all) {
-            return !((double)m < (double)all * (double)top_p);
+        search<true>(cl, sh, sh.bins, 0u, 0ull, by_mass, [&](unsigned long long all) {
+            if (tid == 0) sh.limit = limit_of(all, top_p);
+            __syncthreads();
+            return sh.limit;
         });
         if (sh.bin >= 0) {
-            const double limit = (double)sh.total * (double)top_p;
+            const unsigned long long limit = sh.limit, total = sh.total, base = sh.base_mass;
             const int bin = sh.bin;
-            const unsigned long long base = sh.base_mass;
             // one pass sums what lies above the bin, by segments, and lists the bin's tokens
             unsigned long long mass = 0;
             const float low = below((float)(bin + 1) / to_bin * temp);
@@ -936,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 cl.sync();   // the others leave, as above
                 if (rank == 0) {
                     pick(sh, key, w, entry_of(low, 0), entry_of(above((float)bin / to_bin * temp), kIndexTop), base,
-                         [limit](uint32_t, unsigned long long m) { return !((double)m < limit); });
+                         by_mass, [limit] { return limit; });
 #pragma unroll
                     for (int i = 0; i < kListPer; ++i)
                         if (key[i] != 0 && key[i] >= sh.picked && (exp_of(logit_of(key[i]), r) >= r.min_p || logit_of(key[i]) == r.top)) {
@@ -952,10 +966,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 }
                 return;
             }
-            refine([limit](uint32_t, unsigned long long m, unsigned long long) { return !((double)m < limit); },
-                   [&](uint32_t, unsigned long long m, uint32_t ties, uint32_t weight) {
-                       return kept_ties(limit, m, ties, weight);
-                   });
+            const double share = (double)total * (double)top_p;
+            refine(by_mass, limit, [&](uint32_t, unsigned long long m, uint32_t ties, uint32_t weight) {
+                return kept_ties(share, m, ties, weight);
+            });
         }
     }
 
@@ -986,7 +1000,7 @@ cudaError_t launch_sample(const SampleParams& in, int sms, cudaStream_t stream)
     // As many CTAs a row as give every SM the two it holds, while a slice is more than a round of loads; up
     // to the portable cluster of eight. A row's steps are a chain, so that fewer, longer slices leave it waiting
     // (256 x 100003 FP32: 243 us with one CTA a row, 77 with two, 96 with four; 128 x 131072 bfloat16: 65 with
-    // two, 55 with four, 84 with eight; now 72 and 49). More where a slice would pass kMaxSlice.
+    // two, 55 with four, 84 with eight; now 71 and 48). More where a slice would pass kMaxSlice.
     auto slice_of = [&](int n) { return ((p.vocab + 16 / size + n - 1) / n + step - 1) / step * step; };
     int ctas = 1;
     while (ctas < kMaxCluster && (((long long)p.batch * ctas < 2 * sms && p.vocab / ctas > step) || slice_of(ctas) > kMaxSlice)) ctas *= 2;
