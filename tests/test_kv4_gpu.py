@@ -234,6 +234,32 @@ def test_several_queries(D, dtype, heads, group, nq, window):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("group,nq", [(4, 4), (3, 5), (8, 4), (4, 6)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_batches_of_several_queries(D, dtype, group, nq, window):
+    """Enough rows that segments of 16 are taken where they pay (12 to 16 and 32 rows a KV head, not 24)."""
+    r = np.random.default_rng(group * nq)
+    lens = r.integers(0, nq + 1, 96)
+    lens[:3] = nq
+    seq = lens + r.integers(0, 150, 96) * (r.random(96) < 0.9)
+    seq[1], seq[2] = 777, max(0, nq - 2)
+    args = batch_of([int(x) for x in seq], [int(x) for x in lens], 2, group, D, 16, dtype, nq)
+    assert args[0].shape[0] * args[0].shape[1] > 1024
+    out, lse = run(*args, 16, window)
+    check(*args, 16, window, out, lse)
+    # a poisoned token shows in the row that sees it alone, a missing page hides its tokens
+    q, cache, table, seq, starts = args
+    t = int(seq[1]) - 1
+    cache[table[1, t // 16], 1, 0, 16 * D + 32 + 2 * (t % 16):][:2] = [0, 126]
+    table[0, 0] = -1
+    out, _ = run(*args, 16, window)
+    check(*args, 16, window, out, None)
+    bad = torch.isnan(out).any(-1)
+    assert bad[2 * nq - 1, group:].all() and int(bad.sum()) == group
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_more_queries_than_tokens_leave_rows_empty(D):
     args = batch_of([3, 40], [9, 3], 2, 2, D, 16, "float16", 5)
     out, lse = run(*args, 16)

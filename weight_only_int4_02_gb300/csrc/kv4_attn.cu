@@ -755,6 +755,11 @@ cudaError_t setup_kv4()
 // (Of few tokens the tcgen05 kernel takes fewer rows as well: 3200 over 300 14 / 21. How many tokens
 // are cached is not known on the host.)
 constexpr int kFewRows = 32;
+// Segments of 16 rows cost 1.75 times those of 8, and half as many CTAs fit an SM: 8 where they are fewer than 1.75
+// times as many (9 to 16 rows of 64 requests over 4000 tokens, D = 128, 102 / 118 us with 16 / 8; 17 to 24 rows 184 / 168;
+// 32 rows 188 / 219), and where the rows are too few for throughput to count (one request of 16 rows over 8000 tokens
+// 29 / 21; eight of 16 over 1000 21 / 17; eight of 32 over 8000 59 / 66).
+constexpr int kNarrowRows = 1024;
 constexpr long long prompt_rows(int head_dim) { return head_dim == 128 ? 6400 : 10752; }
 
 cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_q, int path, int sms, cudaStream_t stream)
@@ -764,7 +769,8 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_
     const bool prompt = rows > kFewRows && path != 1 &&
                         (path == 2 || (long long)p.tokens * p.q_heads >= prompt_rows(head_dim));
     p.few_rows = prompt ? kFewRows : INT_MAX;
-    const bool wide = rows > 8;
+    const long long held = prompt && rows > kFewRows ? kFewRows : rows;   // of a request that is this kernel's, at most
+    const bool wide = 4 * ((held + 7) / 8) >= 7 * ((held + 15) / 16) && (long long)p.tokens * p.q_heads > kNarrowRows;
     cudaError_t e;
     if (head_dim == 128) e = wide ? Launch<128, 2>::run(p, sms, stream) : Launch<128, 1>::run(p, sms, stream);
     else e = wide ? Launch<64, 2>::run(p, sms, stream) : Launch<64, 1>::run(p, sms, stream);
