@@ -1,7 +1,7 @@
 // Attention over the 4-bit paged cache for few query rows (a decode step, drafted
 // tokens): O = softmax(scale * Q K^T) V with K, V = (code - zero) * scale.
 //
-// A segment is one request's KV head and up to 8 NR rows (query token, query head of
+// A segment is one request's KV head and up to 8 NR rows, or four (query token, query head of
 // the group); its cached tokens are cut into units of 32, and the units of all segments,
 // laid end to end, are dealt to the CTAs in equal runs (stream-K), so ragged lengths, one
 // long request and a thousand short ones fill the GPU alike. The lengths stay on the
@@ -19,12 +19,14 @@
 // eight columns. Q is scaled per row by a power of two into binary16's range (exact
 // for binary16 and bfloat16 inputs). Probabilities times V's scale are fed as a high
 // and a low binary16 part, 22 bits: one part alone would add a rounding as large as that of
-// a binary16 output, for 5% of the time (62.8 us against 66.3 below). Scores, sums, maxima
-// and outputs are FP32.
+// a binary16 output, for 5% of the time (62.8 us against 66.3 below). Where four rows are enough they stand twice
+// in the eight columns: the second four's lanes, which know the same probabilities, feed the low parts, so
+// that V takes half the MMAs (one request of 131072 tokens 43.2 -> 42.3 us). Scores, sums, maxima and outputs
+// are FP32.
 //
-// Measured, D = 128: 64 requests of 17 to 9000 cached tokens 67 us, 3.8 TB/s, 56% of a copy's rate; one of
-// 131072 tokens 43 us; D = 64, 48 requests of 1 to 5 drafted tokens and a window of 4096 21 us; one of 1000
-// tokens 11 us, most of it latency. Four CTAs an SM (128 registers a thread) keep the issue slots busy for 51% of the
+// Measured, D = 128: 64 requests of 257 to 16384 cached tokens 67 us, 3.8 TB/s, 56% of a copy's rate; one of
+// 131072 tokens 42 us; D = 64, 48 requests of 1 to 5 drafted tokens and a window of 4096 17 us; one of 1000
+// tokens 10.6 us, most of it latency. Four CTAs an SM (128 registers a thread) keep the issue slots busy for 51% of the
 // time and the tensor pipe for 32%: a unit is about 610 warp instructions (241 of them integer, 117 FP32, 71 binary16
 // and MMAs), which wait for one another more than for memory. Eight or two warps a CTA, five CTAs an SM
 // (fewer registers) and tokens' scales through shared memory were slower.
@@ -111,8 +113,10 @@ __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b)
 
 template <int D, int NR>
 struct Attn {
-    static constexpr int ROWS = 8 * NR;
-    static constexpr int CTAS = NR == 1 ? 4 : D == 64 ? 3 : 2;   // on an SM, as registers and rings allow
+    static constexpr bool FOUR = NR == 0;       // four rows, twice in an MMA's eight columns
+    static constexpr int G = FOUR ? 1 : NR;     // columns, in eights
+    static constexpr int ROWS = FOUR ? 4 : 8 * NR;
+    static constexpr int CTAS = NR <= 1 ? 4 : D == 64 ? 3 : 2;   // on an SM, as registers and rings allow
     static constexpr int STAGES = D == 128 ? 3 : 4;   // units in flight per warp
     static constexpr int TB = kv4_tile_bytes(D);
     static constexpr int STAGE = 2 * TB;
@@ -151,7 +155,8 @@ template <int D, int NR>
 __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(const Kv4AttnParams p)
 {
     using A = Attn<D, NR>;
-    constexpr int W = A::W, ROWS = A::ROWS;
+    constexpr int W = A::W, ROWS = A::ROWS, G = A::G;
+    constexpr bool FOUR = A::FOUR;
     extern __shared__ __align__(128) uint8_t smem[];
     typename A::Shared& sh = *reinterpret_cast<typename A::Shared*>(smem + kWarps * A::RING);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -285,12 +290,12 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
         for (int i = 0; i < A::STAGES; ++i) issue_next();
 
         // ---- Q fragments, scaled per row by a power of two; row constants of the columns 2c, 2c + 1
-        uint32_t ql[NR][W][2], qh[NR][W][2];
-        float row_a[NR][2], row_z[NR][2];   // score = row_a * s_k * (MMA + z_k * row_z), in powers of two
-        int row_pos[NR][2];
+        uint32_t ql[G][W][2], qh[G][W][2];
+        float row_a[G][2], row_z[G][2];   // score = row_a * s_k * (MMA + z_k * row_z), in powers of two
+        int row_pos[G][2];
 #pragma unroll
-        for (int g = 0; g < NR; ++g) {
-            const int row = row0 + g * 8 + n;
+        for (int g = 0; g < G; ++g) {
+            const int row = row0 + g * 8 + (FOUR ? n & 3 : n);
             uint32_t raw[4 * W];
 #pragma unroll
             for (int i = 0; i < 4 * W; ++i) raw[i] = 0;
@@ -348,14 +353,14 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                 const float un = __shfl_sync(0xffffffffu, unit, (2 * c + i) * 4);
                 row_a[g][i] = un > 0.0f ? un : FLT_MIN;   // scale 0: all scores nearly equal, masked ones stay -infinity
                 row_z[g][i] = __shfl_sync(0xffffffffu, qsum, (2 * c + i) * 4) * -0x1p-24f;
-                const int rr = row0 + g * 8 + 2 * c + i;
+                const int rr = row0 + g * 8 + (FOUR ? 2 * (c & 1) + i : 2 * c + i);
                 row_pos[g][i] = rr < r.rows ? r.seq - r.nq + rr / p.group : -1;
             }
         }
-        float m[NR][2], l[NR][2], zs[NR][2], o[NR][2 * W][4];
+        float m[G][2], l[G][2], zs[G][2], o[G][2 * W][4];
         int ev = -40;   // V's scales seen so far are at most 2^ev
 #pragma unroll
-        for (int g = 0; g < NR; ++g) {
+        for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 m[g][i] = -CUDART_INF_F;
@@ -380,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
             const bool full = have == 3u && t0 + kUnit - 1 <= pos_min && (p.window <= 0 || t0 > pos_max - p.window);
 
             // s_k times the products of the unit's two tiles: tokens n and n + 8 of each, rows 2c and 2c + 1
-            float sc[2][NR][4];
+            float sc[2][G][4];
             float vs[2][2], vz[2][2];
 #pragma unroll
             for (int tl = 0; tl < 2; ++tl) {
@@ -398,29 +403,29 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                     vz[tl][j] = (float)tile[kv4_v_zero_off(D) + tok];
                     // the sums start from the zero-points' share
 #pragma unroll
-                    for (int g = 0; g < NR; ++g) {
+                    for (int g = 0; g < G; ++g) {
                         sc[tl][g][2 * j] = kz * row_z[g][0];
                         sc[tl][g][2 * j + 1] = kz * row_z[g][1];
                     }
                 }
                 // low and high nibbles in sums of their own: two short chains of MMAs instead of a long one
-                float sh4[NR][4];
+                float sh4[G][4];
 #pragma unroll
-                for (int g = 0; g < NR; ++g)
+                for (int g = 0; g < G; ++g)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sh4[g][i] = 0.0f;
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     const uint32_t ka8 = ka[w] >> 8, kb8 = kb[w] >> 8;
 #pragma unroll
-                    for (int g = 0; g < NR; ++g)
+                    for (int g = 0; g < G; ++g)
                         mma_16816(sc[tl][g], ka[w] & kLow, kb[w] & kLow, ka8 & kLow, kb8 & kLow, ql[g][w][0], ql[g][w][1]);
 #pragma unroll
-                    for (int g = 0; g < NR; ++g)
+                    for (int g = 0; g < G; ++g)
                         mma_16816(sh4[g], ka[w] & kHigh, kb[w] & kHigh, ka8 & kHigh, kb8 & kHigh, qh[g][w][0], qh[g][w][1]);
                 }
 #pragma unroll
-                for (int g = 0; g < NR; ++g)
+                for (int g = 0; g < G; ++g)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sc[tl][g][i] = (sc[tl][g][i] + sh4[g][i]) * ks[i >> 1];
             }
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                         const bool odd = there && vs[tl][j] != vs[tl][j];   // a poisoned row of V
                         if (!there || odd) vs[tl][j] = vz[tl][j] = 0.0f;
 #pragma unroll
-                        for (int g = 0; g < NR; ++g)
+                        for (int g = 0; g < G; ++g)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const bool see = there && key <= row_pos[g][i] &&
@@ -448,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
             float vf = pow2i(15 - kGrow - ev);
             bool grow = false;
 #pragma unroll
-            for (int g = 0; g < NR; ++g)
+            for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float x = fmaxf(fmaxf(sc[0][g][i], sc[0][g][2 + i]), fmaxf(sc[1][g][i], sc[1][g][2 + i]));
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                 const int en = ev_new > ev ? ev_new : ev;
                 const float shift = pow2i(ev - en);
 #pragma unroll
-                for (int g = 0; g < NR; ++g) {
+                for (int g = 0; g < G; ++g) {
                     float f[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -485,19 +490,19 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                 ev = en;
                 vf = pow2i(15 - kGrow - ev);   // probabilities are fed below 2^15, clear of subnormals
             }
-            float ref[NR][2];
+            float ref[G][2];
 #pragma unroll
-            for (int g = 0; g < NR; ++g)
+            for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) ref[g][i] = m[g][i] == -CUDART_INF_F ? 0.0f : m[g][i];
 #pragma unroll
             for (int tl = 0; tl < 2; ++tl) {
-                uint32_t ph[NR][2], pl[NR][2];
+                uint32_t ph[G][2], pl[G][2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float v = vs[tl][j] * vf;
 #pragma unroll
-                    for (int g = 0; g < NR; ++g) {
+                    for (int g = 0; g < G; ++g) {
                         float pv[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -508,8 +513,13 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                         }
                         const uint32_t h = half2_bits(pv[0], pv[1]);
                         const float2 back = bits_half2(h);
-                        ph[g][j] = transpose8(h);
-                        pl[g][j] = transpose8(half2_bits(pv[0] - back.x, pv[1] - back.y));
+                        const uint32_t low = half2_bits(pv[0] - back.x, pv[1] - back.y);
+                        if constexpr (FOUR) {
+                            ph[g][j] = transpose8(c < 2 ? h : low);   // the second four columns are the low parts
+                        } else {
+                            ph[g][j] = transpose8(h);
+                            pl[g][j] = transpose8(low);
+                        }
                     }
                 }
                 const uint8_t* const tile = st + tl * A::TB + kv4_v_off(D);
@@ -520,11 +530,13 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                 for (int w = 0; w < W; ++w) {
                     const uint32_t va8 = va[w] >> 8, vb8 = vb[w] >> 8;
 #pragma unroll
-                    for (int g = 0; g < NR; ++g) {
+                    for (int g = 0; g < G; ++g) {
                         mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, ph[g][0], ph[g][1]);
                         mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, ph[g][0], ph[g][1]);
-                        mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, pl[g][0], pl[g][1]);
-                        mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, pl[g][0], pl[g][1]);
+                        if constexpr (!FOUR) {
+                            mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, pl[g][0], pl[g][1]);
+                            mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, pl[g][0], pl[g][1]);
+                        }
                     }
                 }
             }
@@ -544,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
         float* const mine = reinterpret_cast<float*>(ring);
         const float o_unit = pow2i(ev - (15 - kGrow));
 #pragma unroll
-        for (int g = 0; g < NR; ++g) {
+        for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -552,15 +564,22 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                     l[g][i] += __shfl_xor_sync(0xffffffffu, l[g][i], d);
                     zs[g][i] += __shfl_xor_sync(0xffffffffu, zs[g][i], d);
                 }
-                if (n == 0) {
+                if (n == 0 && (!FOUR || c < 2)) {
                     sh.m[warp][g * 8 + 2 * c + i] = m[g][i];
                     sh.l[warp][g * 8 + 2 * c + i] = l[g][i];
                 }
+            }
+            if constexpr (FOUR) {   // low and high parts of the probabilities
+#pragma unroll
+                for (int w = 0; w < 2 * W; ++w)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[g][w][i] += __shfl_xor_sync(0xffffffffu, o[g][w][i], 2);
             }
 #pragma unroll
             for (int w = 0; w < W; ++w)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
+                    if (FOUR && c >= 2) continue;
                     // codes in low nibbles come as c * 2^-24, in high ones as c * 2^-20
                     float4 x;
                     x.x = (o[g][2 * w][i] * 16777216.0f - zs[g][i]) * o_unit;
@@ -730,8 +749,10 @@ size_t kv4_partial_bytes(int sms)
         const size_t bytes = (size_t)2 * grid * part * sizeof(float);
         need = bytes > need ? bytes : need;
     };
+    most(Launch<64, 0>::grid_of(sms), Attn<64, 0>::PART);
     most(Launch<64, 1>::grid_of(sms), Attn<64, 1>::PART);
     most(Launch<64, 2>::grid_of(sms), Attn<64, 2>::PART);
+    most(Launch<128, 0>::grid_of(sms), Attn<128, 0>::PART);
     most(Launch<128, 1>::grid_of(sms), Attn<128, 1>::PART);
     most(Launch<128, 2>::grid_of(sms), Attn<128, 2>::PART);
     return need;
@@ -740,7 +761,8 @@ size_t kv4_partial_bytes(int sms)
 cudaError_t setup_kv4()
 {
     cudaError_t e;
-    if ((e = Launch<64, 1>::setup()) != cudaSuccess || (e = Launch<64, 2>::setup()) != cudaSuccess ||
+    if ((e = Launch<64, 0>::setup()) != cudaSuccess || (e = Launch<128, 0>::setup()) != cudaSuccess ||
+        (e = Launch<64, 1>::setup()) != cudaSuccess || (e = Launch<64, 2>::setup()) != cudaSuccess ||
         (e = Launch<128, 1>::setup()) != cudaSuccess || (e = Launch<128, 2>::setup()) != cudaSuccess)
         return e;
     return setup_kv4_prompt();
@@ -772,8 +794,10 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_
     const long long held = prompt && rows > kFewRows ? kFewRows : rows;   // of a request that is this kernel's, at most
     const bool wide = 4 * ((held + 7) / 8) >= 7 * ((held + 15) / 16) && (long long)p.tokens * p.q_heads > kNarrowRows;
     cudaError_t e;
-    if (head_dim == 128) e = wide ? Launch<128, 2>::run(p, sms, stream) : Launch<128, 1>::run(p, sms, stream);
-    else e = wide ? Launch<64, 2>::run(p, sms, stream) : Launch<64, 1>::run(p, sms, stream);
+    if (head_dim == 128)
+        e = held <= 4 ? Launch<128, 0>::run(p, sms, stream) : wide ? Launch<128, 2>::run(p, sms, stream) : Launch<128, 1>::run(p, sms, stream);
+    else
+        e = held <= 4 ? Launch<64, 0>::run(p, sms, stream) : wide ? Launch<64, 2>::run(p, sms, stream) : Launch<64, 1>::run(p, sms, stream);
     if (e != cudaSuccess || !prompt) return e;
     return launch_kv4_prompt(p, head_dim, stream);
 }
