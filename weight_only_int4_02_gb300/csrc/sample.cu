@@ -33,8 +33,8 @@
 //
 // Bound by the chain of a row's steps (barriers of the CTA and the cluster, about 1 us each under load), a
 // weight's instructions where weights are summed, and shared atomics where they are binned: 128 rows of 131072
-// bfloat16 logits take 17 us greedy, 33 with no filter or top-k 50, 45 with top-k 500, 86 with top-p 0.95 alone,
-// and 48 mixed; one row of 32000 9.6 us.
+// bfloat16 logits take 17 us greedy, 33 with no filter or top-k 50, 42 with top-k 500, 84 with top-p 0.95 alone,
+// and 47 mixed; one row of 32000 9.6 us.
 #include "launch.cuh"
 #include "ptx.cuh"
 #include "sample.cuh"
@@ -90,6 +90,7 @@ struct Shared {
     unsigned long long limit;            // what a search compares with
     unsigned long long picked, picked_before;
     uint32_t picked_weight;
+    uint32_t few;                        // entries of a bin that a warp looks through
     // the chosen segment
     int seg;
     unsigned long long seg_target;
@@ -311,7 +312,10 @@ __device__ __forceinline__ void pick(Shared& sh, const unsigned long long (&key)
 #pragma unroll
         for (int b = tid; b < kBins; b += kThreads)
             sh.keys.cnt[b] = sh.keys.part[0][b] = sh.keys.part[1][b] = 0;
-        if (tid == 0) sh.bin = -1;
+        if (tid == 0) {
+            sh.bin = -1;
+            sh.few = 0;
+        }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kListPer; ++i)
@@ -336,18 +340,41 @@ __device__ __forceinline__ void pick(Shared& sh, const unsigned long long (&key)
         kmax -= (unsigned long long)sh.bin << shift;
         const unsigned long long low = kmax - ((1ull << shift) - 1ull);
         kmin = low > kmin && low <= kmax ? low : kmin;
-        const bool one = sh.bin_cnt == 1;
-        __syncthreads();
-        if (one) {
-#pragma unroll
-            for (int i = 0; i < kListPer; ++i)
-                if (key[i] != 0 && key[i] >= kmin && key[i] <= kmax) {
-                    sh.picked = key[i];
-                    sh.picked_before = base_mass;
-                    sh.picked_weight = w[i];
-                }
-            break;
+        const uint32_t left = sh.bin_cnt;
+        if (left > 32) {
+            __syncthreads();
+            continue;
         }
+        // few entries in the bin: a warp ranks them
+        unsigned long long* const keys = reinterpret_cast<unsigned long long*>(sh.keys.part[0]);   // the bins have been read
+        uint32_t* const ws = sh.keys.part[1];
+#pragma unroll
+        for (int i = 0; i < kListPer; ++i)
+            if (key[i] != 0 && key[i] >= kmin && key[i] <= kmax) {
+                const uint32_t at = left > 1 ? atomicAdd(&sh.few, 1u) : 0u;
+                keys[at] = key[i];
+                ws[at] = w[i];
+            }
+        __syncthreads();
+        if (tid < 32) {
+            const int lane = tid;
+            const unsigned long long own = lane < (int)left ? keys[lane] : 0ull;
+            const uint32_t own_w = lane < (int)left ? ws[lane] : 0u;
+            const unsigned long long limit = sh.limit;
+            uint32_t c = base_cnt;
+            unsigned long long m = base_mass;
+            for (int o = 0; o < (int)left; ++o) {
+                const bool ahead = keys[o] > own;
+                c += ahead;
+                m += ahead ? ws[o] : 0u;
+            }
+            if (own != 0 && done(c + 1, m + own_w, limit) && !done(c, m, limit)) {
+                sh.picked = own;
+                sh.picked_before = m;
+                sh.picked_weight = own_w;
+            }
+        }
+        break;
     }
     __syncthreads();
 }
