@@ -101,6 +101,7 @@ w4a16_status w4a16_kv4_append(const void* k, int64_t k_token_stride, int64_t k_h
     p.head_dim = head_dim;
     p.page_size = page_size;
     p.dtype = dtype;
+    p.per_head = 0xffffffffu / (uint32_t)kv_heads;
     return report_cuda(launch_kv4_append(p, stream));
 }
 
@@ -125,6 +126,7 @@ w4a16_status w4a16_kv4_read(const uint8_t* cache, int pages, const int64_t* slot
     p.head_dim = head_dim;
     p.page_size = page_size;
     p.dtype = dtype;
+    p.per_head = 0xffffffffu / (uint32_t)kv_heads;
     return report_cuda(launch_kv4_read(p, stream));
 }
 

@@ -57,6 +57,7 @@ struct Kv4RowsParams {
     long long n_slots;           // pages * page_size
     int tokens, kv_heads, head_dim, page_size;
     int dtype;                   // w4a16_dtype
+    uint32_t per_head;           // (2^32 - 1) / kv_heads
 };
 cudaError_t launch_kv4_append(const Kv4RowsParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4RowsParams& p, cudaStream_t stream);

@@ -144,7 +144,7 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b)
 
 __device__ __forceinline__ uint32_t negate2(uint32_t w) { return w ^ 0x80008000u; }
 
-// The larger of each pair; a NaN on either side gives a NaN.
+// The larger (smaller) of each pair; a NaN on either side gives a NaN.
 template <int DTYPE>
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
 {
@@ -153,6 +153,18 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
         return *reinterpret_cast<const uint32_t*>(&m);
     } else {
         const __half2 m = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+}
+
+template <int DTYPE>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b)
+{
+    if constexpr (DTYPE == W4A16_BF16) {
+        const __nv_bfloat162 m = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    } else {
+        const __half2 m = __hmin2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
         return *reinterpret_cast<const uint32_t*>(&m);
     }
 }
@@ -191,8 +203,14 @@ __device__ __forceinline__ Rows rows_of(const Kv4RowsParams& p)
 {
     const uint32_t i = blockIdx.x * (256u / (D / 8)) + threadIdx.x / (D / 8);   // below 2^32: checked on the host
     Rows r;
-    r.token = (int)(i / (uint32_t)p.kv_heads);
-    r.head = (int)(i - (uint32_t)r.token * (uint32_t)p.kv_heads);
+    // i / kv_heads by the reciprocal, rounded down: right or one too small
+    uint32_t token = __umulhi(i, p.per_head), head = i - token * (uint32_t)p.kv_heads;
+    if (head >= (uint32_t)p.kv_heads) {
+        ++token;
+        head -= (uint32_t)p.kv_heads;
+    }
+    r.token = (int)token;
+    r.head = (int)head;
     r.live = r.token < p.tokens;
     return r;
 }
@@ -210,12 +228,13 @@ template <int DTYPE>
 __device__ __forceinline__ uint32_t extremes(const uint4& raw)
 {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t up = w[0], dn = negate2(w[0]);
+    uint32_t up = w[0], dn = w[0];
 #pragma unroll
     for (int i = 1; i < 4; ++i) {
         up = max2<DTYPE>(up, w[i]);
-        dn = max2<DTYPE>(dn, negate2(w[i]));
+        dn = min2<DTYPE>(dn, w[i]);
     }
+    dn = negate2(dn);
     return max2<DTYPE>(__byte_perm(up, dn, 0x5410), __byte_perm(up, dn, 0x7632));
 }
 
@@ -251,19 +270,19 @@ template <int DTYPE>
 __device__ __forceinline__ uint32_t codes_of(const uint4& raw, const Stored& r)
 {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    const int z = (int)r.zero();
+    const int z = (int)r.zero() - __float_as_int(kRound);
     uint32_t code[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float a, b;
         unpack2<DTYPE>(w[i], a, b);
         // one by one: a packed product and sum are made one operation with one rounding
-        code[2 * i] = (uint32_t)__vimin_s32_relu(whole(a, r.inv) + z, 15);
-        code[2 * i + 1] = (uint32_t)__vimin_s32_relu(whole(b, r.inv) + z, 15);
+        code[2 * i] = (uint32_t)__viaddmin_s32_relu(__float_as_int(__fadd_rn(__fmul_rn(a, r.inv), kRound)), z, 15);
+        code[2 * i + 1] = (uint32_t)__viaddmin_s32_relu(__float_as_int(__fadd_rn(__fmul_rn(b, r.inv), kRound)), z, 15);
     }
     uint32_t out = code[7];
 #pragma unroll
-    for (int i = 6; i >= 0; --i) out = out << 4 | code[i];
+    for (int i = 6; i >= 0; --i) out = out * 16u + code[i];
     return r.poisoned() ? 0u : out;
 }
 
@@ -278,7 +297,7 @@ __device__ __forceinline__ int v_word(int tok, int j)
 // Quantises the new rows into their slots. Reads 4 D bytes a token and head and writes
 // 2 (D + 6): bound by bandwidth for a long prompt, by latency for a decode step. A thread has its K and
 // its V load in flight together (8191 tokens of eight heads of 128: 12.6 us against 16.2 with one
-// row a thread), and every lane goes on with one row's extremes and scale (11.4 us). Half of that
+// row a thread), and every lane goes on with one row's extremes and scale (now 10.7 us). Half of that
 // time is the bytes', the rest instructions, V's scattered 2-byte stores and the launch.
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowsParams p)
@@ -315,7 +334,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowsParams p)
 }
 
 // The values that slots stand for, (code - zero) * scale in FP32, rounded once. Lanes as above. Bound by its instructions
-// and the loads' latency: 8191 tokens of eight heads of 128 in 7.5 us (8.5 with a shift a code and scalar sums).
+// and the loads' latency: 8191 tokens of eight heads of 128 in 7.3 us (8.5 with a shift a code and scalar sums).
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4RowsParams p)
 {
