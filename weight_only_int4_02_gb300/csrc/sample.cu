@@ -34,7 +34,7 @@
 // Bound by the chain of a row's steps (barriers of the CTA and the cluster, about 1 us each under load), a
 // weight's instructions where weights are summed, and shared atomics where they are binned: 128 rows of 131072
 // bfloat16 logits take 17 us greedy, 33 with no filter or top-k 50, 42 with top-k 500, 84 with top-p 0.95 alone,
-// and 47 mixed; one row of 32000 9.6 us.
+// and 45 mixed; one row of 32000 9.6 us.
 #include "launch.cuh"
 #include "ptx.cuh"
 #include "sample.cuh"
@@ -395,10 +395,10 @@ struct Settings {
     __device__ __forceinline__ bool greedy() const { return !(temp > 0.0f) || k == 1 || !(top_p > 0.0f) || !(min_p <= 1.0f); }
     __device__ __forceinline__ bool need_k(int vocab) const { return k > 0 && k < vocab; }
     __device__ __forceinline__ bool need_p() const { return top_p < 1.0f; }
-    // The longest first: a cut without a list of top-k's, the sum of all weights, a list, the maximum.
+    // The longest first: a cut without a list of top-k's, a long list, a short one or the sum of all weights, the maximum.
     __device__ __forceinline__ int turn(int vocab) const
     {
-        return greedy() ? 3 : need_k(vocab) ? (k > kListMax / 2 ? 0 : 2) : need_p() ? 0 : 1;
+        return greedy() ? 3 : need_k(vocab) ? (k > kListMax / 2 ? 0 : k > kFew / 2 ? 1 : 2) : need_p() ? 0 : 2;
     }
 };
 
@@ -409,10 +409,31 @@ __device__ __forceinline__ Settings settings_of(const SampleParams& p, int row)
 }
 
 // The row that is number `at` when rows are taken in order of their turns (batches of more than a wave:
-// a long row begun last would leave the GPU waiting for it).
+// a long row begun last would leave the GPU waiting for it; 128 x 131072: 66 -> 55 us when it came in).
 __device__ __forceinline__ int row_in_turn(const SampleParams& p, Shared& sh, int at)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.batch <= kThreads) {   // a row a thread: its place is the rows of earlier turns, and those of its own before it
+        constexpr int kTurns = 4;
+        static_assert(kTurns * kWarps == 64, "two counts a lane");
+        const int turn = tid < p.batch ? settings_of(p, tid).turn(p.vocab) : kTurns;
+        uint32_t* const counts = sh.keys.cnt;   // [turn][warp]
+        int place = 0;
+#pragma unroll
+        for (int q = 0; q < kTurns; ++q) {
+            const uint32_t bits = __ballot_sync(0xffffffffu, turn == q);
+            if (lane == 0) counts[q * kWarps + warp] = __popc(bits);
+            if (turn == q) place = __popc(bits & ((1u << lane) - 1u));
+        }
+        __syncthreads();
+        const uint32_t even = counts[2 * lane], both = even + counts[2 * lane + 1];
+        const uint32_t before = warp_incl(both, lane) - both;
+        const int e = turn * kWarps + warp, from = e >> 1 & 31;
+        const uint32_t upto = __shfl_sync(0xffffffffu, before, from) + __shfl_sync(0xffffffffu, even, from) * (e & 1);
+        if (turn < kTurns && (int)upto + place == at) sh.bin = tid;
+        __syncthreads();
+        return sh.bin;   // not written before the next barrier
+    }
     unsigned long long counts = 0;   // of each turn, sixteen bits
     for (int i = tid; i < p.batch; i += kThreads) counts += 1ull << (16 * settings_of(p, i).turn(p.vocab));
     counts = warp_sum(counts);
@@ -1027,7 +1048,7 @@ cudaError_t launch_sample(const SampleParams& in, int sms, cudaStream_t stream)
     // As many CTAs a row as give every SM the two it holds, while a slice is more than a round of loads; up
     // to the portable cluster of eight. A row's steps are a chain, so that fewer, longer slices leave it waiting
     // (256 x 100003 FP32: 243 us with one CTA a row, 77 with two, 96 with four; 128 x 131072 bfloat16: 65 with
-    // two, 55 with four, 84 with eight; now 71 and 48). More where a slice would pass kMaxSlice.
+    // two, 55 with four, 84 with eight; now 69 and 45). More where a slice would pass kMaxSlice.
     auto slice_of = [&](int n) { return ((p.vocab + 16 / size + n - 1) / n + step - 1) / step * step; };
     int ctas = 1;
     while (ctas < kMaxCluster && (((long long)p.batch * ctas < 2 * sms && p.vocab / ctas > step) || slice_of(ctas) > kMaxSlice)) ctas *= 2;
