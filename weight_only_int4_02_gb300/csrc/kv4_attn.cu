@@ -790,6 +790,10 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_
     const long long rows = (long long)max_q * p.group;
     const bool prompt = rows > kFewRows && path != 1 &&
                         (path == 2 || (long long)p.tokens * p.q_heads >= prompt_rows(head_dim));
+    if (prompt && p.batch == 1) {   // one request is one kernel's, whatever its rows turn out to be
+        p.few_rows = 0;
+        return launch_kv4_prompt(p, head_dim, stream);
+    }
     p.few_rows = prompt ? kFewRows : INT_MAX;
     const long long held = prompt && rows > kFewRows ? kFewRows : rows;   // of a request that is this kernel's, at most
     const bool wide = 4 * ((held + 7) / 8) >= 7 * ((held + 15) / 16) && (long long)p.tokens * p.q_heads > kNarrowRows;
