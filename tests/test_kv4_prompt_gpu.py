@@ -150,3 +150,25 @@ def test_repeats_are_the_same_and_strided_views_too():
     first = w4a16.kv4_attention(q.cuda(), *a, 32, 120)
     w4a16.kv4_attention(wide.cuda()[:, 1:1 + H, :D], *a, 32, 120, out=out[:, 1:])
     assert torch.equal(out[:, 1:], first) and (out[:, 0] == 7.0).all()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "float16"), (64, "bfloat16"), (128, "float16"), (128, "bfloat16")])
+@pytest.mark.parametrize("heads,group,lens,seq", [(2, 4, [40], [3000]), (1, 3, [150, 30], [2500, 1150]), (1, 8, [64], [1024])])
+@pytest.mark.parametrize("window", [0, 1300])
+def test_cached_tokens_are_split_over_several_ctas(D, dtype, heads, group, lens, seq, window):
+    """Few row tiles over many tokens: the parts of a tile are joined, rows that see nothing in a part among them."""
+    args = batch_of(seq, lens, heads, group, D, 64, dtype, sum(seq) + D)
+    out, lse = run_and_check(args, 64, window)
+    again, lse_again = run_and_check(args, 64, window)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
+
+
+def test_a_poisoned_token_of_one_part_shows_in_the_rows_that_see_it():
+    from weight_only_int4_02_gb300 import w4a16
+    q, cache, table, seq, starts = batch_of([2000], [100], 1, 4, 128, 16, "bfloat16", 4)
+    D, t = 128, 700
+    cache[table[0, t // 16], 0, 0, 16 * D + 32 + 2 * (t % 16):][:2] = [0, 126]
+    table[0, 100] = -1     # a missing page hides what it holds
+    for window, rows in ((0, 100), (1250, 50)):     # the first 50 queries see position 700: 1900 + i - 1250 < 700
+        out = w4a16.kv4_attention(q.cuda(), cuda(cache), cuda(table), cuda(seq), cuda(starts), 16, 100, window=window)
+        assert torch.isnan(out[:rows]).all() and not torch.isnan(out[rows:]).any()

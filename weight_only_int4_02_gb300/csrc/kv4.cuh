@@ -79,13 +79,15 @@ struct Kv4AttnParams {
     int batch, tokens, q_heads, kv_heads, group, pages, page_size, table_cols, window;
     int few_rows;                // requests of at most this many rows a KV head are the stream-K kernel's
     int bf16;
+    int splits;                  // CTAs that a pair of row tiles may have (tcgen05 kernel)
 };
 cudaError_t setup_kv4();
 // path: 0 as measured, 1 the stream-K kernel, 2 the tcgen05 kernel for every request of more than 32 rows.
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int head_dim, int max_q, int path, int sms, cudaStream_t stream);
 // The tcgen05 kernel, for requests of more than few_rows rows.
 cudaError_t setup_kv4_prompt();
-cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, int head_dim, int sms, cudaStream_t stream);
+size_t kv4_prompt_partial_bytes(int sms);
 // Bytes of partial sums that launch_kv4_attention may use.
 size_t kv4_partial_bytes(int sms);
 

@@ -744,7 +744,7 @@ struct Launch {
 
 size_t kv4_partial_bytes(int sms)
 {
-    size_t need = 0;
+    size_t need = kv4_prompt_partial_bytes(sms);
     auto most = [&](int grid, int part) {
         const size_t bytes = (size_t)2 * grid * part * sizeof(float);
         need = bytes > need ? bytes : need;
@@ -772,17 +772,16 @@ cudaError_t setup_kv4()
 // tokens times query heads) fill the GPU with its tiles of 256; which request is which is known on
 // the device, so such a batch gets both kernels. With fewer rows the stream-K kernel takes everything:
 // it cuts the cached tokens too. Measured for one request, D = 128, tcgen05 and stream-K in us:
-// 4096 rows over 4000 tokens 82 / 58; 6144 82 / 78; 8192 83 / 98; 16384 84 / 177; 8400 over 300
-// 14 / 30; 800 over 1000 26 / 20. D = 64: 8192 over 4000 80 / 67; 10752 84 / 84; 16384 81 / 119.
-// (Of few tokens the tcgen05 kernel takes fewer rows as well: 3200 over 300 14 / 21. How many tokens
-// are cached is not known on the host.)
+// 800 rows over 1000 tokens 34 / 17; 2048 over 4000 50 / 39; 4096 50 / 58; 8192 53 / 98; 16384
+// 64 / 177; 3200 over 300 14 / 21; 8400 over 300 14 / 30. D = 64: 8192 over 4000 41 / 67; 16384
+// 52 / 119; 5120 over 500 15 / 25. (How many tokens are cached is not known on the host.)
 constexpr int kFewRows = 32;
 // Segments of 16 rows cost 1.75 times those of 8, and half as many CTAs fit an SM: 8 where they are fewer than 1.75
 // times as many (9 to 16 rows of 64 requests over 4000 tokens, D = 128, 102 / 118 us with 16 / 8; 17 to 24 rows 184 / 168;
 // 32 rows 188 / 219), and where the rows are too few for throughput to count (one request of 16 rows over 8000 tokens
 // 29 / 21; eight of 16 over 1000 21 / 17; eight of 32 over 8000 59 / 66).
 constexpr int kNarrowRows = 1024;
-constexpr long long prompt_rows(int head_dim) { return head_dim == 128 ? 6400 : 10752; }
+constexpr long long prompt_rows(int head_dim) { return head_dim == 128 ? 3200 : 4096; }
 
 cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_q, int path, int sms, cudaStream_t stream)
 {
@@ -792,7 +791,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_
                         (path == 2 || (long long)p.tokens * p.q_heads >= prompt_rows(head_dim));
     if (prompt && p.batch == 1) {   // one request is one kernel's, whatever its rows turn out to be
         p.few_rows = 0;
-        return launch_kv4_prompt(p, head_dim, stream);
+        return launch_kv4_prompt(p, head_dim, sms, stream);
     }
     p.few_rows = prompt ? kFewRows : INT_MAX;
     const long long held = prompt && rows > kFewRows ? kFewRows : rows;   // of a request that is this kernel's, at most
@@ -803,7 +802,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& in, int head_dim, int max_
     else
         e = held <= 4 ? Launch<64, 0>::run(p, sms, stream) : wide ? Launch<64, 2>::run(p, sms, stream) : Launch<64, 1>::run(p, sms, stream);
     if (e != cudaSuccess || !prompt) return e;
-    return launch_kv4_prompt(p, head_dim, stream);
+    return launch_kv4_prompt(p, head_dim, sms, stream);
 }
 
 }  // namespace w4a16

@@ -25,6 +25,10 @@
 // Queries and outputs go between registers and memory by way of shared memory, so that 16 (D = 64: 8) lanes
 // read or write a row together; a row a lane cost a CTA 4 us more.
 //
+// Where the pairs of row tiles leave SMs idle, each pair's cached tokens are split over several CTAs (the
+// host allows as many as fit, the device takes parts of four blocks or more), and the last of them to finish
+// joins them through the workspace, in their order: 8192 rows over 4000 tokens 81 -> 53 us, 41 of D = 64.
+//
 // Three requests' chunks of 839 to 4000 tokens behind 5690 to 8200 cached ones, 32 query heads over
 // 8, D = 128, bfloat16: 897 us, 910 TFLOP/s, 48% of what a plain bf16 matrix product reaches. (Scores
 // by whole blocks, one S a tile: 1000 us.) The tensor pipe is busy for half of the time, the issue slots
@@ -54,6 +58,8 @@ constexpr int kThreads = 512;         // four warpgroups, of the last the MMA wa
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kUnpackRegs = 112, kIssueRegs = 96;
 static_assert(2 * kSoftmaxRegs + kUnpackRegs + kIssueRegs <= 4 * kLaunchRegs, "registers of the block");
 constexpr int kScaleStages = 4;       // K's scales live until the softmax has read them: two blocks past K itself
+constexpr int kMaxSplits = 8;
+constexpr int kLeast = 4;             // blocks of a CTA where a request's cached tokens are split over several
 constexpr int kGrow = 8;              // log2 of how far P may grow before O is rescaled
 
 template <int D>
@@ -74,7 +80,7 @@ struct Prompt {
         int ev[2];                           // V's scales so far are below 2^ev
         uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], skfull[kScaleStages], sfull[2][2], pfull[2][2], odone[2][2], teardown;
         uint32_t tmem;
-        int abort_flag, b, rt;
+        int abort_flag, b, rt, last;
     };
     // one CTA an SM: it holds all of the SM's tensor memory
     static constexpr int SMEM = (OFF_MISC + (int)sizeof(Misc) > 120 * 1024 ? OFF_MISC + (int)sizeof(Misc) : 120 * 1024) + 1024;
@@ -148,9 +154,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     chained_kernel();
     // ---- this CTA's rows: CTAs count KV heads fastest, then row tiles, the last rows of a request
     // (which see the most tokens) first
-    const int head = blockIdx.x % p.kv_heads;
+    const int pair = blockIdx.x / p.splits, split = blockIdx.x - pair * p.splits;
+    const int head = pair % p.kv_heads;
     if (warp == 0) {
-        const int want = blockIdx.x / p.kv_heads;
+        const int want = pair / p.kv_heads;
         int at = 0;
         if (lane == 0) sh.b = -1;
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -198,16 +205,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     __syncthreads();
     const int b = sh.b;
     if (b < 0) return;   // more CTAs than row tiles
-    if (warp == kMmaWarp) {
-        tmem_alloc(smem_addr(&sh.tmem), 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = sh.tmem;
-    const WaitCtl ctl{&sh.abort_flag, p.status, p.wait_limit_ns};
-
     const long long held = (long long)p.table_cols * p.page_size;
     int seq = p.seq_lens[b];
     seq = seq < 0 ? 0 : seq < held ? seq : (int)held;
@@ -219,8 +216,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     // cached tokens that some row here sees: from base to end
     const int pos_first = seq - nq + row0 / p.group, pos_last = seq - nq + (end_row - 1) / p.group;
     const int low = p.window > 0 ? pos_first - p.window + 1 : 0;
-    const int base = low > 0 ? low / kBlock * kBlock : 0;
-    const int halves = pos_last >= base ? (pos_last - base) / kHalf + 1 : 0, blocks = (halves + 1) / 2;
+    int base = low > 0 ? low / kBlock * kBlock : 0;
+    int halves = pos_last >= base ? (pos_last - base) / kHalf + 1 : 0, blocks = (halves + 1) / 2;
+    // of them this CTA's part; parts of fewer than kLeast blocks are not worth joining
+    const int most = blocks / kLeast, parts = most < 1 ? 1 : most < p.splits ? most : p.splits;
+    if (split >= parts) return;
+    if (parts > 1) {
+        const int from = (int)((long long)blocks * split / parts), to = (int)((long long)blocks * (split + 1) / parts);
+        halves = (2 * to < halves ? 2 * to : halves) - 2 * from;
+        base += from * kBlock;
+        blocks = to - from;
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(&sh.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const WaitCtl ctl{&sh.abort_flag, p.status, p.wait_limit_ns};
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax: one thread a row
@@ -427,7 +442,91 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
             ok = wait_outputs(halves);
             tc_fence_after();
         }
-        if (ok) {
+        if (parts > 1) {
+            // ---- O, not divided, with its maximum and sum; the last of the parts to be written joins them all
+            float* const first = p.partials + (long long)pair * p.splits * (2 * kRows * (D + 2));
+            float* const mine = first + (long long)split * (2 * kRows * (D + 2));
+            const int r = tile * kRows + warp_row + lane;
+            if (ok) {
+                const float unit = poisoned ? CUDART_NAN_F : pow2i(ev - 7 > -126 ? ev - 7 : -126);
+#pragma unroll
+                for (int c = 0; c < D; c += 16) {
+                    float x[16];
+                    if (halves > 0) tmem_ld_f32<16>(o_at + c, x);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 y = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                                   : make_float4(x[j] * unit, x[j + 1] * unit, x[j + 2] * unit, x[j + 3] * unit);
+                        __stcg(reinterpret_cast<float4*>(mine + r * D + c + j), y);
+                    }
+                }
+                __stcg(mine + 2 * kRows * D + r, l == 0.0f ? -CUDART_INF_F : m * a);
+                __stcg(mine + 2 * kRows * (D + 1) + r, l);
+            }
+            __threadfence();
+            named_bar_sync(2, 2 * kRows);
+            if (tid == 0) {
+                const int before = atomicAdd(p.counters + pair, 1);
+                sh.last = before == parts - 1;
+                if (sh.last) p.counters[pair] = 0;   // ready for the next launch
+                __threadfence();
+            }
+            named_bar_sync(2, 2 * kRows);
+            if (sh.last) {
+                // this row's maximum and sum over the parts, and their weights where the tile's queries were
+                float* const weight = reinterpret_cast<float*>(smem) + tile * kMaxSplits * kRows + warp_row;   // [part][row of the tile]
+                constexpr long long kPart = 2 * kRows * (D + 2);
+                float top = -CUDART_INF_F, sum = 0.0f, mk[kMaxSplits];
+#pragma unroll
+                for (int k = 0; k < kMaxSplits; ++k)
+                    if (k < parts) mk[k] = __ldcg(first + k * kPart + 2 * kRows * D + r);
+#pragma unroll
+                for (int k = 0; k < kMaxSplits; ++k)
+                    if (k < parts) top = fmaxf(top, mk[k]);
+#pragma unroll
+                for (int k = 0; k < kMaxSplits; ++k)
+                    if (k < parts) {
+                        const float f = mk[k] == top ? 1.0f : ex2(mk[k] - top);
+                        sum += f * __ldcg(first + k * kPart + 2 * kRows * (D + 1) + r);
+                        weight[k * kRows + lane] = f;
+                    }
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                if (live && p.lse)
+                    p.lse[(long long)(q0 + qi) * p.q_heads + head * p.group + hq] =
+                        sum == 0.0f ? -CUDART_INF_F : (top + log2f(sum)) * CUDART_LN2_F;
+                __syncwarp();
+                // D / 8 lanes a row, eight values each, as the outputs are written
+#pragma unroll 2
+                for (int i = 0; i < kLanes; ++i) {
+                    const int q = i * kTogether + lane / kLanes;
+                    const float by = __shfl_sync(0xffffffffu, inv, q);
+                    const long long off = __shfl_sync(0xffffffffu, o_off, q);
+                    float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                    if (off >= 0) {
+                        const float4* at = reinterpret_cast<const float4*>(first + (long long)(tile * kRows + warp_row + q) * D) + 2 * (lane % kLanes);
+#pragma unroll 4
+                        for (int k = 0; k < parts; ++k) {
+                            const float4 x = __ldcg(at + k * (kPart / 4)), y = __ldcg(at + k * (kPart / 4) + 1);
+                            const float f = weight[k * kRows + q];
+                            o[0] += f * x.x, o[1] += f * x.y, o[2] += f * x.z, o[3] += f * x.w;
+                            o[4] += f * y.x, o[5] += f * y.y, o[6] += f * y.z, o[7] += f * y.w;
+                        }
+                        uint32_t w[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float u = by == 0.0f ? 0.0f : o[2 * c] * by, v = by == 0.0f ? 0.0f : o[2 * c + 1] * by;
+                            if constexpr (BF) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(u, v);
+                                w[c] = *reinterpret_cast<const uint32_t*>(&h);
+                            } else {
+                                w[c] = half2_bits(u, v);
+                            }
+                        }
+                        *(reinterpret_cast<uint4*>((uint16_t*)p.out + off) + lane % kLanes) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        } else if (ok) {
             const float inv = l == 0.0f ? 0.0f : poisoned ? CUDART_NAN_F : pow2i(ev - 7 > -126 ? ev - 7 : -126) / l;
             // through the tile's queries, which have been read, so that kLanes lanes write a row together
             const uint32_t qb = sbase + tile * C::QT;
@@ -720,6 +819,8 @@ cudaError_t launch_one(const Kv4AttnParams& p, unsigned grid, cudaStream_t strea
 
 }  // namespace
 
+size_t kv4_prompt_partial_bytes(int sms) { return (size_t)sms * 2 * kRows * (128 + 2) * sizeof(float); }
+
 cudaError_t setup_kv4_prompt()
 {
     cudaError_t e;
@@ -729,11 +830,15 @@ cudaError_t setup_kv4_prompt()
     return cudaSuccess;
 }
 
-cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, int head_dim, cudaStream_t stream)
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& in, int head_dim, int sms, cudaStream_t stream)
 {
+    Kv4AttnParams p = in;
     // the row tiles of any split of the tokens over the requests
     const long long tiles = (long long)p.tokens * p.group / (2 * kRows) + p.batch;
-    const long long grid = tiles * p.kv_heads;
+    const long long pairs = tiles * p.kv_heads;
+    // where they leave SMs idle, each pair's cached tokens are split over several CTAs
+    p.splits = pairs * 2 > sms ? 1 : (int)(sms / pairs < kMaxSplits ? sms / pairs : kMaxSplits);
+    const long long grid = pairs * p.splits;
     if (grid >= (1LL << 31)) return cudaErrorInvalidValue;
     if (head_dim == 128) return p.bf16 ? launch_one<128, true>(p, (unsigned)grid, stream) : launch_one<128, false>(p, (unsigned)grid, stream);
     return p.bf16 ? launch_one<64, true>(p, (unsigned)grid, stream) : launch_one<64, false>(p, (unsigned)grid, stream);
