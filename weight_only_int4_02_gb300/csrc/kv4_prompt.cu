@@ -30,7 +30,7 @@
 // joins them through the workspace, in their order: 8192 rows over 4000 tokens 81 -> 53 us, 41 of D = 64.
 //
 // Three requests' chunks of 839 to 4000 tokens behind 5690 to 8200 cached ones, 32 query heads over
-// 8, D = 128, bfloat16: 897 us, 910 TFLOP/s, 48% of what a plain bf16 matrix product reaches. (Scores
+// 8, D = 128, bfloat16: 905 us, 900 TFLOP/s, 47% of what a plain bf16 matrix product reaches. (Scores
 // by whole blocks, one S a tile: 1000 us.) The tensor pipe is busy for half of the time, the issue slots
 // too, shared memory for much of the rest, and none of them alone is the limit: without the
 // exponentials, the scales or the unpacking it takes 0 to 5% less, with an eighth of the products 12%.
@@ -54,8 +54,8 @@ constexpr int kMmaWarp = 12;
 constexpr int kThreads = 512;         // four warpgroups, of the last the MMA warp alone at work
 // Registers a thread: 128 at launch, moved to the softmax from the warps that need fewer. Each
 // of the SM's four quarters holds one warp of every warpgroup and a quarter of the registers.
-// 160/104/88 take 904 us where this takes 897.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kUnpackRegs = 112, kIssueRegs = 96;
+// Below 160 the softmax spills (152/112/96: 933 us where this takes 905).
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kUnpackRegs = 96, kIssueRegs = 80;
 static_assert(2 * kSoftmaxRegs + kUnpackRegs + kIssueRegs <= 4 * kLaunchRegs, "registers of the block");
 constexpr int kScaleStages = 4;       // K's scales live until the softmax has read them: two blocks past K itself
 constexpr int kMaxSplits = 8;
