@@ -526,8 +526,9 @@ size_t w4a16_kv4_workspace_bytes(void);
  *   q, out       device, binary16 or bfloat16 [tokens][q_heads][head_dim] at token and
  *                head strides in elements (multiples of 8, at least head_dim), 16-byte
  *                aligned; out must not overlap an input
- *   block_table  device, int32 rows of table_cols pages, table_stride apart; an entry
- *                outside the cache hides its tokens
+ *   block_table  device, int32 rows of table_cols pages, table_stride apart (at least
+ *                table_cols, or 0: one row for every request); an entry outside the cache
+ *                hides its tokens
  *   seq_lens     device, int32 [batch]; starts: device, int32 [batch + 1], request b's
  *                queries are tokens starts[b] .. starts[b + 1] - 1 (as w4a16_kv4_tables
  *                writes them). Tokens of no request are not written.
@@ -564,8 +565,8 @@ int w4a16_kv4_force_path(int path);
  * kept. The result is the first token, in index order, at which the running kept weight
  * exceeds floor(u * kept weight). NaN logits count as -infinity; a row without a
  * logit above -infinity gives token -1 and probability 0.
- *   logits       device, [batch] rows row_stride elements apart, vocab (at most 262144)
- *                valid; W4A16_FP16, W4A16_BF16 or W4A16_FP32, any element alignment
+ *   logits       device, [batch] rows row_stride elements apart (at least vocab, or 0: one
+ *                row, drawn from batch times), vocab (at most 262144) valid; W4A16_FP16, W4A16_BF16 or W4A16_FP32, any element alignment
  *   u            device, float [batch], uniform in [0, 1)
  *   temperature  device, float [batch], or NULL for 1; not above 0: the largest logit
  *   top_k        device, int32 [batch], or NULL; 0 or less: no limit

@@ -1,0 +1,61 @@
+"""What the serving step's Python calls make of their arguments' strides."""
+import numpy as np
+import pytest
+
+from tests.test_kv4_gpu import batch_of, cuda
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab,batch", [(1, 5), (999, 8), (40000, 200)])
+def test_several_draws_from_one_row_of_logits(dtype, vocab, batch):
+    from weight_only_int4_02_gb300 import w4a16
+    x = (torch.randn(1, vocab, device="cuda") * 3).to(dtype)
+    u = torch.rand(batch, device="cuda")
+    p = torch.full((batch,), 0.9, device="cuda")
+    for rows in (x.expand(batch, -1), x[0].expand(batch, -1)):
+        assert rows.stride(0) == 0
+        got, want = w4a16.sample(rows, u, top_p=p), w4a16.sample(rows.contiguous(), u, top_p=p)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("nq", [1, 3, 40])
+def test_requests_over_one_row_of_the_block_table(nq):
+    """Several requests that share a prompt's pages: stride 0 between the table's rows."""
+    from weight_only_int4_02_gb300 import w4a16
+    n = 5
+    q, cache, table, seq, starts = batch_of([300], [nq], 2, 4, 64, 16, "bfloat16", 3)
+    q = (torch.randn(n * nq, 8, 64) * 0.5).to(q.dtype).cuda()
+    seq = cuda(np.array([300, 41, 299, 160, 0], np.int32))
+    starts = cuda(np.arange(0, n * nq + 1, nq, dtype=np.int32))
+    rows = cuda(table).expand(n, -1)
+    assert rows.stride(0) == 0
+    for path in (0, 2):
+        before = w4a16.kv4_force_path(path)
+        try:
+            got = w4a16.kv4_attention(q, cuda(cache), rows, seq, starts, 16, nq, return_lse=True)
+            want = w4a16.kv4_attention(q, cuda(cache), rows.contiguous(), seq, starts, 16, nq, return_lse=True)
+        finally:
+            w4a16.kv4_force_path(before)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_that_overlap_are_refused():
+    """A stride below a row's length, other than 0, reaches the library as it is and is refused there."""
+    from weight_only_int4_02_gb300 import w4a16
+    x = torch.zeros(64, device="cuda").as_strided((4, 16), (8, 1))
+    with pytest.raises(w4a16.W4A16Error):
+        w4a16.sample(x, torch.zeros(4, device="cuda"))
+    assert w4a16.sample(x[:1], torch.zeros(1, device="cuda"))[0].tolist() == [0]   # a single row's stride is never used
+    q, cache, table, seq, starts = batch_of([90, 70], [1, 1], 1, 2, 64, 16, "float16", 1)
+    rows = torch.zeros(64, dtype=torch.int32, device="cuda").as_strided((2, 7), (5, 1))
+    with pytest.raises(w4a16.W4A16Error):
+        w4a16.kv4_attention(q.cuda(), cuda(cache), rows, cuda(seq), cuda(starts), 16, 1)

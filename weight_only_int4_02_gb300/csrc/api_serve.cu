@@ -29,6 +29,9 @@ bool valid_stride(int64_t stride, int head_dim, int count)
     return count <= 1 || (stride >= head_dim && stride % 8 == 0);
 }
 
+// The stride of rows that are only read: 0 where all of them are one row.
+bool valid_row_stride(int64_t stride, int length) { return stride == 0 || stride >= length; }
+
 // The arguments that append and read share.
 bool valid_rows(const void* cache, int pages, const int64_t* slots, int tokens, int kv_heads, int head_dim,
                 int page_size, int dtype, int dtypes)
@@ -158,7 +161,7 @@ w4a16_status w4a16_kv4_attention(const void* q, int64_t q_token_stride, int64_t 
         return W4A16_ERR_INVALID_ARG;
     if (!valid_stride(q_token_stride, head_dim, tokens) || !valid_stride(q_head_stride, head_dim, q_heads) ||
         !valid_stride(out_token_stride, head_dim, tokens) || !valid_stride(out_head_stride, head_dim, q_heads) ||
-        (batch > 1 && table_stride < table_cols))
+        (batch > 1 && !valid_row_stride(table_stride, table_cols)))
         return W4A16_ERR_INVALID_ARG;
     if (workspace && !aligned(workspace, 256)) return W4A16_ERR_INVALID_ARG;
     DeviceInfo dev;
@@ -214,7 +217,7 @@ w4a16_status w4a16_sample(const void* logits, int64_t row_stride, const float* u
     if (batch < 0 || vocab <= 0 || vocab > kSampleMaxVocab || dtype < 0 || dtype > W4A16_FP32) return W4A16_ERR_INVALID_ARG;
     if (batch > (1 << 27)) return W4A16_ERR_INVALID_ARG;   // CTAs are counted in 31 bits, up to eight a row
     if (batch == 0) return W4A16_OK;
-    if (!logits || !u || !token || row_stride < vocab) return W4A16_ERR_INVALID_ARG;
+    if (!logits || !u || !token || !valid_row_stride(row_stride, vocab)) return W4A16_ERR_INVALID_ARG;
     if (!aligned(logits, dtype == W4A16_FP32 ? 4 : 2) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
         !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(token, 4) || !aligned(prob, 4))
         return W4A16_ERR_INVALID_ARG;

@@ -83,6 +83,10 @@ int dtype_of(at::ScalarType t, const char* what) {
     refuse(what);
 }
 
+// The stride of a matrix's rows. That of a single row is never used and may be anything; of more rows the library
+// sees the tensor's own: 0 where one row stands for all of them, and one below a row's length is refused there.
+int64_t row_stride(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+
 struct Cache {
     const at::Tensor& t;
     int pages, heads, dim;
@@ -219,7 +223,7 @@ PyObject* attention(PyObject* const* a) {
         ws_bytes = w.nbytes();
     }
     check(w4a16_kv4_attention(q.data_ptr(), q.stride(0), q.stride(1), c.t.data_ptr<uint8_t>(), c.pages,
-                              table.data_ptr<int32_t>(), table.stride(0) > cols ? table.stride(0) : cols, cols, seq, starts,
+                              table.data_ptr<int32_t>(), row_stride(table), cols, seq, starts,
                               out.data_ptr(), out.stride(0), out.stride(1), lse.defined() ? lse.data_ptr<float>() : nullptr,
                               batch, tokens, heads, c.heads, c.dim, page_size, integer(a[6], "max_q"), (float)scale,
                               integer(a[8], "window"), dtype, ws, ws_bytes, stream_of(a[12], q)),
@@ -241,7 +245,7 @@ PyObject* sample(PyObject* const* a) {
     const float* min_p = optional_vector<float>(a[5], at::kFloat, batch, "min_p must be a contiguous float32 CUDA tensor [batch]");
     at::Tensor all = empty({2, batch}, at::kInt, x);
     int32_t* const to = all.data_ptr<int32_t>();
-    check(w4a16_sample(x.data_ptr(), x.stride(0) > vocab ? x.stride(0) : vocab, u, temperature, top_k, top_p, min_p, to,
+    check(w4a16_sample(x.data_ptr(), row_stride(x), u, temperature, top_k, top_p, min_p, to,
                        reinterpret_cast<float*>(to + batch), batch, vocab, dtype, stream_of(a[6], x)),
           "w4a16_sample");
     return tuple({part(all, 0, {batch}, at::kInt), part(all, 4 * (int64_t)batch, {batch}, at::kFloat)});

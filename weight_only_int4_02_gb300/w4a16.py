@@ -543,7 +543,7 @@ def kv4_attention(q, cache, block_table, seq_lens, starts, page_size, max_q, sca
     """Causal attention of new query tokens over the 4-bit cache (w4a16_kv4_attention).
 
     q: float16 or bfloat16 [tokens][q_heads][head_dim], last dimension contiguous; block_table:
-    int32 [batch][pages of a request]; seq_lens: int32 [batch], cached tokens with the new
+    int32 [batch][pages of a request], rows contiguous (one row expanded over the batch will do); seq_lens: int32 [batch], cached tokens with the new
     ones; starts: int32 [batch + 1], each request's first query token; max_q: the most query
     tokens of a request; scale: 1 / sqrt(head_dim) by default; window: keys a query sees at
     most, 0 for all; workspace: uint8, kv4_workspace_bytes(), zeroed once, or None for the
@@ -563,9 +563,10 @@ def kv4_force_path(path):
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
-    """One token per row of logits (float16, bfloat16 or float32 [batch][vocab], rows contiguous)
-    from uniform numbers u (float32 [batch]), after temperature, top-k, top-p and min-p
-    (float32, int32, float32, float32 [batch], each or None). Returns (token int32 [batch],
-    its probability among the kept tokens float32 [batch]); see w4a16_sample."""
+    """One token per row of logits (float16, bfloat16 or float32 [batch][vocab], rows contiguous;
+    one row expanded over the batch gives several draws from it) from uniform numbers u (float32
+    [batch]), after temperature, top-k, top-p and min-p (float32, int32, float32, float32 [batch],
+    each or None). Returns (token int32 [batch], its probability among the kept tokens float32
+    [batch]); see w4a16_sample."""
     return (_module or _torch_module()).sample(logits, u, temperature, top_k, top_p, min_p,
                                                None if stream is None else stream.cuda_stream)
