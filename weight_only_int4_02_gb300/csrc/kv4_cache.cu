@@ -265,7 +265,9 @@ __device__ __forceinline__ Stored stored_of(uint32_t ext)
     return r;
 }
 
-// Eight codes, four to a 16-bit word: clamp(rint(x / s) + z, 0, 15).
+// Eight codes, four to a 16-bit word: clamp(rint(x / s) + z, 0, 15). Where the scale stays at 65504, a bfloat16 value may lie
+// so many scales below 0 that the integer sum would pass its range; below -2^20, which no row of a smaller scale reaches,
+// every code is 0, so such values stop there (four instructions more for eight values). Above 0 the sum cannot overflow.
 template <int DTYPE>
 __device__ __forceinline__ uint32_t codes_of(const uint4& raw, const Stored& r)
 {
@@ -275,7 +277,7 @@ __device__ __forceinline__ uint32_t codes_of(const uint4& raw, const Stored& r)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float a, b;
-        unpack2<DTYPE>(w[i], a, b);
+        unpack2<DTYPE>(DTYPE == W4A16_BF16 ? max2<DTYPE>(w[i], 0xc980c980u) : w[i], a, b);
         // one by one: a packed product and sum are made one operation with one rounding
         code[2 * i] = (uint32_t)__viaddmin_s32_relu(__float_as_int(__fadd_rn(__fmul_rn(a, r.inv), kRound)), z, 15);
         code[2 * i + 1] = (uint32_t)__viaddmin_s32_relu(__float_as_int(__fadd_rn(__fmul_rn(b, r.inv), kRound)), z, 15);
