@@ -997,8 +997,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 if (rank == 0 && tid < segs) sh.all_mass[tid] = cl.map_shared_rank(&sh, tid / kWarps)->warp_mass[tid % kWarps];
                 cl.sync();   // the others leave, as above
                 if (rank == 0) {
-                    pick(sh, key, w, entry_of(low, 0), entry_of(above((float)bin / to_bin * temp), kIndexTop), base,
-                         by_mass, [limit] { return limit; });
+                    // the first bin begins at the maximum, whatever the temperature (0 times an infinite one is no distance)
+                    const float high = bin == 0 ? r.top : above((float)bin / to_bin * temp);
+                    pick(sh, key, w, entry_of(low, 0), entry_of(high, kIndexTop), base, by_mass, [limit] { return limit; });
 #pragma unroll
                     for (int i = 0; i < kListPer; ++i)
                         if (key[i] != 0 && key[i] >= sh.picked && (exp_of(logit_of(key[i]), r) >= r.min_p || logit_of(key[i]) == r.top)) {
