@@ -1,4 +1,4 @@
-"""What the serving step's Python calls make of their arguments' strides."""
+"""What the serving step's Python calls make of their arguments' strides and streams."""
 import numpy as np
 import pytest
 
@@ -12,6 +12,10 @@ pytestmark = pytest.mark.gpu
 def _gpu():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
+
+
+def ints(*a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
@@ -59,3 +63,35 @@ def test_rows_that_overlap_are_refused():
     rows = torch.zeros(64, dtype=torch.int32, device="cuda").as_strided((2, 7), (5, 1))
     with pytest.raises(w4a16.W4A16Error):
         w4a16.kv4_attention(q.cuda(), cuda(cache), rows, cuda(seq), cuda(starts), 16, 1)
+
+
+def stream_of(t):
+    """The stream whose pool a tensor's memory belongs to."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not the allocator's memory")
+
+
+def test_outputs_belong_to_the_stream_of_the_call():
+    """As under torch.cuda.stream(s): memory that the current stream may still use is not handed out."""
+    from weight_only_int4_02_gb300 import w4a16
+    q, cache, table, seq, starts = batch_of([90, 30], [1, 1], 2, 2, 64, 16, "float16", 1)
+    q, cache, table, seq, starts = q.cuda(), cuda(cache), cuda(table), cuda(seq), cuda(starts)
+    x, u = torch.randn(2, 1000, device="cuda"), torch.rand(2, device="cuda")
+    free = torch.arange(64, dtype=torch.int32, device="cuda")
+    slots = torch.arange(16, device="cuda")
+    calls = (lambda **k: w4a16.kv4_tables(seq, ints(1, 1), free, table.clone(), 16, 2, **k),
+             lambda **k: w4a16.kv4_read(cache, slots, 16, **k),
+             lambda **k: w4a16.kv4_attention(q, cache, table, seq, starts, 16, 1, return_lse=True, **k),
+             lambda **k: w4a16.sample(x, u, **k))
+    s = torch.cuda.Stream()
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        got = call(stream=s)
+        s.synchronize()
+        for a, b in zip(got, want):
+            assert stream_of(a) == s.cuda_stream and stream_of(b) == torch.cuda.current_stream().cuda_stream
+            assert torch.equal(a, b)
+        assert torch.cuda.current_stream().cuda_stream == torch.cuda.default_stream().cuda_stream

@@ -6,6 +6,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -71,8 +72,8 @@ int count(int64_t n, const char* what) {
     return (int)n;
 }
 
-w4a16_stream_t stream_of(PyObject* o, const at::Tensor& t) {
-    if (o != Py_None) return reinterpret_cast<w4a16_stream_t>(PyLong_AsVoidPtr(o));
+// The current stream: the caller's, or the one asked for (call() makes it current).
+w4a16_stream_t stream_of(const at::Tensor& t) {
     return reinterpret_cast<w4a16_stream_t>(c10::cuda::getCurrentCUDAStream(t.device().index()).stream());
 }
 
@@ -144,7 +145,7 @@ PyObject* tables(PyObject* const* a) {
     check(w4a16_kv4_tables(seq_at, new_at, batch, free_at, n_free, taken, reinterpret_cast<int32_t*>(to + at_after),
                            table.data_ptr<int32_t>(), count(table.size(1), "too many pages"), page_size,
                            reinterpret_cast<int64_t*>(to), reinterpret_cast<int32_t*>(to + at_positions), max_tokens,
-                           reinterpret_cast<int32_t*>(to + at_starts), stream_of(a[7], seq)),
+                           reinterpret_cast<int32_t*>(to + at_starts), stream_of(seq)),
           "w4a16_kv4_tables");
     return tuple({part(all, 0, {max_tokens}, at::kLong), part(all, at_positions, {max_tokens}, at::kInt),
                   part(all, at_starts, {(int64_t)batch + 1}, at::kInt), part(all, at_after, {1}, at::kInt)});
@@ -164,7 +165,7 @@ PyObject* append(PyObject* const* a) {
             refuse(what);
     check(w4a16_kv4_append(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), slots,
                            c.t.data_ptr<uint8_t>(), c.pages, tokens, c.heads, c.dim, page_size,
-                           dtype_of(k.scalar_type(), what), stream_of(a[5], k)),
+                           dtype_of(k.scalar_type(), what), stream_of(k)),
           "w4a16_kv4_append");
     Py_RETURN_NONE;
 }
@@ -180,7 +181,7 @@ PyObject* read(PyObject* const* a) {
     const int64_t half = (int64_t)all.nbytes() / 2;
     char* const to = static_cast<char*>(all.data_ptr());
     check(w4a16_kv4_read(c.t.data_ptr<uint8_t>(), c.pages, slots, to, to + half, tokens, c.heads, c.dim, page_size, dtype,
-                         stream_of(a[4], c.t)),
+                         stream_of(c.t)),
           "w4a16_kv4_read");
     return tuple({part(all, 0, {tokens, c.heads, c.dim}, type), part(all, half, {tokens, c.heads, c.dim}, type)});
 }
@@ -226,7 +227,7 @@ PyObject* attention(PyObject* const* a) {
                               table.data_ptr<int32_t>(), row_stride(table), cols, seq, starts,
                               out.data_ptr(), out.stride(0), out.stride(1), lse.defined() ? lse.data_ptr<float>() : nullptr,
                               batch, tokens, heads, c.heads, c.dim, page_size, integer(a[6], "max_q"), (float)scale,
-                              integer(a[8], "window"), dtype, ws, ws_bytes, stream_of(a[12], q)),
+                              integer(a[8], "window"), dtype, ws, ws_bytes, stream_of(q)),
           "w4a16_kv4_attention");
     return lse.defined() ? tuple({out, lse}) : THPVariable_Wrap(out);
 }
@@ -246,11 +247,29 @@ PyObject* sample(PyObject* const* a) {
     at::Tensor all = empty({2, batch}, at::kInt, x);
     int32_t* const to = all.data_ptr<int32_t>();
     check(w4a16_sample(x.data_ptr(), row_stride(x), u, temperature, top_k, top_p, min_p, to,
-                       reinterpret_cast<float*>(to + batch), batch, vocab, dtype, stream_of(a[6], x)),
+                       reinterpret_cast<float*>(to + batch), batch, vocab, dtype, stream_of(x)),
           "w4a16_sample");
     return tuple({part(all, 0, {batch}, at::kInt), part(all, 4 * (int64_t)batch, {batch}, at::kFloat)});
 }
 
+// Makes a stream asked for (each call's last argument, a handle or None) current while the call runs, as
+// torch.cuda.stream() would: its outputs then come from that stream's pool. From another stream's pool, the memory could
+// still be in use by work there, or be handed out again there while this call's kernel writes it.
+void enter_stream(PyObject* const* args, int n, c10::cuda::OptionalCUDAStreamGuard& guard) {
+    if (args[n - 1] == Py_None) return;
+    void* const handle = PyLong_AsVoidPtr(args[n - 1]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse("stream must be a stream's handle");
+    }
+    for (int i = 0; i < n; ++i)
+        if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).is_cuda()) {
+            guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), THPVariable_Unpack(args[i]).device().index()));
+            return;
+        }
+}
+
+// Each call's arguments, a stream's handle or None the last of them.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS   // torch's own exceptions (out of memory, no driver) keep their Python types
@@ -259,6 +278,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
         return nullptr;
     }
     try {
+        c10::cuda::OptionalCUDAStreamGuard stream;
+        enter_stream(args, N, stream);
         return F(args);
     } catch (const Failure& f) {
         PyObject* e = g_error ? PyObject_CallFunction(g_error, "is", f.status, f.what) : nullptr;

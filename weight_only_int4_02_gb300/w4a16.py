@@ -478,6 +478,8 @@ def sp_gemm(x, packed, scales_packed, N, group_size, bias=None, residual=None, a
 # ---------------------------------------------------------------- the serving step
 # These calls last a few microseconds on the GPU, so their checks, their outputs and the
 # C call are in a compiled module (csrc/binding.cpp). Wrong tensors raise W4A16Error before any launch.
+# stream: a torch.cuda.Stream to run on instead of the current one; the outputs' memory belongs to it, as if the
+# call were made under torch.cuda.stream(stream).
 _MODULE_PATH = os.path.join(os.path.dirname(_LIB_PATH), "_w4a16_torch.so")
 _module = None
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
