@@ -80,8 +80,8 @@ def test_outputs_belong_to_the_stream_of_the_call():
     q, cache, table, seq, starts = q.cuda(), cuda(cache), cuda(table), cuda(seq), cuda(starts)
     x, u = torch.randn(2, 1000, device="cuda"), torch.rand(2, device="cuda")
     free = torch.arange(64, dtype=torch.int32, device="cuda")
-    slots = torch.arange(16, device="cuda")
-    calls = (lambda **k: w4a16.kv4_tables(seq, ints(1, 1), free, table.clone(), 16, 2, **k),
+    slots, new, rows = torch.arange(16, device="cuda"), ints(1, 1), table.clone()
+    calls = (lambda **k: w4a16.kv4_tables(seq, new, free, rows, 16, 2, **k),   # the same rows again and again
              lambda **k: w4a16.kv4_read(cache, slots, 16, **k),
              lambda **k: w4a16.kv4_attention(q, cache, table, seq, starts, 16, 1, return_lse=True, **k),
              lambda **k: w4a16.sample(x, u, **k))
