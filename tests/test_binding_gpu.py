@@ -1,4 +1,4 @@
-"""What the serving step's Python calls make of their arguments' strides and streams."""
+"""What the Python calls make of their arguments' strides and streams."""
 import numpy as np
 import pytest
 
@@ -95,3 +95,34 @@ def test_outputs_belong_to_the_stream_of_the_call():
             assert stream_of(a) == s.cuda_stream and stream_of(b) == torch.cuda.current_stream().cuda_stream
             assert torch.equal(a, b)
         assert torch.cuda.current_stream().cuda_stream == torch.cuda.default_stream().cuda_stream
+
+
+def test_the_matmuls_outputs_belong_to_the_stream_of_the_call():
+    from weight_only_int4_02_gb300 import w4a16
+    K, N, G = 256, 512, 128
+    codes = torch.randint(0, 16, (K, N), dtype=torch.uint8, device="cuda")
+    codes.view(K // 4, 4, N)[:, 2:] = 8              # two of every four: also 2:4 sparse
+    scales = torch.rand(K // G, N, device="cuda").to(torch.float16)
+    zeros = torch.randint(0, 16, (K // G, N), dtype=torch.uint8, device="cuda")
+    x = torch.randn(4, K, device="cuda").to(torch.float16)
+    xb = x.bfloat16()
+    w, zp = w4a16.pack(codes, scales, G), w4a16.pack_zeros(zeros, K, G)
+    wb, w8, ws = w4a16.pack(codes, scales.bfloat16(), G), w4a16.w8_pack(codes, scales, G), w4a16.sp_pack(codes, scales, G)
+    space = torch.zeros(w4a16.workspace_bytes(4, N, K, G), dtype=torch.uint8, device="cuda")
+    calls = (lambda **k: w4a16.pack(codes, scales, G, **k), lambda **k: w4a16.pack_zeros(zeros, K, G, **k),
+             lambda **k: w4a16.w8_pack(codes, scales, G, **k), lambda **k: w4a16.sp_pack(codes, scales, G, **k),
+             lambda **k: w4a16.gemm(x, *w, N, G, **k), lambda **k: w4a16.gemm_ws(x, *w, N, G, space, **k),
+             lambda **k: w4a16.gemm_noalloc(x, *w, N, G, **k), lambda **k: w4a16.gemm_fused(x, *w, N, G, **k),
+             lambda **k: w4a16.gemm_strided(x, *w, N, G, **k), lambda **k: w4a16.gemm_zp(x, *w, zp, N, G, **k),
+             lambda **k: w4a16.w8_gemm(x, *w8, N, G, **k), lambda **k: w4a16.bf16_gemm(xb, *wb, N, G, **k),
+             lambda **k: w4a16.sp_gemm(x, *ws, N, G, **k))
+    s = torch.cuda.Stream()
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        got = call(stream=s)
+        s.synchronize()
+        for a, b in zip(got, want) if isinstance(got, tuple) else ((got, want),):
+            assert stream_of(a) == s.cuda_stream and stream_of(b) == torch.cuda.current_stream().cuda_stream
+            assert torch.equal(a, b)
+    assert w4a16.check_device_status() == w4a16.OK

@@ -128,6 +128,15 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, like, stream):
+    """An output on like's device. With a stream given it is that stream's memory: memory of the current stream may
+    still be in use there, or be handed out again there while the given one writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _check(status, what):
     if status != OK:
         raise W4A16Error(status, what)
@@ -202,8 +211,8 @@ def pack(codes, scales, group_size, stream=None, out=None):
     if nw == 0 or ns == 0:
         raise W4A16Error(ERR_INVALID_ARG, "pack")
     if out is None:
-        packed = torch.empty(nw, dtype=torch.int32, device=codes.device)
-        sp = torch.empty(ns, dtype=scales.dtype, device=codes.device)
+        packed = _empty(nw, torch.int32, codes, stream)
+        sp = _empty(ns, scales.dtype, codes, stream)
     else:
         packed, sp = out
     _check(lib().w4a16_pack(_ptr(codes), _ptr(scales), _ptr(packed), _ptr(sp), K, N, group_size, _stream(stream)),
@@ -216,7 +225,7 @@ def gemm(x, packed, scales_packed, N, group_size, y=None, stream=None):
     M, K = x.shape
     assert x.dtype == torch.float16 and x.is_cuda and x.is_contiguous()
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _empty((M, N), torch.float16, x, stream)
     check_buffers(x, packed, scales_packed, N, group_size, y, 'int4')
     _check(lib().w4a16_gemm(_ptr(x), _ptr(packed), _ptr(scales_packed), _ptr(y), M, N, K, group_size,
                             _stream(stream)), "w4a16_gemm")
@@ -227,7 +236,7 @@ def gemm_ws(x, packed, scales_packed, N, group_size, workspace, y=None, stream=N
     """As gemm, with a caller-owned workspace (uint8 CUDA tensor, zeroed once before first use)."""
     M, K = x.shape
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _empty((M, N), torch.float16, x, stream)
     check_buffers(x, packed, scales_packed, N, group_size, y, 'int4')
     _check(lib().w4a16_gemm_ws(_ptr(x), _ptr(packed), _ptr(scales_packed), _ptr(y), M, N, K, group_size,
                                _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -277,7 +286,7 @@ def gemm_noalloc(x, packed, scales_packed, N, group_size, y=None, stream=None):
     M, K = x.shape
     assert x.dtype == torch.float16 and x.is_cuda and x.is_contiguous()
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _empty((M, N), torch.float16, x, stream)
     check_buffers(x, packed, scales_packed, N, group_size, y, 'int4')
     _check(lib().w4a16_gemm_noalloc(_ptr(x), _ptr(packed), _ptr(scales_packed), _ptr(y), M, N, K, group_size,
                                     _stream(stream)), "w4a16_gemm_noalloc")
@@ -297,7 +306,7 @@ def gemm_fused(x, packed, scales_packed, N, group_size, bias=None, residual=None
         if t is not None:
             assert t.dtype == torch.float16 and t.is_cuda and t.is_contiguous() and tuple(t.shape) == shape
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _empty((M, N), torch.float16, x, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     check_buffers(x, packed, scales_packed, N, group_size, y, 'int4')
     _check(lib().w4a16_gemm_fused(_ptr(x), _ptr(packed), _ptr(scales_packed), _ptr(y), M, N, K, group_size,
@@ -321,7 +330,7 @@ def gemm_strided(x, packed, scales_packed, N, group_size, bias=None, residual=No
     M, K = x.shape
     ldx = _row_stride(x, K, "x")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _empty((M, N), torch.float16, x, stream)
     ldy = _row_stride(y, N, "y")
     ldr = _row_stride(residual, N, "residual") if residual is not None else 0
     if bias is not None:
@@ -346,7 +355,7 @@ def pack_zeros(zeros, K, group_size, stream=None, out=None):
     nb = zeros_bytes(K, N, group_size)
     if nb == 0:
         raise W4A16Error(ERR_INVALID_ARG, "pack_zeros")
-    zp = torch.empty(nb, dtype=torch.uint8, device=zeros.device) if out is None else out
+    zp = _empty(nb, torch.uint8, zeros, stream) if out is None else out
     _check(lib().w4a16_pack_zeros(_ptr(zeros), _ptr(zp), K, N, group_size, _stream(stream)), "w4a16_pack_zeros")
     return zp
 
@@ -362,7 +371,7 @@ def gemm_zp(x, packed, scales_packed, zeros_packed, N, group_size, bias=None, re
         if t is not None:
             assert t.dtype == torch.float16 and t.is_cuda and t.is_contiguous() and tuple(t.shape) == shape
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _empty((M, N), torch.float16, x, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     check_buffers(x, packed, scales_packed, N, group_size, y, 'int4', zeros_packed)
     _check(lib().w4a16_gemm_zp(_ptr(x), _ptr(packed), _ptr(scales_packed), _ptr(zeros_packed), _ptr(y), M, N, K,
@@ -385,8 +394,8 @@ def w8_pack(codes, scales, group_size, stream=None):
     nb, ns = w8_packed_bytes(K, N, group_size), scales_elems(K, N, group_size)
     if nb == 0 or ns == 0:
         raise W4A16Error(ERR_INVALID_ARG, "w8_pack")
-    packed = torch.empty(nb, dtype=torch.uint8, device=codes.device)
-    sp = torch.empty(ns, dtype=torch.float16, device=codes.device)
+    packed = _empty(nb, torch.uint8, codes, stream)
+    sp = _empty(ns, torch.float16, codes, stream)
     _check(lib().w4a16_w8_pack(_ptr(codes), _ptr(scales), _ptr(packed), _ptr(sp), K, N, group_size,
                                _stream(stream)), "w4a16_w8_pack")
     return packed, sp
@@ -402,7 +411,7 @@ def w8_gemm(x, packed, scales_packed, N, group_size, bias=None, residual=None, a
         if t is not None:
             assert t.dtype == torch.float16 and t.is_cuda and t.is_contiguous() and tuple(t.shape) == shape
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _empty((M, N), torch.float16, x, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     check_buffers(x, packed, scales_packed, N, group_size, y, 'w8')
     _check(lib().w4a16_w8_gemm(_ptr(x), _ptr(packed), _ptr(scales_packed), _ptr(y), M, N, K, group_size,
@@ -422,7 +431,7 @@ def bf16_gemm(x, packed, scales_packed, N, group_size, bias=None, residual=None,
         if t is not None:
             assert t.dtype == torch.bfloat16 and t.is_cuda and t.is_contiguous() and tuple(t.shape) == shape
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, N), torch.bfloat16, x, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     check_buffers(x, packed, scales_packed, N, group_size, y, 'int4')
     _check(lib().w4a16_bf16_gemm(_ptr(x), _ptr(packed), _ptr(scales_packed), _ptr(y), M, N, K, group_size,
@@ -449,8 +458,8 @@ def sp_pack(codes, scales, group_size, stream=None, violations=None):
         raise W4A16Error(ERR_INVALID_ARG, "sp_pack")
     if violations is not None:
         assert violations.dtype == torch.int64 and violations.is_cuda and violations.numel() == 1
-    packed = torch.empty(nb, dtype=torch.uint8, device=codes.device)
-    sp = torch.empty(ns, dtype=torch.float16, device=codes.device)
+    packed = _empty(nb, torch.uint8, codes, stream)
+    sp = _empty(ns, torch.float16, codes, stream)
     _check(lib().w4a16_sp_pack(_ptr(codes), _ptr(scales), _ptr(packed), _ptr(sp), K, N, group_size,
                                _ptr(violations), _stream(stream)), "w4a16_sp_pack")
     return packed, sp
@@ -466,7 +475,7 @@ def sp_gemm(x, packed, scales_packed, N, group_size, bias=None, residual=None, a
         if t is not None:
             assert t.dtype == torch.float16 and t.is_cuda and t.is_contiguous() and tuple(t.shape) == shape
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _empty((M, N), torch.float16, x, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     check_buffers(x, packed, scales_packed, N, group_size, y, 'sparse')
     _check(lib().w4a16_sp_gemm(_ptr(x), _ptr(packed), _ptr(scales_packed), _ptr(y), M, N, K, group_size,
