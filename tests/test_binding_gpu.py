@@ -1,4 +1,4 @@
-"""What the Python calls make of their arguments' strides and streams."""
+"""What the Python calls make of their arguments' strides, streams and flags."""
 import numpy as np
 import pytest
 
@@ -126,3 +126,13 @@ def test_the_matmuls_outputs_belong_to_the_stream_of_the_call():
             assert stream_of(a) == s.cuda_stream and stream_of(b) == torch.cuda.current_stream().cuda_stream
             assert torch.equal(a, b)
     assert w4a16.check_device_status() == w4a16.OK
+
+
+@pytest.mark.parametrize("flag", [True, 1, np.bool_(True)])
+def test_any_true_value_asks_for_the_log_sums(flag):
+    from weight_only_int4_02_gb300 import w4a16
+    q, cache, table, seq, starts = batch_of([90], [1], 2, 2, 64, 16, "float16", 1)
+    args = (q.cuda(), cuda(cache), cuda(table), cuda(seq), cuda(starts), 16, 1)
+    out, lse = w4a16.kv4_attention(*args, return_lse=flag)
+    assert lse.shape == (1, 4) and torch.isfinite(lse).all()
+    assert torch.equal(out, w4a16.kv4_attention(*args, return_lse=type(flag)(0)))

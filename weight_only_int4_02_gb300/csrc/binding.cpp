@@ -67,6 +67,16 @@ int integer(PyObject* o, const char* what) {
     return (int)v;
 }
 
+// Python's truth of an object: 1 or a numpy bool is as good as True.
+bool truth(PyObject* o, const char* what) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        refuse(what);
+    }
+    return v != 0;
+}
+
 int count(int64_t n, const char* what) {
     if (n > INT32_MAX) refuse(what);
     return (int)n;
@@ -214,7 +224,7 @@ PyObject* attention(PyObject* const* a) {
             refuse("out must be a CUDA tensor of q's type and shape, the last dimension contiguous");
     }
     at::Tensor lse;
-    if (a[10] == Py_True) lse = empty({tokens, heads}, at::kFloat, q);
+    if (truth(a[10], "return_lse must be true or false")) lse = empty({tokens, heads}, at::kFloat, q);
     void* ws = nullptr;
     size_t ws_bytes = 0;
     if (a[11] != Py_None) {
