@@ -82,7 +82,7 @@ int count(int64_t n, const char* what) {
     return (int)n;
 }
 
-// The current stream: the caller's, or the one asked for (call() makes it current).
+// The current stream: the caller's, or the one asked for (Place makes it current).
 w4a16_stream_t stream_of(const at::Tensor& t) {
     return reinterpret_cast<w4a16_stream_t>(c10::cuda::getCurrentCUDAStream(t.device().index()).stream());
 }
@@ -262,22 +262,35 @@ PyObject* sample(PyObject* const* a) {
     return tuple({part(all, 0, {batch}, at::kInt), part(all, 4 * (int64_t)batch, {batch}, at::kFloat)});
 }
 
-// Makes a stream asked for (each call's last argument, a handle or None) current while the call runs, as
-// torch.cuda.stream() would: its outputs then come from that stream's pool. From another stream's pool, the memory could
-// still be in use by work there, or be handed out again there while this call's kernel writes it.
-void enter_stream(PyObject* const* args, int n, c10::cuda::OptionalCUDAStreamGuard& guard) {
-    if (args[n - 1] == Py_None) return;
-    void* const handle = PyLong_AsVoidPtr(args[n - 1]);
-    if (PyErr_Occurred()) {
-        PyErr_Clear();
-        refuse("stream must be a stream's handle");
-    }
-    for (int i = 0; i < n; ++i)
-        if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).is_cuda()) {
-            guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), THPVariable_Unpack(args[i]).device().index()));
-            return;
+// Where a call runs: on the device that its tensors share (the library launches on the current device), and on the
+// stream asked for, the last argument (a handle or None), as under torch.cuda.stream(): its outputs then come from that stream's
+// pool. From another stream's pool, the memory could still be in use by work there, or be handed out again there
+// while this call's kernel writes it.
+class Place {
+public:
+    Place(PyObject* const* args, int n) {
+        int at = -1;   // no CUDA tensor: the call refuses its arguments
+        for (int i = 0; i < n; ++i) {
+            if (!THPVariable_Check(args[i]) || !THPVariable_Unpack(args[i]).is_cuda()) continue;
+            const int d = THPVariable_Unpack(args[i]).device().index();
+            if (at >= 0 && d != at) refuse("the tensors are not all on one device");
+            at = d;
         }
-}
+        if (at < 0) return;
+        if (c10::cuda::current_device() != at) device_.set_index((c10::DeviceIndex)at);
+        if (args[n - 1] == Py_None) return;
+        void* const handle = PyLong_AsVoidPtr(args[n - 1]);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            refuse("stream must be a stream's handle");
+        }
+        stream_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), (c10::DeviceIndex)at));
+    }
+
+private:
+    c10::cuda::OptionalCUDAGuard device_;
+    c10::cuda::OptionalCUDAStreamGuard stream_;
+};
 
 // Each call's arguments, a stream's handle or None the last of them.
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -288,8 +301,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
         return nullptr;
     }
     try {
-        c10::cuda::OptionalCUDAStreamGuard stream;
-        enter_stream(args, N, stream);
+        const Place place(args, N);
         return F(args);
     } catch (const Failure& f) {
         PyObject* e = g_error ? PyObject_CallFunction(g_error, "is", f.status, f.what) : nullptr;
