@@ -1,8 +1,13 @@
-"""The 4-bit key-value cache's calls at the ends of their arguments' ranges, against their definitions."""
+"""The 4-bit key-value cache's calls at the ends of their arguments' ranges, against their definitions.
+
+Both attention kernels are forced in turn. The stream-K kernel is held to the tolerance derived in test_kv4_gpu.py; the
+tcgen05 kernel, as in test_kv4_prompt_gpu.py, to that and its rounding of probabilities times V's scale to binary16 for
+bfloat16 outputs: a relative 2^-11 of sum p |v|, here bounded by sum p s (c + z)."""
 import numpy as np
 import pytest
 
 from tests import serving_reference as ref
+from tests.test_kv4_gpu import batch_of, check, cuda, run
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -35,3 +40,37 @@ def test_bfloat16_rows_past_the_largest_scale(D):
             code, scale, zero = ref.quantise(y.float().numpy())
             want = (code.astype(np.float32) - zero[..., None]) * scale.astype(np.float32)[..., None]
             assert np.array_equal(got.cpu().numpy(), want)
+
+
+def on_path(path, args, page, window, oracle_table=None):
+    """One call on the forced kernel, checked; oracle_table: what the oracle reads instead of the table given."""
+    from weight_only_int4_02_gb300 import w4a16
+    before = w4a16.kv4_force_path(path)
+    try:
+        out, lse = run(*args, page, window)
+    finally:
+        w4a16.kv4_force_path(before)
+    q, cache, table, seq, starts = args
+    table = table if oracle_table is None else oracle_table
+    if path == 1 or q.dtype == torch.float16:        # two binary16 parts, 2^-21: within the tolerance's own terms
+        check(q, cache, table, seq, starts, page, window, out, lse)
+    else:
+        o, l, smass, vmass = ref.attention(q.double().numpy(), cache, table, seq, starts, page, q.shape[-1] ** -0.5, window)
+        es, n = 16 * 2.0 ** -24 * smass, 2.0 ** -24 * (np.max(seq, initial=0) + 64)
+        ep = (2 * es + 2.0 ** -21)[..., None] + n
+        err = np.abs(out.double().cpu().numpy() - o)
+        assert (err <= 2.0 ** -8 * 1.01 * np.abs(o) + vmass * (2 * ep + 2.0 ** -11) + 2.0 ** -24).all()
+        g, f = lse.double().cpu().numpy(), np.isfinite(l)
+        assert np.array_equal(np.isfinite(g), f)
+        assert (np.abs(g[f] - l[f]) <= (2 * es + 2.0 ** -21 + n + 2.0 ** -23 * np.abs(np.where(f, l, 0)))[f]).all()
+    return out, lse
+
+
+@pytest.mark.parametrize("path", [1, 2])
+@pytest.mark.parametrize("D,dtype", [(64, "bfloat16"), (128, "float16")])
+def test_the_largest_window_hides_nothing(path, D, dtype):
+    """A window of 2^31 - 1 is no window, also where a request has more queries than cached tokens."""
+    args = batch_of([3, 40, 130, 0, 700], [9, 60, 1, 3, 50], 2, 4, D, 16, dtype, 5)
+    out, lse = on_path(path, args, 16, 2 ** 31 - 1)
+    want, want_lse = on_path(path, args, 16, 0)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)

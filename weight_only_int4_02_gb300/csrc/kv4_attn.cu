@@ -104,7 +104,9 @@ __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b)
     r.nq = e - a;
     r.rows = r.nq * p.group;
     r.tiles = r.rows > p.few_rows ? 0 : (r.rows + ROWS - 1) / ROWS;
-    const int first = r.seq - r.nq - p.window + 1;   // first token the first query's window holds
+    // first token that a query's window holds (a query at a negative position sees nothing; none of them: no overflow
+    // whatever the window)
+    const int first = (r.seq > r.nq ? r.seq - r.nq : 0) - p.window + 1;
     r.base = (p.window > 0 && first > 0) ? first / kUnit * kUnit : 0;
     r.units = r.seq > r.base ? (r.seq - r.base + kUnit - 1) / kUnit : 1;   // an empty segment still writes its rows
     r.work = (long long)r.tiles * p.kv_heads * (r.units + kOverhead);
@@ -240,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
         const int last_row = (row0 + ROWS < r.rows ? row0 + ROWS : r.rows) - 1;
         const int pos_min = r.seq - r.nq + row0 / p.group, pos_max = r.seq - r.nq + last_row / p.group;
         const int seen = pos_max >= r.base ? (pos_max - r.base) / kUnit + 1 : 0;
-        const int low = p.window > 0 && pos_min - p.window + 1 > r.base ? (pos_min - p.window + 1 - r.base) / kUnit : 0;
+        const int low_at = (pos_min > 0 ? pos_min : 0) - p.window + 1;   // as in request_of
+        const int low = p.window > 0 && low_at > r.base ? (low_at - r.base) / kUnit : 0;
         const int first = low > pos ? low : pos, last = seen < pos + take ? seen : pos + take;
 
         // ---- copies: a batch of 16 units at a time, lanes 2j and 2j + 1 own the tiles of its unit j

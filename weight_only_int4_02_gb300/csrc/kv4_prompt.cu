@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     const int end_row = row0 + 2 * kRows < rows ? row0 + 2 * kRows : rows;
     // cached tokens that some row here sees: from base to end
     const int pos_first = seq - nq + row0 / p.group, pos_last = seq - nq + (end_row - 1) / p.group;
-    const int low = p.window > 0 ? pos_first - p.window + 1 : 0;
+    // (a row at a negative position sees nothing; none of them: no overflow whatever the window)
+    const int low = p.window > 0 ? (pos_first > 0 ? pos_first : 0) - p.window + 1 : 0;
     int base = low > 0 ? low / kBlock * kBlock : 0;
     int halves = pos_last >= base ? (pos_last - base) / kHalf + 1 : 0, blocks = (halves + 1) / 2;
     // of them this CTA's part; parts of fewer than kLeast blocks are not worth joining
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
                               (p.window <= 0 || t0 > pos_max - p.window);
             // this row's visible columns of the half, where stored: word w's bits
             auto see = [&](int w) -> uint32_t {
-                const int hi = pos - t0 + 1 - 32 * w, lo = (p.window > 0 ? pos - p.window + 1 - t0 : 0) - 32 * w;
+                const int hi = pos - t0 + 1 - 32 * w, lo = p.window > 0 && hi > 0 ? hi - p.window : 0;
                 const uint32_t upto = hi <= 0 ? 0u : hi >= 32 ? 0xffffffffu : (1u << hi) - 1u;
                 const uint32_t below = lo <= 0 ? 0u : lo >= 32 ? 0xffffffffu : (1u << lo) - 1u;
                 return (w ? vw.y : vw.x) & upto & ~below;
