@@ -528,7 +528,7 @@ size_t w4a16_kv4_workspace_bytes(void);
  *                aligned; out must not overlap an input
  *   block_table  device, int32 rows of table_cols pages, table_stride apart (at least
  *                table_cols, or 0: one row for every request); an entry outside the cache
- *                hides its tokens
+ *                hides its tokens, as do tokens past the last column (positions count them)
  *   seq_lens     device, int32 [batch]; starts: device, int32 [batch + 1], request b's
  *                queries are tokens starts[b] .. starts[b + 1] - 1 (as w4a16_kv4_tables
  *                writes them). Tokens of no request are not written.

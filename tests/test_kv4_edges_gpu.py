@@ -74,3 +74,17 @@ def test_the_largest_window_hides_nothing(path, D, dtype):
     out, lse = on_path(path, args, 16, 2 ** 31 - 1)
     want, want_lse = on_path(path, args, 16, 0)
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("path", [1, 2])
+@pytest.mark.parametrize("D,dtype", [(64, "float16"), (128, "bfloat16")])
+@pytest.mark.parametrize("window", [0, 20, 300])
+def test_requests_longer_than_their_table(path, D, dtype, window):
+    """Tokens past the table's columns are hidden; the queries' positions still count them."""
+    q, cache, table, seq, starts = batch_of([480, 512, 100, 400], [70, 1, 40, 33], 2, 4, D, 16, dtype, 7)
+    seq = seq + np.array([60, 20, 0, 900], np.int32)   # the last request's window, where it has one, lies past its table
+    cols = 30                                          # 480 tokens
+    wide = np.full((4, 90), -1, np.int32)
+    wide[:, :cols] = table[:, :cols]
+    out, lse = on_path(path, (q, cache, wide[:, :cols], seq, starts), 16, window, oracle_table=wide)
+    assert window == 0 or (out[starts[3]:] == 0).all()

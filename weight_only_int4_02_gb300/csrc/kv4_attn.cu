@@ -84,7 +84,8 @@ __device__ __forceinline__ float2 bits_half2(uint32_t w) { return __half22float2
 
 // One request as the kernel sees it: every length clamped to what the buffers hold.
 struct Request {
-    int seq, q0, nq, rows, tiles;   // cached tokens, first query token, query tokens, rows, row tiles
+    int seq, q0, nq, rows, tiles;   // cached tokens that the table can hold, first query token, query tokens, rows, row tiles
+    int pos0;                       // the first query's position: of all cached tokens, also those past the table's columns
     int base, units;                // first cached token looked at (a multiple of kUnit), units a segment
     long long work;                 // cost of all its segments: kOverhead, then the units, of each
 };
@@ -102,11 +103,12 @@ __device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b)
     e = e < a ? a : e > p.tokens ? p.tokens : e;
     r.q0 = a;
     r.nq = e - a;
+    r.pos0 = s - r.nq;
     r.rows = r.nq * p.group;
     r.tiles = r.rows > p.few_rows ? 0 : (r.rows + ROWS - 1) / ROWS;
     // first token that a query's window holds (a query at a negative position sees nothing; none of them: no overflow
     // whatever the window)
-    const int first = (r.seq > r.nq ? r.seq - r.nq : 0) - p.window + 1;
+    const int first = (r.pos0 > 0 ? r.pos0 : 0) - p.window + 1;
     r.base = (p.window > 0 && first > 0) ? first / kUnit * kUnit : 0;
     r.units = r.seq > r.base ? (r.seq - r.base + kUnit - 1) / kUnit : 1;   // an empty segment still writes its rows
     r.work = (long long)r.tiles * p.kv_heads * (r.units + kOverhead);
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
         // a unit needs no mask if it lies below the first row's position and inside the last row's window;
         // units that no row of the tile sees are left out: [first, last) of the run are looked at
         const int last_row = (row0 + ROWS < r.rows ? row0 + ROWS : r.rows) - 1;
-        const int pos_min = r.seq - r.nq + row0 / p.group, pos_max = r.seq - r.nq + last_row / p.group;
+        const int pos_min = r.pos0 + row0 / p.group, pos_max = r.pos0 + last_row / p.group;
         const int seen = pos_max >= r.base ? (pos_max - r.base) / kUnit + 1 : 0;
         const int low_at = (pos_min > 0 ? pos_min : 0) - p.window + 1;   // as in request_of
         const int low = p.window > 0 && low_at > r.base ? (low_at - r.base) / kUnit : 0;
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                 row_a[g][i] = un > 0.0f ? un : FLT_MIN;   // scale 0: all scores nearly equal, masked ones stay -infinity
                 row_z[g][i] = __shfl_sync(0xffffffffu, qsum, (2 * c + i) * 4) * -0x1p-24f;
                 const int rr = row0 + g * 8 + (FOUR ? 2 * (c & 1) + i : 2 * c + i);
-                row_pos[g][i] = rr < r.rows ? r.seq - r.nq + rr / p.group : -1;
+                row_pos[g][i] = rr < r.rows ? r.pos0 + rr / p.group : -1;
             }
         }
         float m[G][2], l[G][2], zs[G][2], o[G][2 * W][4];

@@ -206,19 +206,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
     const int b = sh.b;
     if (b < 0) return;   // more CTAs than row tiles
     const long long held = (long long)p.table_cols * p.page_size;
-    int seq = p.seq_lens[b];
-    seq = seq < 0 ? 0 : seq < held ? seq : (int)held;
+    const int len = p.seq_lens[b] < 0 ? 0 : p.seq_lens[b];   // cached tokens, of which the table holds the first `seq`
+    const int seq = len < held ? len : (int)held;
     int q0 = p.starts[b], q1 = p.starts[b + 1];
     q0 = q0 < 0 ? 0 : q0 > p.tokens ? p.tokens : q0;
     q1 = q1 < q0 ? q0 : q1 > p.tokens ? p.tokens : q1;
     const int nq = q1 - q0, rows = nq * p.group, row0 = sh.rt * 2 * kRows;
     const int end_row = row0 + 2 * kRows < rows ? row0 + 2 * kRows : rows;
     // cached tokens that some row here sees: from base to end
-    const int pos_first = seq - nq + row0 / p.group, pos_last = seq - nq + (end_row - 1) / p.group;
+    const int pos0 = len - nq;   // the first query's position
+    const int pos_first = pos0 + row0 / p.group, pos_last = pos0 + (end_row - 1) / p.group;
+    const int last_seen = pos_last < seq ? pos_last : seq - 1;
     // (a row at a negative position sees nothing; none of them: no overflow whatever the window)
     const int low = p.window > 0 ? (pos_first > 0 ? pos_first : 0) - p.window + 1 : 0;
     int base = low > 0 ? low / kBlock * kBlock : 0;
-    int halves = pos_last >= base ? (pos_last - base) / kHalf + 1 : 0, blocks = (halves + 1) / 2;
+    int halves = last_seen >= base ? (last_seen - base) / kHalf + 1 : 0, blocks = (halves + 1) / 2;
     // of them this CTA's part; parts of fewer than kLeast blocks are not worth joining
     const int most = blocks / kLeast, parts = most < 1 ? 1 : most < p.splits ? most : p.splits;
     if (split >= parts) return;
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         const int row = row0 + tile * kRows + (warp & 3) * 32 + lane;
         const bool live = row < rows;
         const int qi = row / p.group, hq = row - qi * p.group;
-        const int pos = live ? seq - nq + qi : -1;
+        const int pos = live ? pos0 + qi : -1;
         // lanes that move a row between memory and shared memory together, and rows of a warp's access
         constexpr int kLanes = D / 8, kTogether = 32 / kLanes;
         const int warp_row = (warp & 3) * 32;   // of the tile's rows
@@ -299,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const Kv4AttnPa
         const uint32_t s_at = lanes + C::S_COL + tile * kBlock, o_at = lanes + C::O_COL + tile * D;
         const int t_row0 = row0 + tile * kRows;
         const int t_last = t_row0 + kRows < rows ? t_row0 + kRows : rows;
-        const int pos_min = t_row0 < rows ? seq - nq + t_row0 / p.group : -1;
-        const int pos_max = t_row0 < rows ? seq - nq + (t_last - 1) / p.group : -1;
+        const int pos_min = t_row0 < rows ? pos0 + t_row0 / p.group : -1;
+        const int pos_max = t_row0 < rows ? pos0 + (t_last - 1) / p.group : -1;
         float m = -CUDART_INF_F;   // of s_k S
         uint64_t l2 = 0;           // sums of even and odd columns
         const uint64_t a2 = pack_f32x2(a, a);
