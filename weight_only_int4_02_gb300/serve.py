@@ -66,9 +66,15 @@ class Decoder:
 
 
 def generate(model, prompts, steps, page_size=16, max_len=512, temperature=0.8, top_k=50, top_p=0.95, seed=0):
-    """Tokens drawn for each prompt (a list of int64 CUDA tensors): int32 [requests][steps]."""
-    n, device = len(prompts), prompts[0].device
+    """Tokens drawn for each prompt (a list of int64 CUDA tensors): int32 [requests][steps]. max_len: cached
+    tokens that a request may come to hold (its prompt and every drawn token but the last), up to whole pages."""
     cols = -(-max_len // page_size)
+    if not prompts or min(len(p) for p in prompts) == 0:
+        raise ValueError("generate wants a prompt of at least one token for every request")
+    if max(len(p) for p in prompts) + steps - 1 > cols * page_size:
+        raise ValueError("a prompt of %d tokens and %d steps do not fit the %d tokens of max_len's pages" %
+                         (max(len(p) for p in prompts), steps, cols * page_size))
+    n, device = len(prompts), prompts[0].device
     caches = model.caches(n * cols, page_size)
     table = torch.full((n, cols), -1, dtype=torch.int32, device=device)
     free = torch.randperm(n * cols, device=device).to(torch.int32)
