@@ -88,3 +88,26 @@ def test_requests_longer_than_their_table(path, D, dtype, window):
     wide[:, :cols] = table[:, :cols]
     out, lse = on_path(path, (q, cache, wide[:, :cols], seq, starts), 16, window, oracle_table=wide)
     assert window == 0 or (out[starts[3]:] == 0).all()
+
+
+@pytest.mark.parametrize("new", [[8191], [1, 3000, 0, 777, 129, 128]])
+def test_tables_of_long_chunks(new):
+    from weight_only_int4_02_gb300 import w4a16
+    r = np.random.default_rng(len(new))
+    page = 32
+    new = np.array(new, np.int32)
+    seq = new + r.integers(0, 5000, len(new)).astype(np.int32)
+    cols = int(-(-seq.max() // page)) - 3            # the longest request ends past its row
+    free = r.permutation(4000).astype(np.int32)
+    held = r.integers(0, 4000, (len(new), cols)).astype(np.int32)
+    want = ref.tables(seq, new, free, held, page, 0)
+    table = cuda(held)
+    slots, positions, starts, taken = w4a16.kv4_tables(cuda(seq), cuda(new), cuda(free), table, page, int(new.sum()))
+    assert np.array_equal(table.cpu().numpy(), want[0]) and slots.tolist() == want[1] and positions.tolist() == want[2]
+    assert starts.tolist() == want[3] and taken.item() == want[4]
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_a_request_of_a_hundred_thousand_tokens(dtype):
+    args = batch_of([100003], [2], 1, 4, 128, 256, dtype, 11)
+    check(*args, 256, 0, *run(*args, 256))
