@@ -111,3 +111,37 @@ def test_tables_of_long_chunks(new):
 def test_a_request_of_a_hundred_thousand_tokens(dtype):
     args = batch_of([100003], [2], 1, 4, 128, 256, dtype, 11)
     check(*args, 256, 0, *run(*args, 256))
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "float16"), (128, "float16"), (128, "bfloat16")])
+@pytest.mark.parametrize("group,nq", [(4, 1), (8, 1), (8, 2)])
+def test_long_sums_have_no_bias(D, dtype, group, nq):
+    """512 requests over one row of 16384 tokens, so that each warp sums about a hundred units of 32 tokens or more.
+    An MMA rounds towards zero. If a unit's two tiles, each with a high and a low part, add its share of sum p s c to sums
+    of either sign, and then sum p s z is taken off, the roundings lose less than 2^-23 of half and of all of that share,
+    twice, 2^-24 on average: 3 * 2^-24 of the whole mass. Outputs are rounded to nearest, which has no bias: five
+    deviations of their mean."""
+    from weight_only_int4_02_gb300 import w4a16
+    n, seq, page = 512, 16384, 256
+    _, cache, table, _, _ = batch_of([seq], [1], 1, group, D, page, dtype, D + group)
+    g = torch.Generator(device="cuda").manual_seed(group)
+    q = torch.randn(n * nq, group, D, generator=g, device="cuda").to(getattr(torch, dtype))
+    rows = cuda(table).expand(n, -1)
+    lens = torch.full((n,), seq, dtype=torch.int32, device="cuda")
+    starts = torch.arange(0, n * nq + 1, nq, dtype=torch.int32, device="cuda")
+    before = w4a16.kv4_force_path(1)
+    try:
+        out = w4a16.kv4_attention(q, cuda(cache), rows, lens, starts, page, nq).double()
+    finally:
+        w4a16.kv4_force_path(before)
+    kc, ks, kz, vc, vs, vz = [torch.from_numpy(x[:seq].astype(np.float64)).cuda()
+                              for x in ref.decode(cache[table[0, :seq // page], 0].reshape(-1, 16 * (D + 6)), D)]
+    x = q.double().view(n, nq, group, D) @ ((kc - kz[:, None]) * ks[:, None]).T * D ** -0.5
+    pos = torch.arange(seq - nq, seq, device="cuda")[None, :, None, None]
+    p = torch.softmax(x.masked_fill(torch.arange(seq, device="cuda") > pos, -np.inf), -1).view(-1, seq)
+    o = (p @ ((vc - vz[:, None]) * vs[:, None])).view(out.shape)
+    mass = float((p @ (vs * vc.amax(-1))).mean())    # sum p s c, with the largest code of each token
+    u = 2.0 ** -11 if dtype == "float16" else 2.0 ** -8
+    noise = 5 * u * float(o.square().mean().sqrt()) / 3 ** 0.5 / out.numel() ** 0.5
+    bias = float((out - o).mean())
+    assert abs(bias) <= 3 * 2.0 ** -24 * mass + noise, (bias, mass, noise)

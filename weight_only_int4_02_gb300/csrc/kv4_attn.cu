@@ -13,8 +13,11 @@
 // output. Mathematics, with c the code, z the zero-point, s the scale of a token:
 //   score = s_k (q . c_k - z_k sum(q)) * scale,   out = sum_t p_t s_v (c_v - z_v) / sum_t p_t
 // so the MMAs multiply by the bare codes: an unpacked register is one logic operation (two
-// codes as binary16 subnormals, exact), K's scale and zero-point act on scores and V's on
-// probabilities, once a (token, row). Tokens are the MMA's M for K (A = 16 tokens x
+// codes as binary16 subnormals, exact), K's scale and zero-point act on scores and V's scale on
+// probabilities, once a (token, row). V's zero-points are taken off the running sums unit by unit, from two MMAs of their
+// own: an MMA rounds towards zero, and in sums of codes alone, some hundred times what is left of them in
+// the end, these roundings added up (over 2^20 tokens to 0.8% of the output, 0.1% for 128 requests of 16384; now
+// nothing beside a binary16 output's rounding, for 4% of the time). Tokens are the MMA's M for K (A = 16 tokens x
 // 16 d) and d is for V (A = 16 d x 16 tokens), so that eight rows are the MMA's N and cost
 // eight columns. Q is scaled per row by a power of two into binary16's range (exact
 // for binary16 and bfloat16 inputs). Probabilities times V's scale are fed as a high
@@ -24,9 +27,9 @@
 // that V takes half the MMAs (one request of 131072 tokens 43.2 -> 42.3 us). Scores, sums, maxima and outputs
 // are FP32.
 //
-// Measured, D = 128: 64 requests of 257 to 16384 cached tokens 67 us, 3.8 TB/s, 56% of a copy's rate; one of
-// 131072 tokens 42 us; D = 64, 48 requests of 1 to 5 drafted tokens and a window of 4096 17 us; one of 1000
-// tokens 10.6 us, most of it latency. Four CTAs an SM (128 registers a thread) keep the issue slots busy for 51% of the
+// Measured, D = 128: 64 requests of 257 to 16384 cached tokens 71 us, 3.6 TB/s, 53% of a copy's rate; one of
+// 131072 tokens 44 us; D = 64, 48 requests of 1 to 5 drafted tokens and a window of 4096 17.6 us; one of 1000
+// tokens 10.9 us, most of it latency. Four CTAs an SM (128 registers a thread) keep the issue slots busy for 51% of the
 // time and the tensor pipe for 32%: a unit is about 610 warp instructions (241 of them integer, 117 FP32, 71 binary16
 // and MMAs), which wait for one another more than for memory. Eight or two warps a CTA, five CTAs an SM
 // (fewer registers) and tokens' scales through shared memory were slower.
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                 row_pos[g][i] = rr < r.rows ? r.pos0 + rr / p.group : -1;
             }
         }
-        float m[G][2], l[G][2], zs[G][2], o[G][2 * W][4];
+        float m[G][2], l[G][2], bad[G][2], o[G][2 * W][4];   // bad: NaN where a row sees a poisoned V, else 0
         int ev = -40;   // V's scales seen so far are at most 2^ev
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
             for (int i = 0; i < 2; ++i) {
                 m[g][i] = -CUDART_INF_F;
                 l[g][i] = 0.0f;
-                zs[g][i] = 0.0f;
+                bad[g][i] = 0.0f;
             }
 #pragma unroll
             for (int w = 0; w < 2 * W; ++w)
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
 
             // s_k times the products of the unit's two tiles: tokens n and n + 8 of each, rows 2c and 2c + 1
             float sc[2][G][4];
-            float vs[2][2], vz[2][2];
+            float vs[2][2];
 #pragma unroll
             for (int tl = 0; tl < 2; ++tl) {
                 const uint8_t* const tile = st + tl * A::TB;
@@ -405,7 +408,6 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                     ks[j] = __half2float(*reinterpret_cast<const __half*>(tile + kv4_k_scale_off(D) + 2 * tok));
                     const float kz = (float)tile[kv4_k_zero_off(D) + tok];
                     vs[tl][j] = __half2float(*reinterpret_cast<const __half*>(tile + kv4_v_scale_off(D) + 2 * tok));
-                    vz[tl][j] = (float)tile[kv4_v_zero_off(D) + tok];
                     // the sums start from the zero-points' share
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                         const int key = t0 + tl * kKv4Tile + n + 8 * j;
                         const bool there = (have >> tl & 1) && key < r.seq;
                         const bool odd = there && vs[tl][j] != vs[tl][j];   // a poisoned row of V
-                        if (!there || odd) vs[tl][j] = vz[tl][j] = 0.0f;
+                        if (!there || odd) vs[tl][j] = 0.0f;
 #pragma unroll
                         for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                                 const bool see = there && key <= row_pos[g][i] &&
                                                  (p.window <= 0 || key > row_pos[g][i] - p.window);
                                 if (!see) sc[tl][g][2 * j + i] = -CUDART_INF_F;
-                                else if (odd) zs[g][i] = CUDART_NAN_F;      // shows in the rows that see it alone
+                                else if (odd) bad[g][i] = CUDART_NAN_F;     // shows in the rows that see it alone
                             }
                     }
             }
@@ -485,7 +487,6 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                         m[g][i] = x;
                         l[g][i] *= f[i];
                         f[i] *= shift;
-                        zs[g][i] *= f[i];
                     }
 #pragma unroll
                     for (int w = 0; w < 2 * W; ++w)
@@ -500,12 +501,19 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
             for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) ref[g][i] = m[g][i] == -CUDART_INF_F ? 0.0f : m[g][i];
+            // The first tile adds p c and the second -p (15 - c), so that neither leaves the sums far from where they were; zo is
+            // the zero-points' share of that (MMAs with V's zero-points in every row of A): o - zo gains p (c - z)
+            float zo[G][4];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) zo[g][i] = 0.0f;
 #pragma unroll
             for (int tl = 0; tl < 2; ++tl) {
                 uint32_t ph[G][2], pl[G][2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float v = vs[tl][j] * vf;
+                    const float v = vs[tl][j] * (tl ? -vf : vf);
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
                         float pv[2];
@@ -514,7 +522,6 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                             const float e = ex2(fmaf(sc[tl][g][2 * j + i], row_a[g][i], -ref[g][i]));
                             l[g][i] += e;
                             pv[i] = e * v;
-                            zs[g][i] = fmaf(pv[i], vz[tl][j], zs[g][i]);
                         }
                         const uint32_t h = half2_bits(pv[0], pv[1]);
                         const float2 back = bits_half2(h);
@@ -531,19 +538,39 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                 uint32_t va[W], vb[W];
                 lds_share<W>(tile + lane * (4 * W), va);
                 lds_share<W>(tile + 4 * D + lane * (4 * W), vb);
+                const uint16_t* const vz = reinterpret_cast<const uint16_t*>(st + tl * A::TB + kv4_v_zero_off(D));
+                const uint32_t flip = tl ? 0xffffffffu : 0u;   // 15 - c is c with every bit turned
+                const uint32_t za = __byte_perm(vz[c] ^ (flip & 0x0f0fu), 0, 0x4140);       // of tokens 2c and 2c + 1
+                const uint32_t zb = __byte_perm(vz[c + 4] ^ (flip & 0x0f0fu), 0, 0x4140);   // of tokens 8 + 2c and 9 + 2c
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    mma_16816(zo[g], za, za, zb, zb, ph[g][0], ph[g][1]);
+                    if constexpr (!FOUR) mma_16816(zo[g], za, za, zb, zb, pl[g][0], pl[g][1]);
+                }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    const uint32_t va8 = va[w] >> 8, vb8 = vb[w] >> 8;
+                    const uint32_t v1 = va[w] ^ flip, v2 = vb[w] ^ flip, v1s = v1 >> 8, v2s = v2 >> 8;
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
-                        mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, ph[g][0], ph[g][1]);
-                        mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, ph[g][0], ph[g][1]);
+                        mma_16816(o[g][2 * w], v1 & kLow, v1s & kLow, v2 & kLow, v2s & kLow, ph[g][0], ph[g][1]);
+                        mma_16816(o[g][2 * w + 1], v1 & kHigh, v1s & kHigh, v2 & kHigh, v2s & kHigh, ph[g][0], ph[g][1]);
                         if constexpr (!FOUR) {
-                            mma_16816(o[g][2 * w], va[w] & kLow, va8 & kLow, vb[w] & kLow, vb8 & kLow, pl[g][0], pl[g][1]);
-                            mma_16816(o[g][2 * w + 1], va[w] & kHigh, va8 & kHigh, vb[w] & kHigh, vb8 & kHigh, pl[g][0], pl[g][1]);
+                            mma_16816(o[g][2 * w], v1 & kLow, v1s & kLow, v2 & kLow, v2s & kLow, pl[g][0], pl[g][1]);
+                            mma_16816(o[g][2 * w + 1], v1 & kHigh, v1s & kHigh, v2 & kHigh, v2s & kHigh, pl[g][0], pl[g][1]);
                         }
                     }
                 }
+            }
+            // The unit's sums less the zero-points' share: running sums of code - zero. An MMA rounds towards zero, so the
+            // roundings of sums that grow without end would all point one way, and show where what is left of them is small.
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint64_t low2 = pack_f32x2(-zo[g][0], -zo[g][1]), high2 = mul_f32x2(low2, pack_f32x2(16.0f, 16.0f));
+#pragma unroll
+                for (int w = 0; w < 2 * W; ++w)
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2)
+                        unpack_f32x2(add_f32x2(pack_f32x2(o[g][w][i], o[g][w][i + 1]), w & 1 ? high2 : low2), o[g][w][i], o[g][w][i + 1]);
             }
             next_stage();
             fence_proxy_async_smem();
@@ -567,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) {
                     l[g][i] += __shfl_xor_sync(0xffffffffu, l[g][i], d);
-                    zs[g][i] += __shfl_xor_sync(0xffffffffu, zs[g][i], d);
+                    bad[g][i] += __shfl_xor_sync(0xffffffffu, bad[g][i], d);
                 }
                 if (n == 0 && (!FOUR || c < 2)) {
                     sh.m[warp][g * 8 + 2 * c + i] = m[g][i];
@@ -587,10 +614,10 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                     if (FOUR && c >= 2) continue;
                     // codes in low nibbles come as c * 2^-24, in high ones as c * 2^-20
                     float4 x;
-                    x.x = (o[g][2 * w][i] * 16777216.0f - zs[g][i]) * o_unit;
-                    x.y = (o[g][2 * w + 1][i] * 1048576.0f - zs[g][i]) * o_unit;
-                    x.z = (o[g][2 * w][2 + i] * 16777216.0f - zs[g][i]) * o_unit;
-                    x.w = (o[g][2 * w + 1][2 + i] * 1048576.0f - zs[g][i]) * o_unit;
+                    x.x = o[g][2 * w][i] * 16777216.0f * o_unit + bad[g][i];
+                    x.y = o[g][2 * w + 1][i] * 1048576.0f * o_unit + bad[g][i];
+                    x.z = o[g][2 * w][2 + i] * 16777216.0f * o_unit + bad[g][i];
+                    x.w = o[g][2 * w + 1][2 + i] * 1048576.0f * o_unit + bad[g][i];
                     *reinterpret_cast<float4*>(mine + (g * 8 + 2 * c + i) * D + n * (D / 8) + 4 * w) = x;
                 }
         }
