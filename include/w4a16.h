@@ -472,7 +472,8 @@ size_t w4a16_kv4_page_bytes(int kv_heads, int head_dim, int page_size);
  *   free_pages   device, int32 [n_free]: pages nobody holds, taken in order
  *   taken_in     device, int32 [1]: how many of them are taken already; NULL: none
  *   taken_out    device out, int32 [1]: how many are taken after this call; more than
- *                n_free means that pages were short. Must not be taken_in.
+ *                n_free means that pages were short. Must not be taken_in. Nothing puts pages
+ *                back: a new free list, with those of requests that have ended, is the caller's
  *   block_table  device in/out, int32 [batch][max_pages]: columns below
  *                ceil((seq - new) / page_size) are kept; those below ceil(seq / page_size)
  *                get pages from the free list, requests in order (-1 where it is short);

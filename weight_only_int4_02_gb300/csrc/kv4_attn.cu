@@ -29,9 +29,9 @@
 //
 // Measured, D = 128: 64 requests of 257 to 16384 cached tokens 71 us, 3.6 TB/s, 53% of a copy's rate; one of
 // 131072 tokens 44 us; D = 64, 48 requests of 1 to 5 drafted tokens and a window of 4096 17.6 us; one of 1000
-// tokens 10.9 us, most of it latency. Four CTAs an SM (128 registers a thread) keep the issue slots busy for 51% of the
-// time and the tensor pipe for 32%: a unit is about 610 warp instructions (241 of them integer, 117 FP32, 71 binary16
-// and MMAs), which wait for one another more than for memory. Eight or two warps a CTA, five CTAs an SM
+// tokens 10.9 us, most of it latency. Four CTAs an SM (128 registers a thread) keep the issue slots busy for 52% of the
+// time and the tensor pipe for 33%: a unit is about 640 warp instructions (the integer pipe is busy
+// for 47%), which wait for one another more than for memory. Eight or two warps a CTA, five CTAs an SM
 // (fewer registers) and tokens' scales through shared memory were slower.
 #include "api_internal.cuh"
 #include "kv4.cuh"
@@ -804,14 +804,19 @@ cudaError_t setup_kv4()
 // tokens times query heads) fill the GPU with its tiles of 256; which request is which is known on
 // the device, so such a batch gets both kernels. With fewer rows the stream-K kernel takes everything:
 // it cuts the cached tokens too. Measured for one request, D = 128, tcgen05 and stream-K in us:
-// 800 rows over 1000 tokens 34 / 17; 2048 over 4000 50 / 39; 4096 50 / 58; 8192 53 / 98; 16384
-// 64 / 177; 3200 over 300 14 / 21; 8400 over 300 14 / 30. D = 64: 8192 over 4000 41 / 67; 16384
-// 52 / 119; 5120 over 500 15 / 25. (How many tokens are cached is not known on the host.)
+// 800 rows over 1000 tokens 34 / 17; 2048 over 4000 50 / 41; 4096 50 / 64; 8192 53 / 105; 16384
+// 64 / 192; 3200 over 300 14 / 21; 8400 over 300 14 / 31. D = 64: 8192 over 4000 42 / 71; 16384
+// 53 / 126; 5120 over 500 16 / 25. (How many tokens are cached is not known on the host.)
+// The rule does not look at the rows of one request, and a tile computes 256: many requests of 33 to 64 rows a KV
+// head would be better off with the stream-K kernel. 48 requests over 4000 tokens, 4 KV heads, D = 128, tcgen05 and
+// stream-K: 36 rows 174 / 116, 64 rows 175 / 155, 72 rows 175 / 186, 128 rows 175 / 288; D = 64: 166 / 80, 166 / 102,
+// 166 / 122, 166 / 188.
 constexpr int kFewRows = 32;
 // Segments of 16 rows cost 1.75 times those of 8, and half as many CTAs fit an SM: 8 where they are fewer than 1.75
-// times as many (9 to 16 rows of 64 requests over 4000 tokens, D = 128, 102 / 118 us with 16 / 8; 17 to 24 rows 184 / 168;
-// 32 rows 188 / 219), and where the rows are too few for throughput to count (one request of 16 rows over 8000 tokens
-// 29 / 21; eight of 16 over 1000 21 / 17; eight of 32 over 8000 59 / 66).
+// times as many (9 to 16 rows of 64 requests over 4000 tokens, D = 128, 112 / 126 us with 16 / 8; 17 to 24 rows 199 / 178;
+// 32 rows 201 / 232; D = 64, where an SM holds three of their CTAs, 75 / 88; 131 / 123; 134 / 160), and where the rows are too
+// few for throughput to count (one request of 16 rows over 8000 tokens 29 / 21; eight of 16 over 1000 21 / 17; eight of 32
+// over 8000 65 / 70).
 constexpr int kNarrowRows = 1024;
 constexpr long long prompt_rows(int head_dim) { return head_dim == 128 ? 3200 : 4096; }
 

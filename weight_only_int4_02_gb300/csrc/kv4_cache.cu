@@ -21,7 +21,7 @@ namespace {
 // latency: the launch, two dependent reads and the stores. A warp per request, so that
 // a thousand requests fill the GPU and a chunk of 512 tokens is 16 steps of its warp, four of
 // whose page lookups are in flight together (8 requests 2.3 us; 1000 requests with 56061
-// new tokens 4.4 us, 7.8 with one lookup at a time).
+// new tokens 4.4 us, 7.8 with one lookup at a time). A long chunk is one warp's all the same: 8191 tokens 26 us.
 constexpr int kTabWarps = 8;
 
 struct Need {
@@ -299,8 +299,8 @@ __device__ __forceinline__ int v_word(int tok, int j)
 // Quantises the new rows into their slots. Reads 4 D bytes a token and head and writes
 // 2 (D + 6): bound by bandwidth for a long prompt, by latency for a decode step. A thread has its K and
 // its V load in flight together (8191 tokens of eight heads of 128: 12.6 us against 16.2 with one
-// row a thread), and every lane goes on with one row's extremes and scale (now 10.7 us). Half of that
-// time is the bytes', the rest instructions, V's scattered 2-byte stores and the launch.
+// row a thread), and every lane goes on with one row's extremes and scale (now 11.0 us). Half of that
+// time is the bytes', the rest instructions (issue slots 77% busy) and the launch; V's 2-byte stores are 0.5 us of it.
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowsParams p)
 {
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4RowsParams p)
 }
 
 // The values that slots stand for, (code - zero) * scale in FP32, rounded once. Lanes as above. Bound by its instructions
-// and the loads' latency: 8191 tokens of eight heads of 128 in 7.3 us (8.5 with a shift a code and scalar sums).
+// and the loads' latency: 8191 tokens of eight heads of 128 in 7.4 us (8.5 with a shift a code and scalar sums).
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4RowsParams p)
 {

@@ -30,10 +30,10 @@
 // joins them through the workspace, in their order: 8192 rows over 4000 tokens 81 -> 53 us, 41 of D = 64.
 //
 // Three requests' chunks of 839 to 4000 tokens behind 5690 to 8200 cached ones, 32 query heads over
-// 8, D = 128, bfloat16: 905 us, 900 TFLOP/s, 47% of what a plain bf16 matrix product reaches. (Scores
-// by whole blocks, one S a tile: 1000 us.) The tensor pipe is busy for half of the time, the issue slots
-// too, shared memory for much of the rest, and none of them alone is the limit: without the
-// exponentials, the scales or the unpacking it takes 0 to 5% less, with an eighth of the products 12%.
+// 8, D = 128, bfloat16: 909 us, 898 TFLOP/s, 47% of what a plain bf16 matrix product reaches. (Scores
+// by whole blocks, one S a tile: 1000 us.) The tensor pipe is busy for 42% of the time, the issue slots for
+// 51%, shared memory for 93% (55% for the warps, 38% for the MMAs' operands), which is the nearest to a limit: without
+// the exponentials, the scales or the unpacking the kernel takes 0 to 5% less, with an eighth of the products 12%.
 // Of a CTA's 110 us its start and end, which nothing overlaps, are about 9; CTAs that stay and
 // take the next rows themselves gained nothing there (929 us).
 #include "api_internal.cuh"

@@ -526,7 +526,9 @@ def kv4_tables(seq_lens, new_lens, free_pages, block_table, page_size, max_token
     seq_lens, new_lens: int32 [batch]; free_pages: int32 [n]; block_table: int32
     [batch][max_pages], updated in place; taken: int32 [1], pages of the free list taken
     before, or None. Returns (slots int64 [max_tokens], positions int32 [max_tokens],
-    starts int32 [batch + 1], taken int32 [1])."""
+    starts int32 [batch + 1], taken int32 [1]). Pages are only handed out here: those of a request
+    that has ended are the caller's to put back, into a free_pages of its own making with
+    taken beginning at 0 again."""
     return (_module or _torch_module()).kv4_tables(seq_lens, new_lens, free_pages, block_table, page_size, max_tokens, taken,
                                                    None if stream is None else stream.cuda_stream)
 
