@@ -145,3 +145,14 @@ def test_long_sums_have_no_bias(D, dtype, group, nq):
     noise = 5 * u * float(o.square().mean().sqrt()) / 3 ** 0.5 / out.numel() ** 0.5
     bias = float((out - o).mean())
     assert abs(bias) <= 3 * 2.0 ** -24 * mass + noise, (bias, mass, noise)
+
+
+@pytest.mark.parametrize("path", [1, 2])
+@pytest.mark.parametrize("batch,nq", [(1000, 2), (70, 40)])
+def test_batches_of_many_requests(path, batch, nq):
+    """More requests than a CTA has threads, and than a warp looks at together; lengths and queries of every size, none too."""
+    r = np.random.default_rng(batch)
+    lens = r.integers(0, nq + 1, batch)
+    seq = (lens + r.integers(0, 60, batch)) * (r.random(batch) < 0.9)
+    args = batch_of([int(x) for x in seq], [int(x) for x in lens], 1, 4, 64, 16, "float16", batch)
+    on_path(path, args, 16, 0)

@@ -51,3 +51,20 @@ def test_low_temperatures(dtype, batch, vocab, temperature):
     for k, p, m in ((50, 1.0, 0.0), (50, 0.95, 0.0), (0, 0.9, 0.0), (0, 1.0, 0.02), (0, 1.0, 0.0), (1500, 0.9, 0.0)):
         args = (u, temperature * one, k * one, p * one, m * one)
         check(x, *args, *sample(x, *args))
+
+
+@pytest.mark.parametrize("batch,vocab", [(700, 300), (1500, 4099), (16384, 70), (20000, 70)])
+def test_batches_of_many_rows(batch, vocab):
+    """Rows are taken in order of their work, by one of two ways or not at all as the batch is large; each gives what it
+    gives in a small batch."""
+    r = np.random.default_rng(batch)
+    x = torch.from_numpy(r.standard_normal((batch, vocab)) * 3).to(torch.bfloat16)
+    args = (r.random(batch).astype(F) * F(0.9999999), np.where(r.random(batch) < 0.2, 0.0, r.uniform(0.3, 2.0, batch)),
+            np.where(r.random(batch) < 0.5, 0, r.integers(1, vocab, batch)), np.where(r.random(batch) < 0.5, 1.0, r.uniform(0.05, 1.0, batch)),
+            np.where(r.random(batch) < 0.5, 0.0, 0.1))
+    token, prob = sample(x, *args)
+    some = np.unique(np.concatenate([[0, batch - 1], r.integers(0, batch, 60)]))
+    few = sample(x[some], *[a[some] for a in args])
+    assert np.array_equal(token[some], few[0]) and np.array_equal(prob[some], few[1])
+    check(x[:200], *[a[:200] for a in args], token[:200], prob[:200])
+    assert (token >= 0).all() and (token < vocab).all() and (prob > 0).all()
