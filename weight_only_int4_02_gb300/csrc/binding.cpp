@@ -271,6 +271,8 @@ public:
     Place(PyObject* const* args, int n) {
         int at = -1;   // no CUDA tensor: the call refuses its arguments
         for (int i = 0; i < n; ++i) {
+            // None and numbers by their own types: asking whether they are tensors takes longer
+            if (args[i] == Py_None || PyLong_Check(args[i]) || PyFloat_Check(args[i])) continue;
             if (!THPVariable_Check(args[i]) || !THPVariable_Unpack(args[i]).is_cuda()) continue;
             const int d = THPVariable_Unpack(args[i]).device().index();
             if (at >= 0 && d != at) refuse("the tensors are not all on one device");
