@@ -14,7 +14,7 @@
 //   score = s_k (q . c_k - z_k sum(q)) * scale,   out = sum_t p_t s_v (c_v - z_v) / sum_t p_t
 // so the MMAs multiply by the bare codes: an unpacked register is one logic operation (two
 // codes as binary16 subnormals, exact), K's scale and zero-point act on scores and V's scale on
-// probabilities, once a (token, row). V's zero-points are taken off the running sums unit by unit, from two MMAs of their
+// probabilities, once a (token, row). V's zero-points are taken off the running sums unit by unit, from MMAs of their
 // own: an MMA rounds towards zero, and in sums of codes alone, some hundred times what is left of them in
 // the end, these roundings added up (over 2^20 tokens to 0.8% of the output, 0.1% for 128 requests of 16384; now
 // nothing beside a binary16 output's rounding, for 4% of the time). Tokens are the MMA's M for K (A = 16 tokens x
