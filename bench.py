@@ -23,6 +23,7 @@ import glob
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -246,14 +247,27 @@ def strip_comments(src):
     return " ".join(p for p in parts if p)
 
 
-def source_digest():
-    """Digest of the CUDA sources' code (comments and layout left out): the key under
-    which profiles/dram_traffic.txt records counters."""
-    h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "weight_only_int4_02_gb300", "csrc", "*"))):
+MATMUL_SOURCES = ("api.cu", "decode.cu", "gemm_tc*.cu", "gemv.cu", "pack.cu")
+
+
+def source_digest(csrc=os.path.join(ROOT, "weight_only_int4_02_gb300", "csrc")):
+    """Digest of the code (comments and layout left out) of the matmuls' CUDA sources and of what
+    they include: the key under which profiles/dram_traffic.txt records counters. The serving
+    step's kernels are not the bench's, and their sources are not in it."""
+    code, todo = {}, [f for p in MATMUL_SOURCES for f in glob.glob(os.path.join(csrc, p))]
+    while todo:
+        f = todo.pop()
+        name = os.path.basename(f)
+        if name in code or not os.path.exists(f):   # includes from elsewhere: CUDA's, and the C ABI's header
+            continue
         with open(f, encoding="utf-8") as fh:
-            h.update(os.path.basename(f).encode())
-            h.update(strip_comments(fh.read()).encode())
+            src = fh.read()
+        code[name] = strip_comments(src)
+        todo += [os.path.join(csrc, i) for i in re.findall(r'^\s*#\s*include\s+"([^"]+)"', src, re.M)]
+    h = hashlib.sha256()
+    for name in sorted(code):
+        h.update(name.encode())
+        h.update(code[name].encode())
     return h.hexdigest()[:16]
 
 

@@ -12,7 +12,6 @@
 #include "gemm_tc.cuh"
 #include "decode.cuh"
 #include "gemv.cuh"
-#include "kv4.cuh"
 #include "w4a16.h"
 
 namespace w4a16 {

@@ -17,6 +17,8 @@ struct DeviceInfo {
 w4a16_status report_cuda(cudaError_t e);
 // The current device, checked to be sm_103, with every kernel's attributes set.
 w4a16_status device_info(DeviceInfo* info);
+// Attributes of the serving step's kernels, set with the matmuls'.
+cudaError_t setup_kv4();
 // The library's own workspace on the current device.
 w4a16_status library_workspace(void** ws, size_t* bytes);
 

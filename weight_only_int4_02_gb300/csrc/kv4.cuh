@@ -81,7 +81,6 @@ struct Kv4AttnParams {
     int bf16;
     int splits;                  // CTAs that a pair of row tiles may have (tcgen05 kernel)
 };
-cudaError_t setup_kv4();
 // path: 0 as measured, 1 the stream-K kernel, 2 the tcgen05 kernel for every request of more than 32 rows.
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int head_dim, int max_q, int path, int sms, cudaStream_t stream);
 // The tcgen05 kernel, for requests of more than few_rows rows.
