@@ -433,9 +433,9 @@ w4a16_status w4a16_gemm_noalloc(const uint16_t* x, const uint32_t* packed,
                                 int M, int N, int K, int group_size, w4a16_stream_t stream);
 
 /* ---------------------------------------------------------------- the serving step
- * What a decoder runs beside its 4-bit matmuls: a paged key-value cache held in 4
- * bits (block tables, new keys and values, attention) and the sampling of the next
- * token. The pages have no counterpart. All calls enqueue on `stream` without
+ * What a decoder runs beside its 4-bit matmuls: norms of queries and keys and their
+ * rotation by position, a paged key-value cache held in 4 or 8 bits (block tables, new
+ * keys and values, attention) and the sampling of the next token. The pages have no counterpart. All calls enqueue on `stream` without
  * synchronising and can be captured into a CUDA Graph (the first call on a device
  * outside capture); lengths, tables and settings are device arrays that are read
  * when the kernels run. Results are the same on every call with equal inputs.
@@ -556,6 +556,93 @@ w4a16_status w4a16_kv4_attention(const void* q, int64_t q_token_stride, int64_t 
  * that there may be one. Applies to every later call in the process. Returns the previous
  * setting, or -1 (nothing changed) for another value. */
 int w4a16_kv4_force_path(int path);
+
+/* Positions.
+ *
+ * A rotation turns the first `rot` values of a head's row (rot a multiple of 8, at most head_dim) by angles of the row's
+ * position: pair i, of angle i, is (x[i], x[i + rot / 2]), or (x[2i], x[2i + 1]) if `interleaved` is 1 (0 otherwise):
+ *   (a, b) -> (a cos - b sin, b cos + a sin)       in FP32, each product and sum rounded
+ * The angles' cosines and sines come from a table, device float [rope_rows][rot], 16-byte aligned: of each position rot / 2
+ * cosines, then rot / 2 sines. Scaled or learned angles are a matter of the table.
+ *
+ * w4a16_rope_table fills one with the angles p * base^(-2i / rot) of positions p = 0 .. rows - 1, computed in 64 bits. */
+w4a16_status w4a16_rope_table(float* table, int rows, int rot, double base, w4a16_stream_t stream);
+
+/*
+ * Norms of queries and keys for each head, then the rotation, in one pass; rounded once:
+ *   y = x / sqrt(mean(x^2) + eps) * weight, over a row of head_dim values, mean and factors in FP32
+ *   q, k       device, binary16 or bfloat16 [tokens][heads][head_dim] at token and head strides in elements (multiples of
+ *              8, at least head_dim), 16-byte aligned. q_heads or kv_heads 0: without queries or keys, whose
+ *              pointers and strides are then not looked at
+ *   q_out, k_out  device out, likewise; the input itself at its own strides (in place), or memory that overlaps no input
+ *   q_weight, k_weight  device, [head_dim] of the inputs' type, 16-byte aligned; NULL: no norm
+ *   positions  device, int32 [tokens]; NULL, with rope: no rotation. Rows of a negative position are not written, those of
+ *              a position past the table's rows become NaN
+ */
+w4a16_status w4a16_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                                const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                                void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
+                                const void* q_weight, const void* k_weight, float eps,
+                                const int32_t* positions, const float* rope, int rope_rows, int rot,
+                                int interleaved, int tokens, int q_heads, int kv_heads, int head_dim,
+                                int dtype, w4a16_stream_t stream);
+
+/* The cache in 8 bits: as the 4-bit one, with codes of 8 bits and one scale for a tile of 16 tokens and head, where the 4-bit
+ * one has a scale and a zero-point for each token: uint8 [pages][kv_heads][page_size / 16][32 * D + 16], 16-byte aligned,
+ * w4a16_kv8_page_bytes() a page. Tables and slots are the same (w4a16_kv4_tables). A tile:
+ *   K codes   [D/64][16][64]: byte i of token t in slab p is d = 64p + i
+ *   V codes   [D/64][2][8][4][4][2][2]: byte (p, h, n, c, j, e, i) is d = 64p + 8n + 2j + i of token 8h + 2c + e
+ *   K scale, V scale  float, of all 16 tokens;  8 bytes unused
+ * A stored value is (code - 128) * scale. Memory of the cache that no slot was written to may hold anything. */
+
+/* Bytes of one page of the cache (0 for sizes it does not have). */
+size_t w4a16_kv8_page_bytes(int kv_heads, int head_dim, int page_size);
+
+/*
+ * Quantises new keys, rotated on the way, and values into their slots. Tokens that are neighbours in the list and
+ * whose slots are neighbours in one tile (s, s + 1, ...) are a run and are stored together, K and V alike, in FP32
+ * with IEEE operations: with a = max |x| / 127 over the run's rows of a head (0 below 2^-40, at most 2^40) and old the tile's
+ * scale, or 0 if the run begins at the tile's first token,
+ *   s = max(old, a), r = 1 / s, code = clamp(rint(x * r), -127, 127) + 128      (s = 0: 128)
+ * and where s > old the codes of the tile's tokens before the run become clamp(rint((code - 128) * (old * r)), -127, 127) + 128.
+ * So a tile's tokens are to be written in their order, from its first one on, as a request's are, and each tile by one run of a
+ * call; two runs of one call in a tile leave any values in it, and one that begins within a tile that was not begun takes
+ * whatever is in memory for its scale. Tokens written again (drafts that were not accepted) are written again in order; the scale stays
+ * as large as it was. A row with an infinity or a NaN, or a key at a position that the table does not have, makes the
+ * scale NaN, which shows in whatever reads a token of that tile and head until the tile is begun again.
+ *   k, v, slots, cache, dtype  as w4a16_kv4_append
+ *   positions, rope, rope_rows, rot, interleaved  the keys' rotation; positions and rope NULL: none
+ */
+w4a16_status w4a16_kv8_append(const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                              const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                              const int64_t* slots, const int32_t* positions, const float* rope,
+                              int rope_rows, int rot, int interleaved, uint8_t* cache, int pages,
+                              int tokens, int kv_heads, int head_dim, int page_size, int dtype,
+                              w4a16_stream_t stream);
+
+/* The values that slots stand for, as w4a16_kv4_read. */
+w4a16_status w4a16_kv8_read(const uint8_t* cache, int pages, const int64_t* slots, void* k, void* v,
+                            int tokens, int kv_heads, int head_dim, int page_size, int dtype,
+                            w4a16_stream_t stream);
+
+/* Bytes of caller workspace w4a16_kv8_attention needs on the current device (0 if the
+ * device cannot be used). */
+size_t w4a16_kv8_workspace_bytes(void);
+
+/* Causal attention of new query tokens over the 8-bit cache: arguments, masks and results as
+ * w4a16_kv4_attention, its workspace w4a16_kv8_workspace_bytes() bytes. */
+w4a16_status w4a16_kv8_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                 const uint8_t* cache, int pages, const int32_t* block_table,
+                                 int64_t table_stride, int table_cols, const int32_t* seq_lens,
+                                 const int32_t* starts, void* out, int64_t out_token_stride,
+                                 int64_t out_head_stride, float* lse, int batch, int tokens,
+                                 int q_heads, int kv_heads, int head_dim, int page_size, int max_q,
+                                 float scale, int window, int dtype, void* workspace,
+                                 size_t ws_bytes, w4a16_stream_t stream);
+
+/* Forces the kernel of w4a16_kv8_attention, as w4a16_kv4_force_path. */
+int w4a16_kv8_force_path(int path);
 
 /*
  * Samples one token per row. With m the row's maximum and e(x) = exp((x - m) / T) in

@@ -103,13 +103,40 @@ struct Cache {
     int pages, heads, dim;
 };
 
-Cache cache_of(PyObject* o, int page_size) {
-    const char* what = "the cache must be a contiguous uint8 CUDA tensor [pages][kv_heads][page_size / 16][16 * (head_dim + 6)]";
+// bits: 4 or 8. The last dimension is a tile: 16 * (head_dim + 6) or 32 * head_dim + 16 bytes.
+Cache cache_of(PyObject* o, int page_size, int bits) {
+    const char* what = bits == 4
+        ? "the cache must be a contiguous uint8 CUDA tensor [pages][kv_heads][page_size / 16][16 * (head_dim + 6)]"
+        : "the cache must be a contiguous uint8 CUDA tensor [pages][kv_heads][page_size / 16][32 * head_dim + 16]";
     const at::Tensor& t = tensor(o, what);
     if (t.scalar_type() != at::kByte || !t.is_cuda() || t.dim() != 4 || !t.is_contiguous() || t.size(2) * 16 != page_size ||
-        t.size(3) % 16 != 0)
+        t.size(3) % 16 != 0 || (bits == 8 && t.size(3) % 32 != 16))
         refuse(what);
-    return {t, count(t.size(0), what), count(t.size(1), what), count(t.size(3) / 16 - 6, what)};
+    const int64_t dim = bits == 4 ? t.size(3) / 16 - 6 : (t.size(3) - 16) / 32;
+    return {t, count(t.size(0), what), count(t.size(1), what), count(dim, what)};
+}
+
+// A rotation's arguments: positions and a table, both or neither.
+struct Turn {
+    const int32_t* positions = nullptr;
+    const float* table = nullptr;
+    int rows = 0, rot = 0, interleaved = 0;
+};
+
+Turn turn_of(PyObject* positions, PyObject* rope, PyObject* interleaved, int tokens) {
+    Turn r;
+    r.interleaved = truth(interleaved, "interleaved must be true or false");
+    if (positions == Py_None && rope == Py_None) return r;
+    if (positions == Py_None || rope == Py_None) refuse("positions and rope go together");
+    const char* what = "rope must be a contiguous float32 CUDA tensor [positions][rot]";
+    r.positions = vector<int32_t>(positions, at::kInt, tokens, "positions must be a contiguous int32 CUDA tensor [tokens]");
+    const at::Tensor& t = tensor(rope, what);
+    if (t.scalar_type() != at::kFloat || !t.is_cuda() || t.dim() != 2 || !t.is_contiguous() || t.numel() == 0) refuse(what);
+    r.table = t.data_ptr<float>();
+    r.rows = count(t.size(0), what);
+    r.rot = count(t.size(1), what);
+    if (tokens == 0) r = Turn();   // an empty tensor has no address
+    return r;
 }
 
 at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Tensor& like) {
@@ -161,46 +188,142 @@ PyObject* tables(PyObject* const* a) {
                   part(all, at_starts, {(int64_t)batch + 1}, at::kInt), part(all, at_after, {1}, at::kInt)});
 }
 
-// (k, v, slots, cache, page_size, stream)
-PyObject* append(PyObject* const* a) {
+// Keys and values of as many tokens as there are slots.
+struct Rows {
+    const at::Tensor &k, &v;
+    const int64_t* slots;
+    int tokens, dtype;
+};
+
+Rows rows_of(PyObject* k_in, PyObject* v_in, PyObject* slots_in, const Cache& c) {
     const char* what = "k and v must be float16 or bfloat16 CUDA tensors [tokens][kv_heads][head_dim], the last dimension contiguous";
-    const int page_size = integer(a[4], "page_size");
-    const Cache c = cache_of(a[3], page_size);
-    const at::Tensor &k = tensor(a[0], what), &v = tensor(a[1], what);
-    const int64_t* slots = vector<int64_t>(a[2], at::kLong, -1, "slots must be a contiguous int64 CUDA tensor");
-    const int tokens = count(THPVariable_Unpack(a[2]).size(0), "too many slots");
+    const at::Tensor &k = tensor(k_in, what), &v = tensor(v_in, what);
+    const int64_t* slots = vector<int64_t>(slots_in, at::kLong, -1, "slots must be a contiguous int64 CUDA tensor");
+    const int tokens = count(THPVariable_Unpack(slots_in).size(0), "too many slots");
     for (const at::Tensor* t : {&k, &v})
         if (t->scalar_type() != k.scalar_type() || !t->is_cuda() || t->dim() != 3 || t->size(0) != tokens ||
             t->size(1) != c.heads || t->size(2) != c.dim || t->stride(2) != 1)
             refuse(what);
-    check(w4a16_kv4_append(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), slots,
-                           c.t.data_ptr<uint8_t>(), c.pages, tokens, c.heads, c.dim, page_size,
-                           dtype_of(k.scalar_type(), what), stream_of(k)),
+    return {k, v, slots, tokens, dtype_of(k.scalar_type(), what)};
+}
+
+// (k, v, slots, cache, page_size, stream)
+PyObject* append(PyObject* const* a) {
+    const int page_size = integer(a[4], "page_size");
+    const Cache c = cache_of(a[3], page_size, 4);
+    const Rows r = rows_of(a[0], a[1], a[2], c);
+    check(w4a16_kv4_append(r.k.data_ptr(), r.k.stride(0), r.k.stride(1), r.v.data_ptr(), r.v.stride(0), r.v.stride(1), r.slots,
+                           c.t.data_ptr<uint8_t>(), c.pages, r.tokens, c.heads, c.dim, page_size, r.dtype, stream_of(r.k)),
           "w4a16_kv4_append");
     Py_RETURN_NONE;
 }
 
+// (k, v, slots, cache, page_size, positions, rope, interleaved, stream)
+PyObject* append8(PyObject* const* a) {
+    const int page_size = integer(a[4], "page_size");
+    const Cache c = cache_of(a[3], page_size, 8);
+    const Rows r = rows_of(a[0], a[1], a[2], c);
+    const Turn turn = turn_of(a[5], a[6], a[7], r.tokens);
+    check(w4a16_kv8_append(r.k.data_ptr(), r.k.stride(0), r.k.stride(1), r.v.data_ptr(), r.v.stride(0), r.v.stride(1), r.slots,
+                           turn.positions, turn.table, turn.rows, turn.rot, turn.interleaved, c.t.data_ptr<uint8_t>(), c.pages,
+                           r.tokens, c.heads, c.dim, page_size, r.dtype, stream_of(r.k)),
+          "w4a16_kv8_append");
+    Py_RETURN_NONE;
+}
+
 // (cache, slots, page_size, dtype as the C ABI's, stream)
+template <int BITS>
 PyObject* read(PyObject* const* a) {
     const int page_size = integer(a[2], "page_size"), dtype = integer(a[3], "dtype");
-    const Cache c = cache_of(a[0], page_size);
+    const Cache c = cache_of(a[0], page_size, BITS);
     const int64_t* slots = vector<int64_t>(a[1], at::kLong, -1, "slots must be a contiguous int64 CUDA tensor");
     const int tokens = count(THPVariable_Unpack(a[1]).size(0), "too many slots");
     const at::ScalarType type = dtype == W4A16_FP16 ? at::kHalf : dtype == W4A16_BF16 ? at::kBFloat16 : at::kFloat;
     at::Tensor all = empty({2, tokens, c.heads, c.dim}, type, c.t);
     const int64_t half = (int64_t)all.nbytes() / 2;
     char* const to = static_cast<char*>(all.data_ptr());
-    check(w4a16_kv4_read(c.t.data_ptr<uint8_t>(), c.pages, slots, to, to + half, tokens, c.heads, c.dim, page_size, dtype,
-                         stream_of(c.t)),
-          "w4a16_kv4_read");
+    check((BITS == 4 ? w4a16_kv4_read : w4a16_kv8_read)(c.t.data_ptr<uint8_t>(), c.pages, slots, to, to + half, tokens, c.heads,
+                                                        c.dim, page_size, dtype, stream_of(c.t)),
+          BITS == 4 ? "w4a16_kv4_read" : "w4a16_kv8_read");
     return tuple({part(all, 0, {tokens, c.heads, c.dim}, type), part(all, half, {tokens, c.heads, c.dim}, type)});
 }
 
+// A [tokens][heads][dim] view whose rows the kernels can take.
+bool heads_view(const at::Tensor& t) {
+    return (t.scalar_type() == at::kHalf || t.scalar_type() == at::kBFloat16) && t.is_cuda() && t.dim() == 3 && t.stride(2) == 1;
+}
+
+// (q, k, positions, rope, q_weight, k_weight, eps, interleaved, q_out, k_out, stream)
+PyObject* norm_rope(PyObject* const* a) {
+    const char* whats[2] = {"q must be a float16 or bfloat16 CUDA tensor [tokens][q_heads][head_dim], the last dimension contiguous, or None",
+                            "k must be a CUDA tensor [tokens][kv_heads][head_dim] of q's type, the last dimension contiguous, or None"};
+    const char* outs[2] = {"q_out must be a CUDA tensor of q's type and shape, the last dimension contiguous",
+                           "k_out must be a CUDA tensor of k's type and shape, the last dimension contiguous"};
+    const char* weights[2] = {"q_weight must be a contiguous CUDA tensor [head_dim] of q's type",
+                              "k_weight must be a contiguous CUDA tensor [head_dim] of k's type"};
+    if (a[0] == Py_None && a[1] == Py_None) refuse("neither q nor k");
+    const at::Tensor* x[2] = {nullptr, nullptr};
+    for (int i = 0; i < 2; ++i)
+        if (a[i] != Py_None) {
+            x[i] = &tensor(a[i], whats[i]);
+            if (!heads_view(*x[i])) refuse(whats[i]);
+        }
+    const at::Tensor& any = x[0] ? *x[0] : *x[1];
+    if (x[0] && x[1] && (x[0]->scalar_type() != x[1]->scalar_type() || x[0]->size(0) != x[1]->size(0) || x[0]->size(2) != x[1]->size(2)))
+        refuse(whats[1]);
+    const int tokens = count(any.size(0), "too many tokens"), dim = count(any.size(2), whats[0]);
+    const Turn turn = turn_of(a[2], a[3], a[7], tokens);
+    const double eps = PyFloat_AsDouble(a[6]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse("eps must be a number");
+    }
+    void *from[2] = {nullptr, nullptr}, *weight[2] = {nullptr, nullptr}, *to[2] = {nullptr, nullptr};
+    int64_t strides[2][4] = {};
+    int heads[2] = {0, 0};
+    at::Tensor out[2];
+    for (int i = 0; i < 2; ++i) {
+        if (!x[i]) {
+            if (a[8 + i] != Py_None || a[4 + i] != Py_None) refuse("a weight or an output without its input");
+            continue;
+        }
+        weight[i] = optional_vector<void>(a[4 + i], any.scalar_type(), dim, weights[i]);
+        if (a[8 + i] == Py_None) {
+            out[i] = empty(x[i]->sizes(), any.scalar_type(), any);
+        } else {
+            out[i] = tensor(a[8 + i], outs[i]);
+            if (!heads_view(out[i]) || out[i].scalar_type() != any.scalar_type() || out[i].sizes() != x[i]->sizes()) refuse(outs[i]);
+        }
+        heads[i] = count(x[i]->size(1), "too many heads");
+        from[i] = x[i]->data_ptr();
+        to[i] = out[i].data_ptr();
+        strides[i][0] = x[i]->stride(0);
+        strides[i][1] = x[i]->stride(1);
+        strides[i][2] = out[i].stride(0);
+        strides[i][3] = out[i].stride(1);
+    }
+    check(w4a16_qk_norm_rope(from[0], strides[0][0], strides[0][1], to[0], strides[0][2], strides[0][3], from[1], strides[1][0],
+                             strides[1][1], to[1], strides[1][2], strides[1][3], weight[0], weight[1], (float)eps, turn.positions,
+                             turn.table, turn.rows, turn.rot, turn.interleaved, tokens, heads[0], heads[1], dim,
+                             dtype_of(any.scalar_type(), whats[0]), stream_of(any)),
+          "w4a16_qk_norm_rope");
+    PyObject* r = PyTuple_New(2);
+    if (!r) return nullptr;
+    for (int i = 0; i < 2; ++i) {
+        PyObject* o = Py_None;
+        if (out[i].defined()) o = THPVariable_Wrap(out[i]);
+        else Py_INCREF(o);
+        PyTuple_SET_ITEM(r, i, o);
+    }
+    return r;
+}
+
 // (q, cache, block_table, seq_lens, starts, page_size, max_q, scale, window, out, return_lse, workspace, stream)
+template <int BITS>
 PyObject* attention(PyObject* const* a) {
     const char* what = "q must be a float16 or bfloat16 CUDA tensor [tokens][q_heads][head_dim], the last dimension contiguous";
     const int page_size = integer(a[5], "page_size");
-    const Cache c = cache_of(a[1], page_size);
+    const Cache c = cache_of(a[1], page_size, BITS);
     const at::Tensor &q = tensor(a[0], what), &table = tensor(a[2], "block_table must be a tensor");
     if (!q.is_cuda() || q.dim() != 3 || q.size(2) != c.dim || q.stride(2) != 1) refuse(what);
     const int dtype = dtype_of(q.scalar_type(), what);
@@ -233,12 +356,12 @@ PyObject* attention(PyObject* const* a) {
         ws = w.data_ptr();
         ws_bytes = w.nbytes();
     }
-    check(w4a16_kv4_attention(q.data_ptr(), q.stride(0), q.stride(1), c.t.data_ptr<uint8_t>(), c.pages,
+    check((BITS == 4 ? w4a16_kv4_attention : w4a16_kv8_attention)(q.data_ptr(), q.stride(0), q.stride(1), c.t.data_ptr<uint8_t>(), c.pages,
                               table.data_ptr<int32_t>(), row_stride(table), cols, seq, starts,
                               out.data_ptr(), out.stride(0), out.stride(1), lse.defined() ? lse.data_ptr<float>() : nullptr,
                               batch, tokens, heads, c.heads, c.dim, page_size, integer(a[6], "max_q"), (float)scale,
                               integer(a[8], "window"), dtype, ws, ws_bytes, stream_of(q)),
-          "w4a16_kv4_attention");
+          BITS == 4 ? "w4a16_kv4_attention" : "w4a16_kv8_attention");
     return lse.defined() ? tuple({out, lse}) : THPVariable_Wrap(out);
 }
 
@@ -325,10 +448,17 @@ PyObject* set_error(PyObject*, PyObject* cls) {
     Py_RETURN_NONE;
 }
 
-#define FAST(f, n) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<f, n>)), METH_FASTCALL
-PyMethodDef g_methods[] = {{"kv4_tables", FAST(tables, 8), nullptr},   {"kv4_append", FAST(append, 6), nullptr},
-                           {"kv4_read", FAST(read, 5), nullptr},       {"kv4_attention", FAST(attention, 13), nullptr},
-                           {"sample", FAST(sample, 7), nullptr},       {"set_error", set_error, METH_O, nullptr},
+#define FAST(f, n) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<(f), n>)), METH_FASTCALL
+PyMethodDef g_methods[] = {{"kv4_tables", FAST(tables, 8), nullptr},
+                           {"kv4_append", FAST(append, 6), nullptr},
+                           {"kv4_read", FAST(read<4>, 5), nullptr},
+                           {"kv4_attention", FAST(attention<4>, 13), nullptr},
+                           {"kv8_append", FAST(append8, 9), nullptr},
+                           {"kv8_read", FAST(read<8>, 5), nullptr},
+                           {"kv8_attention", FAST(attention<8>, 13), nullptr},
+                           {"qk_norm_rope", FAST(norm_rope, 11), nullptr},
+                           {"sample", FAST(sample, 7), nullptr},
+                           {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_w4a16_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

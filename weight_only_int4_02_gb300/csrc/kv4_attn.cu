@@ -35,88 +35,19 @@
 // (fewer registers) and tokens' scales through shared memory were slower.
 #include "api_internal.cuh"
 #include "kv4.cuh"
+#include "kv_attn.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
 
 #include <float.h>
-#include <limits.h>
-#include <math_constants.h>
 
 namespace w4a16 {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = kAttnWarps, kThreads = kAttnThreads, kGrow = kAttnGrow;
 constexpr int kUnit = 32;      // tokens of a unit: two tiles
 constexpr int kOverhead = 12;  // what starting and ending a segment costs, in units
-constexpr int kGrow = 8;       // log2 of how far probabilities may grow before their reference moves
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1)
-{
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t transpose8(uint32_t x)
-{
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // e in -126 .. 127
-
-__device__ __forceinline__ uint32_t half2_bits(float a, float b)
-{
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ float2 bits_half2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
-
-// One request as the kernel sees it: every length clamped to what the buffers hold.
-struct Request {
-    int seq, q0, nq, rows, tiles;   // cached tokens that the table can hold, first query token, query tokens, rows, row tiles
-    int pos0;                       // the first query's position: of all cached tokens, also those past the table's columns
-    int base, units;                // first cached token looked at (a multiple of kUnit), units a segment
-    long long work;                 // cost of all its segments: kOverhead, then the units, of each
-};
-
-template <int ROWS>
-__device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b)
-{
-    Request r;
-    const long long held = (long long)p.table_cols * p.page_size;
-    int s = p.seq_lens[b];
-    s = s < 0 ? 0 : s;
-    r.seq = s < held ? s : (int)held;
-    int a = p.starts[b], e = p.starts[b + 1];
-    a = a < 0 ? 0 : a > p.tokens ? p.tokens : a;
-    e = e < a ? a : e > p.tokens ? p.tokens : e;
-    r.q0 = a;
-    r.nq = e - a;
-    r.pos0 = s - r.nq;
-    r.rows = r.nq * p.group;
-    r.tiles = r.rows > p.few_rows ? 0 : (r.rows + ROWS - 1) / ROWS;
-    // first token that a query's window holds (a query at a negative position sees nothing; none of them: no overflow
-    // whatever the window)
-    const int first = (r.pos0 > 0 ? r.pos0 : 0) - p.window + 1;
-    r.base = (p.window > 0 && first > 0) ? first / kUnit * kUnit : 0;
-    r.units = r.seq > r.base ? (r.seq - r.base + kUnit - 1) / kUnit : 1;   // an empty segment still writes its rows
-    r.work = (long long)r.tiles * p.kv_heads * (r.units + kOverhead);
-    return r;
-}
 
 template <int D, int NR>
 struct Attn {
@@ -131,13 +62,9 @@ struct Attn {
     static constexpr int W = D / 32;            // words of a lane's share
     static constexpr int PART = ROWS * (D + 2); // floats of one partial: O, then m and l
     static_assert(RING >= ROWS * D * 4, "a warp's ring holds its output");
-    struct Shared {
+    static constexpr int DIM = D, UNIT = kUnit, OVERHEAD = kOverhead;
+    struct Shared : RunShared<ROWS> {
         uint64_t bar[kWarps][STAGES];
-        float m[kWarps][ROWS], l[kWarps][ROWS];
-        float weight[kWarps][ROWS];
-        long long scan[kWarps];
-        long long start_off;
-        int start_b, abort_flag, last;
     };
     static constexpr int SMEM = kWarps * RING + sizeof(Shared);
 };
@@ -172,51 +99,13 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
     chained_kernel();
 
     // ---- this CTA's run of units
-    long long sum = 0;
-    const int per = (p.batch + kThreads - 1) / kThreads;
-    const int bl = tid * per, bh = bl + per < p.batch ? bl + per : p.batch;
-    for (int b = bl; b < bh; ++b) sum += request_of<ROWS>(p, b).work;
-    long long incl = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-    }
-    if (lane == 31) sh.scan[warp] = incl;
-    if (tid == 0) {
-        sh.abort_flag = 0;
-        sh.start_b = p.batch;
-    }
     if (lane < A::STAGES) mbar_init(smem_addr(&sh.bar[warp][lane]), 1);
     fence_mbar_init();
-    __syncthreads();
-    long long excl = incl - sum, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) excl += sh.scan[w];
-        total += sh.scan[w];
-    }
-    // as many CTAs as give each warp a unit
-    const long long want = (total + kWarps - 1) / kWarps;
-    const long long ctas = want < gridDim.x ? want : gridDim.x;
-    if (blockIdx.x >= ctas) return;
-    const long long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
-    if (u0 >= excl && u0 < excl + sum) {
-        long long at = excl;
-        for (int b = bl; b < bh; ++b) {
-            const long long w = request_of<ROWS>(p, b).work;
-            if (u0 < at + w) {
-                sh.start_b = b;
-                sh.start_off = u0 - at;
-                break;
-            }
-            at += w;
-        }
-    }
-    __syncthreads();
-    int b = sh.start_b;
-    long long off = sh.start_off;
-    if (b >= p.batch) return;   // cannot happen: u0 < total
+    const Units un = units_of<A>(p, sh);
+    int b = un.b;
+    long long off = un.off;
+    if (b >= p.batch) return;   // more CTAs than units
+    const long long u0 = un.u0, u1 = un.u1;
 
     const WaitCtl ctl{&sh.abort_flag, p.status, p.wait_limit_ns};
     // the ring: stage and phase of the next unit to issue and to use; two bits a stage: tiles present
@@ -225,11 +114,11 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
     bool dead = false;
     const int tpp_shift = __ffs(p.page_size) - 5;   // log2(tiles per page)
 
-    Request r = request_of<ROWS>(p, b);
+    Request r = request_of<A>(p, b);
     for (long long u = u0; u < u1;) {
         while (off >= r.work) {   // next request with work
             off -= r.work;
-            r = request_of<ROWS>(p, ++b);
+            r = request_of<A>(p, ++b);
         }
         const int cost = r.units + kOverhead;
         const long long seg = off / cost;
@@ -621,128 +510,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                     *reinterpret_cast<float4*>(mine + (g * 8 + 2 * c + i) * D + n * (D / 8) + 4 * w) = x;
                 }
         }
-        __syncthreads();
-        const int live = r.rows - row0 < ROWS ? r.rows - row0 : ROWS;
-        const bool whole = pos == 0 && take == r.units;
-        // joined maximum, sum and the warps' weights of each row
-        float* const part = p.partials + (long long)(2 * blockIdx.x + (pos == 0 ? 1 : 0)) * A::PART;
-        if (tid < live) {
-            float mm = -CUDART_INF_F, ll = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][tid]);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = sh.m[w][tid] == mm ? 1.0f : ex2(sh.m[w][tid] - mm);
-                ll += sh.l[w][tid] * f;
-                sh.weight[w][tid] = f;
-            }
-            if (whole) {
-                const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) sh.weight[w][tid] *= inv;
-                if (p.lse) {
-                    const int rr = row0 + tid, qi = rr / p.group;
-                    p.lse[(long long)(r.q0 + qi) * p.q_heads + head * p.group + rr - qi * p.group] =
-                        ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * CUDART_LN2_F;
-                }
-            } else {
-                __stcg(part + ROWS * D + tid, mm);
-                __stcg(part + ROWS * D + ROWS + tid, ll);
-            }
-        }
-        __syncthreads();
-        auto store_row = [&](int row, int d, const float4& x) {
-            const int rr = row0 + row, qi = rr / p.group;
-            uint16_t* dst = (uint16_t*)p.out + (long long)(r.q0 + qi) * p.o_token +
-                            (long long)(head * p.group + rr - qi * p.group) * p.o_head + d;
-            uint2 w;
-            if (p.bf16) {
-                const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), bb = __floats2bfloat162_rn(x.z, x.w);
-                w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&bb));
-            } else {
-                w = make_uint2(half2_bits(x.x, x.y), half2_bits(x.z, x.w));
-            }
-            *reinterpret_cast<uint2*>(dst) = w;
-        };
-        for (int i = tid; i < live * (D / 4); i += kThreads) {
-            const int row = i / (D / 4), d = i % (D / 4) * 4;
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = sh.weight[w][row];
-                const float4 y = *reinterpret_cast<const float4*>(smem + w * A::RING + (row * D + d) * 4);
-                x.x += f * y.x;
-                x.y += f * y.y;
-                x.z += f * y.z;
-                x.w += f * y.w;
-            }
-            if (whole) store_row(row, d, x);
-            else __stcg(reinterpret_cast<float4*>(part + row * D + d), x);
-        }
-        if (!whole) {
-            // ---- the last CTA of the segment to arrive joins the partial results, in the CTAs' order
-            const long long g0 = seg_u + kOverhead;   // the place of the segment's first unit
-            const int ca = (int)(((g0 + 1) * ctas - 1) / total), cb = (int)(((g0 + r.units) * ctas - 1) / total);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int before = atomicAdd(p.counters + ca, 1);
-                sh.last = before == cb - ca;
-                if (sh.last) p.counters[ca] = 0;   // ready for the next launch
-                __threadfence();
-            }
-            __syncthreads();
-            if (sh.last) {
-                // first every partial's weight (all rows and CTAs at once, kept where the rings were), then the sums
-                const int parts = cb - ca + 1;
-                float* const wt = reinterpret_cast<float*>(smem);
-                auto part_of = [&](int k) { return p.partials + (long long)(2 * (ca + k) + (k == 0)) * A::PART; };
-                for (int i = tid; i < parts * live; i += kThreads) wt[i] = __ldcg(part_of(i / live) + ROWS * D + i % live);
-                __syncthreads();
-                if (warp < live) {
-                    for (int row = warp; row < live; row += kWarps) {
-                        float mm = -CUDART_INF_F, ll = 0.0f;
-                        for (int k = lane; k < parts; k += 32) mm = fmaxf(mm, wt[k * live + row]);
-#pragma unroll
-                        for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-                        for (int k = lane; k < parts; k += 32) {
-                            const float mk = wt[k * live + row], f = mk == mm ? 1.0f : ex2(mk - mm);
-                            wt[k * live + row] = f;
-                            ll += f * __ldcg(part_of(k) + ROWS * D + ROWS + row);
-                        }
-#pragma unroll
-                        for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
-                        if (lane == 0) {
-                            sh.l[0][row] = ll == 0.0f ? 0.0f : 1.0f / ll;
-                            if (p.lse) {
-                                const int rr = row0 + row, qi = rr / p.group;
-                                p.lse[(long long)(r.q0 + qi) * p.q_heads + head * p.group + rr - qi * p.group] =
-                                    ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * CUDART_LN2_F;
-                            }
-                        }
-                    }
-                }
-                __syncthreads();
-                for (int i = tid; i < live * (D / 4); i += kThreads) {
-                    const int row = i / (D / 4), d = i % (D / 4) * 4;
-                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-                    for (int k = 0; k < parts; ++k) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(part_of(k) + row * D + d));
-                        const float f = wt[k * live + row];
-                        x.x += f * y.x;
-                        x.y += f * y.y;
-                        x.z += f * y.z;
-                        x.w += f * y.w;
-                    }
-                    const float inv = sh.l[0][row];
-                    store_row(row, d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-                }
-            }
-        }
-        // the rings are read: bulk copies may follow the plain accesses
-        fence_proxy_async_smem();
-        __syncthreads();
+        finish_segment<A>(p, smem, sh, r, head, row0, pos, take, seg_u, un);
     }
 }
 

@@ -1,11 +1,8 @@
 // The 4-bit cache's bookkeeping and rows: block tables and slot maps from request
 // lengths, quantisation of new keys and values into their slots, and the read back.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-
 #include "kv4.cuh"
 #include "launch.cuh"
+#include "pairs.cuh"
 #include "w4a16.h"
 
 namespace w4a16 {
@@ -129,19 +126,6 @@ __global__ void __launch_bounds__(kTabWarps * 32) kv4_tables_kernel(const Kv4Tab
 }
 
 // ---------------------------------------------------------------- rows
-template <int DTYPE>
-__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b)
-{
-    if constexpr (DTYPE == W4A16_BF16) {
-        a = __uint_as_float(w << 16);
-        b = __uint_as_float(w & 0xffff0000u);
-    } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        a = f.x;
-        b = f.y;
-    }
-}
-
 __device__ __forceinline__ uint32_t negate2(uint32_t w) { return w ^ 0x80008000u; }
 
 // The larger (smaller) of each pair; a NaN on either side gives a NaN.
@@ -166,18 +150,6 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b)
     } else {
         const __half2 m = __hmin2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
         return *reinterpret_cast<const uint32_t*>(&m);
-    }
-}
-
-template <int DTYPE>
-__device__ __forceinline__ uint32_t pack2(float a, float b)
-{
-    if constexpr (DTYPE == W4A16_BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
     }
 }
 

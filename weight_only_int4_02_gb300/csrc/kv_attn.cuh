@@ -1,0 +1,287 @@
+// What the attention kernels for few query rows share, whatever the cache's bits: the batch's work as one line of units dealt to
+// the CTAs in equal runs, and the joining of a segment's parts.
+#pragma once
+#include "api_internal.cuh"
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <limits.h>
+#include <math_constants.h>
+
+namespace w4a16 {
+
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr int kAttnGrow = 8;       // log2 of how far probabilities may grow before their reference moves
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // e in -126 .. 127
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 bits_half2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+
+// One request as the kernel sees it: every length clamped to what the buffers hold.
+struct Request {
+    int seq, q0, nq, rows, tiles;   // cached tokens that the table can hold, first query token, query tokens, rows, row tiles
+    int pos0;                       // the first query's position: of all cached tokens, also those past the table's columns
+    int base, units;                // first cached token looked at (a multiple of UNIT), units a segment
+    long long work;                 // cost of all its segments: OVERHEAD, then the units, of each
+};
+
+// A: the kernel's ROWS of a segment, UNIT cached tokens and OVERHEAD, what starting and ending a segment costs, in units.
+template <class A>
+__device__ __forceinline__ Request request_of(const Kv4AttnParams& p, int b)
+{
+    Request r;
+    const long long held = (long long)p.table_cols * p.page_size;
+    int s = p.seq_lens[b];
+    s = s < 0 ? 0 : s;
+    r.seq = s < held ? s : (int)held;
+    int a = p.starts[b], e = p.starts[b + 1];
+    a = a < 0 ? 0 : a > p.tokens ? p.tokens : a;
+    e = e < a ? a : e > p.tokens ? p.tokens : e;
+    r.q0 = a;
+    r.nq = e - a;
+    r.pos0 = s - r.nq;
+    r.rows = r.nq * p.group;
+    r.tiles = r.rows > p.few_rows ? 0 : (r.rows + A::ROWS - 1) / A::ROWS;
+    // first token that a query's window holds (a query at a negative position sees nothing; none of them: no overflow
+    // whatever the window)
+    const int first = (r.pos0 > 0 ? r.pos0 : 0) - p.window + 1;
+    r.base = (p.window > 0 && first > 0) ? first / A::UNIT * A::UNIT : 0;
+    r.units = r.seq > r.base ? (r.seq - r.base + A::UNIT - 1) / A::UNIT : 1;   // an empty segment still writes its rows
+    r.work = (long long)r.tiles * p.kv_heads * (r.units + A::OVERHEAD);
+    return r;
+}
+
+// In shared memory beside a kernel's own.
+template <int ROWS>
+struct RunShared {
+    float m[kAttnWarps][ROWS], l[kAttnWarps][ROWS];   // each warp's maxima and sums
+    float weight[kAttnWarps][ROWS];
+    long long scan[kAttnWarps];
+    long long start_off;
+    int start_b, abort_flag, last;
+};
+
+// A CTA's run of units: u0 .. u1 of the batch's `total`, from `off` on in request b's. Requests without a CTA of this launch (b past
+// the batch) have none. Every thread of the CTA calls it; the lengths stay on the device, so every CTA sums them by itself.
+struct Units {
+    long long u0, u1, total, ctas, off;
+    int b;
+};
+
+template <class A>
+__device__ __forceinline__ Units units_of(const Kv4AttnParams& p, typename A::Shared& sh)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Units u = {};
+    u.b = p.batch;
+    long long sum = 0;
+    const int per = (p.batch + kAttnThreads - 1) / kAttnThreads;
+    const int bl = tid * per, bh = bl + per < p.batch ? bl + per : p.batch;
+    for (int b = bl; b < bh; ++b) sum += request_of<A>(p, b).work;
+    long long incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) sh.scan[warp] = incl;
+    if (tid == 0) {
+        sh.abort_flag = 0;
+        sh.start_b = p.batch;
+    }
+    __syncthreads();
+    long long excl = incl - sum;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < warp) excl += sh.scan[w];
+        u.total += sh.scan[w];
+    }
+    // as many CTAs as give each warp a unit
+    const long long want = (u.total + kAttnWarps - 1) / kAttnWarps;
+    u.ctas = want < gridDim.x ? want : gridDim.x;
+    if (blockIdx.x >= u.ctas) return u;
+    u.u0 = u.total * blockIdx.x / u.ctas, u.u1 = u.total * (blockIdx.x + 1) / u.ctas;
+    if (u.u0 >= excl && u.u0 < excl + sum) {
+        long long at = excl;
+        for (int b = bl; b < bh; ++b) {
+            const long long w = request_of<A>(p, b).work;
+            if (u.u0 < at + w) {
+                sh.start_b = b;
+                sh.start_off = u.u0 - at;
+                break;
+            }
+            at += w;
+        }
+    }
+    __syncthreads();
+    u.b = sh.start_b;
+    u.off = sh.start_off;
+    return u;
+}
+
+// The end of a segment's share: the warps' outputs, each in its own ring [row][D], their maxima and sums in sh, are joined; a whole
+// segment's rows are written, and of a segment cut by a run's end the last CTA to arrive joins the parts, in the CTAs' order.
+// pos, take: the share's first unit and its units; seg_u: the segment's place among all.
+template <class A>
+__device__ __forceinline__ void finish_segment(const Kv4AttnParams& p, uint8_t* smem, typename A::Shared& sh, const Request& r, int head, int row0,
+                                               int pos, int take, long long seg_u, const Units& un)
+{
+    constexpr int ROWS = A::ROWS, D = A::DIM;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __syncthreads();
+    const int live = r.rows - row0 < ROWS ? r.rows - row0 : ROWS;
+    const bool whole = pos == 0 && take == r.units;
+    // joined maximum, sum and the warps' weights of each row
+    float* const part = p.partials + (long long)(2 * blockIdx.x + (pos == 0 ? 1 : 0)) * A::PART;
+    if (tid < live) {
+        float mm = -CUDART_INF_F, ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) mm = fmaxf(mm, sh.m[w][tid]);
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            const float f = sh.m[w][tid] == mm ? 1.0f : ex2(sh.m[w][tid] - mm);
+            ll += sh.l[w][tid] * f;
+            sh.weight[w][tid] = f;
+        }
+        if (whole) {
+            const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) sh.weight[w][tid] *= inv;
+            if (p.lse) {
+                const int rr = row0 + tid, qi = rr / p.group;
+                p.lse[(long long)(r.q0 + qi) * p.q_heads + head * p.group + rr - qi * p.group] =
+                    ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * CUDART_LN2_F;
+            }
+        } else {
+            __stcg(part + ROWS * D + tid, mm);
+            __stcg(part + ROWS * D + ROWS + tid, ll);
+        }
+    }
+    __syncthreads();
+    auto store_row = [&](int row, int d, const float4& x) {
+        const int rr = row0 + row, qi = rr / p.group;
+        uint16_t* dst = (uint16_t*)p.out + (long long)(r.q0 + qi) * p.o_token +
+                        (long long)(head * p.group + rr - qi * p.group) * p.o_head + d;
+        uint2 w;
+        if (p.bf16) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), bb = __floats2bfloat162_rn(x.z, x.w);
+            w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&bb));
+        } else {
+            w = make_uint2(half2_bits(x.x, x.y), half2_bits(x.z, x.w));
+        }
+        *reinterpret_cast<uint2*>(dst) = w;
+    };
+    for (int i = tid; i < live * (D / 4); i += kAttnThreads) {
+        const int row = i / (D / 4), d = i % (D / 4) * 4;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            const float f = sh.weight[w][row];
+            const float4 y = *reinterpret_cast<const float4*>(smem + w * A::RING + (row * D + d) * 4);
+            x.x += f * y.x;
+            x.y += f * y.y;
+            x.z += f * y.z;
+            x.w += f * y.w;
+        }
+        if (whole) store_row(row, d, x);
+        else __stcg(reinterpret_cast<float4*>(part + row * D + d), x);
+    }
+    if (!whole) {
+        // ---- the last CTA of the segment to arrive joins the partial results, in the CTAs' order
+        const long long g0 = seg_u + A::OVERHEAD;   // the place of the segment's first unit
+        const int ca = (int)(((g0 + 1) * un.ctas - 1) / un.total), cb = (int)(((g0 + r.units) * un.ctas - 1) / un.total);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            const int before = atomicAdd(p.counters + ca, 1);
+            sh.last = before == cb - ca;
+            if (sh.last) p.counters[ca] = 0;   // ready for the next launch
+            __threadfence();
+        }
+        __syncthreads();
+        if (sh.last) {
+            // first every partial's weight (all rows and CTAs at once, kept where the rings were), then the sums
+            const int parts = cb - ca + 1;
+            float* const wt = reinterpret_cast<float*>(smem);
+            auto part_of = [&](int k) { return p.partials + (long long)(2 * (ca + k) + (k == 0)) * A::PART; };
+            for (int i = tid; i < parts * live; i += kAttnThreads) wt[i] = __ldcg(part_of(i / live) + ROWS * D + i % live);
+            __syncthreads();
+            if (warp < live) {
+                for (int row = warp; row < live; row += kAttnWarps) {
+                    float mm = -CUDART_INF_F, ll = 0.0f;
+                    for (int k = lane; k < parts; k += 32) mm = fmaxf(mm, wt[k * live + row]);
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+                    for (int k = lane; k < parts; k += 32) {
+                        const float mk = wt[k * live + row], f = mk == mm ? 1.0f : ex2(mk - mm);
+                        wt[k * live + row] = f;
+                        ll += f * __ldcg(part_of(k) + ROWS * D + ROWS + row);
+                    }
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+                    if (lane == 0) {
+                        sh.l[0][row] = ll == 0.0f ? 0.0f : 1.0f / ll;
+                        if (p.lse) {
+                            const int rr = row0 + row, qi = rr / p.group;
+                            p.lse[(long long)(r.q0 + qi) * p.q_heads + head * p.group + rr - qi * p.group] =
+                                ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * CUDART_LN2_F;
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < live * (D / 4); i += kAttnThreads) {
+                const int row = i / (D / 4), d = i % (D / 4) * 4;
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                for (int k = 0; k < parts; ++k) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(part_of(k) + row * D + d));
+                    const float f = wt[k * live + row];
+                    x.x += f * y.x;
+                    x.y += f * y.y;
+                    x.z += f * y.z;
+                    x.w += f * y.w;
+                }
+                const float inv = sh.l[0][row];
+                store_row(row, d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+            }
+        }
+    }
+    // the rings are read: bulk copies may follow the plain accesses
+    fence_proxy_async_smem();
+    __syncthreads();
+}
+
+}  // namespace w4a16

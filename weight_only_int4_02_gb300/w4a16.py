@@ -24,7 +24,9 @@ EXPORTS = ["w4a16_layout_version", "w4a16_status_string", "w4a16_last_cuda_error
            "w4a16_w8_gemm", "w4a16_bf16_gemm", "w4a16_sp_packed_bytes", "w4a16_sp_pack", "w4a16_sp_gemm",
            "w4a16_selftest_wait_timeout", "w4a16_force_path", "w4a16_set_wait_limit_ns", "w4a16_gemm_strided",
            "w4a16_kv4_page_bytes", "w4a16_kv4_tables", "w4a16_kv4_append", "w4a16_kv4_read",
-           "w4a16_kv4_workspace_bytes", "w4a16_kv4_attention", "w4a16_kv4_force_path", "w4a16_sample"]
+           "w4a16_kv4_workspace_bytes", "w4a16_kv4_attention", "w4a16_kv4_force_path", "w4a16_rope_table",
+           "w4a16_qk_norm_rope", "w4a16_kv8_page_bytes", "w4a16_kv8_append", "w4a16_kv8_read", "w4a16_kv8_workspace_bytes",
+           "w4a16_kv8_attention", "w4a16_kv8_force_path", "w4a16_sample"]
 
 ACTIVATIONS = {"none": 0, "silu": 1, "relu": 2}
 
@@ -114,6 +116,22 @@ def lib():
         L.w4a16_kv4_attention.restype = I
         L.w4a16_kv4_force_path.argtypes = [I]
         L.w4a16_kv4_force_path.restype = I
+        L.w4a16_rope_table.argtypes = [P, I, I, ctypes.c_double, P]
+        L.w4a16_rope_table.restype = I
+        L.w4a16_qk_norm_rope.argtypes = [P, L64, L64, P, L64, L64, P, L64, L64, P, L64, L64, P, P, F, P, P, I, I, I, I, I, I, I, I, P]
+        L.w4a16_qk_norm_rope.restype = I
+        L.w4a16_kv8_page_bytes.argtypes = [I, I, I]
+        L.w4a16_kv8_page_bytes.restype = Z
+        L.w4a16_kv8_append.argtypes = [P, L64, L64, P, L64, L64, P, P, P, I, I, I, P, I, I, I, I, I, I, P]
+        L.w4a16_kv8_append.restype = I
+        L.w4a16_kv8_read.argtypes = [P, I, P, P, P, I, I, I, I, I, P]
+        L.w4a16_kv8_read.restype = I
+        L.w4a16_kv8_workspace_bytes.argtypes = []
+        L.w4a16_kv8_workspace_bytes.restype = Z
+        L.w4a16_kv8_attention.argtypes = L.w4a16_kv4_attention.argtypes
+        L.w4a16_kv8_attention.restype = I
+        L.w4a16_kv8_force_path.argtypes = [I]
+        L.w4a16_kv8_force_path.restype = I
         L.w4a16_sample.argtypes = [P, L64, P, P, P, P, P, P, P, I, I, I, P]
         L.w4a16_sample.restype = I
         _lib = L
@@ -572,6 +590,79 @@ def kv4_force_path(path):
     prev = lib().w4a16_kv4_force_path(int(path))
     if prev < 0:
         raise W4A16Error(ERR_INVALID_ARG, "w4a16_kv4_force_path(%r)" % (path,))
+    return prev
+
+
+def rope_table(rows, rot, base=10000.0, device="cuda", stream=None):
+    """The rotation's table, float32 [rows][rot]: of each position rot / 2 cosines of position * base^(-2i / rot), then the
+    sines, computed in 64 bits (w4a16_rope_table). Scaled or learned angles make a table of the same layout."""
+    if rows <= 0 or rot <= 0:
+        raise W4A16Error(ERR_INVALID_ARG, "no rotation table of %d positions of %d values" % (rows, rot))
+    device = torch.device(device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        table = torch.empty((rows, rot), dtype=torch.float32, device=device)
+        _check(lib().w4a16_rope_table(_ptr(table), rows, rot, base, _stream(stream)), "w4a16_rope_table")
+    return table
+
+
+def qk_norm_rope(q, k, positions=None, rope=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+                 k_out=None, stream=None):
+    """Norms of queries and keys for each head and the rotation by their positions, in one pass (w4a16_qk_norm_rope).
+
+    q, k: float16 or bfloat16 [tokens][heads][head_dim] of one type, last dimension contiguous, either of them or None;
+    positions: int32 [tokens] and rope: float32 [positions][rot] (rope_table), or both None for no rotation; q_weight,
+    k_weight: [head_dim] of the inputs' type, None for no norm; interleaved: pairs are neighbours, not halves; q_out,
+    k_out: q and k themselves (in place), other memory, or None for new tensors. Rows at negative positions (padding) are not
+    written, those at positions past the table become NaN. Returns (q_out, k_out)."""
+    return (_module or _torch_module()).qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, interleaved, q_out, k_out,
+                                                     None if stream is None else stream.cuda_stream)
+
+
+def kv8_page_bytes(kv_heads, head_dim, page_size):
+    return lib().w4a16_kv8_page_bytes(kv_heads, head_dim, page_size)
+
+
+def kv8_cache(pages, kv_heads, head_dim, page_size, device="cuda"):
+    """An empty 8-bit key-value cache: uint8 [pages][kv_heads][page_size / 16][32 * head_dim + 16]."""
+    if pages < 0 or kv8_page_bytes(kv_heads, head_dim, page_size) == 0:
+        raise W4A16Error(ERR_INVALID_ARG, "no 8-bit cache of %d KV heads of %d in pages of %d" % (kv_heads, head_dim, page_size))
+    return torch.zeros((pages, kv_heads, page_size // 16, 32 * head_dim + 16), dtype=torch.uint8, device=device)
+
+
+def kv8_append(k, v, slots, cache, page_size, positions=None, rope=None, interleaved=False, stream=None):
+    """Quantise k, rotated by positions (int32 [tokens]) with rope (rope_table) unless both are None, and v into their slots
+    of the 8-bit cache (w4a16_kv8_append). k, v, slots: as kv4_append; one scale for 16 tokens, so a tile's tokens are to come
+    in their order, as a request's do."""
+    (_module or _torch_module()).kv8_append(k, v, slots, cache, page_size, positions, rope, interleaved,
+                                            None if stream is None else stream.cuda_stream)
+
+
+def kv8_read(cache, slots, page_size, dtype=torch.float16, stream=None):
+    """(k, v) [tokens][kv_heads][head_dim] that the slots of the 8-bit cache stand for, in float16, bfloat16 or float32."""
+    if dtype not in _DTYPES:
+        raise W4A16Error(ERR_INVALID_ARG, "kv8_read gives float16, bfloat16 or float32")
+    return (_module or _torch_module()).kv8_read(cache, slots, page_size, _DTYPES[dtype],
+                                                 None if stream is None else stream.cuda_stream)
+
+
+def kv8_workspace_bytes():
+    return lib().w4a16_kv8_workspace_bytes()
+
+
+def kv8_attention(q, cache, block_table, seq_lens, starts, page_size, max_q, scale=None, window=0, out=None,
+                  return_lse=False, workspace=None, stream=None):
+    """Causal attention of new query tokens over the 8-bit cache (w4a16_kv8_attention); arguments and results as
+    kv4_attention, a workspace of kv8_workspace_bytes()."""
+    return (_module or _torch_module()).kv8_attention(q, cache, block_table, seq_lens, starts, page_size, max_q, scale, window,
+                                                      out, return_lse, workspace,
+                                                      None if stream is None else stream.cuda_stream)
+
+
+def kv8_force_path(path):
+    """Force kv8_attention's kernel, as kv4_force_path. Returns the previous setting."""
+    prev = lib().w4a16_kv8_force_path(int(path))
+    if prev < 0:
+        raise W4A16Error(ERR_INVALID_ARG, "w4a16_kv8_force_path(%r)" % (path,))
     return prev
 
 
