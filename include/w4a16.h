@@ -602,7 +602,7 @@ size_t w4a16_kv8_page_bytes(int kv_heads, int head_dim, int page_size);
 /*
  * Quantises new keys, rotated on the way, and values into their slots. Tokens that are neighbours in the list and
  * whose slots are neighbours in one tile (s, s + 1, ...) are a run and are stored together, K and V alike, in FP32
- * with IEEE operations: with a = max |x| / 127 over the run's rows of a head (0 below 2^-40, at most 2^40) and old the tile's
+ * with IEEE operations: with a = max |x| * (1 / 127) over the run's rows of a head (0 below 2^-40, at most 2^40) and old the tile's
  * scale, or 0 if the run begins at the tile's first token,
  *   s = max(old, a), r = 1 / s, code = clamp(rint(x * r), -127, 127) + 128      (s = 0: 128)
  * and where s > old the codes of the tile's tokens before the run become clamp(rint((code - 128) * (old * r)), -127, 127) + 128.

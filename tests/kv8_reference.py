@@ -58,7 +58,7 @@ def encode(kc, vc, ks, vs, unused=None):
 def store(code, old, rows, off):
     """One head's codes uint8 [16][D] and scale of a tile after a run's rows (float32 [count][D]) at off: (codes, scale)."""
     top = np.abs(rows).max() if np.isfinite(rows).all() else F(np.nan)
-    a = F(top) / F(127)
+    a = F(top) * (F(1) / F(127))
     if a < F(2.0 ** -40):
         a = F(0)
     a = a if np.isnan(a) else min(a, F(2.0 ** 40))

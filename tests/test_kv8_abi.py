@@ -141,7 +141,7 @@ def test_the_oracle_stores_to_the_nearest_step():
     code, scale = np.zeros((16, 64), np.uint8), np.float32(7)
     for off in range(16):
         code, scale = ref.store(code, scale, x[off:off + 1], off)
-        assert scale == np.abs(x[:off + 1]).max() / np.float32(127)
+        assert scale == np.abs(x[:off + 1]).max() * (np.float32(1) / np.float32(127))
         value = (code[:off + 1].astype(np.float64) - 128) * float(scale)
         steps = np.abs(value - x[:off + 1]) / float(scale)
         assert (steps[-1] <= 0.5 + 127 * 2.0 ** -23).all() and (steps <= 0.5 * (off + 1) + 0.001).all()

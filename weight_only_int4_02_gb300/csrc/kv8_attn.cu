@@ -40,13 +40,14 @@ __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1
 template <int D_, int NR>
 struct Attn {
     static constexpr int DIM = D_;
+    static constexpr int LEAST = 2;             // units of a warp, where there are too few for all CTAs
     static constexpr bool FOUR = NR == 0;       // four rows, twice in an MMA's eight columns
     static constexpr int G = FOUR ? 1 : NR;     // columns, in eights
     static constexpr int ROWS = FOUR ? 4 : 8 * NR;
     static constexpr int UNIT = 16;             // tokens: a tile
     static constexpr int OVERHEAD = 12;         // what starting and ending a segment costs, in units
-    static constexpr int CTAS = NR <= 1 ? 4 : D_ == 64 ? 3 : 2;   // on an SM, as registers and rings allow
-    static constexpr int STAGES = D_ == 128 ? 3 : 6;   // units in flight per warp
+    static constexpr int CTAS = NR <= 1 ? (D_ == 128 ? 3 : 4) : D_ == 64 ? 3 : 2;   // on an SM, as registers and rings allow
+    static constexpr int STAGES = D_ == 128 ? 4 : 6;   // units in flight per warp
     static constexpr int STAGE = kv8_tile_bytes(D_);
     static constexpr int RING = STAGES * STAGE;
     static constexpr int SLABS = D_ / 64;
@@ -59,7 +60,7 @@ struct Attn {
 };
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(const Kv4AttnParams p)
+__global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(const __grid_constant__ Kv4AttnParams p)
 {
     using A = Attn<D, NR>;
     constexpr int ROWS = A::ROWS, G = A::G, SLABS = A::SLABS, UNIT = A::UNIT, OVERHEAD = A::OVERHEAD;
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
     bool dead = false;
     const int tpp_shift = __ffs(p.page_size) - 5;   // log2(tiles per page)
 
-    Request r = request_of<A>(p, b);
+    Request r = un.r;
     for (long long u = u0; u < u1;) {
         while (off >= r.work) {   // next request with work
             off -= r.work;
@@ -156,7 +157,6 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
         // token's share are its d = 64 s + 16 c + 4 w + 0 .. 3, even ones first
         uint32_t qf[G][SLABS * 4][2];
         float row_a[G][2], row_z[G][2];   // score = row_a * s_k * (MMA from row_z), in powers of two
-        int row_pos[G][2];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const int row = row0 + g * 8 + (FOUR ? n & 3 : n);
@@ -208,18 +208,15 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
                 const float un_i = __shfl_sync(0xffffffffu, unit, (2 * c + i) * 4);
                 row_a[g][i] = un_i > 0.0f ? un_i : FLT_MIN;   // scale 0: all scores nearly equal, masked ones stay -infinity
                 row_z[g][i] = __shfl_sync(0xffffffffu, qsum, (2 * c + i) * 4) * -0x1p-17f;   // 128 * 2^-24
-                const int rr = row0 + g * 8 + (FOUR ? 2 * (c & 1) + i : 2 * c + i);
-                row_pos[g][i] = rr < r.rows ? r.pos0 + rr / p.group : -1;
             }
         }
-        float m[G][2], l[G][2], bad[G][2], o[G][4 * SLABS][4];   // bad: NaN where a row sees a poisoned V, else 0
+        float m[G][2], l[G][2], o[G][4 * SLABS][4];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 m[g][i] = -CUDART_INF_F;
                 l[g][i] = 0.0f;
-                bad[g][i] = 0.0f;
             }
 #pragma unroll
             for (int w = 0; w < 4 * SLABS; ++w)
@@ -269,18 +266,24 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
                 const bool odd = have && sv != sv;   // a poisoned tile of V
                 if (!have || odd) sv = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int key = t0 + n + 8 * j;
-                    const bool there = have && key < r.seq;
+                for (int g = 0; g < G; ++g)
 #pragma unroll
-                    for (int g = 0; g < G; ++g)
+                    for (int i = 0; i < 2; ++i) {
+                        const int row = row0 + g * 8 + (FOUR ? 2 * (c & 1) + i : 2 * c + i);
+                        const int row_pos = row < r.rows ? r.pos0 + row / p.group : -1;
+                        bool sees = false;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const bool see = there && key <= row_pos[g][i] && (p.window <= 0 || key > row_pos[g][i] - p.window);
+                        for (int j = 0; j < 2; ++j) {
+                            const int key = t0 + n + 8 * j;
+                            const bool see = have && key < r.seq && key <= row_pos && (p.window <= 0 || key > row_pos - p.window);
                             if (!see) sc[g][2 * j + i] = -CUDART_INF_F;
-                            else if (odd) bad[g][i] = CUDART_NAN_F;     // shows in the rows that see it alone
+                            sees = sees || see;
                         }
-                }
+                        // a poisoned tile shows in the rows that see some of it alone
+                        if (odd && (__ballot_sync(0xffffffffu, sees) >> c & 0x11111111u))
+#pragma unroll
+                            for (int w = 0; w < 4 * SLABS; ++w) o[g][w][i] = o[g][w][2 + i] = CUDART_NAN_F;
+                    }
             }
             // the references of the running sums move if a score passes its row's by 2^kGrow
             bool grow = false;
@@ -387,10 +390,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    l[g][i] += __shfl_xor_sync(0xffffffffu, l[g][i], d);
-                    bad[g][i] += __shfl_xor_sync(0xffffffffu, bad[g][i], d);
-                }
+                for (int d = 4; d < 32; d <<= 1) l[g][i] += __shfl_xor_sync(0xffffffffu, l[g][i], d);
                 if (n == 0 && (!FOUR || c < 2)) {
                     sh.m[warp][g * 8 + 2 * c + i] = m[g][i];
                     sh.l[warp][g * 8 + 2 * c + i] = l[g][i];
@@ -408,15 +408,15 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
                 for (int i = 0; i < 2; ++i) {
                     if (FOUR && c >= 2) continue;
                     float4 x;   // d = 64 s + 8 n + 2 w .. of the slab's words w and w + 1
-                    x.x = o[g][w][i] * kOut + bad[g][i];
-                    x.y = o[g][w][2 + i] * kOut + bad[g][i];
-                    x.z = o[g][w + 1][i] * kOut + bad[g][i];
-                    x.w = o[g][w + 1][2 + i] * kOut + bad[g][i];
+                    x.x = o[g][w][i] * kOut;
+                    x.y = o[g][w][2 + i] * kOut;
+                    x.z = o[g][w + 1][i] * kOut;
+                    x.w = o[g][w + 1][2 + i] * kOut;
                     *reinterpret_cast<float4*>(mine + (g * 8 + 2 * c + i) * D + (w >> 2) * 64 + n * 8 + 2 * (w & 3)) = x;
                 }
         }
         __syncthreads();
-        finish_segment<A>(p, smem, sh, r, head, row0, pos, take, seg_u, un);
+        finish_segment<A>(p, smem, sh, r, head, row0, pos, take, seg_u);
     }
 }
 

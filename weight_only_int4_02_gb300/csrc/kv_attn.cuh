@@ -89,15 +89,33 @@ struct RunShared {
     float m[kAttnWarps][ROWS], l[kAttnWarps][ROWS];   // each warp's maxima and sums
     float weight[kAttnWarps][ROWS];
     long long scan[kAttnWarps];
-    long long start_off;
-    int start_b, abort_flag, last;
+    long long start_off, total;   // of the run, and all units
+    Request start;
+    int start_b, ctas, abort_flag, last;
 };
 
-// A CTA's run of units: u0 .. u1 of the batch's `total`, from `off` on in request b's. Requests without a CTA of this launch (b past
+// floor(total * n / of) for n up to `of`, at most kWsMaxGrid: 64-bit divisions take a warp a hundred instructions each.
+__device__ __forceinline__ long long share_of(long long total, int n, int of)
+{
+    if (total >> 32) return total * n / of;
+    const uint32_t q = (uint32_t)total / (uint32_t)of, rest = (uint32_t)total - q * (uint32_t)of;
+    return (long long)q * n + rest * (uint32_t)n / (uint32_t)of;
+}
+
+// One more of a segment's parts is there: what was written before by this CTA (behind a barrier) is seen by whoever counts later.
+__device__ __forceinline__ int count_part(int* counter)
+{
+    int before;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    return before;
+}
+
+// A CTA's run of units: u0 .. u1 of all of the batch's, from `off` on in request b's. Requests without a CTA of this launch (b past
 // the batch) have none. Every thread of the CTA calls it; the lengths stay on the device, so every CTA sums them by itself.
 struct Units {
-    long long u0, u1, total, ctas, off;
+    long long u0, u1, off;
     int b;
+    Request r;      // request b
 };
 
 template <class A>
@@ -122,32 +140,38 @@ __device__ __forceinline__ Units units_of(const Kv4AttnParams& p, typename A::Sh
         sh.start_b = p.batch;
     }
     __syncthreads();
-    long long excl = incl - sum;
+    long long excl = incl - sum, total = 0;
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
         if (w < warp) excl += sh.scan[w];
-        u.total += sh.scan[w];
+        total += sh.scan[w];
     }
-    // as many CTAs as give each warp a unit
-    const long long want = (u.total + kAttnWarps - 1) / kAttnWarps;
-    u.ctas = want < gridDim.x ? want : gridDim.x;
-    if (blockIdx.x >= u.ctas) return u;
-    u.u0 = u.total * blockIdx.x / u.ctas, u.u1 = u.total * (blockIdx.x + 1) / u.ctas;
+    // as many CTAs as give each warp LEAST units
+    const long long want = (total + A::LEAST * kAttnWarps - 1) / (A::LEAST * kAttnWarps);
+    const int ctas = (int)(want < gridDim.x ? want : gridDim.x);
+    if ((int)blockIdx.x >= ctas) return u;
+    if (tid == 0) {
+        sh.total = total;
+        sh.ctas = ctas;
+    }
+    u.u0 = share_of(total, blockIdx.x, ctas), u.u1 = share_of(total, blockIdx.x + 1, ctas);
     if (u.u0 >= excl && u.u0 < excl + sum) {
         long long at = excl;
         for (int b = bl; b < bh; ++b) {
-            const long long w = request_of<A>(p, b).work;
-            if (u.u0 < at + w) {
+            const Request r = request_of<A>(p, b);
+            if (u.u0 < at + r.work) {
                 sh.start_b = b;
                 sh.start_off = u.u0 - at;
+                sh.start = r;
                 break;
             }
-            at += w;
+            at += r.work;
         }
     }
     __syncthreads();
     u.b = sh.start_b;
     u.off = sh.start_off;
+    u.r = sh.start;
     return u;
 }
 
@@ -156,7 +180,7 @@ __device__ __forceinline__ Units units_of(const Kv4AttnParams& p, typename A::Sh
 // pos, take: the share's first unit and its units; seg_u: the segment's place among all.
 template <class A>
 __device__ __forceinline__ void finish_segment(const Kv4AttnParams& p, uint8_t* smem, typename A::Shared& sh, const Request& r, int head, int row0,
-                                               int pos, int take, long long seg_u, const Units& un)
+                                               int pos, int take, long long seg_u)
 {
     constexpr int ROWS = A::ROWS, D = A::DIM;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -221,43 +245,54 @@ __device__ __forceinline__ void finish_segment(const Kv4AttnParams& p, uint8_t* 
     if (!whole) {
         // ---- the last CTA of the segment to arrive joins the partial results, in the CTAs' order
         const long long g0 = seg_u + A::OVERHEAD;   // the place of the segment's first unit
-        const int ca = (int)(((g0 + 1) * un.ctas - 1) / un.total), cb = (int)(((g0 + r.units) * un.ctas - 1) / un.total);
-        __threadfence();
+        const long long total = sh.total;
+        const int ctas = sh.ctas;
+        const int ca = (int)(((g0 + 1) * ctas - 1) / total), cb = (int)(((g0 + r.units) * ctas - 1) / total);
         __syncthreads();
         if (tid == 0) {
-            const int before = atomicAdd(p.counters + ca, 1);
-            sh.last = before == cb - ca;
+            sh.last = count_part(p.counters + ca) == cb - ca;
             if (sh.last) p.counters[ca] = 0;   // ready for the next launch
-            __threadfence();
         }
         __syncthreads();
         if (sh.last) {
-            // first every partial's weight (all rows and CTAs at once, kept where the rings were), then the sums
+            // every part's weight, kept where the rings were, then the sums
             const int parts = cb - ca + 1;
             float* const wt = reinterpret_cast<float*>(smem);
-            auto part_of = [&](int k) { return p.partials + (long long)(2 * (ca + k) + (k == 0)) * A::PART; };
-            for (int i = tid; i < parts * live; i += kAttnThreads) wt[i] = __ldcg(part_of(i / live) + ROWS * D + i % live);
-            __syncthreads();
-            if (warp < live) {
-                for (int row = warp; row < live; row += kAttnWarps) {
-                    float mm = -CUDART_INF_F, ll = 0.0f;
-                    for (int k = lane; k < parts; k += 32) mm = fmaxf(mm, wt[k * live + row]);
+            const float* const first = p.partials + (long long)(2 * ca) * A::PART;   // the first CTA's last part, the others' first
+            auto part_of = [&](int k) { return first + (2 * k + (k == 0)) * A::PART; };
+            for (int row = warp; row < live; row += kAttnWarps) {
+                float mm = -CUDART_INF_F, ll = 0.0f;
+                // a lane's first parts stay in registers: their maxima and sums are loaded together
+                constexpr int kMine = 4;
+                float mk[kMine], lk[kMine];
 #pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-                    for (int k = lane; k < parts; k += 32) {
-                        const float mk = wt[k * live + row], f = mk == mm ? 1.0f : ex2(mk - mm);
-                        wt[k * live + row] = f;
-                        ll += f * __ldcg(part_of(k) + ROWS * D + ROWS + row);
-                    }
+                for (int j = 0; j < kMine; ++j) {
+                    const int k = lane + 32 * j;
+                    mk[j] = k < parts ? __ldcg(part_of(k) + ROWS * D + row) : -CUDART_INF_F;
+                    lk[j] = k < parts ? __ldcg(part_of(k) + ROWS * D + ROWS + row) : 0.0f;
+                    mm = fmaxf(mm, mk[j]);
+                }
+                for (int k = lane + 32 * kMine; k < parts; k += 32) mm = fmaxf(mm, __ldcg(part_of(k) + ROWS * D + row));
 #pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
-                    if (lane == 0) {
-                        sh.l[0][row] = ll == 0.0f ? 0.0f : 1.0f / ll;
-                        if (p.lse) {
-                            const int rr = row0 + row, qi = rr / p.group;
-                            p.lse[(long long)(r.q0 + qi) * p.q_heads + head * p.group + rr - qi * p.group] =
-                                ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * CUDART_LN2_F;
-                        }
+                for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+                auto weigh = [&](int k, float m_k, float l_k) {
+                    const float f = m_k == mm ? 1.0f : ex2(m_k - mm);
+                    wt[k * live + row] = f;
+                    ll += f * l_k;
+                };
+#pragma unroll
+                for (int j = 0; j < kMine; ++j)
+                    if (lane + 32 * j < parts) weigh(lane + 32 * j, mk[j], lk[j]);
+                for (int k = lane + 32 * kMine; k < parts; k += 32)
+                    weigh(k, __ldcg(part_of(k) + ROWS * D + row), __ldcg(part_of(k) + ROWS * D + ROWS + row));
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+                if (lane == 0) {
+                    sh.l[0][row] = ll == 0.0f ? 0.0f : 1.0f / ll;
+                    if (p.lse) {
+                        const int rr = row0 + row, qi = rr / p.group;
+                        p.lse[(long long)(r.q0 + qi) * p.q_heads + head * p.group + rr - qi * p.group] =
+                            ll == 0.0f ? -CUDART_INF_F : (mm + log2f(ll)) * CUDART_LN2_F;
                     }
                 }
             }

@@ -11,92 +11,158 @@ namespace w4a16 {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRowsAhead = 4;   // rows of a lane group in flight
+constexpr int kRowsAhead = 4;   // rows of a lane group that are loaded together
+constexpr int kMostPasses = 4;
 
-// y = x / sqrt(mean(x^2) + eps) * weight, then the rotation, rounded once; sums and factors are FP32.
-// Bound by bandwidth: a row is read once and written once. A warp has one token and 32 / (D / 8) * kRowsAhead of its heads, so that
-// the token's angles and the weights are loaded once for them.
+// Four neighbours as two pairs.
+struct Four {
+    uint64_t a, b;
+};
+
+template <int DTYPE>
+__device__ __forceinline__ Four four_of(const uint2& w)
+{
+    float x[4];
+    unpack2<DTYPE>(w.x, x[0], x[1]);
+    unpack2<DTYPE>(w.y, x[2], x[3]);
+    return {pack_f32x2(x[0], x[1]), pack_f32x2(x[2], x[3])};
+}
+
+__device__ __forceinline__ Four four_of(const float4& v) { return {pack_f32x2(v.x, v.y), pack_f32x2(v.z, v.w)}; }
+__device__ __forceinline__ Four operator*(const Four& x, const Four& y) { return {mul_f32x2(x.a, y.a), mul_f32x2(x.b, y.b)}; }
+__device__ __forceinline__ Four operator*(const Four& x, uint64_t f) { return {mul_f32x2(x.a, f), mul_f32x2(x.b, f)}; }
+__device__ __forceinline__ Four fma4(const Four& x, const Four& y, const Four& z) { return {fma_f32x2(x.a, y.a, z.a), fma_f32x2(x.b, y.b, z.b)}; }
+
+template <int DTYPE>
+__device__ __forceinline__ uint2 packed(const Four& x)
+{
+    float v[4];
+    unpack_f32x2(x.a, v[0], v[1]);
+    unpack_f32x2(x.b, v[2], v[3]);
+    return make_uint2(pack2<DTYPE>(v[0], v[1]), pack2<DTYPE>(v[2], v[3]));
+}
+
+// Neighbours in each pair swapped.
+__device__ __forceinline__ uint64_t swapped(uint64_t v)
+{
+    float a, b;
+    unpack_f32x2(v, a, b);
+    return pack_f32x2(b, a);
+}
+
+// y = x / sqrt(mean(x^2) + eps) * weight, then the rotation, rounded once; sums and factors are FP32. With the weights w and the
+// angles of a token fixed, a row's outputs are r (x A + x' B), x' the partners and r = 1 / sqrt(mean(x^2) + eps), with A = w cos
+// and B = -+ w' sin. A warp has one token and some of its query or key heads, so that A and B are made once for them,
+// takes them in passes of which the next one's rows are on their way, and works on pairs of numbers. Bound by bandwidth: a row
+// is read once and written once.
 template <int D, int DTYPE, int MODE>
 __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopeParams p)
 {
     chained_kernel();
     constexpr int kLanes = D / 8, kTogether = 32 / kLanes;
     const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);   // below 2^31 + 8: checked on the host
-    const int token = (int)(item / (uint32_t)p.groups), group = (int)(item - (uint32_t)token * (uint32_t)p.groups);
+    const int all = p.groups[0] + p.groups[1];
+    const int token = (int)(item / (uint32_t)all), group = (int)(item - (uint32_t)token * (uint32_t)all);
     if (token >= p.tokens) return;
+    const int which = group >= p.groups[0];
     const int lane = threadIdx.x & 31, j = lane % kLanes;
     const LaneDims at = lane_dims<MODE>(j, p.rope.rot);
-    const int first = group * kTogether * kRowsAhead + lane / kLanes, all = p.heads[0] + p.heads[1];
-
+    const int heads = which ? p.heads[1] : p.heads[0];
+    constexpr int kPass = kTogether * kRowsAhead;   // heads of a pass
+    int h = (which ? group - p.groups[0] : group) * kPass * p.passes + lane / kLanes;
+    const int end = min(heads, h - lane / kLanes + kPass * p.passes);
+    // plain loads: the outputs may be the inputs
+    const long long step = (which ? p.head[1] : p.head[0]) * kTogether;
+    const uint16_t* x = (const uint16_t*)(which ? p.x[1] : p.x[0]) + token * (which ? p.token[1] : p.token[0]) +
+                        h * (which ? p.head[1] : p.head[0]);
     uint2 raw[kRowsAhead][2];
+    auto load = [&](int from) {
 #pragma unroll
-    for (int i = 0; i < kRowsAhead; ++i) {
-        const int h = first + i * kTogether;
-        raw[i][0] = raw[i][1] = make_uint2(0, 0);
-        if (h < all) {
-            const int which = h >= p.heads[0], hh = which ? h - p.heads[0] : h;
-            // plain loads: the outputs may be the inputs
-            const uint16_t* const x = (const uint16_t*)p.x[which] + token * p.token[which] + hh * p.head[which];
-            raw[i][0] = *reinterpret_cast<const uint2*>(x + at.a);
-            raw[i][1] = *reinterpret_cast<const uint2*>(x + at.b);
+        for (int i = 0; i < kRowsAhead; ++i) {
+            raw[i][0] = raw[i][1] = make_uint2(0, 0);
+            if (from + i * kTogether < end) {
+                raw[i][0] = *reinterpret_cast<const uint2*>(x + at.a);
+                raw[i][1] = *reinterpret_cast<const uint2*>(x + at.b);
+            }
+            x += step;
         }
+    };
+    load(h);
+    const uint16_t* const weight = (const uint16_t*)(which ? p.weight[1] : p.weight[0]);
+    const uint64_t one = pack_f32x2(1.0f, 1.0f);
+    Four w[2] = {{one, one}, {one, one}};
+    if (weight) {
+        w[0] = four_of<DTYPE>(__ldg(reinterpret_cast<const uint2*>(weight + at.a)));
+        w[1] = four_of<DTYPE>(__ldg(reinterpret_cast<const uint2*>(weight + at.b)));
     }
-    uint2 w[2][2];
-#pragma unroll
-    for (int o = 0; o < 2; ++o) {
-        const uint16_t* const weight = (const uint16_t*)p.weight[o];
-        w[o][0] = weight ? __ldg(reinterpret_cast<const uint2*>(weight + at.a)) : make_uint2(0, 0);
-        w[o][1] = weight ? __ldg(reinterpret_cast<const uint2*>(weight + at.b)) : make_uint2(0, 0);
-    }
-    float4 cos4 = make_float4(1, 1, 1, 1), sin4 = make_float4(0, 0, 0, 0);
-    bool past = false;
+    Four A[2] = {w[0], w[1]}, B[2] = {{0, 0}, {0, 0}};
     if constexpr (MODE != kRopeNone) {
         const int pos = p.rope.positions[token];
         if (pos < 0) return;   // padding: its rows stay as they were
-        past = pos >= p.rope.rows;
-        if (!past && at.turned) {
+        if (pos >= p.rope.rows) {   // an error that shows
+            const uint64_t nan = pack_f32x2(CUDART_NAN_F, CUDART_NAN_F);
+            A[0] = A[1] = {nan, nan};
+        } else if (at.turned) {
             const float* const row = p.rope.table + (long long)pos * p.rope.rot + 4 * j;
-            cos4 = __ldg(reinterpret_cast<const float4*>(row));
+            const float4 c = __ldg(reinterpret_cast<const float4*>(row));
             // rot / 2 is a multiple of 4, so these are 16-byte aligned too
-            sin4 = __ldg(reinterpret_cast<const float4*>(row + p.rope.rot / 2));
-        }
-    }
+            const float4 s = __ldg(reinterpret_cast<const float4*>(row + p.rope.rot / 2));
+            if constexpr (MODE == kRopeHalves) {
+                const Four cos4 = four_of(c), sin4 = four_of(s);
+                A[0] = w[0] * cos4;
+                A[1] = w[1] * cos4;
+                B[0] = w[1] * sin4 * pack_f32x2(-1.0f, -1.0f);
+                B[1] = w[0] * sin4;
+            } else {
+                const Four cos4[2] = {{pack_f32x2(c.x, c.x), pack_f32x2(c.y, c.y)}, {pack_f32x2(c.z, c.z), pack_f32x2(c.w, c.w)}};
+                const Four sin4[2] = {{pack_f32x2(-s.x, s.x), pack_f32x2(-s.y, s.y)}, {pack_f32x2(-s.z, s.z), pack_f32x2(-s.w, s.w)}};
 #pragma unroll
-    for (int i = 0; i < kRowsAhead; ++i) {
-        const int h = first + i * kTogether;
-        const int which = h >= p.heads[0], hh = which ? h - p.heads[0] : h;
-        float x[8];
-        unpack2<DTYPE>(raw[i][0].x, x[0], x[1]);
-        unpack2<DTYPE>(raw[i][0].y, x[2], x[3]);
-        unpack2<DTYPE>(raw[i][1].x, x[4], x[5]);
-        unpack2<DTYPE>(raw[i][1].y, x[6], x[7]);
-        float sum = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-#pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (p.weight[which]) {
-            const float r = rsqrtf(sum * (1.0f / D) + p.eps);
-            const uint2 lo = which ? w[1][0] : w[0][0], hi = which ? w[1][1] : w[0][1];
-            const uint32_t words[4] = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float u, v;
-                unpack2<DTYPE>(words[e], u, v);
-                x[2 * e] *= r * u;
-                x[2 * e + 1] *= r * v;
+                for (int o = 0; o < 2; ++o) {
+                    A[o] = w[o] * cos4[o];
+                    B[o] = Four{swapped(w[o].a), swapped(w[o].b)} * sin4[o];
+                }
             }
         }
-        if (MODE != kRopeNone && at.turned) rotate<MODE == kRopeNone ? kRopeHalves : MODE>(x, cos4, sin4);
-        if (past) {   // a position that the table does not have: an error that shows
+    }
+    const long long out_step = (which ? p.out_head[1] : p.out_head[0]) * kTogether;
+    uint16_t* y = (uint16_t*)(which ? p.out[1] : p.out[0]) + token * (which ? p.out_token[1] : p.out_token[0]) +
+                  h * (which ? p.out_head[1] : p.out_head[0]);
+#pragma unroll 1
+    for (;;) {
+        uint2 now[kRowsAhead][2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = CUDART_NAN_F;
+        for (int i = 0; i < kRowsAhead; ++i) {
+            now[i][0] = raw[i][0];
+            now[i][1] = raw[i][1];
         }
-        if (h < all) {
-            uint16_t* const y = (uint16_t*)p.out[which] + token * p.out_token[which] + hh * p.out_head[which];
-            *reinterpret_cast<uint2*>(y + at.a) = make_uint2(pack2<DTYPE>(x[0], x[1]), pack2<DTYPE>(x[2], x[3]));
-            *reinterpret_cast<uint2*>(y + at.b) = make_uint2(pack2<DTYPE>(x[4], x[5]), pack2<DTYPE>(x[6], x[7]));
+        const bool more = h - lane / kLanes + kPass < end;   // the same for the whole warp
+        if (more) load(h + kPass);
+#pragma unroll
+        for (int i = 0; i < kRowsAhead; ++i) {
+            const Four u = four_of<DTYPE>(now[i][0]), v = four_of<DTYPE>(now[i][1]);
+            uint64_t r2 = one;
+            if (weight) {
+                float s0, s1;
+                unpack_f32x2(fma_f32x2(v.b, v.b, fma_f32x2(v.a, v.a, fma_f32x2(u.b, u.b, mul_f32x2(u.a, u.a)))), s0, s1);
+                float sum = s0 + s1;
+#pragma unroll
+                for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                const float r = rsqrtf(sum * (1.0f / D) + p.eps);
+                r2 = pack_f32x2(r, r);
+            }
+            Four lo = u * A[0], hi = v * A[1];
+            if (MODE != kRopeNone && at.turned) {   // what is not turned has no partner, whose infinity times 0 would show
+                lo = fma4(MODE == kRopeHalves ? v : Four{swapped(u.a), swapped(u.b)}, B[0], lo);
+                hi = fma4(MODE == kRopeHalves ? u : Four{swapped(v.a), swapped(v.b)}, B[1], hi);
+            }
+            if (h + i * kTogether < end) {
+                *reinterpret_cast<uint2*>(y + at.a) = packed<DTYPE>(lo * r2);
+                *reinterpret_cast<uint2*>(y + at.b) = packed<DTYPE>(hi * r2);
+            }
+            y += out_step;
         }
+        if (!more) break;
+        h += kPass;
     }
 }
 
@@ -125,13 +191,20 @@ auto* kernel_of(int mode)
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const NormRopeParams& in, cudaStream_t stream)
+cudaError_t launch_norm_rope(const NormRopeParams& in, int sms, cudaStream_t stream)
 {
     NormRopeParams p = in;
-    const long long rows = 32 / (p.head_dim / 8) * kRowsAhead, heads = (long long)p.heads[0] + p.heads[1];
-    const long long groups = (heads + rows - 1) / rows;
+    // More passes a warp where that leaves enough warps, four times what an SM holds: A and B cost as much as a pass (8191 tokens
+    // of 64 and 8 heads of 128: one pass 68.9 us, two 57.4, four 55.3, eight 55.3).
+    const long long pass = 32 / (p.head_dim / 8) * kRowsAhead;
+    auto groups_of = [&](int i) { return (p.heads[i] + pass * p.passes - 1) / (pass * p.passes); };
+    long long groups = 0;
+    for (p.passes = kMostPasses; ; p.passes /= 2) {
+        groups = groups_of(0) + groups_of(1);
+        if (p.passes == 1 || groups * p.tokens >= 96LL * sms) break;
+    }
+    for (int i = 0; i < 2; ++i) p.groups[i] = (int)groups_of(i);
     if (groups * p.tokens >= 1LL << 31) return cudaErrorInvalidValue;
-    p.groups = (int)groups;
     const unsigned blocks = (unsigned)((groups * p.tokens + kWarps - 1) / kWarps);
     const bool bf = p.dtype == W4A16_BF16;
     auto* const kernel = p.head_dim == 128 ? (bf ? kernel_of<128, W4A16_BF16>(p.mode) : kernel_of<128, W4A16_FP16>(p.mode))

@@ -56,9 +56,9 @@ struct NormRopeParams {
     Rope rope;
     float eps;
     int tokens, heads[2], head_dim, dtype, mode;
-    int groups;                  // warps that a token's rows take (set by the launch)
+    int groups[2], passes;       // warps that a token's queries and keys take, and their passes (set by the launch)
 };
-cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_rope_table(float* out, int rows, int rot, double base, cudaStream_t stream);
 
 }  // namespace w4a16
