@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kWarps = kAttnWarps, kThreads = kAttnThreads, kGrow = kAttnGrow;
 constexpr uint32_t kEven = 0x00ff00ffu;          // bytes 0 and 2 of a word
-constexpr uint32_t kMiddle = 0x00800080u;        // two codes of 128
+constexpr uint32_t kMiddle = 0x80808080u;        // -128 * 2^-24, twice
 
 __device__ __forceinline__ uint32_t odd_bytes(uint32_t w) { return __byte_perm(w, 0, 0x4341); }   // bytes 1 and 3
 
@@ -40,15 +40,18 @@ __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1
 template <int D_, int NR>
 struct Attn {
     static constexpr int DIM = D_;
-    static constexpr int LEAST = 2;             // units of a warp, where there are too few for all CTAs
+    static constexpr int JOIN = D_ == 128 ? 16 : 8;   // parts whose outputs a join loads together
+    static constexpr int LEAST = 1;             // units of a warp, where there are too few for all CTAs
     static constexpr bool FOUR = NR == 0;       // four rows, twice in an MMA's eight columns
     static constexpr int G = FOUR ? 1 : NR;     // columns, in eights
     static constexpr int ROWS = FOUR ? 4 : 8 * NR;
-    static constexpr int UNIT = 16;             // tokens: a tile
+    static constexpr int TILES = 2;             // of a unit
+    static constexpr int UNIT = 16 * TILES;     // tokens
     static constexpr int OVERHEAD = 12;         // what starting and ending a segment costs, in units
-    static constexpr int CTAS = NR <= 1 ? (D_ == 128 ? 3 : 4) : D_ == 64 ? 3 : 2;   // on an SM, as registers and rings allow
-    static constexpr int STAGES = D_ == 128 ? 4 : 6;   // units in flight per warp
-    static constexpr int STAGE = kv8_tile_bytes(D_);
+    static constexpr int CTAS = D_ == 128 ? (NR <= 1 ? 3 : 2) : NR <= 1 ? 4 : 3;   // on an SM, as registers and rings allow
+    static constexpr int STAGES = 2;            // units in a warp's ring
+    static constexpr int TB = kv8_tile_bytes(D_);
+    static constexpr int STAGE = TILES * TB;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int SLABS = D_ / 64;
     static constexpr int PART = ROWS * (D_ + 2); // floats of one partial: O, then m and l
@@ -63,7 +66,7 @@ template <int D, int NR>
 __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(const __grid_constant__ Kv4AttnParams p)
 {
     using A = Attn<D, NR>;
-    constexpr int ROWS = A::ROWS, G = A::G, SLABS = A::SLABS, UNIT = A::UNIT, OVERHEAD = A::OVERHEAD;
+    constexpr int ROWS = A::ROWS, G = A::G, SLABS = A::SLABS, TILES = A::TILES, UNIT = A::UNIT, OVERHEAD = A::OVERHEAD;
     constexpr bool FOUR = A::FOUR;
     extern __shared__ __align__(128) uint8_t smem[];
     typename A::Shared& sh = *reinterpret_cast<typename A::Shared*>(smem + kWarps * A::RING);
@@ -82,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
     const long long u0 = un.u0, u1 = un.u1;
 
     const WaitCtl ctl{&sh.abort_flag, p.status, p.wait_limit_ns};
-    // the ring: stage and phase of the next unit to issue and to use; a bit a stage: its tile is stored
+    // the ring: stage and phase of the next unit to issue and to use; TILES bits a stage: its tiles are stored
     int s_issue = 0, s_use = 0;
     uint32_t phase = 0, pending = 0, ok_bits = 0;
     bool dead = false;
@@ -114,31 +117,34 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
         const int low = p.window > 0 && low_at > r.base ? (low_at - r.base) / UNIT : 0;
         const int first = low > pos ? low : pos, last = seen < pos + take ? seen : pos + take;
 
-        // ---- copies: a batch of 32 units at a time, lane j owns its unit j
+        // ---- copies: a batch of 32 tiles at a time, a lane each
+        constexpr int BATCH = 32 / TILES;   // units
         const int32_t* const trow = p.table + (long long)b * p.table_stride;
         const int mine_n = last > first + warp ? (last - first - warp + kWarps - 1) / kWarps : 0;   // units of this warp: first + warp, + kWarps, ...
-        const int tile0 = (r.base >> 4) + first + warp;
-        auto page_of = [&](int k) {   // page of this lane's unit of the batch from unit k on, or -1
-            const int tile = tile0 + (k + lane) * kWarps;
-            return (k + lane < mine_n && tile * UNIT < r.seq) ? trow[tile >> tpp_shift] : -1;
+        const int tile0 = (r.base >> 4) + (first + warp + lane / TILES * kWarps) * TILES + lane % TILES;   // this lane's of the first batch
+        auto page_of = [&](int k) {   // page of this lane's tile of the batch from unit k on, or -1
+            const int tile = tile0 + k * kWarps * TILES;
+            return (k + lane / TILES < mine_n && tile * kKv4Tile < r.seq) ? trow[tile >> tpp_shift] : -1;
         };
         int k_issue = 0, page = page_of(0);
         uint32_t present = 0;
         const uint8_t* src = nullptr;
         auto issue_next = [&]() {
             if (k_issue >= mine_n || dead) return;
-            const int j = k_issue & 31;
+            const int j = k_issue % BATCH;
             if (j == 0) {
-                const int in_page = (tile0 + (k_issue + lane) * kWarps) & ((1 << tpp_shift) - 1);
+                const int in_page = (tile0 + k_issue * kWarps * TILES) & ((1 << tpp_shift) - 1);
                 present = __ballot_sync(0xffffffffu, page >= 0 && page < p.pages);
-                src = p.cache + ((((long long)page * p.kv_heads + head) << tpp_shift) + in_page) * A::STAGE;
-                page = page_of(k_issue + 32);
+                src = p.cache + ((((long long)page * p.kv_heads + head) << tpp_shift) + in_page) * A::TB;
+                page = page_of(k_issue + BATCH);
             }
-            const uint32_t bit = present >> j & 1u;
-            ok_bits = (ok_bits & ~(1u << s_issue)) | bit << s_issue;
+            constexpr uint32_t MASK = (1u << TILES) - 1u;
+            const uint32_t bits = present >> (j * TILES) & MASK;
+            ok_bits = (ok_bits & ~(MASK << (s_issue * TILES))) | bits << (s_issue * TILES);
             const uint32_t bar = smem_addr(&sh.bar[warp][s_issue]);
-            if (lane == 0) mbar_arrive_expect_tx(bar, bit * A::STAGE);
-            if (lane == j && bit) bulk_load(smem_addr(ring + s_issue * A::STAGE), src, A::STAGE, bar);
+            if (lane == 0) mbar_arrive_expect_tx(bar, __popc(bits) * A::TB);
+            if (lane / TILES == j && (bits >> (lane % TILES) & 1u))
+                bulk_load(smem_addr(ring + s_issue * A::STAGE + lane % TILES * A::TB), src, A::TB, bar);
             ++k_issue;
             ++pending;
             s_issue = s_issue + 1 == A::STAGES ? 0 : s_issue + 1;
@@ -230,74 +236,87 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
                 dead = true;
                 break;
             }
-            const uint8_t* const tile = ring + s_use * A::STAGE;
-            const bool have = ok_bits >> s_use & 1u;
+            const uint8_t* const st = ring + s_use * A::STAGE;
+            const uint32_t have = ok_bits >> (s_use * TILES) & ((1u << TILES) - 1u);
             const int t0 = r.base + t * UNIT;
-            const bool full = have && t0 + UNIT - 1 <= pos_min && (p.window <= 0 || t0 > pos_max - p.window);
-            const float2 scales = *reinterpret_cast<const float2*>(tile + kv8_k_scale_off(D));
-            float sv = scales.y;
+            const bool full = have == (1u << TILES) - 1u && t0 + UNIT - 1 <= pos_min && (p.window <= 0 || t0 > pos_max - p.window);
 
-            // s_k times the products: tokens n and n + 8, rows 2c and 2c + 1; two chains of MMAs, one a token's even words
-            float sc[G][4], odd_sc[G][4];
+            // s_k times the products: of each tile tokens n and n + 8, rows 2c and 2c + 1; two chains of MMAs, of even and odd words
+            float sc[TILES][G][4], sv[TILES];
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sc[g][i] = row_z[g][i & 1];
-                    odd_sc[g][i] = 0.0f;
-                }
-#pragma unroll
-            for (int s = 0; s < SLABS; ++s) {
-                const uint4 ka4 = *reinterpret_cast<const uint4*>(tile + s * 1024 + lane * 16);
-                const uint4 kb4 = *reinterpret_cast<const uint4*>(tile + s * 1024 + 512 + lane * 16);
-                const uint32_t ka[4] = {ka4.x, ka4.y, ka4.z, ka4.w}, kb[4] = {kb4.x, kb4.y, kb4.z, kb4.w};
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-#pragma unroll
-                    for (int g = 0; g < G; ++g)
-                        mma_16816(w & 1 ? odd_sc[g] : sc[g], ka[w] & kEven, kb[w] & kEven, odd_bytes(ka[w]), odd_bytes(kb[w]),
-                                  qf[g][4 * s + w][0], qf[g][4 * s + w][1]);
-            }
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sc[g][i] = (sc[g][i] + odd_sc[g][i]) * scales.x;
-            if (!full) {
-                const bool odd = have && sv != sv;   // a poisoned tile of V
-                if (!have || odd) sv = 0.0f;
+            for (int tl = 0; tl < TILES; ++tl) {
+                const uint8_t* const tile = st + tl * A::TB;
+                const float2 scales = *reinterpret_cast<const float2*>(tile + kv8_k_scale_off(D));
+                sv[tl] = scales.y;
+                float odd_sc[G][4];
 #pragma unroll
                 for (int g = 0; g < G; ++g)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int row = row0 + g * 8 + (FOUR ? 2 * (c & 1) + i : 2 * c + i);
-                        const int row_pos = row < r.rows ? r.pos0 + row / p.group : -1;
-                        bool sees = false;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int key = t0 + n + 8 * j;
-                            const bool see = have && key < r.seq && key <= row_pos && (p.window <= 0 || key > row_pos - p.window);
-                            if (!see) sc[g][2 * j + i] = -CUDART_INF_F;
-                            sees = sees || see;
-                        }
-                        // a poisoned tile shows in the rows that see some of it alone
-                        if (odd && (__ballot_sync(0xffffffffu, sees) >> c & 0x11111111u))
-#pragma unroll
-                            for (int w = 0; w < 4 * SLABS; ++w) o[g][w][i] = o[g][w][2 + i] = CUDART_NAN_F;
+                    for (int i = 0; i < 4; ++i) {
+                        sc[tl][g][i] = row_z[g][i & 1];
+                        odd_sc[g][i] = 0.0f;
                     }
+#pragma unroll
+                for (int s = 0; s < SLABS; ++s) {
+                    const uint4 ka4 = *reinterpret_cast<const uint4*>(tile + s * 1024 + lane * 16);
+                    const uint4 kb4 = *reinterpret_cast<const uint4*>(tile + s * 1024 + 512 + lane * 16);
+                    const uint32_t ka[4] = {ka4.x, ka4.y, ka4.z, ka4.w}, kb[4] = {kb4.x, kb4.y, kb4.z, kb4.w};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+                            mma_16816(w & 1 ? odd_sc[g] : sc[tl][g], ka[w] & kEven, kb[w] & kEven, odd_bytes(ka[w]), odd_bytes(kb[w]),
+                                      qf[g][4 * s + w][0], qf[g][4 * s + w][1]);
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[tl][g][i] = (sc[tl][g][i] + odd_sc[g][i]) * scales.x;
             }
+            if (!full) {
+#pragma unroll
+                for (int tl = 0; tl < TILES; ++tl) {
+                    const bool there = have >> tl & 1u, odd = there && sv[tl] != sv[tl];   // a poisoned tile of V
+                    if (!there || odd) sv[tl] = 0.0f;
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int row = row0 + g * 8 + (FOUR ? 2 * (c & 1) + i : 2 * c + i);
+                            const int row_pos = row < r.rows ? r.pos0 + row / p.group : -1;
+                            bool sees = false;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int key = t0 + 16 * tl + n + 8 * j;
+                                const bool see = there && key < r.seq && key <= row_pos && (p.window <= 0 || key > row_pos - p.window);
+                                if (!see) sc[tl][g][2 * j + i] = -CUDART_INF_F;
+                                sees = sees || see;
+                            }
+                            // a poisoned tile shows in the rows that see some of it alone
+                            if (odd && (__ballot_sync(0xffffffffu, sees) >> c & 0x11111111u))
+#pragma unroll
+                                for (int w = 0; w < 4 * SLABS; ++w) o[g][w][i] = o[g][w][2 + i] = CUDART_NAN_F;
+                        }
+                }
+            }
+            auto largest = [&](int g, int i) {
+                float x = fmaxf(sc[0][g][i], sc[0][g][2 + i]);
+                if constexpr (TILES == 2) x = fmaxf(x, fmaxf(sc[1][g][i], sc[1][g][2 + i]));
+                return x;
+            };
             // the references of the running sums move if a score passes its row's by 2^kGrow
             bool grow = false;
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) grow = grow || fmaxf(sc[g][i], sc[g][2 + i]) * row_a[g][i] > m[g][i] + (float)kGrow;
+                for (int i = 0; i < 2; ++i) grow = grow || largest(g, i) * row_a[g][i] > m[g][i] + (float)kGrow;
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     float f[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float x = fmaxf(sc[g][i], sc[g][2 + i]);
+                        float x = largest(g, i);
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * row_a[g][i];
@@ -312,63 +331,61 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
                         for (int i = 0; i < 4; ++i) o[g][w][i] *= f[i & 1];
                 }
             }
-            // probabilities, fed below 2^15, clear of subnormals
-            uint32_t ph[G][2], pl[G][2];
+            float ref[G][2];
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                float ref[2];
+            for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) ref[i] = m[g][i] == -CUDART_INF_F ? 0.0f : m[g][i];
+                for (int i = 0; i < 2; ++i) ref[g][i] = m[g][i] == -CUDART_INF_F ? 0.0f : m[g][i];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float pv[2];
+            for (int tl = 0; tl < TILES; ++tl) {
+                // probabilities, fed below 2^15, clear of subnormals, and -128 times their sum, the same in every row of d
+                uint32_t ph[G][2], pl[G][2];
+                float z[G][4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float e = ex2(fmaf(sc[g][2 * j + i], row_a[g][i], -ref[i]));
-                        l[g][i] += e;
-                        pv[i] = e * (float)(1 << (15 - kGrow));
+                for (int g = 0; g < G; ++g) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float pv[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float e = ex2(fmaf(sc[tl][g][2 * j + i], row_a[g][i], -ref[g][i]));
+                            l[g][i] += e;
+                            pv[i] = e * (float)(1 << (15 - kGrow));
+                        }
+                        const uint32_t h = half2_bits(pv[0], pv[1]);
+                        const float2 back = bits_half2(h);
+                        const uint32_t rest = half2_bits(pv[0] - back.x, pv[1] - back.y);
+                        if constexpr (FOUR) {
+                            ph[g][j] = transpose8(c < 2 ? h : rest);   // the second four columns are the low parts
+                        } else {
+                            ph[g][j] = transpose8(h);
+                            pl[g][j] = transpose8(rest);
+                        }
                     }
-                    const uint32_t h = half2_bits(pv[0], pv[1]);
-                    const float2 back = bits_half2(h);
-                    const uint32_t rest = half2_bits(pv[0] - back.x, pv[1] - back.y);
-                    if constexpr (FOUR) {
-                        ph[g][j] = transpose8(c < 2 ? h : rest);   // the second four columns are the low parts
-                    } else {
-                        ph[g][j] = transpose8(h);
-                        pl[g][j] = transpose8(rest);
-                    }
+                    const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma_from(z[g], kMiddle, kMiddle, kMiddle, kMiddle, ph[g][0], ph[g][1], none);
+                    if constexpr (!FOUR) mma_16816(z[g], kMiddle, kMiddle, kMiddle, kMiddle, pl[g][0], pl[g][1]);
                 }
-            }
-            // -128 sum(p), the same in every row of d
-            float z[G][4];
+                const uint64_t sv2 = pack_f32x2(sv[tl], sv[tl]);
+                const uint8_t* const vt = st + tl * A::TB + kv8_v_off(D) + lane * 16;
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
+                for (int s = 0; s < SLABS; ++s) {
+                    const uint4 va4 = *reinterpret_cast<const uint4*>(vt + s * 1024);
+                    const uint4 vb4 = *reinterpret_cast<const uint4*>(vt + s * 1024 + 512);
+                    const uint32_t va[4] = {va4.x, va4.y, va4.z, va4.w}, vb[4] = {vb4.x, vb4.y, vb4.z, vb4.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[g][i] = 0.0f;
-                mma_16816(z[g], kMiddle, kMiddle, kMiddle, kMiddle, ph[g][0], ph[g][1]);
-                if constexpr (!FOUR) mma_16816(z[g], kMiddle, kMiddle, kMiddle, kMiddle, pl[g][0], pl[g][1]);
+                    for (int w = 0; w < 4; ++w)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[g][i] = -z[g][i];
-            }
-            const uint64_t sv2 = pack_f32x2(sv, sv);
-            const uint8_t* const vt = tile + kv8_v_off(D) + lane * 16;
+                        for (int g = 0; g < G; ++g) {
+                            float d[4];
+                            mma_from(d, va[w] & kEven, odd_bytes(va[w]), vb[w] & kEven, odd_bytes(vb[w]), ph[g][0], ph[g][1], z[g]);
+                            if constexpr (!FOUR) mma_16816(d, va[w] & kEven, odd_bytes(va[w]), vb[w] & kEven, odd_bytes(vb[w]), pl[g][0], pl[g][1]);
+                            float(&to)[4] = o[g][4 * s + w];
 #pragma unroll
-            for (int s = 0; s < SLABS; ++s) {
-                const uint4 va4 = *reinterpret_cast<const uint4*>(vt + s * 1024);
-                const uint4 vb4 = *reinterpret_cast<const uint4*>(vt + s * 1024 + 512);
-                const uint32_t va[4] = {va4.x, va4.y, va4.z, va4.w}, vb[4] = {vb4.x, vb4.y, vb4.z, vb4.w};
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        float d[4];
-                        mma_from(d, va[w] & kEven, odd_bytes(va[w]), vb[w] & kEven, odd_bytes(vb[w]), ph[g][0], ph[g][1], z[g]);
-                        if constexpr (!FOUR) mma_16816(d, va[w] & kEven, odd_bytes(va[w]), vb[w] & kEven, odd_bytes(vb[w]), pl[g][0], pl[g][1]);
-                        float(&to)[4] = o[g][4 * s + w];
-#pragma unroll
-                        for (int i = 0; i < 4; i += 2)
-                            unpack_f32x2(fma_f32x2(pack_f32x2(d[i], d[i + 1]), sv2, pack_f32x2(to[i], to[i + 1])), to[i], to[i + 1]);
-                    }
+                            for (int i = 0; i < 4; i += 2)
+                                unpack_f32x2(fma_f32x2(pack_f32x2(d[i], d[i + 1]), sv2, pack_f32x2(to[i], to[i + 1])), to[i], to[i + 1]);
+                        }
+                }
             }
             next_stage();
             fence_proxy_async_smem();
@@ -460,6 +477,7 @@ size_t kv8_partial_bytes(int sms)
     most(Launch<128, 0>::grid_of(sms), Attn<128, 0>::PART);
     most(Launch<128, 1>::grid_of(sms), Attn<128, 1>::PART);
     most(Launch<128, 2>::grid_of(sms), Attn<128, 2>::PART);
+    most(Launch<128, 3>::grid_of(sms), Attn<128, 3>::PART);
     return need;
 }
 
@@ -468,15 +486,30 @@ cudaError_t setup_kv8()
     cudaError_t e;
     if ((e = Launch<64, 0>::setup()) != cudaSuccess || (e = Launch<128, 0>::setup()) != cudaSuccess ||
         (e = Launch<64, 1>::setup()) != cudaSuccess || (e = Launch<64, 2>::setup()) != cudaSuccess ||
-        (e = Launch<128, 1>::setup()) != cudaSuccess || (e = Launch<128, 2>::setup()) != cudaSuccess)
+        (e = Launch<128, 1>::setup()) != cudaSuccess || (e = Launch<128, 2>::setup()) != cudaSuccess ||
+        (e = Launch<128, 3>::setup()) != cudaSuccess)
         return e;
     return setup_kv8_prompt();
 }
 
-// Which kernel and how many rows a segment has: the 4-bit cache's rules.
+// The tcgen05 kernel takes what the 4-bit cache's does.
 constexpr int kFewRows = 32;
-constexpr int kNarrowRows = 1024;
 constexpr long long prompt_rows(int head_dim) { return head_dim == 128 ? 3200 : 4096; }
+
+// Rows of a segment, in eights (0: four), where requests have up to `held` rows a KV head and the batch has `all`. Of few rows segments
+// of eight are the fastest: latency counts. Otherwise what the segments cost together decides. 64 requests over 4000 tokens of 4
+// KV heads, segments of 8 / 16 / 24 rows, us: D = 128, 16 rows 68 / 65 / 88, 24 rows 126 / 111 / 94, 32 rows 140 / 114 / 161;
+// D = 64, 16 rows 46 / 47, 24 rows 63 / 71, 32 rows 81 / 73 (24 rows gained 5% at 24 and lost elsewhere). Eight requests of 32 rows
+// over 4000 tokens: 27 / 32 / 42 and 19 / 21.
+int segment_rows(long long held, int head_dim, long long all)
+{
+    if (held <= 4) return 0;
+    const long long eights = (held + 7) / 8;
+    if (all <= 1024 || eights == 1) return 1;
+    if (head_dim == 64) return 36 * ((eights + 1) / 2) < 19 * eights ? 2 : 1;
+    const long long cost[3] = {35 * eights, 57 * ((eights + 1) / 2), 78 * ((eights + 2) / 3)};
+    return cost[2] < cost[0] && cost[2] < cost[1] ? 3 : cost[1] < cost[0] ? 2 : 1;
+}
 
 cudaError_t launch_kv8_attention(const Kv4AttnParams& in, int head_dim, int max_q, int path, int sms, cudaStream_t stream)
 {
@@ -490,12 +523,13 @@ cudaError_t launch_kv8_attention(const Kv4AttnParams& in, int head_dim, int max_
     }
     p.few_rows = prompt ? kFewRows : INT_MAX;
     const long long held = prompt && rows > kFewRows ? kFewRows : rows;   // of a request that is this kernel's, at most
-    const bool wide = 4 * ((held + 7) / 8) >= 7 * ((held + 15) / 16) && (long long)p.tokens * p.q_heads > kNarrowRows;
+    const int nr = segment_rows(held, head_dim, (long long)p.tokens * p.q_heads);
     cudaError_t e;
     if (head_dim == 128)
-        e = held <= 4 ? Launch<128, 0>::run(p, sms, stream) : wide ? Launch<128, 2>::run(p, sms, stream) : Launch<128, 1>::run(p, sms, stream);
+        e = nr == 0 ? Launch<128, 0>::run(p, sms, stream) : nr == 1 ? Launch<128, 1>::run(p, sms, stream)
+          : nr == 2 ? Launch<128, 2>::run(p, sms, stream) : Launch<128, 3>::run(p, sms, stream);
     else
-        e = held <= 4 ? Launch<64, 0>::run(p, sms, stream) : wide ? Launch<64, 2>::run(p, sms, stream) : Launch<64, 1>::run(p, sms, stream);
+        e = nr == 0 ? Launch<64, 0>::run(p, sms, stream) : nr == 1 ? Launch<64, 1>::run(p, sms, stream) : Launch<64, 2>::run(p, sms, stream);
     if (e != cudaSuccess || !prompt) return e;
     return launch_kv8_prompt(p, head_dim, sms, stream);
 }

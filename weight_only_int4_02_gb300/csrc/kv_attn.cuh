@@ -300,14 +300,22 @@ __device__ __forceinline__ void finish_segment(const Kv4AttnParams& p, uint8_t* 
             for (int i = tid; i < live * (D / 4); i += kAttnThreads) {
                 const int row = i / (D / 4), d = i % (D / 4) * 4;
                 float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-                for (int k = 0; k < parts; ++k) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4*>(part_of(k) + row * D + d));
-                    const float f = wt[k * live + row];
-                    x.x += f * y.x;
-                    x.y += f * y.y;
-                    x.z += f * y.z;
-                    x.w += f * y.w;
+                const float* const at = first + row * D + d;
+                for (int k0 = 0; k0 < parts; k0 += A::JOIN) {   // JOIN parts' loads together; past the last part they count nothing
+                    float4 y[A::JOIN];
+#pragma unroll
+                    for (int k = 0; k < A::JOIN; ++k) {
+                        const int part = k0 + k < parts ? k0 + k : parts - 1;
+                        y[k] = __ldcg(reinterpret_cast<const float4*>(at + (2 * part + (part == 0)) * A::PART));
+                    }
+#pragma unroll
+                    for (int k = 0; k < A::JOIN; ++k) {
+                        const float f = k0 + k < parts ? wt[(k0 + k) * live + row] : 0.0f;
+                        x.x += f * y[k].x;
+                        x.y += f * y[k].y;
+                        x.z += f * y[k].z;
+                        x.w += f * y[k].w;
+                    }
                 }
                 const float inv = sh.l[0][row];
                 store_row(row, d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
