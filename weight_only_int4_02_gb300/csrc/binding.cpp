@@ -282,13 +282,20 @@ PyObject* norm_rope(PyObject* const* a) {
     int64_t strides[2][4] = {};
     int heads[2] = {0, 0};
     at::Tensor out[2];
+    if (x[0] && x[1] && a[8] == Py_None && a[9] == Py_None) {   // one allocation for both
+        const int64_t q_bytes = 2 * x[0]->numel();
+        at::Tensor all = empty({q_bytes + 2 * x[1]->numel()}, at::kByte, any);
+        out[0] = part(all, 0, x[0]->sizes(), any.scalar_type());
+        out[1] = part(all, q_bytes, x[1]->sizes(), any.scalar_type());
+    }
     for (int i = 0; i < 2; ++i) {
         if (!x[i]) {
             if (a[8 + i] != Py_None || a[4 + i] != Py_None) refuse("a weight or an output without its input");
             continue;
         }
         weight[i] = optional_vector<void>(a[4 + i], any.scalar_type(), dim, weights[i]);
-        if (a[8 + i] == Py_None) {
+        if (out[i].defined()) {
+        } else if (a[8 + i] == Py_None) {
             out[i] = empty(x[i]->sizes(), any.scalar_type(), any);
         } else {
             out[i] = tensor(a[8 + i], outs[i]);

@@ -301,12 +301,12 @@ __global__ void __launch_bounds__(64, 16) kv8_append_kernel(const Kv8RowsParams 
 
 // The values that slots stand for, (code - 128) * scale in FP32, rounded once. D / 8 lanes a token and head, kRead rows of a
 // lane in flight.
-constexpr int kRead = 2;
+constexpr int kRead = 2, kReadThreads = 256;
 template <int D, int DTYPE>
-__global__ void __launch_bounds__(256) kv8_read_kernel(const Kv8RowsParams p)
+__global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const Kv8RowsParams p)
 {
     chained_kernel();
-    constexpr int kLanes = D / 8, kRows = 256 / kLanes;
+    constexpr int kLanes = D / 8, kRows = kReadThreads / kLanes;
     const int j = threadIdx.x % kLanes;
     uint32_t w[kRead][2][2];
     float s[kRead][2];
@@ -395,8 +395,8 @@ cudaError_t launch_kv8_read(const Kv8RowsParams& p, cudaStream_t stream)
     auto* kernel = p.head_dim == 128 ? kv8_read_kernel<128, W4A16_FP32> : kv8_read_kernel<64, W4A16_FP32>;
     if (p.dtype == W4A16_BF16) kernel = p.head_dim == 128 ? kv8_read_kernel<128, W4A16_BF16> : kv8_read_kernel<64, W4A16_BF16>;
     if (p.dtype == W4A16_FP16) kernel = p.head_dim == 128 ? kv8_read_kernel<128, W4A16_FP16> : kv8_read_kernel<64, W4A16_FP16>;
-    const long long per = kRead * 256 / (p.head_dim / 8);
-    return launch_chained(kernel, (unsigned)(((long long)p.tokens * p.kv_heads + per - 1) / per), 256, 0, 1, stream, p);
+    const long long per = kRead * kReadThreads / (p.head_dim / 8);
+    return launch_chained(kernel, (unsigned)(((long long)p.tokens * p.kv_heads + per - 1) / per), kReadThreads, 0, 1, stream, p);
 }
 
 }  // namespace w4a16

@@ -10,7 +10,7 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 2;       // of a CTA: larger ones leave the GPU waiting for their last warps (eight 54.6 us, two 52.0, as below)
 constexpr int kRowsAhead = 4;   // rows of a lane group that are loaded together
 constexpr int kMostPasses = 4;
 
@@ -56,7 +56,7 @@ __device__ __forceinline__ uint64_t swapped(uint64_t v)
 // takes them in passes of which the next one's rows are on their way, and works on pairs of numbers. Bound by bandwidth: a row
 // is read once and written once.
 template <int D, int DTYPE, int MODE>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormRopeParams p)
+__global__ void __launch_bounds__(kWarps * 32, 16) norm_rope_kernel(const NormRopeParams p)
 {
     chained_kernel();
     constexpr int kLanes = D / 8, kTogether = 32 / kLanes;
@@ -195,7 +195,7 @@ cudaError_t launch_norm_rope(const NormRopeParams& in, int sms, cudaStream_t str
 {
     NormRopeParams p = in;
     // More passes a warp where that leaves enough warps, four times what an SM holds: A and B cost as much as a pass (8191 tokens
-    // of 64 and 8 heads of 128: one pass 68.9 us, two 57.4, four 55.3, eight 55.3).
+    // of 64 and 8 heads of 128, in CTAs of eight warps: one pass 68.9 us, two 57.4, four 55.3, eight 55.3).
     const long long pass = 32 / (p.head_dim / 8) * kRowsAhead;
     auto groups_of = [&](int i) { return (p.heads[i] + pass * p.passes - 1) / (pass * p.passes); };
     long long groups = 0;
