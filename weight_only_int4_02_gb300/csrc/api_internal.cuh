@@ -19,7 +19,6 @@ w4a16_status report_cuda(cudaError_t e);
 w4a16_status device_info(DeviceInfo* info);
 // Attributes of the serving step's kernels, set with the matmuls'.
 cudaError_t setup_kv4();
-cudaError_t setup_kv8();
 // The library's own workspace on the current device.
 w4a16_status library_workspace(void** ws, size_t* bytes);
 

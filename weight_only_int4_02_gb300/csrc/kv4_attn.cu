@@ -27,14 +27,14 @@
 // that V takes half the MMAs (one request of 131072 tokens 43.2 -> 42.3 us). Scores, sums, maxima and outputs
 // are FP32.
 //
-// Measured, D = 128: 64 requests of 257 to 16384 cached tokens 71 us, 3.6 TB/s, 53% of a copy's rate; one of
-// 131072 tokens 44 us; D = 64, 48 requests of 1 to 5 drafted tokens and a window of 4096 17.6 us; one of 1000
-// tokens 10.9 us, most of it latency. Four CTAs an SM (128 registers a thread) keep the issue slots busy for 52% of the
+// Measured, D = 128: 64 requests of 257 to 16384 cached tokens 68.5 us, 3.7 TB/s, 55% of a copy's rate; one of
+// 131072 tokens 44 us; D = 64, 48 requests of 1 to 5 drafted tokens and a window of 4096 15.9 us; one of 1000
+// tokens 9.9 us, most of it latency. Four CTAs an SM (128 registers a thread) keep the issue slots busy for 52% of the
 // time and the tensor pipe for 33%: a unit is about 640 warp instructions (the integer pipe is busy
 // for 47%), which wait for one another more than for memory. Eight or two warps a CTA, five CTAs an SM
 // (fewer registers) and tokens' scales through shared memory were slower.
 #include "api_internal.cuh"
-#include "kv4.cuh"
+#include "kv8.cuh"
 #include "kv_attn.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -558,6 +558,7 @@ size_t kv4_partial_bytes(int sms)
     return need;
 }
 
+// The 8-bit cache's too: all of the serving step's.
 cudaError_t setup_kv4()
 {
     cudaError_t e;
@@ -565,7 +566,8 @@ cudaError_t setup_kv4()
         (e = Launch<64, 1>::setup()) != cudaSuccess || (e = Launch<64, 2>::setup()) != cudaSuccess ||
         (e = Launch<128, 1>::setup()) != cudaSuccess || (e = Launch<128, 2>::setup()) != cudaSuccess)
         return e;
-    return setup_kv4_prompt();
+    if ((e = setup_kv4_prompt()) != cudaSuccess) return e;
+    return setup_kv8();
 }
 
 // The tcgen05 kernel takes requests of more than kFewRows rows a KV head where the batch's rows (query

@@ -1,15 +1,22 @@
 // Attention over the 8-bit paged cache for few query rows (a decode step, drafted tokens): O = softmax(scale * Q K^T) V with
 // K, V = (code - 128) * scale, one scale for 16 tokens of a head.
 //
-// Work is dealt and joined as in the 4-bit cache's kernel (segments of up to 8 NR rows, or four, their cached tokens in units,
-// stream-K over the CTAs); a unit here is one tile of 16 tokens. In a CTA, four warps take a run's units in turn, each with its
-// own ring of bulk copies. With c the code and s the scale of a tile:
+// Work is dealt and joined as in the 4-bit cache's kernel (segments of up to 8 NR rows, or four, their cached tokens in units of 32,
+// stream-K over the CTAs). In a CTA, four warps take a run's units in turn, each with its own ring of bulk copies. With c the code
+// and s the scale of a tile:
 //   score = s_k (q . c_k - 128 sum(q)) * scale,   out = sum_tiles s_v sum_t p_t (c_v - 128) / sum_t p_t
 // The MMAs multiply by the bare codes (two binary16 subnormals from a word by one operation, exact), from accumulators that
 // start at the share of the 128s: -128 sum(q) for the scores, -128 sum(p), itself an MMA, for the outputs. V's scale acts on
 // a tile's sums, which go into the running output by an FP32 multiply-add: roundings of the MMAs (towards zero) do
 // not add up over the tiles, and scales of any size keep all of P's bits. P is fed as a high and a low binary16 part, 22 bits. Where four
 // rows are enough they stand twice in the MMA's eight columns, the second time with the low parts.
+//
+// Measured, D = 128: 64 requests of 257 to 16384 cached tokens 97 us, 5.6 TB/s, 83% of a copy's rate; one of 131072 tokens 51 us,
+// 5.2 TB/s; D = 64, 48 requests of 1 to 5 drafted tokens and a window of 4096 19 us; one of 1000 tokens 9.2 us, most of it latency.
+// The bytes bound it while all CTAs are at work; the rest is their ends: SMs finish 15% apart at equal work (of 64 ragged requests
+// after 79 to 108 us, 94 on average), a segment's end takes 2 us, under load 6. Units of one tile took 102, 53.5 and 22 us; four CTAs an SM (128
+// registers, spills) 107, 57 and, D = 64, what they take now. More CTAs than the GPU holds, with shorter runs, took 108 and 69 us;
+// parts counted at the end of a CTA's run instead of at once 100 and 53.
 #include "api_internal.cuh"
 #include "kv8.cuh"
 #include "kv_attn.cuh"
@@ -49,7 +56,7 @@ struct Attn {
     static constexpr int UNIT = 16 * TILES;     // tokens
     static constexpr int OVERHEAD = 12;         // what starting and ending a segment costs, in units
     static constexpr int CTAS = D_ == 128 ? (NR <= 1 ? 3 : 2) : NR <= 1 ? 4 : 3;   // on an SM, as registers and rings allow
-    static constexpr int STAGES = 2;            // units in a warp's ring
+    static constexpr int STAGES = 2;            // units in a warp's ring: one in use and one on its way
     static constexpr int TB = kv8_tile_bytes(D_);
     static constexpr int STAGE = TILES * TB;
     static constexpr int RING = STAGES * STAGE;
@@ -528,7 +535,9 @@ cudaError_t launch_kv8_attention(const Kv4AttnParams& in, int head_dim, int max_
         return launch_kv8_prompt(p, head_dim, sms, stream);
     }
     p.few_rows = prompt ? kFewRows : INT_MAX;
-    const long long held = prompt && rows > kFewRows ? kFewRows : rows;   // of a request that is this kernel's, at most
+    // of a request that is this kernel's, at most; beside prompts it is a single token's more often than not (two prompts of 800
+    // tokens with 30 single tokens over 8000, 8 KV heads, four query heads to each: 182 -> 172 us, D = 64 131 -> 114)
+    const long long held = !prompt ? rows : p.group < 8 ? 8 : p.group < kFewRows ? p.group : kFewRows;
     const int nr = segment_rows(held, head_dim, (long long)p.tokens * p.q_heads);
     cudaError_t e;
     if (head_dim == 128)

@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(64, 16) kv8_append_kernel(const Kv8RowsParams 
 }
 
 // The values that slots stand for, (code - 128) * scale in FP32, rounded once. D / 8 lanes a token and head, kRead rows of a
-// lane in flight.
+// lane in flight; neighbouring lanes' rows are neighbouring tokens, two of which share each 16 bytes of V's codes. Bound by the loads'
+// latency and its instructions: 8191 tokens of eight heads of 128 in 9.6 us (four rows in flight 11.6, one 9.9), 80% of a copy's rate.
 constexpr int kRead = 2, kReadThreads = 256;
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const Kv8RowsParams p)
