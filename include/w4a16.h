@@ -631,7 +631,9 @@ w4a16_status w4a16_kv8_read(const uint8_t* cache, int pages, const int64_t* slot
 size_t w4a16_kv8_workspace_bytes(void);
 
 /* Causal attention of new query tokens over the 8-bit cache: arguments, masks and results as
- * w4a16_kv4_attention, its workspace w4a16_kv8_workspace_bytes() bytes. */
+ * w4a16_kv4_attention, its workspace w4a16_kv8_workspace_bytes() bytes. Requests of many rows (the tcgen05
+ * kernel's) have their probabilities times V's scale fed as binary16 numbers, relative to the largest
+ * scale of the request so far: tiles whose scale is more than 2^20 times smaller lose bits. */
 w4a16_status w4a16_kv8_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                                  const uint8_t* cache, int pages, const int32_t* block_table,
                                  int64_t table_stride, int table_cols, const int32_t* seq_lens,
