@@ -54,7 +54,7 @@ struct Attn {
     static constexpr int ROWS = FOUR ? 4 : 8 * NR;
     static constexpr int TILES = 2;             // of a unit
     static constexpr int UNIT = 16 * TILES;     // tokens
-    static constexpr int OVERHEAD = 12;         // what starting and ending a segment costs, in units
+    static constexpr int OVERHEAD = 12;         // what starting and ending a segment costs, in units (4: 64 ragged requests 105 us, 8: 98, 18: 97)
     static constexpr int CTAS = D_ == 128 ? (NR <= 1 ? 3 : 2) : NR <= 1 ? 4 : 3;   // on an SM, as registers and rings allow
     static constexpr int STAGES = 2;            // units in a warp's ring: one in use and one on its way
     static constexpr int TB = kv8_tile_bytes(D_);

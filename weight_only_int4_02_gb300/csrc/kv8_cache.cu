@@ -94,6 +94,18 @@ struct KeyLane {
     }
 };
 
+// A lane's values of a key, rotated by its position; one that the table does not have poisons the tile.
+template <int MODE>
+__device__ __forceinline__ void turn(const Kv8RowsParams& p, float (&x)[8], int pos, int j, bool turned)
+{
+    if ((unsigned)pos >= (unsigned)p.rope.rows) {
+        x[0] = CUDART_NAN_F;
+    } else if (turned) {
+        const float* const row = p.rope.table + (long long)pos * p.rope.rot + 4 * j;
+        rotate<MODE>(x, __ldg(reinterpret_cast<const float4*>(row)), __ldg(reinterpret_cast<const float4*>(row + p.rope.rot / 2)));
+    }
+}
+
 // A run: neighbours in the list whose slots are neighbours in one tile.
 struct Run {
     uint8_t* tile;
@@ -155,15 +167,7 @@ __device__ __forceinline__ void store_keys(const Kv8RowsParams& p, const Run& ru
     for (int i = 0; i < kSteps; ++i) {
         if constexpr (MODE != kRopeNone) {
             const int tok = place0 + i * kTogether, pos = __shfl_sync(kFull, run.pos, run.lane + tok - run.off & 31);
-            if (WHOLE || run.has(tok)) {
-                if ((unsigned)pos >= (unsigned)p.rope.rows) {
-                    x[i][0] = CUDART_NAN_F;   // a position that the table does not have poisons the tile
-                } else if (my.at.turned) {
-                    const float* const row = p.rope.table + (long long)pos * p.rope.rot + 4 * (lane % kLanes);
-                    rotate<MODE>(x[i], __ldg(reinterpret_cast<const float4*>(row)),
-                                 __ldg(reinterpret_cast<const float4*>(row + p.rope.rot / 2)));
-                }
-            }
+            if (WHOLE || run.has(tok)) turn<MODE>(p, x[i], pos, lane % kLanes, my.at.turned);
         }
         top = top_of(x[i], top);
     }
@@ -251,11 +255,87 @@ __device__ __forceinline__ void store_values(const Kv8RowsParams& p, const Run& 
     if (half == 0 && lane == 0) *reinterpret_cast<float*>(run.tile + kv8_v_scale_off(D)) = s.now;
 }
 
+// The largest of D / 8 lanes' numbers, as warp_top.
+template <int D>
+__device__ __forceinline__ uint32_t lanes_top(float top)
+{
+    uint32_t t = __float_as_uint(top) & 0x7fffffffu;
+#pragma unroll
+    for (int d = 1; d < D / 8; d <<= 1) t = max(t, __shfl_xor_sync(kFull, t, d));
+    return t;
+}
+
+// Runs of one token, as batches of decoding requests have them: D / 8 lanes a run. `fine`: these lanes have one.
+template <int D, int DTYPE, int MODE>
+__device__ __forceinline__ void store_key(const Kv8RowsParams& p, bool fine, long long slot, int token, int pos, int head)
+{
+    const int j = threadIdx.x % (D / 8), off = (int)slot & 15;
+    const KeyLane<D, MODE> my(j, p.rope.rot);
+    uint8_t* const tile = tile_of(p, fine ? slot : 0, head, D);
+    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, old = 0.0f;
+    if (fine) {
+        const uint16_t* const row = (const uint16_t*)p.k + head * p.k_head + token * p.k_token;
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(row + my.at.a)), b = __ldg(reinterpret_cast<const uint2*>(row + my.at.b));
+        if (off > 0) old = *reinterpret_cast<const float*>(tile + kv8_k_scale_off(D));
+        unpack8<DTYPE>(make_uint4(a.x, a.y, b.x, b.y), x);
+        if constexpr (MODE != kRopeNone) turn<MODE>(p, x, pos, j, my.at.turned);
+    }
+    const Scale s = scale_of(lanes_top<D>(top_of(x, 0.0f)), old);
+    if (!fine) return;
+    with_clamp(s, [&](auto clamp) {
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            uint32_t c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] = code_of<clamp.value>(x[4 * o + e], s.inv);
+            *reinterpret_cast<uint32_t*>(tile + off * 64 + my.byte[o]) = s.inv > 0.0f ? bytes4(c[0], c[1], c[2], c[3]) : 0x80808080u;
+        }
+    });
+    if (s.less != 1.0f)
+        for (int t = 0; t < off; ++t)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                uint32_t* const at = reinterpret_cast<uint32_t*>(tile + t * 64 + my.byte[o]);
+                *at = less4(*at, s.less);
+            }
+    if (j == 0) *reinterpret_cast<float*>(tile + kv8_k_scale_off(D)) = s.now;
+}
+
+template <int D, int DTYPE>
+__device__ __forceinline__ void store_value(const Kv8RowsParams& p, bool fine, long long slot, int token, int head)
+{
+    const int j = threadIdx.x % (D / 8), off = (int)slot & 15;
+    uint8_t* const tile = tile_of(p, fine ? slot : 0, head, D);
+    float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, old = 0.0f;
+    if (fine) {
+        const uint4 raw = __ldg(reinterpret_cast<const uint4*>((const uint16_t*)p.v + head * p.v_head + token * p.v_token + 8 * j));
+        if (off > 0) old = *reinterpret_cast<const float*>(tile + kv8_v_scale_off(D));
+        unpack8<DTYPE>(raw, x);
+    }
+    const Scale s = scale_of(lanes_top<D>(top_of(x, 0.0f)), old);
+    if (!fine) return;
+    auto at = [&](int two) { return tile + kv8_v_off(D) + (((j >> 3) * 2 + (two >> 2)) * 8 + (j & 7)) * 64 + (two & 3) * 16; };
+    if (s.less != 1.0f)
+        for (int two = 0; 2 * two < off; ++two) {   // the new token's bytes, where it shares the last 16, are written below
+            uint4 w = *reinterpret_cast<const uint4*>(at(two));
+            w = make_uint4(less4(w.x, s.less), less4(w.y, s.less), less4(w.z, s.less), less4(w.w, s.less));
+            *reinterpret_cast<uint4*>(at(two)) = w;
+        }
+    with_clamp(s, [&](auto clamp) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t c = __byte_perm(code_of<clamp.value>(x[2 * q], s.inv), code_of<clamp.value>(x[2 * q + 1], s.inv), 0x0040);
+            *reinterpret_cast<uint16_t*>(at(off >> 1) + 4 * q + 2 * (off & 1)) = (uint16_t)(s.inv > 0.0f ? c : 0x8080u);
+        }
+    });
+    if (j == 0) *reinterpret_cast<float*>(tile + kv8_v_scale_off(D)) = s.now;
+}
+
 // Quantises new rows into their slots, K rotated on the way, with a scale for a tile of 16 tokens and head:
 //   s = max(old, max |x| * (1 / 127)), code = clamp(rint(x / s), -127, 127) + 128,
 // old being 0 where the run begins at the tile's first token; codes stored before are rounded again where s grew. Reads 4 D bytes
 // a token and head and writes 2 D. A CTA's two warps look at `window` places of the list, find the runs that begin there and store
-// one head's K or V of each. A tile belongs to one CTA, so there is no word between CTAs and no order of theirs that shows. CTAs of
+// one head's K or V of each: runs of one token several at a time, longer ones one after the other, all lanes together. A tile belongs to one CTA, so there is no word between CTAs and no order of theirs that shows. CTAs of
 // four times as many warps made the GPU wait for the last of them: 8191 tokens of eight heads of 128, rotated, 16 us, now 11.
 template <int D, int DTYPE, int MODE>
 __global__ void __launch_bounds__(64, 16) kv8_append_kernel(const Kv8RowsParams p)
@@ -277,6 +357,19 @@ __global__ void __launch_bounds__(64, 16) kv8_append_kernel(const Kv8RowsParams 
     const bool follows = live && (slot & 15) != 0 && before == slot - 1;
     const uint32_t chain = __ballot_sync(kFull, follows);
     uint32_t begins = __ballot_sync(kFull, live && !follows && lane >= 1 && lane <= p.window);
+    // runs of one token: as many at a time as the CTA has rows of lanes
+    uint32_t single = begins & ~(chain >> 1);
+    begins &= ~single;
+    while (single) {
+        uint32_t left = single;
+        for (int i = 0; i < (int)threadIdx.x / (D / 8); ++i) left &= left - 1;
+        const int l = left ? __ffs(left) - 1 : 0;
+        const long long s = __shfl_sync(kFull, slot, l);
+        const int at = __shfl_sync(kFull, pos, l);
+        if (rest & 1) store_value<D, DTYPE>(p, left != 0, s, (int)(w0 - 1 + l), head);
+        else store_key<D, DTYPE, MODE>(p, left != 0, s, (int)(w0 - 1 + l), at, head);
+        for (int i = 0; i < 64 / (D / 8); ++i) single &= single - 1;
+    }
     for (int turn = 0; begins; turn ^= 1) {
         const int l = __ffs(begins) - 1;
         begins &= begins - 1;
@@ -378,12 +471,11 @@ auto* append_of(int mode)
 cudaError_t launch_kv8_append(const Kv8RowsParams& in, cudaStream_t stream)
 {
     Kv8RowsParams p = in;
-    // Places of a pair of warps: few make long chunks slow (pairs that find no run still take their turn), many make batches of
-    // single tokens slow (a pair stores their runs one after the other). Chunks / single tokens with 1, 4 and 16 places,
-    // D = 128: 128 tokens of 8 heads 3.1 / 2.9, 3.2 / 6.2, 4.7 / 20.7 us; 1024 of 8 17.0 / 18.2, 5.2 / 16.6, 5.0 / 24.4; 4096 of 8
-    // 66.6 / 67.6, 17.7 / 53.0, 6.9 / 59.3.
-    const long long rows = (long long)p.tokens * p.kv_heads;
-    p.window = rows <= 1024 ? 1 : rows <= 8192 ? 4 : 16;
+    // Places of a CTA: few make long chunks slow (CTAs that find no run still take their turn), many make small batches wait for runs
+    // stored one after the other. Chunks / single tokens with 4 and 16 places, D = 128, rotated: 64 tokens of 8 heads 3.2 / 2.4,
+    // 5.0 / 4.7 us; 1024 5.4 / 7.1, 5.2 / 8.7; 4096 17.8 / 19.9, 7.0 / 22.1 (with one place 3.3 / 2.5, 17 / 17, 67 / 66; and single
+    // tokens by the whole CTA, as longer runs are, 1024 with 4 places 16.6).
+    p.window = (long long)p.tokens * p.kv_heads <= 8192 ? 4 : 16;
     const long long blocks = ((long long)p.tokens + p.window - 1) / p.window * 2 * p.kv_heads;   // below 2^29, as rows are below 2^31
     const bool bf = p.dtype == W4A16_BF16;
     auto* const kernel = p.head_dim == 128 ? (bf ? append_of<128, W4A16_BF16>(p.mode) : append_of<128, W4A16_FP16>(p.mode))
