@@ -335,8 +335,10 @@ __device__ __forceinline__ void store_value(const Kv8RowsParams& p, bool fine, l
 //   s = max(old, max |x| * (1 / 127)), code = clamp(rint(x / s), -127, 127) + 128,
 // old being 0 where the run begins at the tile's first token; codes stored before are rounded again where s grew. Reads 4 D bytes
 // a token and head and writes 2 D. A CTA's two warps look at `window` places of the list, find the runs that begin there and store
-// one head's K or V of each: runs of one token several at a time, longer ones one after the other, all lanes together. A tile belongs to one CTA, so there is no word between CTAs and no order of theirs that shows. CTAs of
-// four times as many warps made the GPU wait for the last of them: 8191 tokens of eight heads of 128, rotated, 16 us, now 11.
+// one head's K or V of each: runs of one token several at a time, longer ones one after the other, all lanes together. A tile
+// belongs to one CTA, so there is no word between CTAs and no order of theirs that shows. Bound by the latency of a tile's steps (slots,
+// rows and angles, the maximum, codes): 8191 tokens of eight heads of 128, rotated, 11 us, 67% of a copy's rate (16 us with CTAs of
+// eight warps, for whose last ones the GPU waits); a token each of 16 requests with 32 heads 2.3 us.
 template <int D, int DTYPE, int MODE>
 __global__ void __launch_bounds__(64, 16) kv8_append_kernel(const Kv8RowsParams p)
 {
