@@ -22,8 +22,9 @@
 //   O_A(h), S_A(h+2), O_B(h), S_B(h+2), ...
 // O is rescaled only when a row's maximum grew by more than 2^8 (its P stays below 2^15 until then).
 //
-// 8-bit codes are twice the bytes and the same unpacking, a permutation and a difference for two: three requests' chunks of 777 to 4000
-// tokens behind 3001 to 8200, 32 query heads over 8, D = 128, bfloat16, 633 us, 868 TFLOP/s, 45% of a plain product's rate.
+// 8-bit codes are twice the bytes and the same unpacking, a permutation and a difference for two, and a tile's 16 columns have one scale:
+// three requests' chunks of 777 to 4000 tokens behind 3001 to 8200, 32 query heads over 8, D = 128, bfloat16, 605 us, 908 TFLOP/s,
+// 47% of a plain product's rate. (Scales by column: 633; D = 64, 4000 rows over 8000 tokens, binary16, 521 for 458.)
 //
 // Queries and outputs go between registers and memory by way of shared memory, so that 16 (D = 64: 8) lanes
 // read or write a row together; a row a lane cost a CTA 4 us more.
@@ -321,7 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
             }
             tc_fence_after();
             const uint32_t sh_at = s_at + half * kHalf;
-            // x: s_k times the products, then the exponent, pairs of columns
+            // x: s_k times the products, then the exponent, pairs of columns. An 8-bit tile's 16 columns have one scale, which
+            // acts on their maximum and goes into the exponent's factor where nothing is masked (0 or NaN times a masked
+            // column's -infinity would be NaN).
             uint64_t x[kHalf / 2];
             {
                 uint32_t r[64];
@@ -330,16 +333,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
                 for (int j = 0; j < kHalf / 2; ++j)
                     x[j] = pack_f32x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
             }
-#pragma unroll
-            for (int j = 0; j < kHalf / 2; j += 2) {
-                const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sh.sk[s4][half * kHalf + 2 * j]);
-                x[j] = mul_f32x2(x[j], k.x);
-                x[j + 1] = mul_f32x2(x[j + 1], k.y);
-            }
             const int t0 = base + h * kHalf;
             const uint2 vw = *reinterpret_cast<const uint2*>(&sh.valid[s4][2 * half]);
             const bool full = (vw.x & vw.y) == 0xffffffffu && t0 + kHalf - 1 <= pos_min &&
                               (p.window <= 0 || t0 > pos_max - p.window);
+            constexpr int kTiles = kHalf / kKv4Tile, kPairs = kKv4Tile / 2;   // of a half, and pairs of columns of a tile
+            float tile_k[kTiles];
+            if constexpr (BITS == 8) {
+#pragma unroll
+                for (int q = 0; q < kTiles; ++q) tile_k[q] = sh.sk[s4][half * kHalf + q * kKv4Tile];
+            }
+            if (BITS == 4 || !full) {
+#pragma unroll
+                for (int j = 0; j < kHalf / 2; j += 2) {
+                    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sh.sk[s4][half * kHalf + 2 * j]);
+                    x[j] = mul_f32x2(x[j], k.x);
+                    x[j + 1] = mul_f32x2(x[j + 1], k.y);
+                }
+            }
             // this row's visible columns of the half, where stored: word w's bits
             auto see = [&](int w) -> uint32_t {
                 const int hi = pos - t0 + 1 - 32 * w, lo = p.window > 0 && hi > 0 ? hi - p.window : 0;
@@ -367,7 +378,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
             for (int j = 0; j < kHalf / 2; ++j) {
                 float u, v;
                 unpack_f32x2(x[j], u, v);
-                tops[j & 3] = fmaxf(tops[j & 3], fmaxf(u, v));
+                float& t = tops[BITS == 4 ? j & 3 : j / kPairs];
+                t = fmaxf(t, fmaxf(u, v));
+            }
+            uint64_t factor[kTiles];
+#pragma unroll
+            for (int q = 0; q < kTiles; ++q) {
+                factor[q] = a2;
+                if (BITS == 8 && full) {
+                    tops[q] = fmaxf(tops[q] * tile_k[q], -CUDART_INF_F);   // drops a NaN
+                    factor[q] = pack_f32x2(tile_k[q] * a, tile_k[q] * a);
+                }
             }
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             if (half == 0 && !wait_warp(smem_addr(&sh.vfull[s2]), (i >> 1) & 1, ctl)) {
@@ -415,11 +436,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
-                    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&sh.sv[s2][half * kHalf + 32 * c + 2 * j]);
+                    ulonglong2 v;
+                    if constexpr (BITS == 4) {
+                        v = *reinterpret_cast<const ulonglong2*>(&sh.sv[s2][half * kHalf + 32 * c + 2 * j]);
+                    } else {
+                        const float tile_v = sh.sv[s2][half * kHalf + (16 * c + j) / kPairs * kKv4Tile];
+                        v.x = v.y = pack_f32x2(tile_v, tile_v);
+                    }
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         float u0, u1;
-                        unpack_f32x2(fma_f32x2(x[16 * c + j + q], a2, ma2), u0, u1);
+                        unpack_f32x2(fma_f32x2(x[16 * c + j + q], BITS == 4 ? a2 : factor[(16 * c + j) / kPairs], ma2), u0, u1);
                         const uint64_t e = pack_f32x2(ex2(u0), ex2(u1));
                         l2 = add_f32x2(l2, e);
                         float p0, p1;
