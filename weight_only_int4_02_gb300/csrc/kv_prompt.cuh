@@ -138,6 +138,12 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// Four 8 x 8 matrices of 16-bit values: lane 8m + g has the address of row g of matrix m, whose words lanes 4g .. 4g + 3 hold.
+__device__ __forceinline__ void stmatrix4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 template <int D, bool BF, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnParams p)
 {
@@ -599,8 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
         const int32_t* const trow = p.table + (long long)b * p.table_stride;
         const int tpp_shift = __ffs(p.page_size) - 1 - 4;
         // K: token t, of tile t / 16. V: tokens 8 vh .. 8 vh + 7 of tile vt, values vn D/8 .. of d, so
-        // that the eight 16-byte chunks of a swizzled row are written by eight neighbouring lanes
-        const int vh = t & 1, vt = (t >> 6) * 4 + ((t >> 1) & 3), vn = (t >> 3) & 7;
+        // that the eight 16-byte chunks of a swizzled row are written by eight neighbouring lanes.
+        // 8 bits: neighbouring lanes load neighbouring 16 bytes, half a warp 4 tokens' 64 keys at a time and four lanes the 64
+        // bytes of 8 tokens x 8 values (values vn + r of every 8 by the r-th load), a pair of tokens' each, which stmatrix puts together.
+        const int vh = (BITS == 4 ? t : t >> 2) & 1, vt = (t >> 6) * 4 + ((BITS == 4 ? t >> 1 : t >> 3) & 3);
+        const int vn = BITS == 4 ? (t >> 3) & 7 : (t >> 5 & 1) * 4;
         auto page_of = [&](int i, int tile) {   // the page that holds a tile of block i, or -1
             const int g = (base + i * kBlock) / kKv4Tile + tile;
             if (i >= blocks || g * kKv4Tile >= seq) return -1;
@@ -624,8 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
             if (BITS == 8 && page >= 0) {
                 const uint8_t* const tile = tile_at(i, t >> 4, page);
 #pragma unroll
-                for (int j = 0; j < kWords; ++j)
-                    kw[j] = __ldg(reinterpret_cast<const uint4*>(tile + (j >> 2) * 1024 + (t & 15) * 64) + (j & 3));
+                for (int j = 0; j < kWords; ++j) kw[j] = __ldg(reinterpret_cast<const uint4*>(tile) + j * 16 + (t & 15));
                 if (here) {
                     const uint2 both = __ldg(reinterpret_cast<const uint2*>(tile + kv8_k_scale_off(D)));
                     ks = both.x;
@@ -649,9 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
             for (int j = 0; j < kWords; ++j) vw[j] = make_uint4(0, 0, 0, 0);
             vz = make_uint2(0, 0);
             if (BITS == 8 && page >= 0) {
-                const uint8_t* const at = tile_at(i, vt, page) + kv8_v_off(D) + (vh * 8 + vn) * 64;
+                const uint8_t* const at = tile_at(i, vt, page) + kv8_v_off(D) + (vh * 8 + vn) * 64 + (t & 3) * 16;
 #pragma unroll
-                for (int j = 0; j < kWords; ++j) vw[j] = __ldg(reinterpret_cast<const uint4*>(at + (j >> 2) * 1024) + (j & 3));
+                for (int j = 0; j < kWords; ++j) vw[j] = __ldg(reinterpret_cast<const uint4*>(at + (j >> 2) * 1024 + (j & 3) * 64));
             }
             if (BITS == 4 && page >= 0) {
                 const uint8_t* const tile = tile_at(i, vt, page);
@@ -694,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
                     } else {
 #pragma unroll
                         for (int q = 0; q < 4; q += 2)
-                            sts128(kb + swizzled(t, 2 * j + q / 2, kBlock), pair8(w[q], 0x4140), pair8(w[q], 0x4342),
+                            sts128(kb + swizzled((t & ~15) + (j & 3) * 4 + (t >> 2 & 3), (j >> 2) * 8 + (t & 3) * 2 + q / 2, kBlock), pair8(w[q], 0x4140), pair8(w[q], 0x4342),
                                    pair8(w[q + 1], 0x4140), pair8(w[q + 1], 0x4342));
                     }
                 }
@@ -764,20 +772,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
                             sts128(vb + swizzled(vn * (D / 8) + 4 * j + q, chunk, D), r[0][q], r[1][q], r[2][q], r[3][q]);
                     }
                 } else {
+                    // rows 4h .. 4h + 3 of each 8 values at once: lane 8m + g has the address of row 4h + m in the 8 tokens that
+                    // lanes 4g .. 4g + 3 loaded, two tokens a lane, so that the eight chunks of a row are written together
+                    const uint32_t row_at = vb + swizzled(vn * 8 + (lane >> 3), (t >> 6) * 8 + (lane & 7), D);
 #pragma unroll
-                    for (int s = 0; s < D / 64; ++s) {
-                        // word j of tokens 2c and 2c + 1: d = 64 s + 8 vn + 2 j and the next, neighbouring bytes
-                        const uint4* const w = vw + 4 * s;
-                        const uint32_t words[4][4] = {{w[0].x, w[1].x, w[2].x, w[3].x}, {w[0].y, w[1].y, w[2].y, w[3].y},
-                                                      {w[0].z, w[1].z, w[2].z, w[3].z}, {w[0].w, w[1].w, w[2].w, w[3].w}};
+                    for (int r = 0; r < kWords; ++r) {
+                        const uint32_t at = row_at + ((r >> 2) * 64 + (r & 3) * 8) * 128;
+                        const uint32_t w[4] = {vw[r].x, vw[r].y, vw[r].z, vw[r].w};   // word j: values 2j and 2j + 1 of both tokens
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t pick = e ? 0x4341u : 0x4240u;
-                                sts128(vb + swizzled(64 * s + 8 * vn + 2 * j + e, chunk, D), pair8(words[j][0], pick), pair8(words[j][1], pick),
-                                       pair8(words[j][2], pick), pair8(words[j][3], pick));
-                            }
+                        for (int h = 0; h < 2; ++h)
+                            stmatrix4((at ^ (h << 6)) + h * 512, pair8(w[2 * h], 0x4240), pair8(w[2 * h], 0x4341),
+                                      pair8(w[2 * h + 1], 0x4240), pair8(w[2 * h + 1], 0x4341));
                     }
                 }
             }
