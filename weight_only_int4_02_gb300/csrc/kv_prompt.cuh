@@ -23,8 +23,8 @@
 // O is rescaled only when a row's maximum grew by more than 2^8 (its P stays below 2^15 until then).
 //
 // 8-bit codes are twice the bytes and the same unpacking, a permutation and a difference for two, and a tile's 16 columns have one scale:
-// three requests' chunks of 777 to 4000 tokens behind 3001 to 8200, 32 query heads over 8, D = 128, bfloat16, 605 us, 908 TFLOP/s,
-// 47% of a plain product's rate. (Scales by column: 633; D = 64, 4000 rows over 8000 tokens, binary16, 521 for 458.)
+// three requests' chunks of 777 to 4000 tokens behind 3001 to 8200, 32 query heads over 8, D = 128, bfloat16, 494 us, 1110 TFLOP/s,
+// 58% of a plain product's rate. (Scales by column: 633 where this took 605; a lane's 64 bytes of K or V on its own: 605 for 591.)
 //
 // Queries and outputs go between registers and memory by way of shared memory, so that 16 (D = 64: 8) lanes
 // read or write a row together; a row a lane cost a CTA 4 us more.
@@ -34,10 +34,9 @@
 // joins them through the workspace, in their order: 8192 rows over 4000 tokens 81 -> 53 us, 41 of D = 64.
 //
 // Three requests' chunks of 839 to 4000 tokens behind 5690 to 8200 cached ones, 32 query heads over
-// 8, D = 128, bfloat16: 909 us, 898 TFLOP/s, 47% of what a plain bf16 matrix product reaches. (Scores
-// by whole blocks, one S a tile: 1000 us.) The tensor pipe is busy for 42% of the time, the issue slots for
-// 51%, shared memory for 93% (55% for the warps, 38% for the MMAs' operands), which is the nearest to a limit: without
-// the exponentials, the scales or the unpacking the kernel takes 0 to 5% less, with an eighth of the products 12%.
+// 8, D = 128, bfloat16: 868 us, 940 TFLOP/s, 49% of what a plain bf16 matrix product reaches. (Scores
+// by whole blocks, one S a tile: 1000 us where this took 909.) The loads and stores of the unpacking and the MMAs' operands keep shared
+// memory busy for most of the cycles: a lane's 64 bytes of codes on its own are 16 lines of a request.
 // Of a CTA's 110 us its start and end, which nothing overlaps, are about 9; CTAs that stay and
 // take the next rows themselves gained nothing there (929 us).
 #pragma once
@@ -61,10 +60,10 @@ constexpr int kThreads = 512;         // four warpgroups, of the last the MMA wa
 // Registers a thread: 128 at launch, moved to the softmax from the warps that need fewer. Each
 // of the SM's four quarters holds one warp of every warpgroup and a quarter of the registers.
 // Below 160 the softmax spills (152/112/96: 933 us where this takes 905).
-// A block of 8-bit codes on its way takes the unpack warps twice the registers.
+// A block of 8-bit codes on its way takes the unpack warps twice the registers. Fewer than 72 for the MMAs' thread spill.
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168;
-template <int BITS> constexpr int kUnpackRegs = BITS == 4 ? 96 : 120;
-template <int BITS> constexpr int kIssueRegs = BITS == 4 ? 80 : 56;
+template <int BITS> constexpr int kUnpackRegs = BITS == 4 ? 96 : 104;
+template <int BITS> constexpr int kIssueRegs = BITS == 4 ? 80 : 72;
 static_assert(2 * kSoftmaxRegs + kUnpackRegs<4> + kIssueRegs<4> <= 4 * kLaunchRegs, "registers of the block");
 static_assert(2 * kSoftmaxRegs + kUnpackRegs<8> + kIssueRegs<8> <= 4 * kLaunchRegs, "registers of the block");
 constexpr int kScaleStages = 4;       // K's scales live until the softmax has read them: two blocks past K itself
@@ -321,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
 #pragma unroll 1
         for (int h = 0; h < halves; ++h) {
             const int i = h >> 1, half = h & 1, s4 = i % kScaleStages, s2 = i & 1;
-            if (!wait_warp(smem_addr(&sh.skfull[s4]), (i / kScaleStages) & 1, ctl) ||
+            if ((half == 0 && !wait_warp(smem_addr(&sh.skfull[s4]), (i / kScaleStages) & 1, ctl)) ||
                 !wait_warp(smem_addr(&sh.sfull[tile][half]), i & 1, ctl)) {
                 ok = false;
                 break;
@@ -610,12 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
         // bytes of 8 tokens x 8 values (values vn + r of every 8 by the r-th load), a pair of tokens' each, which stmatrix puts together.
         const int vh = (BITS == 4 ? t : t >> 2) & 1, vt = (t >> 6) * 4 + ((BITS == 4 ? t >> 1 : t >> 3) & 3);
         const int vn = BITS == 4 ? (t >> 3) & 7 : (t >> 5 & 1) * 4;
-        auto page_of = [&](int i, int tile) {   // the page that holds a tile of block i, or -1
+        // the table's entry for a tile of block i, or -1. It is looked at where the page is read, a block later: a comparison
+        // here waits for the entry
+        auto page_of = [&](int i, int tile) {
             const int g = (base + i * kBlock) / kKv4Tile + tile;
-            if (i >= blocks || g * kKv4Tile >= seq) return -1;
-            const int page = trow[g >> tpp_shift];
-            return page >= 0 && page < p.pages ? page : -1;
+            return i >= blocks || g * kKv4Tile >= seq ? -1 : trow[g >> tpp_shift];
         };
+        auto held_page = [&](int page) { return page >= 0 && page < p.pages; };
         auto tile_at = [&](int i, int tile, int page) {
             const int g = (base + i * kBlock) / kKv4Tile + tile;
             return p.cache + ((((long long)page * p.kv_heads + head) << tpp_shift) + (g & ((1 << tpp_shift) - 1))) * C::TB;
@@ -629,8 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
 #pragma unroll
             for (int j = 0; j < kWords; ++j) kw[j] = make_uint4(0, 0, 0, 0);
             kz = ks = vs = 0;
-            here = page >= 0 && base + i * kBlock + t < seq;
-            if (BITS == 8 && page >= 0) {
+            const bool found = held_page(page);
+            here = found && base + i * kBlock + t < seq;
+            if (BITS == 8 && found) {
                 const uint8_t* const tile = tile_at(i, t >> 4, page);
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) kw[j] = __ldg(reinterpret_cast<const uint4*>(tile) + j * 16 + (t & 15));
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
                     vs = both.y;
                 }
             }
-            if (BITS == 4 && page >= 0) {
+            if (BITS == 4 && found) {
                 const uint8_t* const tile = tile_at(i, t >> 4, page);
                 const uint4* at = reinterpret_cast<const uint4*>(tile + (t & 15) * (D / 2));
 #pragma unroll
@@ -656,12 +657,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
 #pragma unroll
             for (int j = 0; j < kWords; ++j) vw[j] = make_uint4(0, 0, 0, 0);
             vz = make_uint2(0, 0);
-            if (BITS == 8 && page >= 0) {
+            const bool found = held_page(page);
+            if (BITS == 8 && found) {
                 const uint8_t* const at = tile_at(i, vt, page) + kv8_v_off(D) + (vh * 8 + vn) * 64 + (t & 3) * 16;
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) vw[j] = __ldg(reinterpret_cast<const uint4*>(at + (j >> 2) * 1024 + (j & 3) * 64));
             }
-            if (BITS == 4 && page >= 0) {
+            if (BITS == 4 && found) {
                 const uint8_t* const tile = tile_at(i, vt, page);
                 const uint4* at = reinterpret_cast<const uint4*>(tile + kv4_v_off(D) + (vh * 8 + vn) * (16 * W));
 #pragma unroll
@@ -796,70 +798,78 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
         setmaxnreg_dec<kIssueRegs<BITS>>();
         if (warp == kMmaWarp) {
         constexpr uint32_t idesc_s = idesc_f16_f32(128, kHalf), idesc_o = idesc_f16_f32(128, D);
-        // S of a tile for half h: K's tokens 64 (h mod 2) .. of its block
-        auto scores = [&](int tile, int h) {
-            const uint64_t qd = smem_desc_k_sw128(sbase + tile * C::QT);
-            const uint64_t kd = smem_desc_k_sw128(sbase + C::OFF_K + (h >> 1 & 1) * C::QT + (h & 1) * kHalf * 128);
-            const uint32_t d = tmem + C::S_COL + tile * kBlock + (h & 1) * kHalf;
+        // S of a tile for a half of the block in K's stage s: tokens 64 half .. of it
+        auto scores = [&](int tile, int half, int s) {
+            uint32_t at = sbase;
+            asm volatile("" : "+r"(at));   // or the compiler keeps all descriptors in registers, and spills
+            const uint64_t qd = smem_desc_k_sw128(at + tile * C::QT);
+            const uint64_t kd = smem_desc_k_sw128(at + C::OFF_K + s * C::QT + half * kHalf * 128);
+            const uint32_t d = tmem + C::S_COL + tile * kBlock + half * kHalf;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint64_t off = (uint64_t)((k >> 2) * (kRows * 8) + (k & 3) * 2);
                 mma_f16_ss(d, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
             }
         };
-        auto outputs = [&](int tile, int h) {
-            const uint64_t vd = smem_desc_k_sw128(sbase + C::OFF_V + (h >> 1 & 1) * C::QT + (h & 1) * D * 128);
-            const uint32_t d = tmem + C::O_COL + tile * D, a = tmem + C::S_COL + tile * kBlock + (h & 1) * kHalf;
+        auto outputs = [&](int tile, int half, int s, bool first) {
+            uint32_t at = sbase;
+            asm volatile("" : "+r"(at));
+            const uint64_t vd = smem_desc_k_sw128(at + C::OFF_V + s * C::QT + half * D * 128);
+            const uint32_t d = tmem + C::O_COL + tile * D, a = tmem + C::S_COL + tile * kBlock + half * kHalf;
             // 32 columns of P lie in the first 16 of S's columns for them, their low parts in the others
 #pragma unroll
             for (int k = 0; k < kHalf / 16; ++k)
-                mma_f16_ts(d, a + (k >> 1) * 32 + (k & 1) * 8, vd + (uint64_t)(k * 2), idesc_o, (h > 0 || k > 0) ? 1u : 0u);
+                mma_f16_ts(d, a + (k >> 1) * 32 + (k & 1) * 8, vd + (uint64_t)(k * 2), idesc_o, (!first || k > 0) ? 1u : 0u);
             if constexpr (!BF) {
 #pragma unroll
                 for (int k = 0; k < kHalf / 16; ++k)
                     mma_f16_ts(d, a + (k >> 1) * 32 + 16 + (k & 1) * 8, vd + (uint64_t)(k * 2), idesc_o, 1u);
             }
         };
-        bool ok = halves > 0 && wait_warp(smem_addr(&sh.qfull), 0, ctl) && wait_warp(smem_addr(&sh.kfull[0]), 0, ctl);
-        if (ok) {
-            tc_fence_after();
-            if (elect_one()) {
-                for (int h = 0; h < 2 && h < halves; ++h)
-                    for (int tile = 0; tile < 2; ++tile) {
-                        scores(tile, h);
-                        mma_commit(smem_addr(&sh.sfull[tile][h]));
-                    }
+        // The MMAs' thread was what the kernel waited for: a step of waits, descriptors and issue took it 1300 cycles a tile where the
+        // products take 640. So one thread, without votes, and the halves and tiles of a block in code of their own, where descriptors are
+        // sums of constants: 4000 rows over 8000 tokens, D = 128, bfloat16, 8 bits, 457 -> 378 us.
+        if (elect_one()) {
+            bool ok = halves > 0 && wait_one(smem_addr(&sh.qfull), 0, ctl) && wait_one(smem_addr(&sh.kfull[0]), 0, ctl);
+            if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int tile = 0; tile < 2; ++tile)
+                        if (half < halves) {
+                            scores(tile, half, 0);
+                            mma_commit(smem_addr(&sh.sfull[tile][half]));
+                        }
                 mma_commit(smem_addr(&sh.kempty[0]));
             }
-            __syncwarp();
-        }
-        for (int h = 0; ok && h < halves; ++h) {
-            const int half = h & 1, i = h >> 1, s2 = i & 1, n = i + 1;   // h + 2 is of block n
-            const bool more = h + 2 < halves;
-            if (half == 0) {
-                if (!wait_warp(smem_addr(&sh.vfull[s2]), (i >> 1) & 1, ctl)) break;
-                if (more && !wait_warp(smem_addr(&sh.kfull[n & 1]), (n >> 1) & 1, ctl)) break;
-            }
 #pragma unroll 1
-            for (int tile = 0; tile < 2; ++tile) {
-                if (ok && !wait_warp(smem_addr(&sh.pfull[tile][half]), i & 1, ctl)) ok = false;
-                if (!ok) continue;
-                tc_fence_after();
-                if (elect_one()) {
-                    outputs(tile, h);
-                    mma_commit(smem_addr(&sh.odone[tile][half]));
-                    if (tile == 1 && half == 1) mma_commit(smem_addr(&sh.vempty[s2]));
-                    if (more) {
-                        scores(tile, h + 2);
-                        mma_commit(smem_addr(&sh.sfull[tile][half]));
-                        if (tile == 1 && half == 1) mma_commit(smem_addr(&sh.kempty[n & 1]));
+            for (int i = 0; ok && 2 * i < halves; ++i) {
+                const int s2 = i & 1, n = i + 1;   // h + 2 is of block n
+                ok = wait_one(smem_addr(&sh.vfull[s2]), (i >> 1) & 1, ctl) &&
+                     (2 * n >= halves || wait_one(smem_addr(&sh.kfull[n & 1]), (n >> 1) & 1, ctl));
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int h = 2 * i + half;
+                    const bool more = h + 2 < halves;
+#pragma unroll
+                    for (int tile = 0; tile < 2; ++tile) {
+                        if (!ok || h >= halves) continue;
+                        ok = wait_one(smem_addr(&sh.pfull[tile][half]), i & 1, ctl);
+                        if (!ok) continue;
+                        tc_fence_after();
+                        outputs(tile, half, s2, h == 0);
+                        mma_commit(smem_addr(&sh.odone[tile][half]));
+                        if (tile == 1 && half == 1) mma_commit(smem_addr(&sh.vempty[s2]));
+                        if (more) {
+                            scores(tile, half, n & 1);
+                            mma_commit(smem_addr(&sh.sfull[tile][half]));
+                            if (tile == 1 && half == 1) mma_commit(smem_addr(&sh.kempty[n & 1]));
+                        }
                     }
                 }
-                __syncwarp();
             }
-        }
-        // every MMA issued so far completes before the tensor memory is freed
-        if (elect_one()) {
+            // every MMA issued so far completes before the tensor memory is freed
             mma_commit(smem_addr(&sh.teardown));
             wait_drain(smem_addr(&sh.teardown), 0, 1000000000LL);
         }
