@@ -23,8 +23,8 @@
 // O is rescaled only when a row's maximum grew by more than 2^8 (its P stays below 2^15 until then).
 //
 // 8-bit codes are twice the bytes and the same unpacking, a permutation and a difference for two, and a tile's 16 columns have one scale:
-// three requests' chunks of 777 to 4000 tokens behind 3001 to 8200, 32 query heads over 8, D = 128, bfloat16, 494 us, 1110 TFLOP/s,
-// 58% of a plain product's rate. (Scales by column: 633 where this took 605; a lane's 64 bytes of K or V on its own: 605 for 591.)
+// three requests' chunks of 777 to 4000 tokens behind 3001 to 8200, 32 query heads over 8, D = 128, bfloat16, 460 us, 1190 TFLOP/s,
+// 62% of a plain product's rate. (Scales by column: 633 where this took 605; a lane's 64 bytes of K or V on its own: 605 for 591.)
 //
 // Queries and outputs go between registers and memory by way of shared memory, so that 16 (D = 64: 8) lanes
 // read or write a row together; a row a lane cost a CTA 4 us more.
@@ -34,7 +34,7 @@
 // joins them through the workspace, in their order: 8192 rows over 4000 tokens 81 -> 53 us, 41 of D = 64.
 //
 // Three requests' chunks of 839 to 4000 tokens behind 5690 to 8200 cached ones, 32 query heads over
-// 8, D = 128, bfloat16: 868 us, 940 TFLOP/s, 49% of what a plain bf16 matrix product reaches. (Scores
+// 8, D = 128, bfloat16: 839 us, 972 TFLOP/s, 51% of what a plain bf16 matrix product reaches. (Scores
 // by whole blocks, one S a tile: 1000 us where this took 909.) The loads and stores of the unpacking and the MMAs' operands keep shared
 // memory busy for most of the cycles: a lane's 64 bytes of codes on its own are 16 lines of a request.
 // Of a CTA's 110 us its start and end, which nothing overlaps, are about 9; CTAs that stay and
@@ -402,36 +402,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
             }
             const int en = sh.ev[s2];
             const uint2 ow = *reinterpret_cast<const uint2*>(&sh.odd[s2][2 * half]);
-            if (ow.x | ow.y)   // a NaN in V's scales shows in the rows that see it
-                poisoned = poisoned || ((ow.x & see(0)) | (ow.y & see(1))) != 0u;
-            float f = 1.0f;
-            if (top > m) {
-                if (m == -CUDART_INF_F) {
-                    m = top;       // nothing so far: l and O are zero
-                } else if ((top - m) * a > (float)kGrow) {
-                    f = ex2((m - top) * a);
+            // seldom: rows whose maximum grew (a first one by infinity), larger scales of V, a NaN among them. One vote for all of it,
+            // where a branch for each took 400 of a half's 2260 cycles (378 -> 345 us, as above)
+            const bool grew = (top - m) * a > (float)kGrow;
+            if (__any_sync(0xffffffffu, grew || en != ev || (ow.x | ow.y) != 0u)) {
+                if (ow.x | ow.y)   // a NaN in V's scales shows in the rows that see it
+                    poisoned = poisoned || ((ow.x & see(0)) | (ow.y & see(1))) != 0u;
+                float f = 1.0f;
+                if (grew) {
+                    if (m != -CUDART_INF_F) {   // else nothing so far: l and O are zero
+                        f = ex2((m - top) * a);
+                        l2 = mul_f32x2(l2, pack_f32x2(f, f));
+                    }
                     m = top;
-                    l2 = mul_f32x2(l2, pack_f32x2(f, f));
                 }
-            }
-            if (en != ev) {
-                if (ev > -126) f *= pow2i(ev - en > -126 ? ev - en : -126);
-                ev = en;
-            }
-            if (h > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-                if (!wait_outputs(h)) {
-                    ok = false;
-                    break;
+                if (en != ev) {
+                    if (ev > -126) f *= pow2i(ev - en > -126 ? ev - en : -126);
+                    ev = en;
                 }
-                tc_fence_after();
+                if (h > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                    if (!wait_outputs(h)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float y[16];
-                    uint32_t r[16];
-                    tmem_ld_f32<16>(o_at + c, y);
+                    for (int c = 0; c < D; c += 16) {
+                        float y[16];
+                        uint32_t r[16];
+                        tmem_ld_f32<16>(o_at + c, y);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(y[j] * f);
-                    tmem_st16(o_at + c, r);
+                        for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(y[j] * f);
+                        tmem_st16(o_at + c, r);
+                    }
                 }
             }
             const float ma = m == -CUDART_INF_F ? 0.0f : m * a;
