@@ -501,13 +501,14 @@ cudaError_t setup_kv8()
 
 // The tcgen05 kernel takes requests of more than kFewRows rows a KV head where the batch's rows fill the GPU with its tiles of 256, but
 // no batch whose requests all have few enough rows that such a tile is mostly empty. Which request has how many is known on the
-// device, so other batches get both kernels. tcgen05 and stream-K, us: one request, D = 128, over 4000 tokens, 2048 rows 51 / 43,
-// 3200 51 / 55, 4096 51 / 69, 8192 54 / 112; over 300 tokens 3200 15 / 24; D = 64, 2048 over 4000 28 / 28, 4096 35 / 44, 8192 42 / 69.
-// 48 requests over 4000 tokens of 4 KV heads, 36, 64, 72, 128 rows a KV head: D = 128 198 / 127, 161, 182, 296; D = 64 168 / 74,
-// 103, 124, 190. (How many tokens are cached is not known on the host: 2048 rows over 16000 would be 80 / 108.)
+// device, so other batches get both kernels. tcgen05 and stream-K, us: one request, D = 128, over 4000 tokens, 2048 rows 49 / 43,
+// 2400 49 / 47, 2816 49 / 51, 4096 48 / 69, 8192 47 / 112; over 300 tokens 3200 13 / 24, over 1000 33 / 31; D = 64, 2048 over 4000 26 / 28,
+// 2400 27 / 29, 4096 31 / 44, 8192 36 / 70; over 300 tokens 3200 11 / 15, over 1000 23 / 20. 48 requests over 4000 tokens of 4 KV heads,
+// 36, 48, 64, 72, 128 rows a KV head: D = 128 154 / 128, 130, 161, 183, 297; D = 64 142 / 75, 80, 103, 125, 190. (How many tokens are
+// cached is not known on the host: 2048 rows over 16000 would be 70 / 108, D = 64 47 / 67.)
 constexpr int kFewRows = 32;
-constexpr int sparse_rows(int head_dim) { return head_dim == 128 ? 72 : 96; }
-constexpr long long prompt_rows(int head_dim) { return head_dim == 128 ? 3200 : 4096; }
+constexpr int sparse_rows(int head_dim) { return head_dim == 128 ? 60 : 96; }
+constexpr long long kPromptRows = 2400;
 
 // Rows of a segment, in eights (0: four), where requests have up to `held` rows a KV head and the batch has `all`. Of few rows segments
 // of eight are the fastest: latency counts. Otherwise what the segments cost together decides. 64 requests over 4000 tokens of 4
@@ -529,7 +530,7 @@ cudaError_t launch_kv8_attention(const Kv4AttnParams& in, int head_dim, int max_
     Kv4AttnParams p = in;
     const long long rows = (long long)max_q * p.group;
     const bool prompt = path != 1 && (path == 2 ? rows > kFewRows
-                                                : rows > sparse_rows(head_dim) && (long long)p.tokens * p.q_heads >= prompt_rows(head_dim));
+                                                : rows > sparse_rows(head_dim) && (long long)p.tokens * p.q_heads >= kPromptRows);
     if (prompt && p.batch == 1) {   // one request is one kernel's, whatever its rows turn out to be
         p.few_rows = 0;
         return launch_kv8_prompt(p, head_dim, sms, stream);
