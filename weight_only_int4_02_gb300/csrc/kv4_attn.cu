@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
             const int t0 = r.base + t * kUnit;
             const bool full = have == 3u && t0 + kUnit - 1 <= pos_min && (p.window <= 0 || t0 > pos_max - p.window);
 
-            // s_k times the products of the unit's two tiles: tokens n and n + 8 of each, rows 2c and 2c + 1
+            // scores in powers of two, of the unit's two tiles: tokens n and n + 8 of each, rows 2c and 2c + 1. They are rounded before
+            // a reference is taken off, which is one of them, so that the largest weight is one however large they are
             float sc[2][G][4];
             float vs[2][2];
 #pragma unroll
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
 #pragma unroll
                 for (int g = 0; g < G; ++g)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[tl][g][i] = (sc[tl][g][i] + sh4[g][i]) * ks[i >> 1];
+                    for (int i = 0; i < 4; ++i) sc[tl][g][i] = (sc[tl][g][i] + sh4[g][i]) * (ks[i >> 1] * row_a[g][i & 1]);
             }
             if (!full) {
 #pragma unroll
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float x = fmaxf(fmaxf(sc[0][g][i], sc[0][g][2 + i]), fmaxf(sc[1][g][i], sc[1][g][2 + i]));
-                    grow = grow || x * row_a[g][i] > m[g][i] + (float)kGrow;
+                    grow = grow || x - m[g][i] > (float)kGrow;
                 }
             const float vmax = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));   // drops NaN
             grow = grow || vmax * vf > (float)(1 << (15 - kGrow));
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                         float x = fmaxf(fmaxf(sc[0][g][i], sc[0][g][2 + i]), fmaxf(sc[1][g][i], sc[1][g][2 + i]));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * row_a[g][i];
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                         x = fmaxf(x, m[g][i]);
                         f[i] = x == m[g][i] ? 1.0f : ex2(m[g][i] - x);
                         m[g][i] = x;
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv4_attn_kernel(c
                         float pv[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float e = ex2(fmaf(sc[tl][g][2 * j + i], row_a[g][i], -ref[g][i]));
+                            const float e = ex2(sc[tl][g][2 * j + i] - ref[g][i]);
                             l[g][i] += e;
                             pv[i] = e * v;
                         }

@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
             const int t0 = r.base + t * UNIT;
             const bool full = have == (1u << TILES) - 1u && t0 + UNIT - 1 <= pos_min && (p.window <= 0 || t0 > pos_max - p.window);
 
-            // s_k times the products: of each tile tokens n and n + 8, rows 2c and 2c + 1; two chains of MMAs, of even and odd words
+            // scores in powers of two: of each tile tokens n and n + 8, rows 2c and 2c + 1; two chains of MMAs, of even and odd words.
+            // They are rounded before a reference is taken off, which is one of them, so that the largest weight is one however large they are
             float sc[TILES][G][4], sv[TILES];
 #pragma unroll
             for (int tl = 0; tl < TILES; ++tl) {
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
 #pragma unroll
                 for (int g = 0; g < G; ++g)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[tl][g][i] = (sc[tl][g][i] + odd_sc[g][i]) * scales.x;
+                    for (int i = 0; i < 4; ++i) sc[tl][g][i] = (sc[tl][g][i] + odd_sc[g][i]) * (scales.x * row_a[g][i & 1]);
             }
             if (!full) {
 #pragma unroll
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) grow = grow || largest(g, i) * row_a[g][i] > m[g][i] + (float)kGrow;
+                for (int i = 0; i < 2; ++i) grow = grow || largest(g, i) - m[g][i] > (float)kGrow;
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
                         float x = largest(g, i);
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * row_a[g][i];
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                         x = fmaxf(x, m[g][i]);
                         f[i] = x == m[g][i] ? 1.0f : ex2(m[g][i] - x);
                         m[g][i] = x;
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
                         float pv[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float e = ex2(fmaf(sc[tl][g][2 * j + i], row_a[g][i], -ref[g][i]));
+                            const float e = ex2(sc[tl][g][2 * j + i] - ref[g][i]);
                             l[g][i] += e;
                             pv[i] = e * (float)(1 << (15 - kGrow));
                         }

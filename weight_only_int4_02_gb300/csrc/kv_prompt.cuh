@@ -70,6 +70,7 @@ constexpr int kScaleStages = 4;       // K's scales live until the softmax has r
 constexpr int kMaxSplits = 8;
 constexpr int kLeast = 4;             // blocks of a CTA where a request's cached tokens are split over several
 constexpr int kGrow = 8;              // log2 of how far P may grow before O is rescaled
+constexpr float kFar = 1048576.0f;    // the largest reference, in powers of two, whose spacing in FP32 is small beside 2^kGrow
 
 template <int D, int BITS>
 struct Prompt {
@@ -310,7 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
         const int t_last = t_row0 + kRows < rows ? t_row0 + kRows : rows;
         const int pos_min = t_row0 < rows ? pos0 + t_row0 / p.group : -1;
         const int pos_max = t_row0 < rows ? pos0 + (t_last - 1) / p.group : -1;
-        float m = -CUDART_INF_F;   // of s_k S
+        // The reference of the row's sums, of s_k S, is m0 + m. A score is x a - m a, rounded once; past kFar that would be off by half of
+        // FP32's spacing for the largest score too, whose weight is to be one. A warp that meets such a score (far) takes m0 off x first.
+        float m = -CUDART_INF_F, m0 = 0.0f;
+        bool far = false;
         uint64_t l2 = 0;           // sums of even and odd columns
         const uint64_t a2 = pack_f32x2(a, a);
         int ev = -126;
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
             }
             const int t0 = base + h * kHalf;
             const uint2 vw = *reinterpret_cast<const uint2*>(&sh.valid[s4][2 * half]);
-            const bool full = (vw.x & vw.y) == 0xffffffffu && t0 + kHalf - 1 <= pos_min &&
+            const bool full = !far && (vw.x & vw.y) == 0xffffffffu && t0 + kHalf - 1 <= pos_min &&
                               (p.window <= 0 || t0 > pos_max - p.window);
             constexpr int kTiles = kHalf / kKv4Tile, kPairs = kKv4Tile / 2;   // of a half, and pairs of columns of a tile
             float tile_k[kTiles];
@@ -372,6 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
                     for (int j = 0; j < 16; ++j) {
                         float u, v;
                         unpack_f32x2(x[16 * w + j], u, v);
+                        u = __fsub_rn(u, m0);
+                        v = __fsub_rn(v, m0);
                         u = bits >> (2 * j) & 1u ? u : -CUDART_INF_F;
                         v = bits >> (2 * j + 1) & 1u ? v : -CUDART_INF_F;
                         x[16 * w + j] = pack_f32x2(u, v);
@@ -436,6 +442,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
                         tmem_st16(o_at + c, r);
                     }
                 }
+                if (__any_sync(0xffffffffu, m != -CUDART_INF_F && fabsf(m * a) > kFar)) {
+                    // sums and O are of the new reference already: this half again, with it taken off x
+                    far = true;
+                    if (m != -CUDART_INF_F) {
+                        m0 += m;   // rounded, by more than kFar stands for only where such a jump has left nothing of the sums: then
+                        m = l2 == 0 ? -CUDART_INF_F : 0.0f;   // the half's maximum is looked for again, less m0
+                    }
+                    --h;
+                    continue;
+                }
             }
             const float ma = m == -CUDART_INF_F ? 0.0f : m * a;
             const uint64_t ma2 = pack_f32x2(-ma, -ma);
@@ -474,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
             tc_fence_before();
             mbar_arrive(smem_addr(&sh.pfull[tile][half]));
         }
+        m += m0;
         float l, l_odd;
         unpack_f32x2(l2, l, l_odd);
         l += l_odd;
