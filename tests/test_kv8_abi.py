@@ -160,3 +160,10 @@ def test_the_oracle_turns_pairs_by_their_angles():
         y = ref.rotate(x, pos, table, interleaved)
         got = y[..., 0:rot:2] + 1j * y[..., 1:rot:2] if interleaved else y[..., :rot // 2] + 1j * y[..., rot // 2:rot]
         assert np.abs(got - z * turn).max() < 1e-6 and np.array_equal(y[..., rot:], x[..., rot:])
+
+
+def test_append_refuses_heads_past_its_grid(lib, ptr):
+    """Two CTAs and more take a head of a window of the list: 2^30 heads of a few tokens are 2^31 of them."""
+    p = ptr
+    good = [p, 256, 128, p, 256, 128, p, p, p, 9, 128, 0, p, 4, 1, 2, 128, 16, 0, None]
+    refuses(lib.w4a16_kv8_append, good, [(15, (1 << 29) + 1), (15, 1 << 30), (15, (1 << 31) - 300)])

@@ -323,6 +323,7 @@ w4a16_status w4a16_kv8_append(const void* k, int64_t k_token_stride, int64_t k_h
     if (!valid_rows(cache, pages, slots, tokens, kv_heads, head_dim, page_size, dtype, W4A16_FP32) ||
         !valid_rope(positions, rope, rope_rows, rot, interleaved, head_dim))
         return W4A16_ERR_INVALID_ARG;
+    if (kv_heads > 1 << 29) return W4A16_ERR_INVALID_ARG;   // CTAs are counted in 31 bits, two and more for each head
     if (tokens == 0) return W4A16_OK;
     if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return W4A16_ERR_INVALID_ARG;
     if (!valid_stride(k_token_stride, head_dim, tokens) || !valid_stride(k_head_stride, head_dim, kv_heads) ||

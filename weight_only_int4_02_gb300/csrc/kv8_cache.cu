@@ -478,7 +478,7 @@ cudaError_t launch_kv8_append(const Kv8RowsParams& in, cudaStream_t stream)
     // 5.0 / 4.7 us; 1024 5.4 / 7.1, 5.2 / 8.7; 4096 17.8 / 19.9, 7.0 / 22.1 (with one place 3.3 / 2.5, 17 / 17, 67 / 66; and single
     // tokens by the whole CTA, as longer runs are, 1024 with 4 places 16.6).
     p.window = (long long)p.tokens * p.kv_heads <= 8192 ? 4 : 16;
-    const long long blocks = ((long long)p.tokens + p.window - 1) / p.window * 2 * p.kv_heads;   // below 2^29, as rows are below 2^31
+    const long long blocks = ((long long)p.tokens + p.window - 1) / p.window * 2 * p.kv_heads;   // below 2^28 + 2^30: rows are below 2^31, heads at most 2^29
     const bool bf = p.dtype == W4A16_BF16;
     auto* const kernel = p.head_dim == 128 ? (bf ? append_of<128, W4A16_BF16>(p.mode) : append_of<128, W4A16_FP16>(p.mode))
                                            : (bf ? append_of<64, W4A16_BF16>(p.mode) : append_of<64, W4A16_FP16>(p.mode));
