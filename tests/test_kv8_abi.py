@@ -167,3 +167,10 @@ def test_append_refuses_heads_past_its_grid(lib, ptr):
     p = ptr
     good = [p, 256, 128, p, 256, 128, p, p, p, 9, 128, 0, p, 4, 1, 2, 128, 16, 0, None]
     refuses(lib.w4a16_kv8_append, good, [(15, (1 << 29) + 1), (15, 1 << 30), (15, (1 << 31) - 300)])
+
+
+def test_norms_refuse_heads_whose_last_pass_overflows(lib, ptr):
+    """A warp takes up to 64 heads: where the last warp begins less than that below 2^31, the head behind its rows has no number."""
+    p = ptr
+    good = [p, 512, 128, p, 512, 128, p, 256, 128, p, 256, 128, p, p, 1e-6, p, p, 9, 128, 0, 1, 4, 2, 128, 0, None]
+    refuses(lib.w4a16_qk_norm_rope, good, [(21, (1 << 31) - 30), ((21, 0), (22, (1 << 31) - 30)), ((21, 0), (22, (1 << 31) - 60), (23, 64))])

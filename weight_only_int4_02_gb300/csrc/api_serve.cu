@@ -271,8 +271,8 @@ w4a16_status w4a16_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q
         !(eps >= 0.0f) || !(eps <= 3.0e38f) || !valid_rope(positions, rope, rope_rows, rot, interleaved, head_dim))
         return W4A16_ERR_INVALID_ARG;
     const int64_t heads = (int64_t)q_heads + kv_heads;
-    // warps of eight rows of queries or of keys, and more, counted in 31 bits
-    if (heads > INT32_MAX - 16 || (int64_t)tokens * (((int64_t)q_heads + 7) / 8 + ((int64_t)kv_heads + 7) / 8) >= ((int64_t)1 << 31) - 8)
+    // warps of eight rows of queries or of keys, and more, counted in 31 bits, as is the head behind a warp's last pass
+    if (heads > INT32_MAX - 256 || (int64_t)tokens * (((int64_t)q_heads + 7) / 8 + ((int64_t)kv_heads + 7) / 8) >= ((int64_t)1 << 31) - 8)
         return W4A16_ERR_INVALID_ARG;
     if (tokens == 0 || heads == 0) return W4A16_OK;
     NormRopeParams p = {};
