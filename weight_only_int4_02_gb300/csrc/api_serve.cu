@@ -138,6 +138,16 @@ w4a16_status attention(const CacheKind& kind, const void* q, int64_t q_token_str
 
 }  // namespace
 
+namespace w4a16 {
+
+cudaError_t setup_kv4()
+{
+    const cudaError_t e = setup_kv4_attention();
+    return e != cudaSuccess ? e : setup_kv8_attention();
+}
+
+}  // namespace w4a16
+
 extern "C" {
 
 size_t w4a16_kv4_page_bytes(int kv_heads, int head_dim, int page_size)

@@ -34,7 +34,7 @@
 // for 47%), which wait for one another more than for memory. Eight or two warps a CTA, five CTAs an SM
 // (fewer registers) and tokens' scales through shared memory were slower.
 #include "api_internal.cuh"
-#include "kv8.cuh"
+#include "kv4.cuh"
 #include "kv_attn.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
@@ -559,16 +559,14 @@ size_t kv4_partial_bytes(int sms)
     return need;
 }
 
-// The 8-bit cache's too: all of the serving step's.
-cudaError_t setup_kv4()
+cudaError_t setup_kv4_attention()
 {
     cudaError_t e;
     if ((e = Launch<64, 0>::setup()) != cudaSuccess || (e = Launch<128, 0>::setup()) != cudaSuccess ||
         (e = Launch<64, 1>::setup()) != cudaSuccess || (e = Launch<64, 2>::setup()) != cudaSuccess ||
         (e = Launch<128, 1>::setup()) != cudaSuccess || (e = Launch<128, 2>::setup()) != cudaSuccess)
         return e;
-    if ((e = setup_kv4_prompt()) != cudaSuccess) return e;
-    return setup_kv8();
+    return setup_kv4_prompt();
 }
 
 // The tcgen05 kernel takes requests of more than kFewRows rows a KV head where the batch's rows (query

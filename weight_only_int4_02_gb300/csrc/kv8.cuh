@@ -42,7 +42,7 @@ cudaError_t launch_kv8_read(const Kv8RowsParams& p, cudaStream_t stream);
 
 // path: 0 as measured, 1 the stream-K kernel, 2 the tcgen05 kernel for every request of more than 32 rows.
 cudaError_t launch_kv8_attention(const Kv4AttnParams& p, int head_dim, int max_q, int path, int sms, cudaStream_t stream);
-cudaError_t setup_kv8();   // attributes of the attention kernels
+cudaError_t setup_kv8_attention();   // attributes of the attention kernels
 // The tcgen05 kernel, for requests of more than few_rows rows.
 cudaError_t setup_kv8_prompt();
 cudaError_t launch_kv8_prompt(const Kv4AttnParams& p, int head_dim, int sms, cudaStream_t stream);

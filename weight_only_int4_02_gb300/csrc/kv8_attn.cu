@@ -489,7 +489,7 @@ size_t kv8_partial_bytes(int sms)
     return need;
 }
 
-cudaError_t setup_kv8()
+cudaError_t setup_kv8_attention()
 {
     cudaError_t e;
     if ((e = Launch<64, 0>::setup()) != cudaSuccess || (e = Launch<128, 0>::setup()) != cudaSuccess ||
