@@ -48,7 +48,6 @@ template <int D_, int NR>
 struct Attn {
     static constexpr int DIM = D_;
     static constexpr int JOIN = D_ == 128 ? 16 : 8;   // parts whose outputs a join loads together
-    static constexpr int LEAST = 1;             // units of a warp, where there are too few for all CTAs
     static constexpr bool FOUR = NR == 0;       // four rows, twice in an MMA's eight columns
     static constexpr int G = FOUR ? 1 : NR;     // columns, in eights
     static constexpr int ROWS = FOUR ? 4 : 8 * NR;
@@ -308,9 +307,8 @@ __global__ void __launch_bounds__(kThreads, Attn<D, NR>::CTAS) kv8_attn_kernel(c
                 }
             }
             auto largest = [&](int g, int i) {
-                float x = fmaxf(sc[0][g][i], sc[0][g][2 + i]);
-                if constexpr (TILES == 2) x = fmaxf(x, fmaxf(sc[1][g][i], sc[1][g][2 + i]));
-                return x;
+                static_assert(TILES == 2, "both tiles' scores");
+                return fmaxf(fmaxf(sc[0][g][i], sc[0][g][2 + i]), fmaxf(sc[1][g][i], sc[1][g][2 + i]));
             };
             // the references of the running sums move if a score passes its row's by 2^kGrow
             bool grow = false;
