@@ -54,10 +54,12 @@ __device__ __forceinline__ uint64_t swapped(uint64_t v)
 // angles of a token fixed, a row's outputs are r (x A + x' B), x' the partners and r = 1 / sqrt(mean(x^2) + eps), with A = w cos
 // and B = -+ w' sin. A warp has one token and some of its query or key heads, so that A and B are made once for them,
 // takes them in passes of which the next one's rows are on their way, and works on pairs of numbers. Bound by bandwidth: a row
-// is read once and written once. 8191 tokens of 64 and 8 heads of 128: 52 us, 5.9 TB/s, 87% of a copy's rate (issue slots 59%
-// busy); with scalar arithmetic and one pass 67. 16 tokens of 40 heads take 2.4 us.
+// is read once and written once. 8191 tokens of 64 and 8 heads of 128: 50.8 us, 6.0 TB/s, 89% of a copy's rate; with scalar arithmetic
+// and one pass 67. 16 tokens of 40 heads take 2.4 us. Fourteen CTAs an SM leave 72 registers, of which the forms that rotate want a few more (8 to 24
+// bytes spilled): sixteen, with 64, spilled 52 to 92 and took 51.8; twelve spill none, 52.7 (1003 tokens of 32 heads of 64, 32 of them
+// turned: 3.8, 4.4 and 3.4 us).
 template <int D, int DTYPE, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, 16) norm_rope_kernel(const NormRopeParams p)
+__global__ void __launch_bounds__(kWarps * 32, 14) norm_rope_kernel(const NormRopeParams p)
 {
     chained_kernel();
     constexpr int kLanes = D / 8, kTogether = 32 / kLanes;
@@ -195,7 +197,7 @@ auto* kernel_of(int mode)
 cudaError_t launch_norm_rope(const NormRopeParams& in, int sms, cudaStream_t stream)
 {
     NormRopeParams p = in;
-    // More passes a warp where that leaves enough warps, four times what an SM holds: A and B cost as much as a pass (8191 tokens
+    // More passes a warp where that leaves enough warps, three times what an SM holds: A and B cost as much as a pass (8191 tokens
     // of 64 and 8 heads of 128, in CTAs of eight warps: one pass 68.9 us, two 57.4, four 55.3, eight 55.3).
     const long long pass = 32 / (p.head_dim / 8) * kRowsAhead;
     auto groups_of = [&](int i) { return (p.heads[i] + pass * p.passes - 1) / (pass * p.passes); };
