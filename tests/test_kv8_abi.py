@@ -174,3 +174,11 @@ def test_norms_refuse_heads_whose_last_pass_overflows(lib, ptr):
     p = ptr
     good = [p, 512, 128, p, 512, 128, p, 256, 128, p, 256, 128, p, p, 1e-6, p, p, 9, 128, 0, 1, 4, 2, 128, 0, None]
     refuses(lib.w4a16_qk_norm_rope, good, [(21, (1 << 31) - 30), ((21, 0), (22, (1 << 31) - 30)), ((21, 0), (22, (1 << 31) - 60), (23, 64))])
+
+
+def test_rotation_tables_past_32_bits_are_refused():
+    """Rows that the C call would count as 4 or 0: refused before any memory is taken (there is no such device here either)."""
+    from weight_only_int4_02_gb300 import w4a16 as w
+    for rows, rot in (((1 << 32) + 4, 64), (1 << 32, 64), (1 << 31, 8), (4, (1 << 32) + 64), (4, 65544)):
+        with pytest.raises(w.W4A16Error):
+            w.rope_table(rows, rot)

@@ -596,7 +596,7 @@ def kv4_force_path(path):
 def rope_table(rows, rot, base=10000.0, device="cuda", stream=None):
     """The rotation's table, float32 [rows][rot]: of each position rot / 2 cosines of position * base^(-2i / rot), then the
     sines, computed in 64 bits (w4a16_rope_table). Scaled or learned angles make a table of the same layout."""
-    if rows <= 0 or rot <= 0:
+    if not 0 < rows < 1 << 31 or not 0 < rot <= 65536:   # the C call counts in 32 bits
         raise W4A16Error(ERR_INVALID_ARG, "no rotation table of %d positions of %d values" % (rows, rot))
     device = torch.device(device)
     with torch.cuda.device(device), torch.cuda.stream(stream):
