@@ -561,8 +561,9 @@ int w4a16_kv4_force_path(int path);
  *
  * A rotation turns the first `rot` values of a head's row (rot a multiple of 8, at most head_dim) by angles of the row's
  * position: pair i, of angle i, is (x[i], x[i + rot / 2]), or (x[2i], x[2i + 1]) if `interleaved` is 1 (0 otherwise):
- *   (a, b) -> (a cos - b sin, b cos + a sin)       in FP32, each product and sum rounded
- * The angles' cosines and sines come from a table, device float [rope_rows][rot], 16-byte aligned: of each position rot / 2
+ *   (a, b) -> (a cos - b sin, b cos + a sin)       in FP32
+ * w4a16_kv8_append rounds each product and sum of it; w4a16_qk_norm_rope puts its factors together first and sums by fused
+ * operations, so the two may differ in an FP32 number's last bits. The angles' cosines and sines come from a table, device float [rope_rows][rot], 16-byte aligned: of each position rot / 2
  * cosines, then rot / 2 sines. Scaled or learned angles are a matter of the table.
  *
  * w4a16_rope_table fills one with the angles p * base^(-2i / rot) of positions p = 0 .. rows - 1, computed in 64 bits. */
@@ -571,6 +572,7 @@ w4a16_status w4a16_rope_table(float* table, int rows, int rot, double base, w4a1
 /*
  * Norms of queries and keys for each head, then the rotation, in one pass; rounded once:
  *   y = x / sqrt(mean(x^2) + eps) * weight, over a row of head_dim values, mean and factors in FP32
+ * Before that rounding a result is within 2^-20 of |y| (rotated: of |a cos| + |b sin|) of its value.
  *   q, k       device, binary16 or bfloat16 [tokens][heads][head_dim] at token and head strides in elements (multiples of
  *              8, at least head_dim), 16-byte aligned. q_heads or kv_heads 0: without queries or keys, whose
  *              pointers and strides are then not looked at
@@ -611,6 +613,9 @@ size_t w4a16_kv8_page_bytes(int kv_heads, int head_dim, int page_size);
  * whatever is in memory for its scale. Tokens written again (drafts that were not accepted) are written again in order; the scale stays
  * as large as it was. A row with an infinity or a NaN, or a key at a position that the table does not have, makes the
  * scale NaN, which shows in whatever reads a token of that tile and head until the tile is begun again.
+ * Tokens stored earlier thus change with their tile's later ones, by up to half a step of the new scale: where the 4-bit cache's partly
+ * filled pages may be shared by requests that go on apart, or read on another stream while their tails are written, this one's
+ * may not (its full tiles may). Each such request wants a copy of the tile, and a reader of it to wait.
  *   k, v, slots, cache, dtype  as w4a16_kv4_append
  *   positions, rope, rope_rows, rot, interleaved  the keys' rotation; positions and rope NULL: none
  */
@@ -633,7 +638,10 @@ size_t w4a16_kv8_workspace_bytes(void);
 /* Causal attention of new query tokens over the 8-bit cache: arguments, masks and results as
  * w4a16_kv4_attention, its workspace w4a16_kv8_workspace_bytes() bytes. Requests of many rows (the tcgen05
  * kernel's) have their probabilities times V's scale fed as binary16 numbers, relative to the largest
- * scale of the request so far: tiles whose scale is more than 2^20 times smaller lose bits. */
+ * scale of the request so far: tiles whose scale is more than 2^20 times smaller lose bits. For bfloat16
+ * outputs it is one such number, 11 bits, an eighth of an output's rounding; for binary16 outputs, and for
+ * few rows whatever the output, 22 bits. Which requests have many rows (more than 32 of a KV head, in batches with
+ * a request of more than 60, or 96 of head_dim 64, and 2400 rows of all heads) is a choice by speed alone. */
 w4a16_status w4a16_kv8_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                                  const uint8_t* cache, int pages, const int32_t* block_table,
                                  int64_t table_stride, int table_cols, const int32_t* seq_lens,

@@ -332,7 +332,7 @@ __device__ __forceinline__ void store_value(const Kv8RowsParams& p, bool fine, l
 }
 
 // Quantises new rows into their slots, K rotated on the way, with a scale for a tile of 16 tokens and head:
-//   s = max(old, max |x| * (1 / 127)), code = clamp(rint(x / s), -127, 127) + 128,
+//   s = max(old, max |x| * (1 / 127)), code = clamp(rint(x * (1 / s)), -127, 127) + 128, each operation rounded,
 // old being 0 where the run begins at the tile's first token; codes stored before are rounded again where s grew. Reads 4 D bytes
 // a token and head and writes 2 D. A CTA's two warps look at `window` places of the list, find the runs that begin there and store
 // one head's K or V of each: runs of one token several at a time, longer ones one after the other, all lanes together. A tile

@@ -613,7 +613,8 @@ def qk_norm_rope(q, k, positions=None, rope=None, q_weight=None, k_weight=None, 
     positions: int32 [tokens] and rope: float32 [positions][rot] (rope_table), or both None for no rotation; q_weight,
     k_weight: [head_dim] of the inputs' type, None for no norm; interleaved: pairs are neighbours, not halves; q_out,
     k_out: q and k themselves (in place), other memory, or None for new tensors. Rows at negative positions (padding) are not
-    written, those at positions past the table become NaN. Returns (q_out, k_out)."""
+    written, those at positions past the table become NaN. Returns (q_out, k_out); two new ones are views of one allocation,
+    which lives as long as either: clone the one that is to be kept or saved without the other."""
     return (_module or _torch_module()).qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, interleaved, q_out, k_out,
                                                      None if stream is None else stream.cuda_stream)
 
@@ -632,13 +633,15 @@ def kv8_cache(pages, kv_heads, head_dim, page_size, device="cuda"):
 def kv8_append(k, v, slots, cache, page_size, positions=None, rope=None, interleaved=False, stream=None):
     """Quantise k, rotated by positions (int32 [tokens]) with rope (rope_table) unless both are None, and v into their slots
     of the 8-bit cache (w4a16_kv8_append). k, v, slots: as kv4_append; one scale for 16 tokens, so a tile's tokens are to come
-    in their order, as a request's do."""
+    in their order, as a request's do, and those stored earlier change a little with later ones: a tile that is not full is one
+    request's alone."""
     (_module or _torch_module()).kv8_append(k, v, slots, cache, page_size, positions, rope, interleaved,
                                             None if stream is None else stream.cuda_stream)
 
 
 def kv8_read(cache, slots, page_size, dtype=torch.float16, stream=None):
-    """(k, v) [tokens][kv_heads][head_dim] that the slots of the 8-bit cache stand for, in float16, bfloat16 or float32."""
+    """(k, v) [tokens][kv_heads][head_dim] that the slots of the 8-bit cache stand for, in float16, bfloat16 or float32: views of
+    one allocation."""
     if dtype not in _DTYPES:
         raise W4A16Error(ERR_INVALID_ARG, "kv8_read gives float16, bfloat16 or float32")
     return (_module or _torch_module()).kv8_read(cache, slots, page_size, _DTYPES[dtype],
