@@ -505,6 +505,14 @@ cudaError_t setup_kv8_attention()
 // 2400 27 / 29, 4096 31 / 44, 8192 36 / 70; over 300 tokens 3200 11 / 15, over 1000 23 / 20. 48 requests over 4000 tokens of 4 KV heads,
 // 36, 48, 64, 72, 128 rows a KV head: D = 128 154 / 128, 130, 161, 183, 297; D = 64 142 / 75, 80, 103, 125, 190. (How many tokens are
 // cached is not known on the host: 2048 rows over 16000 would be 70 / 108, D = 64 47 / 67.)
+// Between these, requests of 8 KV heads, over 400, 1000 and 4000 tokens, D = 128: four of 96 rows 17 / 25, 37 / 30, 53 / 54, of
+// 128 17 / 24, 37 / 30, 53 / 63; eight of 40 18 / 24, 37 / 30, 64 / 53, of 64 18 / 24, 27 / 30, 79 / 63, of 96 18 / 32, 28 /
+// 43, 80 / 92; 16 of 40 18 / 31, 28 / 41, 85 / 92, of 64 18 / 33, 28 / 45, 84 / 113. D = 64: four of 128 14 / 16, 25 / 23, 41 /
+// 45; eight of 64 15 / 18, 24 / 22, 75 / 45, of 96 15 / 22, 24 / 26, 75 / 57, of 128 15 / 23, 24 / 31, 75 / 71; 16 of 96 16 /
+// 29, 25 / 41, 76 / 102. So the rule takes the slower kernel by up to 1.26 times where it takes tcgen05 (eight of 64 over 4000;
+// one or two requests of few blocks over 1000), and by up to 1.8 where it does not (16 of 40 rows, or of 96 with D = 64, over
+// 400). Both limits are times alone, and they decide a precision: with bfloat16 outputs the tcgen05 kernel feeds weights in 11
+// bits, the stream-K kernel in 22 (errors against 64 bits 1% larger, of which an output's rounding is the rest).
 constexpr int kFewRows = 32;
 constexpr int sparse_rows(int head_dim) { return head_dim == 128 ? 60 : 96; }
 constexpr long long kPromptRows = 2400;
@@ -535,8 +543,9 @@ cudaError_t launch_kv8_attention(const Kv4AttnParams& in, int head_dim, int max_
         return launch_kv8_prompt(p, head_dim, sms, stream);
     }
     p.few_rows = prompt ? kFewRows : INT_MAX;
-    // of a request that is this kernel's, at most; beside prompts it is a single token's more often than not (two prompts of 800
-    // tokens with 30 single tokens over 8000, 8 KV heads, four query heads to each: 182 -> 172 us, D = 64 131 -> 114)
+    // of a request that is this kernel's, at most; beside prompts it is a single token's more often than not (two prompts of 800 new
+    // tokens behind 1200 with 30 single tokens over 8000, 8 KV heads, four query heads to each: 182 -> 172 us, D = 64 131 -> 114; 154 and 103
+    // since the prompt kernel is faster. The single tokens' bytes are 73 us of it, the prompts' products 22)
     const long long held = !prompt ? rows : p.group < 8 ? 8 : p.group < kFewRows ? p.group : kFewRows;
     const int nr = segment_rows(held, head_dim, (long long)p.tokens * p.q_heads);
     cudaError_t e;

@@ -23,8 +23,8 @@
 // O is rescaled only when a row's maximum grew by more than 2^8 (its P stays below 2^15 until then).
 //
 // 8-bit codes are twice the bytes and the same unpacking, a permutation and a difference for two, and a tile's 16 columns have one scale:
-// three requests' chunks of 777 to 4000 tokens behind 3001 to 8200, 32 query heads over 8, D = 128, bfloat16, 460 us, 1190 TFLOP/s,
-// 62% of a plain product's rate. (Scales by column: 633 where this took 605; a lane's 64 bytes of K or V on its own: 605 for 591.)
+// three requests' chunks of 777 to 4000 tokens behind 3001 to 8200, 32 query heads over 8, D = 128, bfloat16, 465 us, 1180 TFLOP/s,
+// 61% of a plain product's rate. (Scales by column: 633 where this took 605; a lane's 64 bytes of K or V on its own: 605 for 591.)
 //
 // Queries and outputs go between registers and memory by way of shared memory, so that 16 (D = 64: 8) lanes
 // read or write a row together; a row a lane cost a CTA 4 us more.
@@ -34,11 +34,11 @@
 // joins them through the workspace, in their order: 8192 rows over 4000 tokens 81 -> 53 us, 41 of D = 64.
 //
 // Three requests' chunks of 839 to 4000 tokens behind 5690 to 8200 cached ones, 32 query heads over
-// 8, D = 128, bfloat16: 839 us, 972 TFLOP/s, 51% of what a plain bf16 matrix product reaches. (Scores
+// 8, D = 128, bfloat16: 850 us, 960 TFLOP/s, 50% of what a plain bf16 matrix product reaches. (Scores
 // by whole blocks, one S a tile: 1000 us where this took 909.) The loads and stores of the unpacking and the MMAs' operands keep shared
-// memory busy for most of the cycles: a lane's 64 bytes of codes on its own are 16 lines of a request.
-// Of a CTA's 110 us its start and end, which nothing overlaps, are about 9; CTAs that stay and
-// take the next rows themselves gained nothing there (929 us).
+// memory busy for 85% of the cycles (42 and 43; over 8 bits for 75, 25 and 50): a lane's 64 bytes of 4-bit codes on its own are 16 lines of a request.
+// When that case took 909 us, a CTA's start and end, which nothing overlaps, were about 9 of its 110; CTAs that stay and
+// take the next rows themselves gained nothing there (929).
 #pragma once
 #include "api_internal.cuh"
 #include "kv8.cuh"
@@ -59,7 +59,7 @@ constexpr int kMmaWarp = 12;
 constexpr int kThreads = 512;         // four warpgroups, of the last the MMA warp alone at work
 // Registers a thread: 128 at launch, moved to the softmax from the warps that need fewer. Each
 // of the SM's four quarters holds one warp of every warpgroup and a quarter of the registers.
-// Below 160 the softmax spills (152/112/96: 933 us where this takes 905).
+// Below 160 the softmax spills (152/112/96: 933 us of 4 bits where this took 905).
 // A block of 8-bit codes on its way takes the unpack warps twice the registers. Fewer than 72 for the MMAs' thread spill.
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168;
 template <int BITS> constexpr int kUnpackRegs = BITS == 4 ? 96 : 104;
@@ -312,7 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
         const int pos_min = t_row0 < rows ? pos0 + t_row0 / p.group : -1;
         const int pos_max = t_row0 < rows ? pos0 + (t_last - 1) / p.group : -1;
         // The reference of the row's sums, of s_k S, is m0 + m. A score is x a - m a, rounded once; past kFar that would be off by half of
-        // FP32's spacing for the largest score too, whose weight is to be one. A warp that meets such a score (far) takes m0 off x first.
+        // FP32's spacing for the largest score too, whose weight is to be one. A warp that meets such a score (far) takes m0 off x first,
+        // where its masked columns are selected. (The listed 8-bit case 460 -> 466 us; as a branch before the exponents 498, in code of its
+        // own 465 to 476 and a microsecond more for short prompts.)
         float m = -CUDART_INF_F, m0 = 0.0f;
         bool far = false;
         uint64_t l2 = 0;           // sums of even and odd columns
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
             const int en = sh.ev[s2];
             const uint2 ow = *reinterpret_cast<const uint2*>(&sh.odd[s2][2 * half]);
             // seldom: rows whose maximum grew (a first one by infinity), larger scales of V, a NaN among them. One vote for all of it,
-            // where a branch for each took 400 of a half's 2260 cycles (378 -> 345 us, as above)
+            // where a branch for each took 400 of a half's 2260 cycles (378 -> 345 us, 4000 rows over 8000 tokens)
             const bool grew = (top - m) * a > (float)kGrow;
             if (__any_sync(0xffffffffu, grew || en != ev || (ow.x | ow.y) != 0u)) {
                 if (ow.x | ow.y)   // a NaN in V's scales shows in the rows that see it

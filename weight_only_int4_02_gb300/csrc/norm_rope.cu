@@ -10,7 +10,7 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kWarps = 2;       // of a CTA: larger ones leave the GPU waiting for their last warps (eight 54.6 us, two 52.0, as below)
+constexpr int kWarps = 2;       // of a CTA: larger ones leave the GPU waiting for their last warps (eight 54.6 us where two took 52.0, as below)
 constexpr int kRowsAhead = 4;   // rows of a lane group that are loaded together
 constexpr int kMostPasses = 4;
 
