@@ -563,8 +563,9 @@ int w4a16_kv4_force_path(int path);
  * position: pair i, of angle i, is (x[i], x[i + rot / 2]), or (x[2i], x[2i + 1]) if `interleaved` is 1 (0 otherwise):
  *   (a, b) -> (a cos - b sin, b cos + a sin)       in FP32
  * w4a16_kv8_append rounds each product and sum of it; w4a16_qk_norm_rope puts its factors together first and sums by fused
- * operations, so the two may differ in an FP32 number's last bits. The angles' cosines and sines come from a table, device float [rope_rows][rot], 16-byte aligned: of each position rot / 2
- * cosines, then rot / 2 sines. Scaled or learned angles are a matter of the table.
+ * operations, so the two may differ in an FP32 number's last bits. The angles' cosines and sines come from a table, device
+ * float [rope_rows][rot], 16-byte aligned: of each position rot / 2 cosines, then rot / 2 sines. Scaled or learned angles
+ * are a matter of the table.
  *
  * w4a16_rope_table fills one with the angles p * base^(-2i / rot) of positions p = 0 .. rows - 1, computed in 64 bits. */
 w4a16_status w4a16_rope_table(float* table, int rows, int rot, double base, w4a16_stream_t stream);
@@ -572,7 +573,8 @@ w4a16_status w4a16_rope_table(float* table, int rows, int rot, double base, w4a1
 /*
  * Norms of queries and keys for each head, then the rotation, in one pass; rounded once:
  *   y = x / sqrt(mean(x^2) + eps) * weight, over a row of head_dim values, mean and factors in FP32
- * Before that rounding a result is within 2^-20 of |y| (rotated: of |a cos| + |b sin|) of its value.
+ * Before that rounding a result is within 2^-20 of |y| (rotated: of |a cos| + |b sin|) of its value, where no square or
+ * sum of squares passes FP32's range (bfloat16 values above 2^63 have an infinite mean, and their row becomes 0).
  *   q, k       device, binary16 or bfloat16 [tokens][heads][head_dim] at token and head strides in elements (multiples of
  *              8, at least head_dim), 16-byte aligned. q_heads or kv_heads 0: without queries or keys, whose
  *              pointers and strides are then not looked at

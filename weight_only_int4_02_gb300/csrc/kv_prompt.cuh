@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const Kv4AttnPar
         const int pos_max = t_row0 < rows ? pos0 + (t_last - 1) / p.group : -1;
         // The reference of the row's sums, of s_k S, is m0 + m. A score is x a - m a, rounded once; past kFar that would be off by half of
         // FP32's spacing for the largest score too, whose weight is to be one. A warp that meets such a score (far) takes m0 off x first,
-        // where its masked columns are selected. (The listed 8-bit case 460 -> 466 us; as a branch before the exponents 498, in code of its
+        // where its masked columns are selected. (Three requests' chunks over 8 bits, as above, 460 -> 466 us; as a branch before the exponents 498, in code of its
         // own 465 to 476 and a microsecond more for short prompts.)
         float m = -CUDART_INF_F, m0 = 0.0f;
         bool far = false;
