@@ -574,7 +574,7 @@ w4a16_status w4a16_rope_table(float* table, int rows, int rot, double base, w4a1
  * Norms of queries and keys for each head, then the rotation, in one pass; rounded once:
  *   y = x / sqrt(mean(x^2) + eps) * weight, over a row of head_dim values, mean and factors in FP32
  * Before that rounding a result is within 2^-20 of |y| (rotated: of |a cos| + |b sin|) of its value, where no square or
- * sum of squares passes FP32's range (bfloat16 values above 2^63 have an infinite mean, and their row becomes 0).
+ * sum of squares passes FP32's range (the mean of bfloat16 values above 2^63 is infinite).
  *   q, k       device, binary16 or bfloat16 [tokens][heads][head_dim] at token and head strides in elements (multiples of
  *              8, at least head_dim), 16-byte aligned. q_heads or kv_heads 0: without queries or keys, whose
  *              pointers and strides are then not looked at
