@@ -20,7 +20,7 @@ def _gpu():
         pytest.skip("no CUDA device")
 
 
-def compare(bits, path, nq, dtype, k, v, q, powers, scales, least=1000):
+def compare(bits, path, nq, dtype, k, v, q, powers, scales, least=1000, window=0):
     """Attention of the last nq tokens over keys and values [seq][heads][D], for queries q [nq][2 heads * group][D] of several
     sizes. Keys that are not the largest lie `least` below it; those that are equal share."""
     from weight_only_int4_02_gb300 import w4a16
@@ -39,9 +39,10 @@ def compare(bits, path, nq, dtype, k, v, q, powers, scales, least=1000):
         for power in powers:
             for scale in scales if power < 110 else (1.0,):
                 x = (q * (2.0 ** power if scale > 0 else -2.0 ** power)).to(t)
-                out, lse = attention(x.cuda(), cache, table, lens, starts, page, nq, scale=scale, return_lse=True)
+                out, lse = attention(x.cuda(), cache, table, lens, starts, page, nq, scale=scale, window=window, return_lse=True)
                 s = torch.einsum("thgd,khd->thgk", x.double().view(nq, heads, group, D), key) * scale
-                s = s.masked_fill(torch.arange(seq) > torch.arange(seq - nq, seq).view(-1, 1, 1, 1), -np.inf)
+                at, pos = torch.arange(seq), torch.arange(seq - nq, seq).view(-1, 1, 1, 1)
+                s = s.masked_fill((at > pos) | (at <= pos - (window or seq)), -np.inf)
                 top = s.amax(-1, keepdim=True)
                 equal = s >= top * (1 - 1e-12)
                 assert (equal | (s < top - least)).all()
@@ -88,3 +89,18 @@ def test_scores_that_pass_the_far_ones_step_by_step(bits, path, nq, D, dtype, or
     k, v = along * size.view(-1, 1, 1), torch.randn(seq, heads, D, generator=g)
     q = along.repeat_interleave(group, 0).expand(nq, -1, -1).double()
     compare(bits, path, nq, dtype, k, v, q, (8, 12, 14) if dtype == "float16" else (8, 12, 14, 18, 40), (1.0, 17.3, -17.3))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("path,nq", [(1, 2), (2, 70)])
+@pytest.mark.parametrize("D,dtype", [(64, "bfloat16"), (128, "float16")])
+@pytest.mark.parametrize("window", [0, 777])
+def test_far_scores_in_the_parts_of_a_long_request(bits, path, nq, D, dtype, window):
+    """Parts whose references lie far apart are joined, some of them with nothing but small scores; a window's edge moves with the query."""
+    heads, group, seq = 1, 3, 3100
+    g = torch.Generator().manual_seed(seq)
+    along = torch.randn(heads, D, generator=g).sign()
+    step = torch.randint(0, 20, (seq // 50 + 1,), generator=g).repeat_interleave(50)[:seq]
+    k, v = along * (0.875 ** step).view(-1, 1, 1), torch.randn(seq, heads, D, generator=g) * torch.exp(torch.randn(seq, 1, 1, generator=g))
+    q = along.repeat_interleave(group, 0).expand(nq, -1, -1).double()
+    compare(bits, path, nq, dtype, k, v, q, (12, 14) if dtype == "float16" else (12, 18, 40), (1.0, -17.3), least=100, window=window)
